@@ -336,6 +336,48 @@ int dgc_sum_shared_workspace(int32_t W, size_t* bytes);
 int dgc_sum_shared(const float* const* vals, int32_t W, const int64_t* count, int64_t max_count,
                    float* out, int32_t* status, void* ws, size_t ws_bytes, dgc_stream_t stream);
 
+/* ------------------------------------------------- gradient tensors: norm and clipping */
+
+/* Element types of the calls below. */
+enum { DGC_F32 = 0, DGC_F16 = 1, DGC_BF16 = 2 };
+
+/* One tensor as a run of n entries in memory. */
+typedef struct {
+    void* data;       /* device, aligned to the element size (16-byte alignment is faster) */
+    int64_t n;        /* entries; 0 allowed (data may then be NULL) */
+    int32_t dtype;    /* DGC_F32, DGC_F16 or DGC_BF16 */
+    int32_t reserved; /* 0 */
+} dgc_tensor;
+
+/* Bytes of workspace the two calls below need for a list of count tensors. */
+int dgc_grad_workspace(const dgc_tensor* src, int32_t count, size_t* bytes);
+
+/* The global L2 norm of a step's gradient tensors, and the factor that clips them to it.
+ * dgc_compress clips every segment by the segment's own norm; this is the norm over all of them.
+ *   norm  = sqrt(sum over all tensors and entries of g^2)
+ *   scale = max_norm / norm where norm > max_norm, else 1
+ * Squares are summed in binary32 over at most 64 entries of a thread and in binary64 from there
+ * on, in an order that depends on the sizes alone: the same inputs give the same bits on every
+ * run. Magnitudes whose squares leave the binary32 range are summed scaled, so the norm is right
+ * for every finite input whose norm is. A NaN entry makes norm NaN (scale 1, as in
+ * dgc_compress), else an infinite one makes it +inf (scale 0).
+ *   src       host array of count tensors (0 allowed: norm 0, scale 1); read only
+ *   max_norm  <= 0 or +inf: no clipping (scale 1); NaN returns DGC_EINVAL
+ *   norm, scale  device, one binary32 each
+ *   ws        device workspace, ws_bytes >= dgc_grad_workspace(...)
+ * Both calls enqueue kernels only and read the host arrays before they return. */
+int dgc_grad_norm(const dgc_tensor* src, int32_t count, float max_norm, float* norm, float* scale,
+                  void* ws, size_t ws_bytes, dgc_stream_t stream);
+
+/* dgc_grad_norm, then dst_i = src_i * scale (one binary32 product, rounded to dst's type).
+ *   dst  host array of count tensors with src's entry counts and any of the types; NULL or src's
+ *        own addresses and types: in place (then nothing is written where scale is 1). Tensors
+ *        of dst may be consecutive pieces of one binary32 array: the clipped gradient is then
+ *        in the flat bucket that dgc_compress takes. Apart from equal addresses, dst must not
+ *        overlap src. */
+int dgc_grad_clip(const dgc_tensor* src, const dgc_tensor* dst, int32_t count, float max_norm,
+                  float* norm, float* scale, void* ws, size_t ws_bytes, dgc_stream_t stream);
+
 /* -------------------------------------------------------------------------- utilities */
 
 /* Synchronize `stream`, then return the int32 at status_dev (or DGC_ECUDA). */

@@ -22,6 +22,8 @@ __all__ = [
     "dgc_encode_quant", "dgc_decode_workspace_quant", "dgc_decode_accumulate_quant",
     "dgc_decode_apply_quant", "dgc_compress_shared", "dgc_sum_shared_workspace",
     "dgc_sum_shared",
+    "F32", "F16", "BF16", "dgc_tensor", "TensorList",
+    "dgc_grad_workspace", "dgc_grad_norm", "dgc_grad_clip",
     "dgc_read_status", "dgc_status_string", "dgc_launch_count", "dgc_selftest_wait_timeout",
     "dgc_set_l2_fetch_granularity",
     "dgc_profile_stream_pass",
@@ -31,6 +33,7 @@ __all__ = [
 OK, EINVAL, ECAPACITY, ECUDA, ETIMEOUT, ECORRUPT, EUNSUPPORTED = 0, -1, -2, -3, -4, -5, -6
 SELECT_EXACT, SELECT_SAMPLED, SELECT_ADACOMP = 0, 1, 2
 FLAG_MASK_MOMENTUM = 1
+F32, F16, BF16 = 0, 1, 2
 
 
 class dgc_params(ctypes.Structure):
@@ -58,6 +61,15 @@ class dgc_seg_stats(ctypes.Structure):
         ("reselected", ctypes.c_uint32),
         ("clip_scale", ctypes.c_float),
         ("clip_sumsq", ctypes.c_double),
+    ]
+
+
+class dgc_tensor(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
     ]
 
 
@@ -111,6 +123,9 @@ def lib():
                                           vp, vp, vp, sz, vp]
         L.dgc_sum_shared_workspace.argtypes = [i32, P(sz)]
         L.dgc_sum_shared.argtypes = [vp, i32, vp, i64, vp, vp, vp, sz, vp]
+        L.dgc_grad_workspace.argtypes = [vp, i32, P(sz)]
+        L.dgc_grad_norm.argtypes = [vp, i32, f32, vp, vp, vp, sz, vp]
+        L.dgc_grad_clip.argtypes = [vp, vp, i32, f32, vp, vp, vp, sz, vp]
         L.dgc_read_status.argtypes = [vp, vp]
         L.dgc_status_string.argtypes = [ctypes.c_int]
         L.dgc_status_string.restype = ctypes.c_char_p
@@ -130,6 +145,7 @@ def lib():
                   "dgc_encode_quant", "dgc_decode_workspace_quant",
                   "dgc_decode_accumulate_quant", "dgc_decode_apply_quant",
                   "dgc_compress_shared", "dgc_sum_shared_workspace", "dgc_sum_shared",
+                  "dgc_grad_workspace", "dgc_grad_norm", "dgc_grad_clip",
                   "dgc_read_status",
                   "dgc_selftest_wait_timeout"):
             getattr(L, f).restype = ctypes.c_int
@@ -401,6 +417,63 @@ def dgc_sum_shared(vals, count, max_count: int, out, status, ws, ws_bytes: int |
     return _check(lib().dgc_sum_shared(ctypes.cast(ptrs, ctypes.c_void_p), W, _ptr(count),
                                        int(max_count), _ptr(out), _ptr(status), _ptr(ws),
                                        int(ws_bytes), _stream(stream)), "dgc_sum_shared")
+
+
+# ------------------------------------------------------- gradient tensors: norm and clipping
+def _dtype_code(t) -> int:
+    import torch
+
+    codes = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+    if t.dtype not in codes:
+        raise DGCError(EINVAL, f"tensor of type {t.dtype}")
+    return codes[t.dtype]
+
+
+class TensorList:
+    """The tensors of one call as the host array the C calls take. It keeps the tensors alive
+    and reads their addresses once: build it when the gradient buffers are allocated and pass it
+    to every step's calls."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        self.array = (dgc_tensor * max(len(self.tensors), 1))()
+        for i, t in enumerate(self.tensors):
+            if not t.is_contiguous():
+                raise DGCError(EINVAL, f"TensorList: tensor {i} is not contiguous")
+            self.array[i] = dgc_tensor(t.data_ptr(), t.numel(), _dtype_code(t), 0)
+        self.address = ctypes.addressof(self.array)
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def dgc_grad_workspace(src: TensorList) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().dgc_grad_workspace(src.address, len(src), ctypes.byref(out)),
+           "dgc_grad_workspace")
+    return out.value
+
+
+def dgc_grad_norm(src: TensorList, max_norm: float, norm, scale, ws, ws_bytes: int | None = None,
+                  stream=None) -> int:
+    """norm, scale: float32 CUDA tensors (1): the global L2 norm of src's tensors, and the factor
+    that clips them to max_norm."""
+    ws_bytes = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    return _check(lib().dgc_grad_norm(src.address, len(src), float(max_norm), _ptr(norm),
+                                      _ptr(scale), _ptr(ws), int(ws_bytes), _stream(stream)),
+                  "dgc_grad_norm")
+
+
+def dgc_grad_clip(src: TensorList, dst: TensorList | None, max_norm: float, norm, scale, ws,
+                  ws_bytes: int | None = None, stream=None) -> int:
+    """dgc_grad_norm, then dst = src * scale (dst None: in place). With dst the pieces of a flat
+    float32 buffer, the clipped gradients land where dgc_compress reads them."""
+    ws_bytes = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    if dst is not None and len(dst) != len(src):
+        raise DGCError(EINVAL, "dgc_grad_clip: lists of different lengths")
+    return _check(lib().dgc_grad_clip(src.address, None if dst is None else dst.address, len(src),
+                                      float(max_norm), _ptr(norm), _ptr(scale), _ptr(ws),
+                                      int(ws_bytes), _stream(stream)), "dgc_grad_clip")
 
 
 # ----------------------------------------------------------------------------- utilities

@@ -1,0 +1,489 @@
+// grad.cu -- the global norm of a step's gradient tensors, and clipping by it (sm_103a).
+//
+//   k_grad_table   writes the table of tensors into the workspace when it is too long for a
+//                  kernel's parameters (a launch per kTableCap tensors).
+//   k_grad_norm    one pass over all tensors: partial sums of squares, one binary64 per block.
+//   k_grad_finish  joins the partial sums: norm and scale (dgc_grad_norm).
+//   k_grad_scale   joins the partial sums in every block, then dst = src * scale
+//                  (dgc_grad_clip).
+//
+// The work unit is a warp tile of 2048 entries of one tensor. Warps take contiguous ranges of
+// tiles, so a warp looks its tensor up once and then steps through the table; no warp waits on
+// another until the block's last reduction.
+#include <cmath>
+#include <type_traits>
+
+#include "dgc_device.cuh"
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace dgc {
+namespace {
+
+constexpr int kGradThreads = 256;
+constexpr int kGradWarps = kGradThreads / 32;
+constexpr uint32_t kWarpTile = 2048;
+constexpr int kTableCap = 960;      // tensors in one kernel's parameters (27 KB of 32 KB)
+constexpr int kMidTable = 192;      // ... of the variants for shorter lists, whose launches
+constexpr int kSmallTable = 24;     // copy fewer bytes
+constexpr int kBlocksPerSm = 3;      // 85 registers a thread: at 64 the norm kernel spills
+constexpr int64_t kMaxTensors = 1 << 20;
+
+// One tensor: source, destination (0 for the norm alone), entries, types, first warp tile.
+struct GradEntry {
+    const void* src;
+    void* dst;
+    uint64_t n;          // entries in bits 0..55, source type in 56..59, destination in 60..63
+    __host__ __device__ uint64_t count() const { return n & ((1ull << 56) - 1); }
+    __host__ __device__ int src_type() const { return (int)(n >> 56) & 15; }
+    __host__ __device__ int dst_type() const { return (int)(n >> 60) & 15; }
+};
+
+template <int kCap>
+struct GradTable {
+    GradEntry e[kCap];
+    uint32_t first[kCap + 1];  // first[count] = number of warp tiles
+};
+
+struct GradArgs {
+    const GradEntry* entries;  // in the workspace; null: the table is in the parameters
+    const uint32_t* first;
+    int32_t count;
+    uint32_t tiles;
+    double* partial;           // one per block of k_grad_norm
+    int32_t nparts;
+    float max_norm;            // 0: no clipping
+    int32_t in_place;
+    float *norm, *scale;
+};
+
+__device__ __forceinline__ void pdl_wait() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_launch() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+__global__ void __launch_bounds__(256) k_grad_table(const __grid_constant__ GradTable<kTableCap> t,
+                                                    int32_t n, GradEntry* entries,
+                                                    uint32_t* first) {
+    for (int i = threadIdx.x; i < n; i += blockDim.x) entries[i] = t.e[i];
+    for (int i = threadIdx.x; i <= n; i += blockDim.x) first[i] = t.first[i];
+}
+
+template <typename T>
+struct Cvt;
+template <>
+struct Cvt<float> {
+    __device__ static float up(float x) { return x; }
+    __device__ static float down(float x) { return x; }
+};
+template <>
+struct Cvt<__half> {
+    __device__ static float up(__half x) { return __half2float(x); }
+    __device__ static __half down(float x) { return __float2half_rn(x); }
+};
+template <>
+struct Cvt<__nv_bfloat16> {
+    __device__ static float up(__nv_bfloat16 x) { return __bfloat162float(x); }
+    __device__ static __nv_bfloat16 down(float x) { return __float2bfloat16_rn(x); }
+};
+
+template <typename T, int kN>
+struct alignas(sizeof(T) * kN) Vec {
+    T v[kN];
+};
+
+// ------------------------------------------------------------------------------- the sum
+// A lane's squares of up to 64 entries, as one binary64 number. The squares are summed in
+// binary32 (four chains of at most 16 fused multiply-adds; all terms are positive, so the chains
+// lose at most 16 * 2^-24 of their sum) and the chains joined in binary64: binary64 for every
+// entry would be bound by its arithmetic, 1/64 of binary32's rate. A sum outside [2^-90, 2^126]
+// may have lost squares to underflow or overflow: it is taken again with the entries scaled by
+// 2^90 or 2^-70, where neither can happen to any finite entry (below the first limit every entry
+// is under 2^-45, and the least subnormal's square becomes 2^-118; above the second limit the
+// largest square becomes 2^116). What is still not finite there holds an infinity or a NaN.
+template <typename T, int kV, int kN>
+__device__ __forceinline__ float chain_sum(const Vec<T, kV> (&w)[kN], float f) {
+    static_assert(kV * kN <= 64, "four chains of at most 16");
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+            const float y = Cvt<T>::up(w[i].v[j]) * f;
+            s[(i * kV + j) & 3] = fmaf(y, y, s[(i * kV + j) & 3]);
+        }
+    return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+template <typename T, int kV, int kN>
+__device__ __forceinline__ double squares(const Vec<T, kV> (&w)[kN]) {
+    const float s = chain_sum(w, 1.0f);
+    if (s >= 0x1p-90f && s <= 0x1p126f) return (double)s;
+    if (s < 0x1p-90f) return (double)chain_sum(w, 0x1p90f) * 0x1p-180;
+    return (double)chain_sum(w, 0x1p-70f) * 0x1p140;
+}
+
+// Entries [begin, begin + 2048) of one tensor, by one warp: 16-byte loads where the address
+// allows (kV entries each), entry by entry at the ends and for unaligned tensors.
+template <typename T>
+__device__ __forceinline__ double tile_squares(const T* p, uint64_t n, uint64_t begin) {
+    constexpr int kV = 16 / sizeof(T);
+    constexpr int kLoads = kWarpTile / 32 / kV;         // 16 or 8 loads of 16 bytes a lane
+    constexpr int kStep = kLoads < 8 ? kLoads : 8;      // in flight together
+    const int lane = threadIdx.x & 31;
+    const uint32_t m = (uint32_t)umin64(kWarpTile, n - begin);
+    const T* q = p + begin;
+    double sum = 0.0;
+    if (m == kWarpTile && ((uintptr_t)q & 15u) == 0) {
+#pragma unroll 1
+        for (int h = 0; h < kLoads; h += kStep) {
+            Vec<T, kV> w[kStep];
+#pragma unroll
+            for (int i = 0; i < kStep; ++i)
+                w[i] = *reinterpret_cast<const Vec<T, kV>*>(q + ((h + i) * 32 + lane) * kV);
+            sum += squares(w);
+        }
+        return sum;
+    }
+    for (uint32_t h = 0; h < m; h += 32 * 8) {
+        Vec<T, 1> x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t at = h + i * 32 + lane;
+            x[i].v[0] = at < m ? q[at] : Cvt<T>::down(0.0f);
+        }
+        sum += squares(x);
+    }
+    return sum;
+}
+
+// The block's sum of one binary64 per thread, in a fixed order; valid in every thread.
+__device__ __forceinline__ double block_sum(double x, double* sm) {
+    x = warp_sum(x);
+    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = x;
+    __syncthreads();
+    double s = 0.0;
+#pragma unroll
+    for (int w = 0; w < kGradWarps; ++w) s += sm[w];
+    __syncthreads();
+    return s;
+}
+
+// The warp's tiles: [t0, t1) of all tiles, by an even split.
+__device__ __forceinline__ void warp_range(uint32_t tiles, uint32_t* t0, uint32_t* t1) {
+    const uint64_t w = (uint64_t)blockIdx.x * kGradWarps + (threadIdx.x >> 5);
+    const uint64_t all = (uint64_t)gridDim.x * kGradWarps;
+    *t0 = (uint32_t)(w * tiles / all);
+    *t1 = (uint32_t)((w + 1) * tiles / all);
+}
+
+// Bound by HBM: one read of every entry, one multiply-add each (16-bit types: and a conversion).
+template <int kCap>
+__global__ void __launch_bounds__(kGradThreads, kBlocksPerSm)
+    k_grad_norm(const __grid_constant__ GradArgs a, const __grid_constant__ GradTable<kCap> tab) {
+    __shared__ double sm[kGradWarps];
+    pdl_wait();
+    pdl_launch();
+    const GradEntry* entries = a.entries ? a.entries : tab.e;
+    const uint32_t* first = a.entries ? a.first : tab.first;
+    uint32_t t0, t1;
+    warp_range(a.tiles, &t0, &t1);
+    double sum = 0.0;
+    if (t0 < t1) {
+        int e = upper_bound_minus1(first, a.count, t0);
+        for (uint32_t t = t0; t < t1; ++t) {
+            while (t >= first[e + 1]) ++e;
+            const GradEntry g = entries[e];
+            const uint64_t begin = (uint64_t)(t - first[e]) * kWarpTile;
+            if (g.src_type() == DGC_F32)
+                sum += tile_squares((const float*)g.src, g.count(), begin);
+            else if (g.src_type() == DGC_F16)
+                sum += tile_squares((const __half*)g.src, g.count(), begin);
+            else
+                sum += tile_squares((const __nv_bfloat16*)g.src, g.count(), begin);
+        }
+    }
+    sum = block_sum(sum, sm);
+    if (threadIdx.x == 0) a.partial[blockIdx.x] = sum;
+}
+
+// norm = sqrt(sum of the partial sums), scale = max_norm / norm where norm > max_norm, else 1
+// (a NaN norm compares false: scale 1; an infinite one gives 0). Binary64, rounded once.
+__device__ __forceinline__ float join(const GradArgs& a, double* sm, bool write) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < a.nparts; i += kGradThreads) s += a.partial[i];
+    const double norm = sqrt(block_sum(s, sm));
+    const float scale =
+        (a.max_norm > 0.0f && norm > (double)a.max_norm) ? (float)((double)a.max_norm / norm) : 1.0f;
+    if (write && threadIdx.x == 0) {
+        *a.norm = (float)norm;
+        *a.scale = scale;
+    }
+    return scale;
+}
+
+__global__ void __launch_bounds__(kGradThreads) k_grad_finish(const __grid_constant__ GradArgs a) {
+    __shared__ double sm[kGradWarps];
+    pdl_wait();
+    join(a, sm, true);
+}
+
+// ------------------------------------------------------------------------------- clipping
+template <typename S, typename D>
+__device__ __forceinline__ void tile_scale(const S* p, D* d, uint64_t n, uint64_t begin, float f) {
+    constexpr int kV = (sizeof(S) == 4 || sizeof(D) == 4) ? 4 : 8;
+    constexpr int kSteps = kWarpTile / 32 / kV;
+    constexpr int kStep = 8;  // loads in flight together
+    const int lane = threadIdx.x & 31;
+    const uint32_t m = (uint32_t)umin64(kWarpTile, n - begin);
+    const S* q = p + begin;
+    D* o = d + begin;
+    if (m == kWarpTile && ((uintptr_t)q & (sizeof(S) * kV - 1)) == 0 &&
+        ((uintptr_t)o & (sizeof(D) * kV - 1)) == 0) {
+#pragma unroll 1
+        for (int h = 0; h < kSteps; h += kStep) {
+            Vec<S, kV> w[kStep];
+#pragma unroll
+            for (int i = 0; i < kStep; ++i)
+                w[i] = *reinterpret_cast<const Vec<S, kV>*>(q + ((h + i) * 32 + lane) * kV);
+#pragma unroll
+            for (int i = 0; i < kStep; ++i) {
+                Vec<D, kV> r;
+#pragma unroll
+                for (int j = 0; j < kV; ++j) r.v[j] = Cvt<D>::down(Cvt<S>::up(w[i].v[j]) * f);
+                *reinterpret_cast<Vec<D, kV>*>(o + ((h + i) * 32 + lane) * kV) = r;
+            }
+        }
+        return;
+    }
+    for (uint32_t h = 0; h < m; h += 32 * 8) {
+        S x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t at = h + i * 32 + lane;
+            x[i] = at < m ? q[at] : Cvt<S>::down(0.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t at = h + i * 32 + lane;
+            if (at < m) o[at] = Cvt<D>::down(Cvt<S>::up(x[i]) * f);
+        }
+    }
+}
+
+template <typename S>
+__device__ __forceinline__ void tile_scale_to(const GradEntry& g, uint64_t begin, float f) {
+    const S* p = (const S*)g.src;
+    if (g.dst_type() == DGC_F32)
+        tile_scale(p, (float*)g.dst, g.count(), begin, f);
+    else if (g.dst_type() == DGC_F16)
+        tile_scale(p, (__half*)g.dst, g.count(), begin, f);
+    else
+        tile_scale(p, (__nv_bfloat16*)g.dst, g.count(), begin, f);
+}
+
+// Bound by HBM: every entry read again and written. A warp walks the tiles that the same warp of
+// k_grad_norm read, from the last one back, so that what the norm read last is still in L2.
+template <int kCap>
+__global__ void __launch_bounds__(kGradThreads, kBlocksPerSm)
+    k_grad_scale(const __grid_constant__ GradArgs a, const __grid_constant__ GradTable<kCap> tab) {
+    __shared__ double sm[kGradWarps];
+    const GradEntry* entries = a.entries ? a.entries : tab.e;
+    const uint32_t* first = a.entries ? a.first : tab.first;
+    pdl_wait();
+    const float f = join(a, sm, blockIdx.x == 0);
+    if (a.in_place && f == 1.0f) return;
+    uint32_t t0, t1;
+    warp_range(a.tiles, &t0, &t1);
+    if (t0 >= t1) return;
+    int e = upper_bound_minus1(first, a.count, t1 - 1);
+    for (uint32_t t = t1; t-- > t0;) {
+        while (t < first[e]) --e;
+        const GradEntry g = entries[e];
+        const uint64_t begin = (uint64_t)(t - first[e]) * kWarpTile;
+        if (g.src_type() == DGC_F32)
+            tile_scale_to<float>(g, begin, f);
+        else if (g.src_type() == DGC_F16)
+            tile_scale_to<__half>(g, begin, f);
+        else
+            tile_scale_to<__nv_bfloat16>(g, begin, f);
+    }
+}
+
+// ----------------------------------------------------------------------------------- host
+size_t type_size(int32_t t) { return t == DGC_F32 ? 4 : 2; }
+
+// Checks a list and counts its warp tiles.
+int check_list(const dgc_tensor* t, int32_t count, uint64_t* tiles) {
+    if (count < 0 || (count > 0 && !t)) return DGC_EINVAL;
+    if (count > kMaxTensors) return DGC_EUNSUPPORTED;
+    uint64_t sum = 0;
+    for (int32_t i = 0; i < count; ++i) {
+        if (t[i].n < 0 || t[i].reserved != 0) return DGC_EINVAL;
+        if (t[i].dtype != DGC_F32 && t[i].dtype != DGC_F16 && t[i].dtype != DGC_BF16)
+            return DGC_EINVAL;
+        if (t[i].n > 0 && (!t[i].data || ((uintptr_t)t[i].data & (type_size(t[i].dtype) - 1))))
+            return DGC_EINVAL;
+        if (t[i].n > (1ll << 42)) return DGC_EUNSUPPORTED;
+        sum += ((uint64_t)t[i].n + kWarpTile - 1) / kWarpTile;
+        if (sum > 0x7FFFFFFFull) return DGC_EUNSUPPORTED;
+    }
+    *tiles = sum;
+    return DGC_OK;
+}
+
+struct GradLayout {
+    size_t partial, entries, first, total;
+};
+GradLayout grad_layout(int32_t count) {
+    auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    GradLayout L{};
+    L.partial = 0;
+    L.entries = up(sizeof(double) * 4096);  // blocks of k_grad_norm: at most 4096
+    L.first = L.entries;
+    L.total = L.entries;
+    if (count > kTableCap) {
+        L.first = up(L.entries + sizeof(GradEntry) * (size_t)count);
+        L.total = up(L.first + sizeof(uint32_t) * ((size_t)count + 1));
+    }
+    return L;
+}
+
+// A launch that may start while the kernel ahead of it ends (it waits before it reads).
+template <typename... A>
+int launch(void (*kernel)(A...), unsigned grid, cudaStream_t s, const std::decay_t<A>&... args) {
+    void* ptrs[] = {const_cast<void*>(static_cast<const void*>(&args))...};
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(grid);
+    c.blockDim = dim3(kGradThreads);
+    c.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = at;
+    c.numAttrs = 1;
+    if (cudaLaunchKernelExC(&c, reinterpret_cast<const void*>(kernel), ptrs) != cudaSuccess) {
+        cudaGetLastError();
+        return DGC_ECUDA;
+    }
+    dgc_internal_count_launches(1);
+    return DGC_OK;
+}
+
+template <int kCap>
+void fill(GradTable<kCap>* t, const dgc_tensor* src, const dgc_tensor* dst, int32_t count,
+          uint32_t* tile) {
+    for (int32_t i = 0; i < count; ++i) {
+        const dgc_tensor& d = dst ? dst[i] : src[i];
+        t->e[i].src = src[i].data;
+        t->e[i].dst = d.data;
+        t->e[i].n = (uint64_t)src[i].n | ((uint64_t)src[i].dtype << 56) | ((uint64_t)d.dtype << 60);
+        t->first[i] = *tile;
+        *tile += (uint32_t)(((uint64_t)src[i].n + kWarpTile - 1) / kWarpTile);
+    }
+    t->first[count] = *tile;
+}
+
+template <int kCap>
+int run(const dgc_tensor* src, const dgc_tensor* dst, int32_t count, bool clip, GradArgs a,
+        unsigned grid, cudaStream_t s) {
+    GradTable<kCap> tab;
+    if (!a.entries) {
+        uint32_t tile = 0;
+        fill(&tab, src, dst, count, &tile);
+    }
+    int rc = launch(k_grad_norm<kCap>, grid, s, a, tab);
+    if (rc) return rc;
+    if (!clip) return launch(k_grad_finish, 1, s, a);
+    return launch(k_grad_scale<kCap>, grid, s, a, tab);
+}
+
+int grad_call(const dgc_tensor* src, const dgc_tensor* dst, int32_t count, float max_norm,
+              bool clip, float* norm, float* scale, void* ws, size_t ws_bytes,
+              dgc_stream_t stream) {
+    uint64_t tiles = 0, dst_tiles = 0;
+    if (std::isnan(max_norm) || !norm || !scale || !ws || ((uintptr_t)ws & 255u)) return DGC_EINVAL;
+    int rc = check_list(src, count, &tiles);
+    if (rc) return rc;
+    bool in_place = true;
+    if (clip && dst) {
+        rc = check_list(dst, count, &dst_tiles);
+        if (rc) return rc;
+        for (int32_t i = 0; i < count; ++i) {
+            if (dst[i].n != src[i].n) return DGC_EINVAL;
+            if (src[i].n == 0) continue;
+            if (dst[i].data != src[i].data)
+                in_place = false;
+            else if (dst[i].dtype != src[i].dtype)
+                return DGC_EINVAL;
+        }
+    }
+    const GradLayout L = grad_layout(count);
+    if (ws_bytes < L.total) return DGC_EINVAL;
+    const int sms = dgc_internal_sm_count();
+    if (sms <= 0) return DGC_ECUDA;
+
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    char* w = static_cast<char*>(ws);
+    GradArgs a{};
+    a.count = count;
+    a.tiles = (uint32_t)tiles;
+    a.partial = reinterpret_cast<double*>(w + L.partial);
+    a.max_norm = (max_norm > 0.0f && !std::isinf(max_norm)) ? max_norm : 0.0f;
+    a.in_place = in_place;
+    a.norm = norm;
+    a.scale = scale;
+    const uint64_t want = (tiles + kGradWarps - 1) / kGradWarps;
+    const uint64_t most = umin64(4096, (uint64_t)sms * kBlocksPerSm);
+    const unsigned grid = (unsigned)umin64(want ? want : 1, most);
+    a.nparts = (int32_t)grid;
+    if (count <= kSmallTable) return run<kSmallTable>(src, dst, count, clip, a, grid, s);
+    if (count <= kMidTable) return run<kMidTable>(src, dst, count, clip, a, grid, s);
+    if (count <= kTableCap) return run<kTableCap>(src, dst, count, clip, a, grid, s);
+
+    // a long list: its table goes to the workspace in the parameters of a launch per part
+    GradEntry* entries = reinterpret_cast<GradEntry*>(w + L.entries);
+    uint32_t* first = reinterpret_cast<uint32_t*>(w + L.first);
+    uint32_t tile = 0;
+    for (int32_t at = 0; at < count; at += kTableCap) {
+        GradTable<kTableCap> tab;
+        const int32_t m = count - at < kTableCap ? count - at : kTableCap;
+        fill(&tab, src + at, dst ? dst + at : nullptr, m, &tile);
+        k_grad_table<<<1, 256, 0, s>>>(tab, m, entries + at, first + at);
+        if (cudaPeekAtLastError() != cudaSuccess) {
+            cudaGetLastError();
+            return DGC_ECUDA;
+        }
+        dgc_internal_count_launches(1);
+    }
+    a.entries = entries;
+    a.first = first;
+    return run<kSmallTable>(src, dst, count, clip, a, grid, s);
+}
+
+}  // namespace
+}  // namespace dgc
+
+using namespace dgc;
+
+extern "C" int dgc_grad_workspace(const dgc_tensor* src, int32_t count, size_t* bytes) {
+    uint64_t tiles = 0;
+    if (!bytes) return DGC_EINVAL;
+    const int rc = check_list(src, count, &tiles);
+    if (rc) return rc;
+    *bytes = grad_layout(count).total;
+    return DGC_OK;
+}
+
+extern "C" int dgc_grad_norm(const dgc_tensor* src, int32_t count, float max_norm, float* norm,
+                             float* scale, void* ws, size_t ws_bytes, dgc_stream_t stream) {
+    return grad_call(src, nullptr, count, max_norm, false, norm, scale, ws, ws_bytes, stream);
+}
+
+extern "C" int dgc_grad_clip(const dgc_tensor* src, const dgc_tensor* dst, int32_t count,
+                             float max_norm, float* norm, float* scale, void* ws, size_t ws_bytes,
+                             dgc_stream_t stream) {
+    return grad_call(src, dst, count, max_norm, true, norm, scale, ws, ws_bytes, stream);
+}
