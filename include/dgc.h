@@ -378,6 +378,67 @@ int dgc_grad_norm(const dgc_tensor* src, int32_t count, float max_norm, float* n
 int dgc_grad_clip(const dgc_tensor* src, const dgc_tensor* dst, int32_t count, float max_norm,
                   float* norm, float* scale, void* ws, size_t ws_bytes, dgc_stream_t stream);
 
+/* --------------------------------------------------------- gated feed-forward block */
+
+/* A matrix of rows x cols entries, row r at data + r * ld entries. */
+typedef struct {
+    void* data;       /* device; 16-byte aligned (the weight gradient: 4-byte aligned) */
+    int64_t rows, cols;
+    int64_t ld;       /* entries from a row to the next, >= cols; a multiple of 8 for 16-bit types
+                         (any for the weight gradient; not read where rows is 1) */
+    int32_t dtype;    /* DGC_F16 or DGC_BF16; the weight gradient DGC_F32 */
+    int32_t reserved; /* 0 */
+} dgc_matrix;
+
+enum { DGC_ACT_SILU = 0, DGC_ACT_GELU = 1, DGC_ACT_GELU_TANH = 2, DGC_ACT_RELU = 3 };
+
+/* The block y = (act(x Wg^T) o (x Wu^T)) Wd^T + r and its backward pass, whose weight gradients
+ * are binary32 and land in (or are added to) the bucket that dgc_compress takes. x is M x D
+ * (M tokens), w_gate and w_up are F x D, w_down is D x F. All 16-bit matrices of a call have one
+ * type. Products are summed in binary32; every result is rounded once, from binary32.
+ *   act      SiLU g/(1+e^-g); GELU g(1+erf(g/sqrt 2))/2; its tanh form
+ *            g(1+tanh(sqrt(2/pi)(g+0.044715 g^3)))/2; ReLU (slope 0 at 0)
+ *   status   device int32 (see conventions): DGC_ETIMEOUT if a bounded wait gave up
+ * Results must not overlap operands, except that a result may be the matrix of the call that is
+ * read in its place: y the residual, d_gate the gate, d_up the up, dx the residual.
+ * Any extent may be 0: no rows or columns of the result, nothing is done; an empty sum gives 0.
+ * Entries that are not finite go through the sums as they do in IEEE arithmetic. Extents above
+ * 2^24 return DGC_EUNSUPPORTED. Every result is deterministic. One ordinary call of each kind
+ * on the device must precede its stream capture. */
+
+/* hidden = act(x w_gate^T) o (x w_up^T), M x F, in one kernel; gate and up (both or neither,
+ * NULL): x w_gate^T and x w_up^T, for the backward pass. */
+int dgc_ffn_gate(const dgc_matrix* x, const dgc_matrix* w_gate, const dgc_matrix* w_up,
+                 int32_t act, const dgc_matrix* hidden, const dgc_matrix* gate,
+                 const dgc_matrix* up, int32_t* status, dgc_stream_t stream);
+
+/* y = hidden w_down^T + residual (NULL: none), M x D. */
+int dgc_ffn_down(const dgc_matrix* hidden, const dgc_matrix* w_down, const dgc_matrix* residual,
+                 const dgc_matrix* y, int32_t* status, dgc_stream_t stream);
+
+/* From dy (M x D): dh = dy w_down, d_gate = dh o up o act'(gate), d_up = dh o act(gate). */
+int dgc_ffn_down_backward(const dgc_matrix* dy, const dgc_matrix* w_down, const dgc_matrix* gate,
+                          const dgc_matrix* up, int32_t act, const dgc_matrix* d_gate,
+                          const dgc_matrix* d_up, int32_t* status, dgc_stream_t stream);
+
+/* dx = d_gate w_gate + d_up w_up + residual (NULL: none), M x D, in one kernel. With
+ * residual = dy it is the gradient through y = x + block(x). */
+int dgc_ffn_gate_backward(const dgc_matrix* d_gate, const dgc_matrix* d_up,
+                          const dgc_matrix* w_gate, const dgc_matrix* w_up,
+                          const dgc_matrix* residual, const dgc_matrix* dx, int32_t* status,
+                          dgc_stream_t stream);
+
+/* Workspace of dgc_ffn_weight_grad for a rows x cols gradient over tokens (0: none needed). */
+int dgc_ffn_weight_grad_workspace(int64_t rows, int64_t cols, int64_t tokens, size_t* bytes);
+
+/* dw = dy^T x (accumulate 0) or dw + dy^T x: the gradient of a weight with y = x w^T, for
+ * dy tokens x rows and x tokens x cols. dw is binary32 and may be any 4-byte aligned piece of a
+ * flat bucket (16-byte aligned rows are faster). The three weight gradients of the block:
+ * (d_gate, x), (d_up, x) and (dy, hidden). */
+int dgc_ffn_weight_grad(const dgc_matrix* dy, const dgc_matrix* x, int32_t accumulate,
+                        const dgc_matrix* dw, int32_t* status, void* ws, size_t ws_bytes,
+                        dgc_stream_t stream);
+
 /* -------------------------------------------------------------------------- utilities */
 
 /* Synchronize `stream`, then return the int32 at status_dev (or DGC_ECUDA). */

@@ -24,6 +24,9 @@ __all__ = [
     "dgc_sum_shared",
     "F32", "F16", "BF16", "dgc_tensor", "TensorList",
     "dgc_grad_workspace", "dgc_grad_norm", "dgc_grad_clip",
+    "ACT_SILU", "ACT_GELU", "ACT_GELU_TANH", "ACT_RELU", "dgc_matrix", "matrix",
+    "dgc_ffn_gate", "dgc_ffn_down", "dgc_ffn_down_backward", "dgc_ffn_gate_backward",
+    "dgc_ffn_weight_grad_workspace", "dgc_ffn_weight_grad",
     "dgc_read_status", "dgc_status_string", "dgc_launch_count", "dgc_selftest_wait_timeout",
     "dgc_set_l2_fetch_granularity",
     "dgc_profile_stream_pass",
@@ -34,6 +37,7 @@ OK, EINVAL, ECAPACITY, ECUDA, ETIMEOUT, ECORRUPT, EUNSUPPORTED = 0, -1, -2, -3, 
 SELECT_EXACT, SELECT_SAMPLED, SELECT_ADACOMP = 0, 1, 2
 FLAG_MASK_MOMENTUM = 1
 F32, F16, BF16 = 0, 1, 2
+ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU = 0, 1, 2, 3
 
 
 class dgc_params(ctypes.Structure):
@@ -68,6 +72,17 @@ class dgc_tensor(ctypes.Structure):
     _fields_ = [
         ("data", ctypes.c_void_p),
         ("n", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class dgc_matrix(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("ld", ctypes.c_int64),
         ("dtype", ctypes.c_int32),
         ("reserved", ctypes.c_int32),
     ]
@@ -126,6 +141,12 @@ def lib():
         L.dgc_grad_workspace.argtypes = [vp, i32, P(sz)]
         L.dgc_grad_norm.argtypes = [vp, i32, f32, vp, vp, vp, sz, vp]
         L.dgc_grad_clip.argtypes = [vp, vp, i32, f32, vp, vp, vp, sz, vp]
+        L.dgc_ffn_gate.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, vp]
+        L.dgc_ffn_down.argtypes = [vp, vp, vp, vp, vp, vp]
+        L.dgc_ffn_down_backward.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, vp]
+        L.dgc_ffn_gate_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp]
+        L.dgc_ffn_weight_grad_workspace.argtypes = [i64, i64, i64, P(sz)]
+        L.dgc_ffn_weight_grad.argtypes = [vp, vp, i32, vp, vp, vp, sz, vp]
         L.dgc_read_status.argtypes = [vp, vp]
         L.dgc_status_string.argtypes = [ctypes.c_int]
         L.dgc_status_string.restype = ctypes.c_char_p
@@ -146,6 +167,9 @@ def lib():
                   "dgc_decode_accumulate_quant", "dgc_decode_apply_quant",
                   "dgc_compress_shared", "dgc_sum_shared_workspace", "dgc_sum_shared",
                   "dgc_grad_workspace", "dgc_grad_norm", "dgc_grad_clip",
+                  "dgc_ffn_gate", "dgc_ffn_down", "dgc_ffn_down_backward",
+                  "dgc_ffn_gate_backward", "dgc_ffn_weight_grad_workspace",
+                  "dgc_ffn_weight_grad",
                   "dgc_read_status",
                   "dgc_selftest_wait_timeout"):
             getattr(L, f).restype = ctypes.c_int
@@ -474,6 +498,69 @@ def dgc_grad_clip(src: TensorList, dst: TensorList | None, max_norm: float, norm
     return _check(lib().dgc_grad_clip(src.address, None if dst is None else dst.address, len(src),
                                       float(max_norm), _ptr(norm), _ptr(scale), _ptr(ws),
                                       int(ws_bytes), _stream(stream)), "dgc_grad_clip")
+
+
+# ------------------------------------------------------------- gated feed-forward block
+def matrix(t) -> dgc_matrix:
+    """The C view of a two-dimensional tensor whose rows are contiguous. The calls below build it
+    from the tensors they get; a program with fixed buffers builds it once (and keeps the tensor
+    alive, which the view does not)."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise DGCError(EINVAL, "matrix: a two-dimensional tensor with contiguous rows is wanted")
+    return dgc_matrix(t.data_ptr(), t.shape[0], t.shape[1], t.stride(0), _dtype_code(t), 0)
+
+
+def _mat(m):
+    if m is None:
+        return None
+    return ctypes.byref(m if isinstance(m, dgc_matrix) else matrix(m))
+
+
+def dgc_ffn_gate(x, w_gate, w_up, act: int, hidden, gate, up, status, stream=None) -> int:
+    """hidden = act(x w_gate^T) o (x w_up^T); gate, up: the two products, or None. Every matrix:
+    a float16 or bfloat16 CUDA tensor, or its matrix() view."""
+    return _check(lib().dgc_ffn_gate(_mat(x), _mat(w_gate), _mat(w_up), int(act), _mat(hidden),
+                                     _mat(gate), _mat(up), _ptr(status), _stream(stream)),
+                  "dgc_ffn_gate")
+
+
+def dgc_ffn_down(hidden, w_down, residual, y, status, stream=None) -> int:
+    """y = hidden w_down^T + residual (or None)."""
+    return _check(lib().dgc_ffn_down(_mat(hidden), _mat(w_down), _mat(residual), _mat(y),
+                                     _ptr(status), _stream(stream)), "dgc_ffn_down")
+
+
+def dgc_ffn_down_backward(dy, w_down, gate, up, act: int, d_gate, d_up, status,
+                          stream=None) -> int:
+    """d_gate, d_up: the gradients of gate and up, from dy."""
+    return _check(lib().dgc_ffn_down_backward(_mat(dy), _mat(w_down), _mat(gate), _mat(up),
+                                              int(act), _mat(d_gate), _mat(d_up), _ptr(status),
+                                              _stream(stream)), "dgc_ffn_down_backward")
+
+
+def dgc_ffn_gate_backward(d_gate, d_up, w_gate, w_up, residual, dx, status, stream=None) -> int:
+    """dx = d_gate w_gate + d_up w_up + residual (or None)."""
+    return _check(lib().dgc_ffn_gate_backward(_mat(d_gate), _mat(d_up), _mat(w_gate), _mat(w_up),
+                                              _mat(residual), _mat(dx), _ptr(status),
+                                              _stream(stream)), "dgc_ffn_gate_backward")
+
+
+def dgc_ffn_weight_grad_workspace(rows: int, cols: int, tokens: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().dgc_ffn_weight_grad_workspace(int(rows), int(cols), int(tokens),
+                                               ctypes.byref(out)),
+           "dgc_ffn_weight_grad_workspace")
+    return out.value
+
+
+def dgc_ffn_weight_grad(dy, x, dw, accumulate: bool, status, ws, ws_bytes: int | None = None,
+                        stream=None) -> int:
+    """dw (float32) = dy^T x, or dw + dy^T x; ws may be None where the workspace query says 0."""
+    if ws_bytes is None:
+        ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    return _check(lib().dgc_ffn_weight_grad(_mat(dy), _mat(x), int(bool(accumulate)), _mat(dw),
+                                            _ptr(status), _ptr(ws), int(ws_bytes),
+                                            _stream(stream)), "dgc_ffn_weight_grad")
 
 
 # ----------------------------------------------------------------------------- utilities

@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdgc.so")
-SOURCES = ["compress.cu", "codec.cu", "abi.cu", "noalloc.cu", "grad.cu"]
+SOURCES = ["compress.cu", "codec.cu", "abi.cu", "noalloc.cu", "grad.cu", "ffn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE]
 _lock = threading.Lock()

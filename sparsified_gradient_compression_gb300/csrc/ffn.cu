@@ -1,0 +1,937 @@
+// ffn.cu -- the gated feed-forward block and its backward pass (sm_103a): five matrix products
+// with what surrounds them in their epilogues, on the tensor cores.
+//
+//   x [M,D], w_gate, w_up [F,D], w_down [D,F]; act one of SiLU, GELU (erf or tanh), ReLU
+//   gate          G = x Wg^T, U = x Wu^T, H = act(G) o U     one accumulator tile holds both
+//   down          y = H Wd^T + r
+//   down_backward dH = dy Wd; dG = dH o U o act'(G), dU = dH o act(G)     dH is never stored
+//   gate_backward dx = dG Wg + dU Wu + r                     one sum over both products
+//   weight_grad   dW = dy^T x, binary32, or dW += dy^T x
+//
+// One kernel, k_ffn, for all five. A persistent block per SM computes 128-row output tiles:
+// warp 0 brings the operands' 64-deep slices by TMA into a ring of shared-memory stages, warp 1
+// issues tcgen05.mma on them into one of two accumulators in tensor memory, warps 4-7 empty the
+// other one: tcgen05.ld, the epilogue's arithmetic in binary32, one rounding, and a TMA store
+// from shared memory. Operands whose long axis is the sum's (x, H, dy, dG, dU and the weights of
+// the forward pass) are read along it ("K-major"); the others (the weights of the backward pass,
+// both operands of the weight gradient) are read across it, in place: no transposed copy is made.
+//
+// Every wait is bounded: a block whose wait runs out reports DGC_ETIMEOUT, waits (bounded) for
+// the copies it has in flight, frees its tensor memory and returns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "dgc_device.cuh"
+
+namespace dgc {
+namespace {
+
+enum Kind { kGate = 0, kDown = 1, kDownBwd = 2, kGateBwd = 3, kWGrad = 4 };
+
+constexpr int kFfnThreads = 256;
+constexpr int kBlockM = 128;
+constexpr int kBlockK = 64;                    // 128 bytes of 16-bit entries: the swizzle's span
+constexpr uint32_t kStageA = kBlockM * kBlockK * 2;
+constexpr int kMaxStages = 8;
+constexpr uint32_t kEpilogueBytes = 48 * 1024; // staging of warps 4-7, 12 KB each
+constexpr uint32_t kSmemLimit = 232448;        // 227 KB
+constexpr uint32_t kFfnWaitLimit = 1u << 23;   // polls; the longest sum takes far fewer
+constexpr int64_t kMaxExtent = 1 << 24;
+
+struct FfnArgs {
+    CUtensorMap a0, a1, b0, b1;       // operands; a1, b1: the second product's, or B's up half
+    CUtensorMap in0, in1;             // residual; gate and up
+    CUtensorMap out0, out1, out2;
+    uint32_t m, n;                    // the output's extents
+    uint32_t kb0, kb;                 // 64-deep slices of the first product, of both
+    uint32_t tiles_m, tiles_n, tiles; // tiles = tiles_m * tiles_n * splits
+    uint32_t group;                   // row tiles that are walked together
+    uint32_t kb_split;                // weight gradient: slices of one split
+    uint32_t split_rows;              // ... and rows of the workspace between splits
+    uint32_t bn, stages, a_rows, stage_bytes, load_bytes;
+    uint32_t idesc, tmem_cols;
+    int32_t act, half, residual, accumulate;
+    // The results as plain matrices. TMA writes whole 16-byte pieces: where the last piece of a
+    // row is not all the matrix's own (ragged), the columns of the last box are stored one by
+    // one, and every column where TMA cannot address the rows at all (unaligned).
+    void* out[3];
+    uint64_t ld[3];
+    int32_t ragged, unaligned;
+    int32_t* status;
+};
+
+// ------------------------------------------------------------------- tensor-core PTX
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int32_t x, int32_t y,
+                                         uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* src, int32_t x,
+                                          int32_t y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];"
+                 ::"l"(map), "r"(x), "r"(y), "r"(smem_addr(src))
+                 : "memory");
+}
+__device__ __forceinline__ void tma_add(const CUtensorMap* map, const void* src, int32_t x,
+                                        int32_t y) {
+    asm volatile(
+        "cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%1, %2}], [%3];"
+        ::"l"(map), "r"(x), "r"(y), "r"(smem_addr(src))
+        : "memory");
+}
+template <int kN>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kN) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 ::"r"(smem_addr(slot)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_16bit(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+        ::"r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tmem_fence_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_fence_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// 32 columns of this warp's 32 rows: lane i gets row i.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait_load() {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Shared-memory operand descriptor, 128-byte swizzle. K-major: rows of 128 bytes (64 entries of
+// the sum), 8 rows a swizzle atom, atoms 1024 bytes apart. Across the sum: slices of 64 rows (one
+// per step of the sum) of 128 bytes (64 entries of the operand's own axis); 8 steps are 1024
+// bytes apart, the next 64 entries of the own axis one slice (8192 bytes) further.
+template <bool kAcross>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+    constexpr uint64_t lead = kAcross ? 8192 >> 4 : 1, stride = 1024 >> 4;
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (lead << 16) | (stride << 32) | (1ull << 46) |
+           (2ull << 61);
+}
+
+// ----------------------------------------------------------------------- activations
+// Values and slopes in binary32. The fast exponential and division (relative error about 1e-6)
+// are followed by a rounding to 16 bits (2^-12 at the finest).
+struct ActValue {
+    float value, slope;
+};
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+
+constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+
+__device__ __forceinline__ float act_value(int act, float g) {
+    if (act == DGC_ACT_SILU) return __fdividef(g, 1.0f + __expf(-g));
+    if (act == DGC_ACT_GELU) return 0.5f * g * (1.0f + erff(g * 0.7071067811865476f));
+    if (act == DGC_ACT_GELU_TANH) {  // (1 + tanh z) / 2 = sigmoid(2 z)
+        const float z = 2.0f * kGeluC * g * fmaf(kGeluA * g, g, 1.0f);
+        return __fdividef(g, 1.0f + __expf(-z));
+    }
+    return g <= 0.0f ? 0.0f : g;
+}
+__device__ __forceinline__ ActValue act_both(int act, float g) {
+    ActValue r;
+    if (act == DGC_ACT_SILU) {
+        const float s = sigmoid(g);
+        r.value = g * s;
+        r.slope = s * fmaf(g, 1.0f - s, 1.0f);
+    } else if (act == DGC_ACT_GELU) {
+        const float p = 0.5f * (1.0f + erff(g * 0.7071067811865476f));
+        r.value = g * p;
+        r.slope = fmaf(g * 0.3989422804014327f, __expf(-0.5f * g * g), p);
+    } else if (act == DGC_ACT_GELU_TANH) {
+        const float g2 = g * g;
+        const float s = sigmoid(2.0f * kGeluC * g * fmaf(kGeluA, g2, 1.0f));
+        r.value = g * s;
+        r.slope = s * fmaf(2.0f * kGeluC * g * fmaf(3.0f * kGeluA, g2, 1.0f), 1.0f - s, 1.0f);
+    } else {
+        r.value = g <= 0.0f ? 0.0f : g;
+        r.slope = g > 0.0f ? 1.0f : 0.0f;
+    }
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack2(float x, float y, bool half) {
+    if (half) {
+        const __half2 h = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w, bool half) {
+    if (half) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+}
+
+// --------------------------------------------------------------------------- the kernel
+struct FfnShared {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t acc_full[2], acc_empty[2];
+    uint64_t in_full[4][3];
+    uint64_t drain;
+    uint32_t tmem;
+    volatile uint32_t abort;
+};
+
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, FfnShared* sh,
+                                         int32_t* status) {
+    for (uint32_t i = 0; i < kFfnWaitLimit; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 15u) == 15u && sh->abort) return false;
+    }
+    report(status, DGC_ETIMEOUT);
+    sh->abort = 1;
+    return false;
+}
+// For the way out of a block that gave up: no report, its own limit.
+__device__ __forceinline__ void wait_quietly(uint64_t* bar, uint32_t parity) {
+    for (uint32_t i = 0; i < (1u << 18); ++i)
+        if (mbar_try_wait(bar, parity)) return;
+}
+
+struct Tile {
+    uint32_t mt, nt, split;
+};
+// Tiles in groups of `group` row tiles, columns outside, rows inside: the tiles that run at the
+// same time share few operand slices, which stay in L2.
+__device__ __forceinline__ Tile tile_at(const FfnArgs& a, uint32_t t) {
+    Tile r;
+    const uint32_t per = a.tiles_m * a.tiles_n;
+    r.split = t / per;
+    t -= r.split * per;
+    const uint32_t g = t / (a.group * a.tiles_n);
+    const uint32_t first = g * a.group;
+    const uint32_t rows = min(a.group, a.tiles_m - first);
+    t -= first * a.tiles_n;
+    r.nt = t / rows;
+    r.mt = first + (t - r.nt * rows);
+    return r;
+}
+__device__ __forceinline__ void k_range(const FfnArgs& a, const Tile& t, uint32_t* k0,
+                                        uint32_t* k1) {
+    *k0 = t.split * a.kb_split;
+    *k1 = min(a.kb, *k0 + a.kb_split);
+}
+
+template <int kKind>
+struct Epilogue {
+    static constexpr int kIn = kKind == kDownBwd ? 2 : (kKind == kDown || kKind == kGateBwd) ? 1 : 0;
+    static constexpr int kOut = kKind == kGate ? 3 : kKind == kDownBwd ? 2 : 1;
+    static constexpr int kBufs = kOut > kIn ? kOut : kIn;       // 32 x 32 boxes of one set
+    static constexpr uint32_t kBox = kKind == kWGrad ? 4096 : 2048;
+    static constexpr int kSets = kKind == kGate ? 2 : 3;
+    static_assert(kSets * kBufs * kBox * 4 <= kEpilogueBytes, "staging");
+};
+
+template <int kKind>
+__device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* staging,
+                                         uint32_t tmem) {
+    using E = Epilogue<kKind>;
+    const int warp = (threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
+    char* mine = staging + warp * (kEpilogueBytes / 4);
+    auto buf = [&](uint32_t set, int i) { return mine + (set * E::kBufs + i) * E::kBox; };
+    const uint32_t out_cols = kKind == kGate ? a.bn / 2 : a.bn;  // columns of one tile's output
+    const uint32_t chunks = out_cols / 32;
+    const bool has_in = E::kIn > 0 && (kKind == kDownBwd || a.residual);
+
+    // The loads of one chunk's inputs; chunks outside the output have none.
+    uint32_t load_tile = blockIdx.x, load_chunk = 0, load_n = 0;
+    auto issue_load = [&]() {  // lane 0: the next chunk's inputs, if there is one left
+        while (load_tile < a.tiles) {
+            const Tile t = tile_at(a, load_tile);
+            const uint32_t y = t.mt * kBlockM + warp * 32, x = t.nt * out_cols + load_chunk * 32;
+            if (y >= a.m || x >= a.n) {  // the rest of this tile lies outside
+                load_chunk = 0;
+                load_tile += gridDim.x;
+                continue;
+            }
+            const uint32_t set = load_n % E::kSets;
+            uint64_t* bar = &sh->in_full[warp][set];
+            mbar_arrive_expect_tx(bar, 2048u * E::kIn);
+            tma_load(buf(set, 0), &a.in0, x, y, bar);
+            if (E::kIn > 1) tma_load(buf(set, 1), &a.in1, x, y, bar);
+            ++load_n;
+            if (++load_chunk == chunks) {
+                load_chunk = 0;
+                load_tile += gridDim.x;
+            }
+            return;
+        }
+    };
+    if (has_in && lane == 0)
+        for (int i = 0; i < E::kSets - 1; ++i) issue_load();
+
+    uint32_t done = 0;  // chunks this warp has finished
+    uint32_t it = 0;
+    bool ok = true;
+    for (uint32_t ti = blockIdx.x; ti < a.tiles && ok; ti += gridDim.x, ++it) {
+        const Tile t = tile_at(a, ti);
+        const uint32_t acc = it & 1, y = t.mt * kBlockM + warp * 32;
+        uint32_t k0, k1;
+        k_range(a, t, &k0, &k1);
+        ok = __all_sync(kFull, wait_bar(&sh->acc_full[acc], (it >> 1) & 1, sh, a.status));
+        if (!ok) break;
+        tmem_fence_after();
+        const uint32_t src = tmem + acc * a.bn + ((uint32_t)(warp * 32) << 16);
+        for (uint32_t c = 0; c < chunks && y < a.m; ++c) {
+            const uint32_t x = t.nt * out_cols + c * 32;
+            if (x >= a.n) break;
+            const uint32_t set = done % E::kSets;
+            uint32_t v[32], u[32];
+            tmem_load32(src + c * 32, v);
+            if (kKind == kGate) tmem_load32(src + out_cols + c * 32, u);
+            tmem_wait_load();
+            if (k0 >= k1) {  // an empty sum: the accumulator was never written
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = u[i] = 0;
+            }
+            if (has_in) {
+                ok = __all_sync(kFull, wait_bar(&sh->in_full[warp][set], (done / E::kSets) & 1, sh,
+                                                a.status));
+                if (!ok) break;
+            } else {
+                // the set's last store has left it (one set is written while the others leave)
+                if (lane == 0) bulk_wait_read<E::kSets - 1>();
+                __syncwarp();
+            }
+            // 16-byte pieces of this lane's row, in the swizzled order of the TMA box
+#pragma unroll
+            for (int p = 0; p < (kKind == kWGrad ? 8 : 4); ++p) {
+                if (kKind == kWGrad) {
+                    uint4 w = make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
+                    *reinterpret_cast<uint4*>(buf(set, 0) + lane * 128 + ((p ^ (lane & 7)) << 4)) = w;
+                    continue;
+                }
+                const uint32_t at = lane * 64 + ((p ^ ((lane >> 1) & 3)) << 4);
+                uint32_t o0[4], o1[4], o2[4], i0[4], i1[4];
+                if (has_in) {
+                    const uint4 q = *reinterpret_cast<const uint4*>(buf(set, 0) + at);
+                    i0[0] = q.x, i0[1] = q.y, i0[2] = q.z, i0[3] = q.w;
+                    if (E::kIn > 1) {
+                        const uint4 s = *reinterpret_cast<const uint4*>(buf(set, 1) + at);
+                        i1[0] = s.x, i1[1] = s.y, i1[2] = s.z, i1[3] = s.w;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float v0 = __uint_as_float(v[8 * p + 2 * j]);
+                    const float v1 = __uint_as_float(v[8 * p + 2 * j + 1]);
+                    if (kKind == kGate) {
+                        const float u0 = __uint_as_float(u[8 * p + 2 * j]);
+                        const float u1 = __uint_as_float(u[8 * p + 2 * j + 1]);
+                        o0[j] = pack2(act_value(a.act, v0) * u0, act_value(a.act, v1) * u1, a.half);
+                        o1[j] = pack2(v0, v1, a.half);
+                        o2[j] = pack2(u0, u1, a.half);
+                    } else if (kKind == kDownBwd) {
+                        const float2 g = unpack2(i0[j], a.half), w = unpack2(i1[j], a.half);
+                        const ActValue f0 = act_both(a.act, g.x), f1 = act_both(a.act, g.y);
+                        o0[j] = pack2(v0 * w.x * f0.slope, v1 * w.y * f1.slope, a.half);
+                        o1[j] = pack2(v0 * f0.value, v1 * f1.value, a.half);
+                    } else {
+                        float2 r = make_float2(0.0f, 0.0f);
+                        if (has_in) r = unpack2(i0[j], a.half);
+                        o0[j] = pack2(v0 + r.x, v1 + r.y, a.half);
+                    }
+                }
+                *reinterpret_cast<uint4*>(buf(set, 0) + at) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+                if (E::kOut > 1)
+                    *reinterpret_cast<uint4*>(buf(set, 1) + at) =
+                        make_uint4(o1[0], o1[1], o1[2], o1[3]);
+                if (E::kOut > 2)
+                    *reinterpret_cast<uint4*>(buf(set, E::kOut > 2 ? 2 : 0) + at) =
+                        make_uint4(o2[0], o2[1], o2[2], o2[3]);
+            }
+            if (a.unaligned || (a.ragged && x + 32 > a.n)) {
+                // a row of up to 32 columns per step, one column a lane
+                __syncwarp();
+                const uint32_t rows = min(32u, a.m - y);
+                const int outs = kKind == kGate ? (a.residual ? 3 : 1) : E::kOut;
+                if (x + lane < a.n)
+                    for (uint32_t r = 0; r < rows; ++r)
+                        for (int i = 0; i < outs; ++i) {
+                            const uint64_t to = (uint64_t)(y + r) * a.ld[i] + x + lane;
+                            if (kKind == kWGrad) {
+                                const float f = *reinterpret_cast<const float*>(
+                                    buf(set, 0) + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) +
+                                    (lane & 3) * 4);
+                                float* d = static_cast<float*>(a.out[0]) + to;
+                                *d = a.accumulate ? *d + f : f;
+                            } else {
+                                static_cast<uint16_t*>(a.out[i])[to] =
+                                    *reinterpret_cast<const uint16_t*>(
+                                        buf(set, i) + r * 64 +
+                                        (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
+                            }
+                        }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    bulk_commit();  // an empty group: the sets are counted by groups
+                    if (has_in) {
+                        bulk_wait_read<1>();
+                        issue_load();
+                    }
+                }
+            } else {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (kKind == kWGrad) {
+                        if (a.accumulate)
+                            tma_add(&a.out0, buf(set, 0), x, y + t.split * a.split_rows);
+                        else
+                            tma_store(&a.out0, buf(set, 0), x, y + t.split * a.split_rows);
+                    } else {
+                        tma_store(&a.out0, buf(set, 0), x, y);
+                        if (kKind == kDownBwd) tma_store(&a.out1, buf(set, 1), x, y);
+                        if (kKind == kGate && a.residual) {  // gate and up are wanted
+                            tma_store(&a.out1, buf(set, 1), x, y);
+                            tma_store(&a.out2, buf(set, E::kOut > 2 ? 2 : 0), x, y);
+                        }
+                    }
+                    bulk_commit();
+                    if (has_in) {
+                        bulk_wait_read<1>();  // the set before this one has left
+                        issue_load();
+                    }
+                }
+            }
+            ++done;
+        }
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->acc_empty[acc]);
+    }
+    if (lane == 0) {
+        // inputs still on their way to a block that gave up
+        if (!ok && has_in)
+            for (uint32_t i = done; i < load_n; ++i)
+                wait_quietly(&sh->in_full[warp][i % E::kSets], (i / E::kSets) & 1);
+        bulk_wait_all();
+    }
+}
+
+template <int kKind>
+__global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ FfnArgs a) {
+    constexpr bool kAcrossA = kKind == kWGrad;
+    constexpr bool kAcrossB = kKind == kDownBwd || kKind == kGateBwd || kKind == kWGrad;
+    extern __shared__ char dyn[];
+    __shared__ FfnShared shared;
+    FfnShared* sh = &shared;
+    char* base = dyn + ((1024u - (smem_addr(dyn) & 1023u)) & 1023u);
+    char* staging = base + a.stages * a.stage_bytes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kMaxStages; ++i) {
+            mbar_init(&sh->full[i], 1);
+            mbar_init(&sh->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh->acc_full[i], 1);
+            mbar_init(&sh->acc_empty[i], 4);
+        }
+        for (int w = 0; w < 4; ++w)
+            for (int i = 0; i < 3; ++i) mbar_init(&sh->in_full[w][i], 1);
+        mbar_init(&sh->drain, 1);
+        mbar_init_fence();
+        sh->abort = 0;
+    }
+    if (warp == 2) tmem_alloc(&sh->tmem, a.tmem_cols);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = sh->tmem;
+
+    // One lane of warps 0 and 1 works; the others wait for it before the block's last barrier.
+    if (warp == 0 && lane == 0) {
+        uint32_t n = 0;  // stages filled so far
+        bool ok = true;
+        for (uint32_t ti = blockIdx.x; ti < a.tiles && ok; ti += gridDim.x) {
+            const Tile t = tile_at(a, ti);
+            const int32_t row = t.mt * kBlockM;
+            uint32_t k0, k1;
+            k_range(a, t, &k0, &k1);
+            for (uint32_t kb = k0; kb < k1; ++kb, ++n) {
+                const uint32_t s = n % a.stages;
+                if (!(ok = wait_bar(&sh->empty[s], ((n / a.stages) & 1) ^ 1, sh, a.status))) break;
+                char* sa = base + s * a.stage_bytes;
+                char* sb = sa + kStageA;
+                uint64_t* bar = &sh->full[s];
+                mbar_arrive_expect_tx(bar, a.load_bytes);
+                const bool second = kKind == kGateBwd && kb >= a.kb0;
+                const int32_t k = (int32_t)(second ? kb - a.kb0 : kb) * kBlockK;
+                const CUtensorMap* ma = second ? &a.a1 : &a.a0;
+                const CUtensorMap* mb = second ? &a.b1 : &a.b0;
+                if (kAcrossA) {
+                    tma_load(sa, ma, row, k, bar);
+                    tma_load(sa + 8192, ma, row + 64, k, bar);
+                } else {
+                    tma_load(sa, ma, k, row, bar);
+                }
+                if (kAcrossB) {
+                    for (uint32_t c = 0; c < a.bn / 64; ++c)
+                        tma_load(sb + c * 8192, mb, t.nt * a.bn + c * 64, k, bar);
+                } else if (kKind == kGate) {
+                    tma_load(sb, &a.b0, k, t.nt * (a.bn / 2), bar);
+                    tma_load(sb + a.bn / 2 * 128, &a.b1, k, t.nt * (a.bn / 2), bar);
+                } else {
+                    tma_load(sb, mb, k, t.nt * a.bn, bar);
+                }
+            }
+        }
+        if (!ok || sh->abort)  // copies in flight to a block that gives up
+            for (uint32_t i = n > a.stages ? n - a.stages : 0; i < n; ++i)
+                wait_quietly(&sh->full[i % a.stages], (i / a.stages) & 1);
+    } else if (warp == 1 && lane == 0) {
+        uint32_t n = 0, it = 0;
+        bool ok = true;
+        for (uint32_t ti = blockIdx.x; ti < a.tiles && ok; ti += gridDim.x, ++it) {
+            const Tile t = tile_at(a, ti);
+            uint32_t k0, k1;
+            k_range(a, t, &k0, &k1);
+            const uint32_t acc = it & 1;
+            if (!(ok = wait_bar(&sh->acc_empty[acc], ((it >> 1) & 1) ^ 1, sh, a.status))) break;
+            tmem_fence_after();
+            const uint32_t d = tmem + acc * a.bn;
+            for (uint32_t kb = k0; kb < k1; ++kb, ++n) {
+                const uint32_t s = n % a.stages;
+                if (!(ok = wait_bar(&sh->full[s], (n / a.stages) & 1, sh, a.status))) break;
+                tmem_fence_after();
+                const uint32_t sa = smem_addr(base + s * a.stage_bytes);
+                const uint64_t da = operand_desc<kAcrossA>(sa);
+                const uint64_t db = operand_desc<kAcrossB>(sa + kStageA);
+#pragma unroll
+                for (int k = 0; k < kBlockK / 16; ++k)  // 16 of the sum: 32 bytes, or 16 rows
+                    mma_16bit(d, da + k * (kAcrossA ? 2048 >> 4 : 2),
+                              db + k * (kAcrossB ? 2048 >> 4 : 2), a.idesc, kb > k0 || k > 0);
+                mma_commit(&sh->empty[s]);
+            }
+            if (ok) mma_commit(&sh->acc_full[acc]);
+        }
+        mma_commit(&sh->drain);  // every product this thread issued is done before the block ends
+        wait_quietly(&sh->drain, 0);
+    } else if (warp >= 4) {
+        epilogue<kKind>(a, sh, staging, tmem);
+    }
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == 2) tmem_free(tmem, a.tmem_cols);
+}
+
+// The splits of a weight gradient, added in order: dW = (dW +) sum over s of part_s.
+__global__ void __launch_bounds__(256) k_wgrad_join(const float* part, uint64_t part_ld,
+                                                    uint64_t split_stride, uint32_t splits,
+                                                    float* dw, uint64_t ld, uint32_t rows,
+                                                    uint32_t cols, int accumulate) {
+    const uint32_t x = blockIdx.x * 256 + threadIdx.x;
+    if (x >= cols) return;
+    for (uint32_t y = blockIdx.y; y < rows; y += gridDim.y) {
+        const float* p = part + (uint64_t)y * part_ld + x;
+        float s = 0.0f;
+        for (uint32_t i = 0; i < splits; ++i) s += p[i * split_stride];
+        float* d = dw + (uint64_t)y * ld + x;
+        *d = accumulate ? *d + s : s;
+    }
+}
+
+// Empty sums over no rows at all: dW = 0.
+__global__ void __launch_bounds__(256) k_wgrad_zero(float* dw, uint64_t ld, uint32_t rows,
+                                                    uint32_t cols) {
+    const uint32_t x = blockIdx.x * 256 + threadIdx.x;
+    if (x >= cols) return;
+    for (uint32_t y = blockIdx.y; y < rows; y += gridDim.y) dw[(uint64_t)y * ld + x] = 0.0f;
+}
+
+// ----------------------------------------------------------------------------------- host
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static EncodeFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+
+struct Mat {  // a checked matrix
+    void* p;
+    uint64_t rows, cols, ld;
+    int32_t dtype;
+};
+
+// A matrix argument of 16-bit entries whose rows TMA can address.
+int check_matrix(const dgc_matrix* m, Mat* out, int32_t dtype) {
+    if (!m || m->rows < 0 || m->cols < 0 || m->reserved != 0) return DGC_EINVAL;
+    if (m->dtype != DGC_F16 && m->dtype != DGC_BF16) return DGC_EINVAL;
+    if (dtype >= 0 && m->dtype != dtype) return DGC_EINVAL;
+    if (m->rows > kMaxExtent || m->cols > kMaxExtent) return DGC_EUNSUPPORTED;
+    *out = Mat{m->data, (uint64_t)m->rows, (uint64_t)m->cols, (uint64_t)m->ld, m->dtype};
+    if (m->rows == 0 || m->cols == 0) return DGC_OK;
+    if (!m->data || ((uintptr_t)m->data & 15u)) return DGC_EINVAL;
+    if (m->rows == 1) {
+        out->ld = ((uint64_t)m->cols + 7) & ~7ull;
+        return DGC_OK;
+    }
+    if (m->ld < m->cols || (m->ld & 7)) return DGC_EINVAL;
+    if (m->ld > (1ll << 36)) return DGC_EUNSUPPORTED;
+    return DGC_OK;
+}
+bool shaped(const Mat& m, uint64_t rows, uint64_t cols) { return m.rows == rows && m.cols == cols; }
+
+// A box of bc x br entries of a matrix; bytes of a box row: 64 or 128, which is the swizzle too.
+int make_map(CUtensorMap* map, const Mat& m, uint32_t bc, uint32_t br) {
+    EncodeFn fn = encode_fn();
+    if (!fn) return DGC_ECUDA;
+    const uint32_t es = m.dtype == DGC_F32 ? 4 : 2;
+    const cuuint64_t dims[2] = {m.cols, m.rows};
+    const cuuint64_t strides[1] = {m.ld * es};
+    const cuuint32_t box[2] = {bc, br}, step[2] = {1, 1};
+    const CUtensorMapDataType type = m.dtype == DGC_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : m.dtype == DGC_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                          : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUresult r = fn(map, type, 2, m.p, dims, strides, box, step,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          bc * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? DGC_OK : DGC_ECUDA;
+}
+
+uint32_t ceil_div(uint64_t a, uint64_t b) { return (uint32_t)((a + b - 1) / b); }
+
+// Output columns of a tile: the widest tile (fewest operand bytes per product) that still gives
+// every SM one, else the narrowest.
+uint32_t choose_bn(uint64_t tiles_m, uint64_t n, uint32_t out_per_bn_num, uint32_t narrowest,
+                   int sms) {
+    for (uint32_t bn = 256; bn > narrowest; bn /= 2)
+        if (tiles_m * ceil_div(n, bn / out_per_bn_num) >= (uint64_t)sms) return bn;
+    return narrowest;
+}
+
+template <int kKind>
+int launch_ffn(FfnArgs& a, int32_t dtype, int sms, cudaStream_t s) {
+    constexpr bool kAcrossA = kKind == kWGrad;
+    constexpr bool kAcrossB = kKind == kDownBwd || kKind == kGateBwd || kKind == kWGrad;
+    a.stage_bytes = kStageA + a.bn * 128;
+    a.stages = std::min<uint32_t>(kMaxStages, (kSmemLimit - 2048 - kEpilogueBytes) / a.stage_bytes);
+    a.load_bytes = (kAcrossA ? kBlockM : a.a_rows) * 128 + a.bn * 128;
+    a.tmem_cols = std::max(32u, 2 * a.bn);
+    a.half = dtype == DGC_F16;
+    const uint32_t type = dtype == DGC_F16 ? 0 : 1;
+    a.idesc = (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)kAcrossA << 15) |
+              ((uint32_t)kAcrossB << 16) | ((a.bn >> 3) << 17) | ((kBlockM >> 4) << 24);
+    a.group = 16;
+    const uint32_t smem = a.stages * a.stage_bytes + kEpilogueBytes + 1024;
+    static bool set[128] = {false};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 128 || !set[dev]) {
+        if (cudaFuncSetAttribute(k_ffn<kKind>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)(kSmemLimit - 1024)) != cudaSuccess) {
+            cudaGetLastError();
+            return DGC_ECUDA;
+        }
+        if (dev >= 0 && dev < 128) set[dev] = true;
+    }
+    k_ffn<kKind><<<std::min<uint32_t>(a.tiles, (uint32_t)sms), kFfnThreads, smem, s>>>(a);
+    if (cudaPeekAtLastError() != cudaSuccess) {
+        cudaGetLastError();
+        return DGC_ECUDA;
+    }
+    dgc_internal_count_launches(1);
+    return DGC_OK;
+}
+
+// A product along rows: A [m, k] K-major, against B [n, k] K-major or [k, n] across.
+struct Product {
+    const Mat *a, *b;
+};
+
+template <int kKind>
+int rows_product(Product p0, const Product* p1, const Mat* b_up, const Mat* in0, const Mat* in1,
+                 const Mat* out0, const Mat* out1, const Mat* out2, int32_t act, int32_t* status,
+                 dgc_stream_t stream) {
+    constexpr bool kAcrossB = kKind == kDownBwd || kKind == kGateBwd;
+    const int sms = dgc_internal_sm_count();
+    if (sms <= 0) return DGC_ECUDA;
+    FfnArgs a{};
+    a.m = (uint32_t)out0->rows;
+    a.n = (uint32_t)out0->cols;
+    a.tiles_m = ceil_div(a.m, kBlockM);
+    constexpr uint32_t halves = kKind == kGate ? 2 : 1;
+    a.bn = choose_bn(a.tiles_m, a.n, halves, kKind == kDown ? 32 : 64, sms);
+    a.tiles_n = ceil_div(a.n, a.bn / halves);
+    a.tiles = a.tiles_m * a.tiles_n;
+    a.a_rows = std::min<uint32_t>(kBlockM, (a.m + 7) & ~7u);
+    a.kb0 = ceil_div(p0.a->cols, kBlockK);
+    a.kb = a.kb0 + (p1 ? ceil_div(p1->a->cols, kBlockK) : 0);
+    a.kb_split = a.kb;
+    a.act = act;
+    a.status = status;
+    int rc = DGC_OK;
+    auto operand = [&](CUtensorMap* map, const Mat& m, uint32_t bc, uint32_t br) {
+        if (!rc && m.rows && m.cols) rc = make_map(map, m, bc, br);
+    };
+    auto b_map = [&](CUtensorMap* map, const Mat& m) {
+        if (kAcrossB)
+            operand(map, m, 64, kBlockK);
+        else
+            operand(map, m, kBlockK, a.bn / halves);
+    };
+    operand(&a.a0, *p0.a, kBlockK, a.a_rows);
+    b_map(&a.b0, *p0.b);
+    if (b_up) b_map(&a.b1, *b_up);
+    if (p1) {
+        operand(&a.a1, *p1->a, kBlockK, a.a_rows);
+        b_map(&a.b1, *p1->b);
+    }
+    const Mat* outs[3] = {out0, out1, out2};
+    for (int i = 0; i < 3; ++i)
+        if (outs[i]) {
+            a.out[i] = outs[i]->p;
+            a.ld[i] = outs[i]->ld;
+        }
+    a.ragged = (a.n & 7) != 0;
+    operand(&a.out0, *out0, 32, 32);
+    if (out1) operand(&a.out1, *out1, 32, 32);
+    if (out2) operand(&a.out2, *out2, 32, 32);
+    if (in0) operand(&a.in0, *in0, 32, 32);
+    if (in1) operand(&a.in1, *in1, 32, 32);
+    if (rc) return rc;
+    a.residual = kKind == kGate ? out1 != nullptr : in0 != nullptr;
+    return launch_ffn<kKind>(a, out0->dtype, sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+bool bad_act(int32_t act) { return act < DGC_ACT_SILU || act > DGC_ACT_RELU; }
+
+// Splits of a weight gradient's sum over the tokens: where the output has fewer tiles than there
+// are SMs, enough splits to fill them, each of at least 8 slices (512 tokens).
+uint32_t wgrad_splits(uint64_t tiles, uint64_t kb) {
+    constexpr uint64_t kFill = 152;
+    if (tiles == 0 || tiles >= kFill) return 1;
+    return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(kFill / tiles, kb / 8));
+}
+uint32_t wgrad_bn(uint64_t cols) { return cols > 128 ? 256 : cols > 64 ? 128 : 64; }
+uint64_t wgrad_workspace(uint64_t rows, uint64_t cols, uint64_t tokens) {
+    const uint32_t bn = wgrad_bn(cols);
+    const uint64_t splits = wgrad_splits((uint64_t)ceil_div(rows, kBlockM) * ceil_div(cols, bn),
+                                         ceil_div(tokens, kBlockK));
+    if (splits < 2) return 0;
+    return splits * ceil_div(rows, kBlockM) * kBlockM * ((cols + 3) & ~3ull) * sizeof(float);
+}
+
+}  // namespace
+}  // namespace dgc
+
+using namespace dgc;
+
+extern "C" int dgc_ffn_gate(const dgc_matrix* x, const dgc_matrix* w_gate, const dgc_matrix* w_up,
+                            int32_t act, const dgc_matrix* hidden, const dgc_matrix* gate,
+                            const dgc_matrix* up, int32_t* status, dgc_stream_t stream) {
+    Mat mx, mg, mu, mh, og, ou;
+    int rc;
+    if (!x || !status || bad_act(act) || (gate == nullptr) != (up == nullptr)) return DGC_EINVAL;
+    if ((rc = check_matrix(x, &mx, -1)) || (rc = check_matrix(w_gate, &mg, mx.dtype)) ||
+        (rc = check_matrix(w_up, &mu, mx.dtype)) || (rc = check_matrix(hidden, &mh, mx.dtype)))
+        return rc;
+    if (gate && ((rc = check_matrix(gate, &og, mx.dtype)) || (rc = check_matrix(up, &ou, mx.dtype))))
+        return rc;
+    const uint64_t m = mx.rows, d = mx.cols, f = mg.rows;
+    if (!shaped(mg, f, d) || !shaped(mu, f, d) || !shaped(mh, m, f)) return DGC_EINVAL;
+    if (gate && (!shaped(og, m, f) || !shaped(ou, m, f))) return DGC_EINVAL;
+    if (m == 0 || f == 0) return DGC_OK;
+    return rows_product<kGate>({&mx, &mg}, nullptr, &mu, nullptr, nullptr, &mh,
+                               gate ? &og : nullptr, gate ? &ou : nullptr, act, status, stream);
+}
+
+extern "C" int dgc_ffn_down(const dgc_matrix* hidden, const dgc_matrix* w_down,
+                            const dgc_matrix* residual, const dgc_matrix* y, int32_t* status,
+                            dgc_stream_t stream) {
+    Mat mh, mw, mr, my;
+    int rc;
+    if (!hidden || !status) return DGC_EINVAL;
+    if ((rc = check_matrix(hidden, &mh, -1)) || (rc = check_matrix(w_down, &mw, mh.dtype)) ||
+        (rc = check_matrix(y, &my, mh.dtype)))
+        return rc;
+    if (residual && (rc = check_matrix(residual, &mr, mh.dtype))) return rc;
+    const uint64_t m = mh.rows, f = mh.cols, d = mw.rows;
+    if (!shaped(mw, d, f) || !shaped(my, m, d)) return DGC_EINVAL;
+    if (residual && !shaped(mr, m, d)) return DGC_EINVAL;
+    if (m == 0 || d == 0) return DGC_OK;
+    return rows_product<kDown>({&mh, &mw}, nullptr, nullptr, residual ? &mr : nullptr, nullptr, &my,
+                               nullptr, nullptr, 0, status, stream);
+}
+
+extern "C" int dgc_ffn_down_backward(const dgc_matrix* dy, const dgc_matrix* w_down,
+                                     const dgc_matrix* gate, const dgc_matrix* up, int32_t act,
+                                     const dgc_matrix* d_gate, const dgc_matrix* d_up,
+                                     int32_t* status, dgc_stream_t stream) {
+    Mat my, mw, mg, mu, og, ou;
+    int rc;
+    if (!dy || !status || bad_act(act)) return DGC_EINVAL;
+    if ((rc = check_matrix(dy, &my, -1)) || (rc = check_matrix(w_down, &mw, my.dtype)) ||
+        (rc = check_matrix(gate, &mg, my.dtype)) || (rc = check_matrix(up, &mu, my.dtype)) ||
+        (rc = check_matrix(d_gate, &og, my.dtype)) || (rc = check_matrix(d_up, &ou, my.dtype)))
+        return rc;
+    const uint64_t m = my.rows, d = my.cols, f = mw.cols;
+    if (!shaped(mw, d, f) || !shaped(mg, m, f) || !shaped(mu, m, f) || !shaped(og, m, f) ||
+        !shaped(ou, m, f))
+        return DGC_EINVAL;
+    if (m == 0 || f == 0) return DGC_OK;
+    return rows_product<kDownBwd>({&my, &mw}, nullptr, nullptr, &mg, &mu, &og, &ou, nullptr, act,
+                                  status, stream);
+}
+
+extern "C" int dgc_ffn_gate_backward(const dgc_matrix* d_gate, const dgc_matrix* d_up,
+                                     const dgc_matrix* w_gate, const dgc_matrix* w_up,
+                                     const dgc_matrix* residual, const dgc_matrix* dx,
+                                     int32_t* status, dgc_stream_t stream) {
+    Mat ag, au, mg, mu, mr, mx;
+    int rc;
+    if (!d_gate || !status) return DGC_EINVAL;
+    if ((rc = check_matrix(d_gate, &ag, -1)) || (rc = check_matrix(d_up, &au, ag.dtype)) ||
+        (rc = check_matrix(w_gate, &mg, ag.dtype)) || (rc = check_matrix(w_up, &mu, ag.dtype)) ||
+        (rc = check_matrix(dx, &mx, ag.dtype)))
+        return rc;
+    if (residual && (rc = check_matrix(residual, &mr, ag.dtype))) return rc;
+    const uint64_t m = ag.rows, f = ag.cols, d = mg.cols;
+    if (!shaped(au, m, f) || !shaped(mg, f, d) || !shaped(mu, f, d) || !shaped(mx, m, d))
+        return DGC_EINVAL;
+    if (residual && !shaped(mr, m, d)) return DGC_EINVAL;
+    if (m == 0 || d == 0) return DGC_OK;
+    const Product second{&au, &mu};
+    return rows_product<kGateBwd>({&ag, &mg}, &second, nullptr, residual ? &mr : nullptr, nullptr,
+                                  &mx, nullptr, nullptr, 0, status, stream);
+}
+
+extern "C" int dgc_ffn_weight_grad_workspace(int64_t rows, int64_t cols, int64_t tokens,
+                                             size_t* bytes) {
+    if (!bytes || rows < 0 || cols < 0 || tokens < 0) return DGC_EINVAL;
+    if (rows > kMaxExtent || cols > kMaxExtent || tokens > kMaxExtent) return DGC_EUNSUPPORTED;
+    *bytes = (size_t)wgrad_workspace((uint64_t)rows, (uint64_t)cols, (uint64_t)tokens);
+    return DGC_OK;
+}
+
+extern "C" int dgc_ffn_weight_grad(const dgc_matrix* dy, const dgc_matrix* x, int32_t accumulate,
+                                   const dgc_matrix* dw, int32_t* status, void* ws,
+                                   size_t ws_bytes, dgc_stream_t stream) {
+    Mat my, mx;
+    int rc;
+    if (!dy || !dw || !status) return DGC_EINVAL;
+    if ((rc = check_matrix(dy, &my, -1)) || (rc = check_matrix(x, &mx, my.dtype))) return rc;
+    if (dw->rows < 0 || dw->cols < 0 || dw->reserved != 0 || dw->dtype != DGC_F32) return DGC_EINVAL;
+    if (mx.rows != my.rows || (uint64_t)dw->rows != my.cols || (uint64_t)dw->cols != mx.cols)
+        return DGC_EINVAL;
+    if (dw->rows == 0 || dw->cols == 0) return DGC_OK;
+    if (!dw->data || ((uintptr_t)dw->data & 3u) || (dw->rows > 1 && dw->ld < dw->cols))
+        return DGC_EINVAL;
+    if (dw->ld > (1ll << 36)) return DGC_EUNSUPPORTED;
+    const uint64_t rows = my.cols, cols = mx.cols, tokens = my.rows;
+    const uint64_t need = wgrad_workspace(rows, cols, tokens);
+    if (ws_bytes < need || (need && (!ws || ((uintptr_t)ws & 255u)))) return DGC_EINVAL;
+    const int sms = dgc_internal_sm_count();
+    if (sms <= 0) return DGC_ECUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    auto launched = [] {
+        if (cudaPeekAtLastError() != cudaSuccess) {
+            cudaGetLastError();
+            return (int)DGC_ECUDA;
+        }
+        dgc_internal_count_launches(1);
+        return (int)DGC_OK;
+    };
+    const Mat out{dw->data, rows, cols, rows == 1 ? (cols + 3) & ~3ull : (uint64_t)dw->ld, DGC_F32};
+    const dim3 grid2(ceil_div(cols, 256), (unsigned)std::min<uint64_t>(rows, 4096));
+    if (tokens == 0) {
+        if (accumulate) return DGC_OK;
+        k_wgrad_zero<<<grid2, 256, 0, s>>>((float*)out.p, out.ld, (uint32_t)rows, (uint32_t)cols);
+        return launched();
+    }
+    FfnArgs a{};
+    a.m = (uint32_t)rows;
+    a.n = (uint32_t)cols;
+    a.bn = wgrad_bn(cols);
+    a.tiles_m = ceil_div(rows, kBlockM);
+    a.tiles_n = ceil_div(cols, a.bn);
+    a.a_rows = kBlockM;
+    a.kb0 = a.kb = ceil_div(tokens, kBlockK);
+    const uint32_t want = wgrad_splits((uint64_t)a.tiles_m * a.tiles_n, a.kb);
+    a.kb_split = ceil_div(a.kb, want);
+    const uint32_t splits = ceil_div(a.kb, a.kb_split);
+    a.tiles = a.tiles_m * a.tiles_n * splits;
+    a.status = status;
+    if ((rc = make_map(&a.a0, my, 64, kBlockK)) || (rc = make_map(&a.b0, mx, 64, kBlockK))) return rc;
+    if (splits > 1) {
+        a.split_rows = a.tiles_m * kBlockM;
+        const Mat part{ws, (uint64_t)a.split_rows * splits, cols, (cols + 3) & ~3ull, DGC_F32};
+        if ((rc = make_map(&a.out0, part, 32, 32))) return rc;
+        if ((rc = launch_ffn<kWGrad>(a, my.dtype, sms, s))) return rc;
+        k_wgrad_join<<<grid2, 256, 0, s>>>((const float*)ws, part.ld, part.ld * a.split_rows, splits,
+                                           (float*)out.p, out.ld, (uint32_t)rows, (uint32_t)cols,
+                                           accumulate != 0);
+        return launched();
+    }
+    a.accumulate = accumulate != 0;
+    a.out[0] = out.p;
+    a.ld[0] = out.ld;
+    a.ragged = (cols & 3) != 0;
+    a.unaligned = ((uintptr_t)out.p & 15u) || (out.ld & 3u);
+    if (!a.unaligned && (rc = make_map(&a.out0, out, 32, 32))) return rc;
+    return launch_ffn<kWGrad>(a, my.dtype, sms, s);
+}
