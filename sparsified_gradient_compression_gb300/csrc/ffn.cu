@@ -64,13 +64,23 @@ struct FfnArgs {
 };
 
 // ------------------------------------------------------------------- tensor-core PTX
+// kCg: blocks that compute a tile together. With 2, `bar` is an address in the cluster's window:
+// the barrier of the pair's first block counts the bytes of both.
+template <int kCg>
 __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int32_t x, int32_t y,
-                                         uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];"
-        ::"r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
-        : "memory");
+                                         uint32_t bar) {
+    if (kCg == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];"
+            ::"r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global"
+            ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+            ::"r"(smem_addr(dst)), "l"(map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
 }
 __device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* src, int32_t x,
                                           int32_t y) {
@@ -92,30 +102,98 @@ __device__ __forceinline__ void bulk_wait_read() {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
-__device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                 ::"r"(smem_addr(slot)), "r"(cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+// The address of the same shared variable in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
+    return r;
 }
-__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                  : "memory");
 }
-__device__ __forceinline__ void mma_16bit(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                          bool add) {
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
         : "memory");
+    return ok != 0;
 }
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+template <int kCg>
+__device__ __forceinline__ void block_sync() {  // of the block, or of the pair
+    if (kCg == 1)
+        __syncthreads();
+    else
+        cluster_sync();
+}
+template <int kCg>
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {
+    if (kCg == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_addr(slot)), "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_addr(slot)), "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+template <int kCg>
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+    if (kCg == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
+                     : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
+                     : "memory");
+}
+template <int kCg>
+__device__ __forceinline__ void mma_16bit(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          bool add) {
+    if (kCg == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+            : "memory");
+}
+// Arrives at `bar` (of both blocks of a pair) when the products issued so far are done.
+template <int kCg>
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-        ::"r"(smem_addr(bar))
-        : "memory");
+    if (kCg == 1)
+        asm volatile(
+            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+            ::"r"(smem_addr(bar))
+            : "memory");
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+            ".multicast::cluster.b64 [%0], %1;"
+            ::"r"(smem_addr(bar)), "h"((uint16_t)3)
+            : "memory");
 }
 __device__ __forceinline__ void tmem_fence_before() {
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -216,10 +294,11 @@ struct FfnShared {
     volatile uint32_t abort;
 };
 
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, FfnShared* sh,
                                          int32_t* status) {
     for (uint32_t i = 0; i < kFfnWaitLimit; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
         if ((i & 15u) == 15u && sh->abort) return false;
     }
     report(status, DGC_ETIMEOUT);
@@ -266,9 +345,9 @@ struct Epilogue {
     static_assert(kSets * kBufs * kBox * 4 <= kEpilogueBytes, "staging");
 };
 
-template <int kKind>
+template <int kKind, int kCg>
 __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* staging,
-                                         uint32_t tmem) {
+                                         uint32_t tmem, uint32_t rank) {
     using E = Epilogue<kKind>;
     const int warp = (threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
     char* mine = staging + warp * (kEpilogueBytes / 4);
@@ -276,27 +355,31 @@ __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* 
     const uint32_t out_cols = kKind == kGate ? a.bn / 2 : a.bn;  // columns of one tile's output
     const uint32_t chunks = out_cols / 32;
     const bool has_in = E::kIn > 0 && (kKind == kDownBwd || a.residual);
+    const uint32_t first_tile = blockIdx.x / kCg, tile_step = gridDim.x / kCg;
+    const uint32_t row_in_tile = rank * kBlockM + warp * 32;
+    const uint32_t acc_empty = kCg == 1 ? 0 : peer_addr(sh->acc_empty, 0);
 
     // The loads of one chunk's inputs; chunks outside the output have none.
-    uint32_t load_tile = blockIdx.x, load_chunk = 0, load_n = 0;
+    uint32_t load_tile = first_tile, load_chunk = 0, load_n = 0;
     auto issue_load = [&]() {  // lane 0: the next chunk's inputs, if there is one left
         while (load_tile < a.tiles) {
             const Tile t = tile_at(a, load_tile);
-            const uint32_t y = t.mt * kBlockM + warp * 32, x = t.nt * out_cols + load_chunk * 32;
+            const uint32_t y = t.mt * kBlockM * kCg + row_in_tile;
+            const uint32_t x = t.nt * out_cols + load_chunk * 32;
             if (y >= a.m || x >= a.n) {  // the rest of this tile lies outside
                 load_chunk = 0;
-                load_tile += gridDim.x;
+                load_tile += tile_step;
                 continue;
             }
             const uint32_t set = load_n % E::kSets;
             uint64_t* bar = &sh->in_full[warp][set];
             mbar_arrive_expect_tx(bar, 2048u * E::kIn);
-            tma_load(buf(set, 0), &a.in0, x, y, bar);
-            if (E::kIn > 1) tma_load(buf(set, 1), &a.in1, x, y, bar);
+            tma_load<1>(buf(set, 0), &a.in0, x, y, smem_addr(bar));
+            if (E::kIn > 1) tma_load<1>(buf(set, 1), &a.in1, x, y, smem_addr(bar));
             ++load_n;
             if (++load_chunk == chunks) {
                 load_chunk = 0;
-                load_tile += gridDim.x;
+                load_tile += tile_step;
             }
             return;
         }
@@ -307,9 +390,9 @@ __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* 
     uint32_t done = 0;  // chunks this warp has finished
     uint32_t it = 0;
     bool ok = true;
-    for (uint32_t ti = blockIdx.x; ti < a.tiles && ok; ti += gridDim.x, ++it) {
+    for (uint32_t ti = first_tile; ti < a.tiles && ok; ti += tile_step, ++it) {
         const Tile t = tile_at(a, ti);
-        const uint32_t acc = it & 1, y = t.mt * kBlockM + warp * 32;
+        const uint32_t acc = it & 1, y = t.mt * kBlockM * kCg + row_in_tile;
         uint32_t k0, k1;
         k_range(a, t, &k0, &k1);
         ok = __all_sync(kFull, wait_bar(&sh->acc_full[acc], (it >> 1) & 1, sh, a.status));
@@ -443,7 +526,12 @@ __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* 
         }
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->acc_empty[acc]);
+        if (lane == 0) {
+            if (kCg == 1)
+                mbar_arrive(&sh->acc_empty[acc]);
+            else
+                mbar_arrive_peer(acc_empty + acc * 8);
+        }
     }
     if (lane == 0) {
         // inputs still on their way to a block that gave up
@@ -454,7 +542,7 @@ __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* 
     }
 }
 
-template <int kKind>
+template <int kKind, int kCg>
 __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ FfnArgs a) {
     constexpr bool kAcrossA = kKind == kWGrad;
     constexpr bool kAcrossB = kKind == kDownBwd || kKind == kGateBwd || kKind == kWGrad;
@@ -464,6 +552,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
     char* base = dyn + ((1024u - (smem_addr(dyn) & 1023u)) & 1023u);
     char* staging = base + a.stages * a.stage_bytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = kCg == 1 ? 0 : cluster_rank();
+    const uint32_t first_tile = blockIdx.x / kCg, tile_step = gridDim.x / kCg;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
@@ -472,7 +562,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh->acc_full[i], 1);
-            mbar_init(&sh->acc_empty[i], 4);
+            mbar_init(&sh->acc_empty[i], 4 * kCg);
         }
         for (int w = 0; w < 4; ++w)
             for (int i = 0; i < 3; ++i) mbar_init(&sh->in_full[w][i], 1);
@@ -480,19 +570,23 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
         mbar_init_fence();
         sh->abort = 0;
     }
-    if (warp == 2) tmem_alloc(&sh->tmem, a.tmem_cols);
+    if (warp == 2) tmem_alloc<kCg>(&sh->tmem, a.tmem_cols);
     tmem_fence_before();
     __syncthreads();
+    block_sync<kCg>();
     tmem_fence_after();
     const uint32_t tmem = sh->tmem;
 
     // One lane of warps 0 and 1 works; the others wait for it before the block's last barrier.
     if (warp == 0 && lane == 0) {
+        const uint32_t cols = a.bn / kCg;  // of B, loaded by this block
+        const uint32_t full = kCg == 1 ? smem_addr(sh->full) : peer_addr(sh->full, 0);
         uint32_t n = 0;  // stages filled so far
         bool ok = true;
-        for (uint32_t ti = blockIdx.x; ti < a.tiles && ok; ti += gridDim.x) {
+        for (uint32_t ti = first_tile; ti < a.tiles && ok; ti += tile_step) {
             const Tile t = tile_at(a, ti);
-            const int32_t row = t.mt * kBlockM;
+            const int32_t row = (t.mt * kCg + rank) * kBlockM;
+            const int32_t col = t.nt * a.bn + rank * cols;
             uint32_t k0, k1;
             k_range(a, t, &k0, &k1);
             for (uint32_t kb = k0; kb < k1; ++kb, ++n) {
@@ -500,41 +594,52 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
                 if (!(ok = wait_bar(&sh->empty[s], ((n / a.stages) & 1) ^ 1, sh, a.status))) break;
                 char* sa = base + s * a.stage_bytes;
                 char* sb = sa + kStageA;
-                uint64_t* bar = &sh->full[s];
-                mbar_arrive_expect_tx(bar, a.load_bytes);
+                const uint32_t bar = full + s * 8;
+                if (rank == 0) mbar_arrive_expect_tx(&sh->full[s], a.load_bytes);
                 const bool second = kKind == kGateBwd && kb >= a.kb0;
                 const int32_t k = (int32_t)(second ? kb - a.kb0 : kb) * kBlockK;
                 const CUtensorMap* ma = second ? &a.a1 : &a.a0;
                 const CUtensorMap* mb = second ? &a.b1 : &a.b0;
                 if (kAcrossA) {
-                    tma_load(sa, ma, row, k, bar);
-                    tma_load(sa + 8192, ma, row + 64, k, bar);
+                    tma_load<kCg>(sa, ma, row, k, bar);
+                    tma_load<kCg>(sa + 8192, ma, row + 64, k, bar);
                 } else {
-                    tma_load(sa, ma, k, row, bar);
+                    tma_load<kCg>(sa, ma, k, row, bar);
                 }
                 if (kAcrossB) {
-                    for (uint32_t c = 0; c < a.bn / 64; ++c)
-                        tma_load(sb + c * 8192, mb, t.nt * a.bn + c * 64, k, bar);
+                    for (uint32_t c = 0; c < cols / 64; ++c)
+                        tma_load<kCg>(sb + c * 8192, mb, col + c * 64, k, bar);
                 } else if (kKind == kGate) {
-                    tma_load(sb, &a.b0, k, t.nt * (a.bn / 2), bar);
-                    tma_load(sb + a.bn / 2 * 128, &a.b1, k, t.nt * (a.bn / 2), bar);
+                    // gate rows, then up rows; of a pair, one block brings each
+                    const int32_t f = t.nt * (a.bn / 2);
+                    if (kCg == 1) {
+                        tma_load<kCg>(sb, &a.b0, k, f, bar);
+                        tma_load<kCg>(sb + a.bn / 2 * 128, &a.b1, k, f, bar);
+                    } else {
+                        tma_load<kCg>(sb, rank == 0 ? &a.b0 : &a.b1, k, f, bar);
+                    }
                 } else {
-                    tma_load(sb, mb, k, t.nt * a.bn, bar);
+                    tma_load<kCg>(sb, mb, k, col, bar);
                 }
             }
         }
         if (!ok || sh->abort)  // copies in flight to a block that gives up
-            for (uint32_t i = n > a.stages ? n - a.stages : 0; i < n; ++i)
-                wait_quietly(&sh->full[i % a.stages], (i / a.stages) & 1);
-    } else if (warp == 1 && lane == 0) {
+            for (uint32_t i = n > a.stages ? n - a.stages : 0; i < n; ++i) {
+                if (rank == 0)
+                    wait_quietly(&sh->full[i % a.stages], (i / a.stages) & 1);
+                else
+                    wait_quietly(&sh->empty[i % a.stages], (i / a.stages) & 1);
+            }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
         uint32_t n = 0, it = 0;
         bool ok = true;
-        for (uint32_t ti = blockIdx.x; ti < a.tiles && ok; ti += gridDim.x, ++it) {
+        for (uint32_t ti = first_tile; ti < a.tiles && ok; ti += tile_step, ++it) {
             const Tile t = tile_at(a, ti);
             uint32_t k0, k1;
             k_range(a, t, &k0, &k1);
             const uint32_t acc = it & 1;
-            if (!(ok = wait_bar(&sh->acc_empty[acc], ((it >> 1) & 1) ^ 1, sh, a.status))) break;
+            if (!(ok = wait_bar<kCg == 2>(&sh->acc_empty[acc], ((it >> 1) & 1) ^ 1, sh, a.status)))
+                break;
             tmem_fence_after();
             const uint32_t d = tmem + acc * a.bn;
             for (uint32_t kb = k0; kb < k1; ++kb, ++n) {
@@ -546,22 +651,26 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
                 const uint64_t db = operand_desc<kAcrossB>(sa + kStageA);
 #pragma unroll
                 for (int k = 0; k < kBlockK / 16; ++k)  // 16 of the sum: 32 bytes, or 16 rows
-                    mma_16bit(d, da + k * (kAcrossA ? 2048 >> 4 : 2),
-                              db + k * (kAcrossB ? 2048 >> 4 : 2), a.idesc, kb > k0 || k > 0);
-                mma_commit(&sh->empty[s]);
+                    mma_16bit<kCg>(d, da + k * (kAcrossA ? 2048 >> 4 : 2),
+                                   db + k * (kAcrossB ? 2048 >> 4 : 2), a.idesc, kb > k0 || k > 0);
+                mma_commit<kCg>(&sh->empty[s]);
             }
-            if (ok) mma_commit(&sh->acc_full[acc]);
+            if (ok) mma_commit<kCg>(&sh->acc_full[acc]);
         }
-        mma_commit(&sh->drain);  // every product this thread issued is done before the block ends
+        mma_commit<kCg>(&sh->drain);  // every product issued is done before the block ends
         wait_quietly(&sh->drain, 0);
     } else if (warp >= 4) {
-        epilogue<kKind>(a, sh, staging, tmem);
+        epilogue<kKind, kCg>(a, sh, staging, tmem, rank);
     }
     __syncwarp();
     tmem_fence_before();
     __syncthreads();
+    // the pair's last commit has arrived here before this block's shared memory goes
+    if (kCg == 2 && rank == 1 && threadIdx.x == 32) wait_quietly(&sh->drain, 0);
+    __syncthreads();
+    block_sync<kCg>();
     tmem_fence_after();
-    if (warp == 2) tmem_free(tmem, a.tmem_cols);
+    if (warp == 2) tmem_free<kCg>(tmem, a.tmem_cols);
 }
 
 // The splits of a weight gradient, added in order: dW = (dW +) sum over s of part_s.
@@ -664,38 +773,53 @@ uint32_t choose_bn(uint64_t tiles_m, uint64_t n, uint32_t out_per_bn_num, uint32
     return narrowest;
 }
 
-template <int kKind>
+template <int kKind, int kCg>
 int launch_ffn(FfnArgs& a, int32_t dtype, int sms, cudaStream_t s) {
     constexpr bool kAcrossA = kKind == kWGrad;
     constexpr bool kAcrossB = kKind == kDownBwd || kKind == kGateBwd || kKind == kWGrad;
-    a.stage_bytes = kStageA + a.bn * 128;
+    a.stage_bytes = kStageA + a.bn / kCg * 128;
     a.stages = std::min<uint32_t>(kMaxStages, (kSmemLimit - 2048 - kEpilogueBytes) / a.stage_bytes);
-    a.load_bytes = (kAcrossA ? kBlockM : a.a_rows) * 128 + a.bn * 128;
+    a.load_bytes = (kAcrossA ? kBlockM : a.a_rows) * 128 * kCg + a.bn * 128;
     a.tmem_cols = std::max(32u, 2 * a.bn);
     a.half = dtype == DGC_F16;
     const uint32_t type = dtype == DGC_F16 ? 0 : 1;
     a.idesc = (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)kAcrossA << 15) |
-              ((uint32_t)kAcrossB << 16) | ((a.bn >> 3) << 17) | ((kBlockM >> 4) << 24);
-    a.group = 16;
+              ((uint32_t)kAcrossB << 16) | ((a.bn >> 3) << 17) | ((kBlockM * kCg >> 4) << 24);
+    a.group = 16 / kCg;
     const uint32_t smem = a.stages * a.stage_bytes + kEpilogueBytes + 1024;
     static bool set[128] = {false};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 128 || !set[dev]) {
-        if (cudaFuncSetAttribute(k_ffn<kKind>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(k_ffn<kKind, kCg>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)(kSmemLimit - 1024)) != cudaSuccess) {
             cudaGetLastError();
             return DGC_ECUDA;
         }
         if (dev >= 0 && dev < 128) set[dev] = true;
     }
-    k_ffn<kKind><<<std::min<uint32_t>(a.tiles, (uint32_t)sms), kFfnThreads, smem, s>>>(a);
-    if (cudaPeekAtLastError() != cudaSuccess) {
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(std::min<uint32_t>(a.tiles, (uint32_t)sms / kCg) * kCg);
+    c.blockDim = dim3(kFfnThreads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kCg;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    c.attrs = at;
+    c.numAttrs = kCg > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&c, k_ffn<kKind, kCg>, a) != cudaSuccess) {
         cudaGetLastError();
         return DGC_ECUDA;
     }
     dgc_internal_count_launches(1);
     return DGC_OK;
+}
+
+// Pairs of blocks (256 x 256 tiles) where there are tiles enough for every pair.
+bool use_pairs(uint64_t m, uint64_t n, uint32_t halves, int sms) {
+    return m > kBlockM && (uint64_t)ceil_div(m, 2 * kBlockM) * ceil_div(n, 256 / halves) >= (uint64_t)sms / 2;
 }
 
 // A product along rows: A [m, k] K-major, against B [n, k] K-major or [k, n] across.
@@ -713,9 +837,10 @@ int rows_product(Product p0, const Product* p1, const Mat* b_up, const Mat* in0,
     FfnArgs a{};
     a.m = (uint32_t)out0->rows;
     a.n = (uint32_t)out0->cols;
-    a.tiles_m = ceil_div(a.m, kBlockM);
     constexpr uint32_t halves = kKind == kGate ? 2 : 1;
-    a.bn = choose_bn(a.tiles_m, a.n, halves, kKind == kDown ? 32 : 64, sms);
+    const bool pairs = use_pairs(a.m, a.n, halves, sms);
+    a.tiles_m = ceil_div(a.m, pairs ? 2 * kBlockM : kBlockM);
+    a.bn = pairs ? 256 : choose_bn(a.tiles_m, a.n, halves, kKind == kDown ? 32 : 64, sms);
     a.tiles_n = ceil_div(a.n, a.bn / halves);
     a.tiles = a.tiles_m * a.tiles_n;
     a.a_rows = std::min<uint32_t>(kBlockM, (a.m + 7) & ~7u);
@@ -732,7 +857,7 @@ int rows_product(Product p0, const Product* p1, const Mat* b_up, const Mat* in0,
         if (kAcrossB)
             operand(map, m, 64, kBlockK);
         else
-            operand(map, m, kBlockK, a.bn / halves);
+            operand(map, m, kBlockK, a.bn / (pairs ? 2 : halves));
     };
     operand(&a.a0, *p0.a, kBlockK, a.a_rows);
     b_map(&a.b0, *p0.b);
@@ -755,7 +880,9 @@ int rows_product(Product p0, const Product* p1, const Mat* b_up, const Mat* in0,
     if (in1) operand(&a.in1, *in1, 32, 32);
     if (rc) return rc;
     a.residual = kKind == kGate ? out1 != nullptr : in0 != nullptr;
-    return launch_ffn<kKind>(a, out0->dtype, sms, reinterpret_cast<cudaStream_t>(stream));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return pairs ? launch_ffn<kKind, 2>(a, out0->dtype, sms, s)
+                 : launch_ffn<kKind, 1>(a, out0->dtype, sms, s);
 }
 
 bool bad_act(int32_t act) { return act < DGC_ACT_SILU || act > DGC_ACT_RELU; }
@@ -907,11 +1034,13 @@ extern "C" int dgc_ffn_weight_grad(const dgc_matrix* dy, const dgc_matrix* x, in
     a.m = (uint32_t)rows;
     a.n = (uint32_t)cols;
     a.bn = wgrad_bn(cols);
-    a.tiles_m = ceil_div(rows, kBlockM);
+    const bool pairs = use_pairs(rows, cols, 1, sms);
+    if (pairs) a.bn = 256;
+    a.tiles_m = ceil_div(rows, pairs ? 2 * kBlockM : kBlockM);
     a.tiles_n = ceil_div(cols, a.bn);
     a.a_rows = kBlockM;
     a.kb0 = a.kb = ceil_div(tokens, kBlockK);
-    const uint32_t want = wgrad_splits((uint64_t)a.tiles_m * a.tiles_n, a.kb);
+    const uint32_t want = pairs ? 1 : wgrad_splits((uint64_t)a.tiles_m * a.tiles_n, a.kb);
     a.kb_split = ceil_div(a.kb, want);
     const uint32_t splits = ceil_div(a.kb, a.kb_split);
     a.tiles = a.tiles_m * a.tiles_n * splits;
@@ -921,7 +1050,7 @@ extern "C" int dgc_ffn_weight_grad(const dgc_matrix* dy, const dgc_matrix* x, in
         a.split_rows = a.tiles_m * kBlockM;
         const Mat part{ws, (uint64_t)a.split_rows * splits, cols, (cols + 3) & ~3ull, DGC_F32};
         if ((rc = make_map(&a.out0, part, 32, 32))) return rc;
-        if ((rc = launch_ffn<kWGrad>(a, my.dtype, sms, s))) return rc;
+        if ((rc = launch_ffn<kWGrad, 1>(a, my.dtype, sms, s))) return rc;
         k_wgrad_join<<<grid2, 256, 0, s>>>((const float*)ws, part.ld, part.ld * a.split_rows, splits,
                                            (float*)out.p, out.ld, (uint32_t)rows, (uint32_t)cols,
                                            accumulate != 0);
@@ -933,5 +1062,6 @@ extern "C" int dgc_ffn_weight_grad(const dgc_matrix* dy, const dgc_matrix* x, in
     a.ragged = (cols & 3) != 0;
     a.unaligned = ((uintptr_t)out.p & 15u) || (out.ld & 3u);
     if (!a.unaligned && (rc = make_map(&a.out0, out, 32, 32))) return rc;
-    return launch_ffn<kWGrad>(a, my.dtype, sms, s);
+    return pairs ? launch_ffn<kWGrad, 2>(a, my.dtype, sms, s)
+                 : launch_ffn<kWGrad, 1>(a, my.dtype, sms, s);
 }
