@@ -582,6 +582,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
         const uint32_t cols = a.bn / kCg;  // of B, loaded by this block
         const uint32_t full = kCg == 1 ? smem_addr(sh->full) : peer_addr(sh->full, 0);
         uint32_t n = 0;  // stages filled so far
+        uint32_t s = 0, phase = 1;
         bool ok = true;
         for (uint32_t ti = first_tile; ti < a.tiles && ok; ti += tile_step) {
             const Tile t = tile_at(a, ti);
@@ -590,8 +591,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
             uint32_t k0, k1;
             k_range(a, t, &k0, &k1);
             for (uint32_t kb = k0; kb < k1; ++kb, ++n) {
-                const uint32_t s = n % a.stages;
-                if (!(ok = wait_bar(&sh->empty[s], ((n / a.stages) & 1) ^ 1, sh, a.status))) break;
+                if (!(ok = wait_bar(&sh->empty[s], phase, sh, a.status))) break;
                 char* sa = base + s * a.stage_bytes;
                 char* sb = sa + kStageA;
                 const uint32_t bar = full + s * 8;
@@ -621,6 +621,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
                 } else {
                     tma_load<kCg>(sb, mb, k, col, bar);
                 }
+                if (++s == a.stages) s = 0, phase ^= 1;
             }
         }
         if (!ok || sh->abort)  // copies in flight to a block that gives up
@@ -631,7 +632,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
                     wait_quietly(&sh->empty[i % a.stages], (i / a.stages) & 1);
             }
     } else if (warp == 1 && lane == 0 && rank == 0) {
-        uint32_t n = 0, it = 0;
+        uint32_t s = 0, phase = 0, it = 0;
+        const uint32_t smem = smem_addr(base);
         bool ok = true;
         for (uint32_t ti = first_tile; ti < a.tiles && ok; ti += tile_step, ++it) {
             const Tile t = tile_at(a, ti);
@@ -642,11 +644,10 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
                 break;
             tmem_fence_after();
             const uint32_t d = tmem + acc * a.bn;
-            for (uint32_t kb = k0; kb < k1; ++kb, ++n) {
-                const uint32_t s = n % a.stages;
-                if (!(ok = wait_bar(&sh->full[s], (n / a.stages) & 1, sh, a.status))) break;
+            for (uint32_t kb = k0; kb < k1; ++kb) {
+                if (!(ok = wait_bar(&sh->full[s], phase, sh, a.status))) break;
                 tmem_fence_after();
-                const uint32_t sa = smem_addr(base + s * a.stage_bytes);
+                const uint32_t sa = smem + s * a.stage_bytes;
                 const uint64_t da = operand_desc<kAcrossA>(sa);
                 const uint64_t db = operand_desc<kAcrossB>(sa + kStageA);
 #pragma unroll
@@ -654,6 +655,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
                     mma_16bit<kCg>(d, da + k * (kAcrossA ? 2048 >> 4 : 2),
                                    db + k * (kAcrossB ? 2048 >> 4 : 2), a.idesc, kb > k0 || k > 0);
                 mma_commit<kCg>(&sh->empty[s]);
+                if (++s == a.stages) s = 0, phase ^= 1;
             }
             if (ok) mma_commit<kCg>(&sh->acc_full[acc]);
         }
