@@ -123,6 +123,17 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
         : "memory");
     return ok != 0;
 }
+// One lane of a converged warp. Under this predicate the compiler knows that one lane issues, and
+// keeps operands in uniform registers; under a test of the lane's number it does not.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -577,10 +588,11 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
     tmem_fence_after();
     const uint32_t tmem = sh->tmem;
 
-    // One lane of warps 0 and 1 works; the others wait for it before the block's last barrier.
-    if (warp == 0 && lane == 0) {
+    // Warps 0 and 1 run their loops whole, and one elected lane issues.
+    if (warp == 0) {
         const uint32_t cols = a.bn / kCg;  // of B, loaded by this block
         const uint32_t full = kCg == 1 ? smem_addr(sh->full) : peer_addr(sh->full, 0);
+        const uint32_t stages = a.stages, stage_bytes = a.stage_bytes;
         uint32_t n = 0;  // stages filled so far
         uint32_t s = 0, phase = 1;
         bool ok = true;
@@ -591,75 +603,88 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
             uint32_t k0, k1;
             k_range(a, t, &k0, &k1);
             for (uint32_t kb = k0; kb < k1; ++kb, ++n) {
-                if (!(ok = wait_bar(&sh->empty[s], phase, sh, a.status))) break;
-                char* sa = base + s * a.stage_bytes;
-                char* sb = sa + kStageA;
-                const uint32_t bar = full + s * 8;
-                if (rank == 0) mbar_arrive_expect_tx(&sh->full[s], a.load_bytes);
-                const bool second = kKind == kGateBwd && kb >= a.kb0;
-                const int32_t k = (int32_t)(second ? kb - a.kb0 : kb) * kBlockK;
-                const CUtensorMap* ma = second ? &a.a1 : &a.a0;
-                const CUtensorMap* mb = second ? &a.b1 : &a.b0;
-                if (kAcrossA) {
-                    tma_load<kCg>(sa, ma, row, k, bar);
-                    tma_load<kCg>(sa + 8192, ma, row + 64, k, bar);
-                } else {
-                    tma_load<kCg>(sa, ma, k, row, bar);
-                }
-                if (kAcrossB) {
-                    for (uint32_t c = 0; c < cols / 64; ++c)
-                        tma_load<kCg>(sb + c * 8192, mb, col + c * 64, k, bar);
-                } else if (kKind == kGate) {
-                    // gate rows, then up rows; of a pair, one block brings each
-                    const int32_t f = t.nt * (a.bn / 2);
-                    if (kCg == 1) {
-                        tma_load<kCg>(sb, &a.b0, k, f, bar);
-                        tma_load<kCg>(sb + a.bn / 2 * 128, &a.b1, k, f, bar);
+                ok = __all_sync(kFull, wait_bar(&sh->empty[s], phase, sh, a.status));
+                if (!ok) break;
+                if (elect_one()) {
+                    char* sa = base + s * stage_bytes;
+                    char* sb = sa + kStageA;
+                    const uint32_t bar = full + s * 8;
+                    if (rank == 0) mbar_arrive_expect_tx(&sh->full[s], a.load_bytes);
+                    const bool second = kKind == kGateBwd && kb >= a.kb0;
+                    const int32_t k = (int32_t)(second ? kb - a.kb0 : kb) * kBlockK;
+                    const CUtensorMap* ma = second ? &a.a1 : &a.a0;
+                    const CUtensorMap* mb = second ? &a.b1 : &a.b0;
+                    if (kAcrossA) {
+                        tma_load<kCg>(sa, ma, row, k, bar);
+                        tma_load<kCg>(sa + 8192, ma, row + 64, k, bar);
                     } else {
-                        tma_load<kCg>(sb, rank == 0 ? &a.b0 : &a.b1, k, f, bar);
+                        tma_load<kCg>(sa, ma, k, row, bar);
                     }
-                } else {
-                    tma_load<kCg>(sb, mb, k, col, bar);
+                    if (kAcrossB) {
+                        for (uint32_t c = 0; c < cols / 64; ++c)
+                            tma_load<kCg>(sb + c * 8192, mb, col + c * 64, k, bar);
+                    } else if (kKind == kGate) {
+                        // gate rows, then up rows; of a pair, one block brings each
+                        const int32_t f = t.nt * (a.bn / 2);
+                        if (kCg == 1) {
+                            tma_load<kCg>(sb, &a.b0, k, f, bar);
+                            tma_load<kCg>(sb + a.bn / 2 * 128, &a.b1, k, f, bar);
+                        } else {
+                            tma_load<kCg>(sb, rank == 0 ? &a.b0 : &a.b1, k, f, bar);
+                        }
+                    } else {
+                        tma_load<kCg>(sb, mb, k, col, bar);
+                    }
                 }
-                if (++s == a.stages) s = 0, phase ^= 1;
+                __syncwarp();
+                if (++s == stages) s = 0, phase ^= 1;
             }
         }
         if (!ok || sh->abort)  // copies in flight to a block that gives up
-            for (uint32_t i = n > a.stages ? n - a.stages : 0; i < n; ++i) {
+            for (uint32_t i = n > stages ? n - stages : 0; i < n; ++i) {
                 if (rank == 0)
-                    wait_quietly(&sh->full[i % a.stages], (i / a.stages) & 1);
+                    wait_quietly(&sh->full[i % stages], (i / stages) & 1);
                 else
-                    wait_quietly(&sh->empty[i % a.stages], (i / a.stages) & 1);
+                    wait_quietly(&sh->empty[i % stages], (i / stages) & 1);
             }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
+        const uint32_t stages = a.stages, stage_bytes = a.stage_bytes, idesc = a.idesc;
+        const uint64_t da0 = operand_desc<kAcrossA>(smem_addr(base));
+        const uint64_t db0 = operand_desc<kAcrossB>(smem_addr(base) + kStageA);
         uint32_t s = 0, phase = 0, it = 0;
-        const uint32_t smem = smem_addr(base);
         bool ok = true;
         for (uint32_t ti = first_tile; ti < a.tiles && ok; ti += tile_step, ++it) {
             const Tile t = tile_at(a, ti);
             uint32_t k0, k1;
             k_range(a, t, &k0, &k1);
             const uint32_t acc = it & 1;
-            if (!(ok = wait_bar<kCg == 2>(&sh->acc_empty[acc], ((it >> 1) & 1) ^ 1, sh, a.status)))
-                break;
+            ok = __all_sync(kFull, wait_bar<kCg == 2>(&sh->acc_empty[acc], ((it >> 1) & 1) ^ 1, sh,
+                                                      a.status));
+            if (!ok) break;
             tmem_fence_after();
             const uint32_t d = tmem + acc * a.bn;
             for (uint32_t kb = k0; kb < k1; ++kb) {
-                if (!(ok = wait_bar(&sh->full[s], phase, sh, a.status))) break;
+                ok = __all_sync(kFull, wait_bar(&sh->full[s], phase, sh, a.status));
+                if (!ok) break;
                 tmem_fence_after();
-                const uint32_t sa = smem + s * a.stage_bytes;
-                const uint64_t da = operand_desc<kAcrossA>(sa);
-                const uint64_t db = operand_desc<kAcrossB>(sa + kStageA);
+                if (elect_one()) {
+                    const uint64_t da = da0 + (s * stage_bytes >> 4);
+                    const uint64_t db = db0 + (s * stage_bytes >> 4);
 #pragma unroll
-                for (int k = 0; k < kBlockK / 16; ++k)  // 16 of the sum: 32 bytes, or 16 rows
-                    mma_16bit<kCg>(d, da + k * (kAcrossA ? 2048 >> 4 : 2),
-                                   db + k * (kAcrossB ? 2048 >> 4 : 2), a.idesc, kb > k0 || k > 0);
-                mma_commit<kCg>(&sh->empty[s]);
-                if (++s == a.stages) s = 0, phase ^= 1;
+                    for (int k = 0; k < kBlockK / 16; ++k)  // 16 of the sum: 32 bytes, or 16 rows
+                        mma_16bit<kCg>(d, da + k * (kAcrossA ? 2048 >> 4 : 2),
+                                       db + k * (kAcrossB ? 2048 >> 4 : 2), idesc,
+                                       kb > k0 || k > 0);
+                    mma_commit<kCg>(&sh->empty[s]);
+                }
+                __syncwarp();
+                if (++s == stages) s = 0, phase ^= 1;
             }
-            if (ok) mma_commit<kCg>(&sh->acc_full[acc]);
+            if (ok && elect_one()) mma_commit<kCg>(&sh->acc_full[acc]);
+            __syncwarp();
         }
-        mma_commit<kCg>(&sh->drain);  // every product issued is done before the block ends
+        if (elect_one()) mma_commit<kCg>(&sh->drain);  // what was issued is done before the end
+        __syncwarp();
         wait_quietly(&sh->drain, 0);
     } else if (warp >= 4) {
         epilogue<kKind, kCg>(a, sh, staging, tmem, rank);
