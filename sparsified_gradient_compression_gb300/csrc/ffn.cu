@@ -10,7 +10,7 @@
 //
 // One kernel, k_ffn, for all five. A persistent block per SM computes 128-row output tiles:
 // warp 0 brings the operands' 64-deep slices by TMA into a ring of shared-memory stages, warp 1
-// issues tcgen05.mma on them into one of two accumulators in tensor memory, warps 4-7 empty the
+// issues tcgen05.mma on them into one of two accumulators in tensor memory, warps 4-11 empty the
 // other one: tcgen05.ld, the epilogue's arithmetic in binary32, one rounding, and a TMA store
 // from shared memory. Operands whose long axis is the sum's (x, H, dy, dG, dU and the weights of
 // the forward pass) are read along it ("K-major"); the others (the weights of the backward pass,
@@ -31,12 +31,14 @@ namespace {
 
 enum Kind { kGate = 0, kDown = 1, kDownBwd = 2, kGateBwd = 3, kWGrad = 4 };
 
-constexpr int kFfnThreads = 256;
+constexpr int kEpilogueWarps = 8;
+constexpr int kFfnThreads = 128 + 32 * kEpilogueWarps;
 constexpr int kBlockM = 128;
 constexpr int kBlockK = 64;                    // 128 bytes of 16-bit entries: the swizzle's span
 constexpr uint32_t kStageA = kBlockM * kBlockK * 2;
 constexpr int kMaxStages = 8;
-constexpr uint32_t kEpilogueBytes = 48 * 1024; // staging of warps 4-7, 12 KB each
+constexpr uint32_t kWarpStaging = 8192;
+constexpr uint32_t kEpilogueBytes = kWarpStaging * kEpilogueWarps;
 constexpr uint32_t kSmemLimit = 232448;        // 227 KB
 constexpr uint32_t kFfnWaitLimit = 1u << 23;   // polls; the longest sum takes far fewer
 constexpr int64_t kMaxExtent = 1 << 24;
@@ -251,26 +253,28 @@ __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f
 constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
-__device__ __forceinline__ float act_value(int act, float g) {
-    if (act == DGC_ACT_SILU) return __fdividef(g, 1.0f + __expf(-g));
-    if (act == DGC_ACT_GELU) return 0.5f * g * (1.0f + erff(g * 0.7071067811865476f));
-    if (act == DGC_ACT_GELU_TANH) {  // (1 + tanh z) / 2 = sigmoid(2 z)
+template <int kAct>
+__device__ __forceinline__ float act_value(float g) {
+    if (kAct == DGC_ACT_SILU) return __fdividef(g, 1.0f + __expf(-g));
+    if (kAct == DGC_ACT_GELU) return 0.5f * g * (1.0f + erff(g * 0.7071067811865476f));
+    if (kAct == DGC_ACT_GELU_TANH) {  // (1 + tanh z) / 2 = sigmoid(2 z)
         const float z = 2.0f * kGeluC * g * fmaf(kGeluA * g, g, 1.0f);
         return __fdividef(g, 1.0f + __expf(-z));
     }
     return g <= 0.0f ? 0.0f : g;
 }
-__device__ __forceinline__ ActValue act_both(int act, float g) {
+template <int kAct>
+__device__ __forceinline__ ActValue act_both(float g) {
     ActValue r;
-    if (act == DGC_ACT_SILU) {
+    if (kAct == DGC_ACT_SILU) {
         const float s = sigmoid(g);
         r.value = g * s;
         r.slope = s * fmaf(g, 1.0f - s, 1.0f);
-    } else if (act == DGC_ACT_GELU) {
+    } else if (kAct == DGC_ACT_GELU) {
         const float p = 0.5f * (1.0f + erff(g * 0.7071067811865476f));
         r.value = g * p;
         r.slope = fmaf(g * 0.3989422804014327f, __expf(-0.5f * g * g), p);
-    } else if (act == DGC_ACT_GELU_TANH) {
+    } else if (kAct == DGC_ACT_GELU_TANH) {
         const float g2 = g * g;
         const float s = sigmoid(2.0f * kGeluC * g * fmaf(kGeluA, g2, 1.0f));
         r.value = g * s;
@@ -282,16 +286,18 @@ __device__ __forceinline__ ActValue act_both(int act, float g) {
     return r;
 }
 
-__device__ __forceinline__ uint32_t pack2(float x, float y, bool half) {
-    if (half) {
+template <bool kHalf>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+    if (kHalf) {
         const __half2 h = __floats2half2_rn(x, y);
         return *reinterpret_cast<const uint32_t*>(&h);
     }
     const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
     return *reinterpret_cast<const uint32_t*>(&b);
 }
-__device__ __forceinline__ float2 unpack2(uint32_t w, bool half) {
-    if (half) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+template <bool kHalf>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if (kHalf) return __half22float2(*reinterpret_cast<const __half2*>(&w));
     return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
 }
 
@@ -299,7 +305,7 @@ __device__ __forceinline__ float2 unpack2(uint32_t w, bool half) {
 struct FfnShared {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t acc_full[2], acc_empty[2];
-    uint64_t in_full[4][3];
+    uint64_t in_full[kEpilogueWarps][4];
     uint64_t drain;
     uint32_t tmem;
     volatile uint32_t abort;
@@ -352,33 +358,79 @@ struct Epilogue {
     static constexpr int kOut = kKind == kGate ? 3 : kKind == kDownBwd ? 2 : 1;
     static constexpr int kBufs = kOut > kIn ? kOut : kIn;       // 32 x 32 boxes of one set
     static constexpr uint32_t kBox = kKind == kWGrad ? 4096 : 2048;
-    static constexpr int kSets = kKind == kGate ? 2 : 3;
-    static_assert(kSets * kBufs * kBox * 4 <= kEpilogueBytes, "staging");
+    // sets: one is written while the others' stores leave and their loads arrive
+    static constexpr int kSets = kKind == kGate ? 1 : (kKind == kDownBwd || kKind == kWGrad) ? 2 : 4;
+    static_assert(kSets * kBufs * kBox <= kWarpStaging, "staging");
 };
 
-template <int kKind, int kCg>
+// A chunk's 32 rows x 32 columns, a row a lane: v (and u) from the accumulator, the inputs from the
+// staging boxes i0, i1, the results into o0.. in their place, 16 bytes at a time in the swizzled
+// order of a TMA box.
+template <int kKind, int kAct, bool kHalf>
+__device__ __forceinline__ void chunk_16bit(const uint32_t (&v)[32], const uint32_t (&u)[32],
+                                            bool residual, char* b0, char* b1, char* b2, int lane) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const uint32_t at = lane * 64 + ((p ^ ((lane >> 1) & 3)) << 4);
+        uint32_t o0[4], o1[4], o2[4];
+        uint4 q = make_uint4(0, 0, 0, 0), w = q;
+        if (kKind == kDownBwd || ((kKind == kDown || kKind == kGateBwd) && residual))
+            q = *reinterpret_cast<const uint4*>(b0 + at);
+        if (kKind == kDownBwd) w = *reinterpret_cast<const uint4*>(b1 + at);
+        const uint32_t i0[4] = {q.x, q.y, q.z, q.w}, i1[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float v0 = __uint_as_float(v[8 * p + 2 * j]);
+            const float v1 = __uint_as_float(v[8 * p + 2 * j + 1]);
+            if (kKind == kGate) {
+                const float u0 = __uint_as_float(u[8 * p + 2 * j]);
+                const float u1 = __uint_as_float(u[8 * p + 2 * j + 1]);
+                o0[j] = pack2<kHalf>(act_value<kAct>(v0) * u0, act_value<kAct>(v1) * u1);
+                o1[j] = pack2<kHalf>(v0, v1);
+                o2[j] = pack2<kHalf>(u0, u1);
+            } else if (kKind == kDownBwd) {
+                const float2 g = unpack2<kHalf>(i0[j]), x = unpack2<kHalf>(i1[j]);
+                const ActValue f0 = act_both<kAct>(g.x), f1 = act_both<kAct>(g.y);
+                o0[j] = pack2<kHalf>(v0 * x.x * f0.slope, v1 * x.y * f1.slope);
+                o1[j] = pack2<kHalf>(v0 * f0.value, v1 * f1.value);
+            } else {
+                const float2 r = unpack2<kHalf>(i0[j]);
+                o0[j] = residual ? pack2<kHalf>(v0 + r.x, v1 + r.y) : pack2<kHalf>(v0, v1);
+            }
+        }
+        *reinterpret_cast<uint4*>(b0 + at) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+        if (kKind == kGate || kKind == kDownBwd)
+            *reinterpret_cast<uint4*>(b1 + at) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+        if (kKind == kGate)
+            *reinterpret_cast<uint4*>(b2 + at) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+    }
+}
+
+// Warps 4-11: two for each quarter of the accumulator's rows (the quarter a warp may read is its
+// number modulo 4), taking every other chunk of 32 columns.
+template <int kKind, int kCg, int kAct>
 __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* staging,
                                          uint32_t tmem, uint32_t rank) {
     using E = Epilogue<kKind>;
     const int warp = (threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
-    char* mine = staging + warp * (kEpilogueBytes / 4);
+    char* mine = staging + warp * kWarpStaging;
     auto buf = [&](uint32_t set, int i) { return mine + (set * E::kBufs + i) * E::kBox; };
     const uint32_t out_cols = kKind == kGate ? a.bn / 2 : a.bn;  // columns of one tile's output
-    const uint32_t chunks = out_cols / 32;
+    const uint32_t chunks = out_cols / 32, first_chunk = warp >> 2;
     const bool has_in = E::kIn > 0 && (kKind == kDownBwd || a.residual);
     const uint32_t first_tile = blockIdx.x / kCg, tile_step = gridDim.x / kCg;
-    const uint32_t row_in_tile = rank * kBlockM + warp * 32;
+    const uint32_t row_in_tile = rank * kBlockM + (warp & 3) * 32;
     const uint32_t acc_empty = kCg == 1 ? 0 : peer_addr(sh->acc_empty, 0);
 
     // The loads of one chunk's inputs; chunks outside the output have none.
-    uint32_t load_tile = first_tile, load_chunk = 0, load_n = 0;
+    uint32_t load_tile = first_tile, load_chunk = first_chunk, load_n = 0;
     auto issue_load = [&]() {  // lane 0: the next chunk's inputs, if there is one left
         while (load_tile < a.tiles) {
             const Tile t = tile_at(a, load_tile);
             const uint32_t y = t.mt * kBlockM * kCg + row_in_tile;
             const uint32_t x = t.nt * out_cols + load_chunk * 32;
-            if (y >= a.m || x >= a.n) {  // the rest of this tile lies outside
-                load_chunk = 0;
+            if (y >= a.m || x >= a.n || load_chunk >= chunks) {  // none left in this tile
+                load_chunk = first_chunk;
                 load_tile += tile_step;
                 continue;
             }
@@ -388,10 +440,7 @@ __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* 
             tma_load<1>(buf(set, 0), &a.in0, x, y, smem_addr(bar));
             if (E::kIn > 1) tma_load<1>(buf(set, 1), &a.in1, x, y, smem_addr(bar));
             ++load_n;
-            if (++load_chunk == chunks) {
-                load_chunk = 0;
-                load_tile += tile_step;
-            }
+            load_chunk += 2;
             return;
         }
     };
@@ -409,74 +458,45 @@ __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* 
         ok = __all_sync(kFull, wait_bar(&sh->acc_full[acc], (it >> 1) & 1, sh, a.status));
         if (!ok) break;
         tmem_fence_after();
-        const uint32_t src = tmem + acc * a.bn + ((uint32_t)(warp * 32) << 16);
-        for (uint32_t c = 0; c < chunks && y < a.m; ++c) {
+        const uint32_t src = tmem + acc * a.bn + ((uint32_t)((warp & 3) * 32) << 16);
+        for (uint32_t c = first_chunk; c < chunks && y < a.m; c += 2) {
             const uint32_t x = t.nt * out_cols + c * 32;
             if (x >= a.n) break;
             const uint32_t set = done % E::kSets;
             uint32_t v[32], u[32];
             tmem_load32(src + c * 32, v);
             if (kKind == kGate) tmem_load32(src + out_cols + c * 32, u);
+            if (has_in) {
+                // the store before this one has left its set: the next inputs go there
+                if (lane == 0) {
+                    bulk_wait_read<0>();
+                    issue_load();
+                }
+                __syncwarp();
+                ok = __all_sync(kFull, wait_bar(&sh->in_full[warp][set], (done / E::kSets) & 1, sh,
+                                                a.status));
+                if (!ok) break;
+            } else {
+                // the last store from this set has left it
+                if (lane == 0) bulk_wait_read<E::kSets - 1>();
+                __syncwarp();
+            }
             tmem_wait_load();
             if (k0 >= k1) {  // an empty sum: the accumulator was never written
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = u[i] = 0;
             }
-            if (has_in) {
-                ok = __all_sync(kFull, wait_bar(&sh->in_full[warp][set], (done / E::kSets) & 1, sh,
-                                                a.status));
-                if (!ok) break;
+            if (kKind == kWGrad) {
+#pragma unroll
+                for (int p = 0; p < 8; ++p)
+                    *reinterpret_cast<uint4*>(buf(set, 0) + lane * 128 + ((p ^ (lane & 7)) << 4)) =
+                        make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
+            } else if (a.half) {
+                chunk_16bit<kKind, kAct, true>(v, u, has_in, buf(set, 0), buf(set, E::kBufs > 1),
+                                               buf(set, E::kBufs - 1), lane);
             } else {
-                // the set's last store has left it (one set is written while the others leave)
-                if (lane == 0) bulk_wait_read<E::kSets - 1>();
-                __syncwarp();
-            }
-            // 16-byte pieces of this lane's row, in the swizzled order of the TMA box
-#pragma unroll
-            for (int p = 0; p < (kKind == kWGrad ? 8 : 4); ++p) {
-                if (kKind == kWGrad) {
-                    uint4 w = make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
-                    *reinterpret_cast<uint4*>(buf(set, 0) + lane * 128 + ((p ^ (lane & 7)) << 4)) = w;
-                    continue;
-                }
-                const uint32_t at = lane * 64 + ((p ^ ((lane >> 1) & 3)) << 4);
-                uint32_t o0[4], o1[4], o2[4], i0[4], i1[4];
-                if (has_in) {
-                    const uint4 q = *reinterpret_cast<const uint4*>(buf(set, 0) + at);
-                    i0[0] = q.x, i0[1] = q.y, i0[2] = q.z, i0[3] = q.w;
-                    if (E::kIn > 1) {
-                        const uint4 s = *reinterpret_cast<const uint4*>(buf(set, 1) + at);
-                        i1[0] = s.x, i1[1] = s.y, i1[2] = s.z, i1[3] = s.w;
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float v0 = __uint_as_float(v[8 * p + 2 * j]);
-                    const float v1 = __uint_as_float(v[8 * p + 2 * j + 1]);
-                    if (kKind == kGate) {
-                        const float u0 = __uint_as_float(u[8 * p + 2 * j]);
-                        const float u1 = __uint_as_float(u[8 * p + 2 * j + 1]);
-                        o0[j] = pack2(act_value(a.act, v0) * u0, act_value(a.act, v1) * u1, a.half);
-                        o1[j] = pack2(v0, v1, a.half);
-                        o2[j] = pack2(u0, u1, a.half);
-                    } else if (kKind == kDownBwd) {
-                        const float2 g = unpack2(i0[j], a.half), w = unpack2(i1[j], a.half);
-                        const ActValue f0 = act_both(a.act, g.x), f1 = act_both(a.act, g.y);
-                        o0[j] = pack2(v0 * w.x * f0.slope, v1 * w.y * f1.slope, a.half);
-                        o1[j] = pack2(v0 * f0.value, v1 * f1.value, a.half);
-                    } else {
-                        float2 r = make_float2(0.0f, 0.0f);
-                        if (has_in) r = unpack2(i0[j], a.half);
-                        o0[j] = pack2(v0 + r.x, v1 + r.y, a.half);
-                    }
-                }
-                *reinterpret_cast<uint4*>(buf(set, 0) + at) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-                if (E::kOut > 1)
-                    *reinterpret_cast<uint4*>(buf(set, 1) + at) =
-                        make_uint4(o1[0], o1[1], o1[2], o1[3]);
-                if (E::kOut > 2)
-                    *reinterpret_cast<uint4*>(buf(set, E::kOut > 2 ? 2 : 0) + at) =
-                        make_uint4(o2[0], o2[1], o2[2], o2[3]);
+                chunk_16bit<kKind, kAct, false>(v, u, has_in, buf(set, 0), buf(set, E::kBufs > 1),
+                                                buf(set, E::kBufs - 1), lane);
             }
             if (a.unaligned || (a.ragged && x + 32 > a.n)) {
                 // a row of up to 32 columns per step, one column a lane
@@ -502,13 +522,7 @@ __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* 
                         }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) {
-                    bulk_commit();  // an empty group: the sets are counted by groups
-                    if (has_in) {
-                        bulk_wait_read<1>();
-                        issue_load();
-                    }
-                }
+                if (lane == 0) bulk_commit();  // an empty group: the sets are counted by groups
             } else {
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -523,14 +537,10 @@ __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* 
                         if (kKind == kDownBwd) tma_store(&a.out1, buf(set, 1), x, y);
                         if (kKind == kGate && a.residual) {  // gate and up are wanted
                             tma_store(&a.out1, buf(set, 1), x, y);
-                            tma_store(&a.out2, buf(set, E::kOut > 2 ? 2 : 0), x, y);
+                            tma_store(&a.out2, buf(set, 2), x, y);
                         }
                     }
                     bulk_commit();
-                    if (has_in) {
-                        bulk_wait_read<1>();  // the set before this one has left
-                        issue_load();
-                    }
                 }
             }
             ++done;
@@ -562,7 +572,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
     FfnShared* sh = &shared;
     char* base = dyn + ((1024u - (smem_addr(dyn) & 1023u)) & 1023u);
     char* staging = base + a.stages * a.stage_bytes;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
     const uint32_t rank = kCg == 1 ? 0 : cluster_rank();
     const uint32_t first_tile = blockIdx.x / kCg, tile_step = gridDim.x / kCg;
 
@@ -573,10 +583,10 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh->acc_full[i], 1);
-            mbar_init(&sh->acc_empty[i], 4 * kCg);
+            mbar_init(&sh->acc_empty[i], kEpilogueWarps * kCg);
         }
-        for (int w = 0; w < 4; ++w)
-            for (int i = 0; i < 3; ++i) mbar_init(&sh->in_full[w][i], 1);
+        for (int w = 0; w < kEpilogueWarps; ++w)
+            for (int i = 0; i < 4; ++i) mbar_init(&sh->in_full[w][i], 1);
         mbar_init(&sh->drain, 1);
         mbar_init_fence();
         sh->abort = 0;
@@ -687,7 +697,16 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
         __syncwarp();
         wait_quietly(&sh->drain, 0);
     } else if (warp >= 4) {
-        epilogue<kKind, kCg>(a, sh, staging, tmem, rank);
+        if (kKind != kGate && kKind != kDownBwd)
+            epilogue<kKind, kCg, DGC_ACT_RELU>(a, sh, staging, tmem, rank);
+        else if (a.act == DGC_ACT_SILU)
+            epilogue<kKind, kCg, DGC_ACT_SILU>(a, sh, staging, tmem, rank);
+        else if (a.act == DGC_ACT_GELU)
+            epilogue<kKind, kCg, DGC_ACT_GELU>(a, sh, staging, tmem, rank);
+        else if (a.act == DGC_ACT_GELU_TANH)
+            epilogue<kKind, kCg, DGC_ACT_GELU_TANH>(a, sh, staging, tmem, rank);
+        else
+            epilogue<kKind, kCg, DGC_ACT_RELU>(a, sh, staging, tmem, rank);
     }
     __syncwarp();
     tmem_fence_before();
