@@ -40,7 +40,9 @@ constexpr int kMaxStages = 8;
 constexpr uint32_t kWarpStaging = 8192;
 constexpr uint32_t kEpilogueBytes = kWarpStaging * kEpilogueWarps;
 constexpr uint32_t kSmemLimit = 232448;        // 227 KB
-constexpr uint32_t kFfnWaitLimit = 1u << 23;   // polls; the longest sum takes far fewer
+constexpr uint32_t kFfnWaitLimit = 1u << 23;   // probes of a wait, and its time: the longest sum
+constexpr uint64_t kFfnWaitNs = 2000000000;    // takes far less
+constexpr uint32_t kSleepNs = 20000;
 constexpr int64_t kMaxExtent = 1 << 24;
 
 struct FfnArgs {
@@ -114,16 +116,32 @@ __device__ __forceinline__ void mbar_arrive_peer(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                  : "memory");
 }
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+// Probes that may put the thread to sleep for up to `ns` while the phase is not complete.
+template <bool kCluster>
+__device__ __forceinline__ bool mbar_sleep_wait(uint64_t* bar, uint32_t parity, uint32_t ns) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
+    if (kCluster)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_addr(bar)), "r"(parity), "r"(ns)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_addr(bar)), "r"(parity), "r"(ns)
+            : "memory");
     return ok != 0;
+}
+__device__ __forceinline__ uint64_t global_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
 }
 // One lane of a converged warp. Under this predicate the compiler knows that one lane issues, and
 // keeps operands in uniform registers; under a test of the lane's number it does not.
@@ -311,12 +329,16 @@ struct FfnShared {
     volatile uint32_t abort;
 };
 
+// At most kFfnWaitLimit probes and about kFfnWaitNs.
 template <bool kCluster = false>
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, FfnShared* sh,
                                          int32_t* status) {
+    if (mbar_sleep_wait<kCluster>(bar, parity, kSleepNs)) return true;
+    const uint64_t begin = global_ns();
     for (uint32_t i = 0; i < kFfnWaitLimit; ++i) {
-        if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
-        if ((i & 15u) == 15u && sh->abort) return false;
+        if (mbar_sleep_wait<kCluster>(bar, parity, kSleepNs)) return true;
+        if (sh->abort) return false;
+        if (global_ns() - begin > kFfnWaitNs) break;
     }
     report(status, DGC_ETIMEOUT);
     sh->abort = 1;
