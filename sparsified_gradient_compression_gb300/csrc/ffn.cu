@@ -620,8 +620,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
     tmem_fence_after();
     const uint32_t tmem = sh->tmem;
 
-    // Warps 0 and 1 run their loops whole, and one elected lane issues.
-    if (warp == 0) {
+    // One elected lane of warps 0 and 1 works.
+    if (warp == 0 && elect_one()) {
         const uint32_t cols = a.bn / kCg;  // of B, loaded by this block
         const uint32_t full = kCg == 1 ? smem_addr(sh->full) : peer_addr(sh->full, 0);
         const uint32_t stages = a.stages, stage_bytes = a.stage_bytes;
@@ -635,9 +635,9 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
             uint32_t k0, k1;
             k_range(a, t, &k0, &k1);
             for (uint32_t kb = k0; kb < k1; ++kb, ++n) {
-                ok = __all_sync(kFull, wait_bar(&sh->empty[s], phase, sh, a.status));
+                ok = wait_bar(&sh->empty[s], phase, sh, a.status);
                 if (!ok) break;
-                if (elect_one()) {
+                {
                     char* sa = base + s * stage_bytes;
                     char* sb = sa + kStageA;
                     const uint32_t bar = full + s * 8;
@@ -668,7 +668,6 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
                         tma_load<kCg>(sb, mb, k, col, bar);
                     }
                 }
-                __syncwarp();
                 if (++s == stages) s = 0, phase ^= 1;
             }
         }
@@ -679,7 +678,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
                 else
                     wait_quietly(&sh->empty[i % stages], (i / stages) & 1);
             }
-    } else if (warp == 1 && rank == 0) {
+    } else if (warp == 1 && rank == 0 && elect_one()) {
         const uint32_t stages = a.stages, stage_bytes = a.stage_bytes, idesc = a.idesc;
         const uint64_t da0 = operand_desc<kAcrossA>(smem_addr(base));
         const uint64_t db0 = operand_desc<kAcrossB>(smem_addr(base) + kStageA);
@@ -690,16 +689,15 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
             uint32_t k0, k1;
             k_range(a, t, &k0, &k1);
             const uint32_t acc = it & 1;
-            ok = __all_sync(kFull, wait_bar<kCg == 2>(&sh->acc_empty[acc], ((it >> 1) & 1) ^ 1, sh,
-                                                      a.status));
+            ok = wait_bar<kCg == 2>(&sh->acc_empty[acc], ((it >> 1) & 1) ^ 1, sh, a.status);
             if (!ok) break;
             tmem_fence_after();
             const uint32_t d = tmem + acc * a.bn;
             for (uint32_t kb = k0; kb < k1; ++kb) {
-                ok = __all_sync(kFull, wait_bar(&sh->full[s], phase, sh, a.status));
+                ok = wait_bar(&sh->full[s], phase, sh, a.status);
                 if (!ok) break;
                 tmem_fence_after();
-                if (elect_one()) {
+                {
                     const uint64_t da = da0 + (s * stage_bytes >> 4);
                     const uint64_t db = db0 + (s * stage_bytes >> 4);
 #pragma unroll
@@ -709,14 +707,11 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
                                        kb > k0 || k > 0);
                     mma_commit<kCg>(&sh->empty[s]);
                 }
-                __syncwarp();
                 if (++s == stages) s = 0, phase ^= 1;
             }
-            if (ok && elect_one()) mma_commit<kCg>(&sh->acc_full[acc]);
-            __syncwarp();
+            if (ok) mma_commit<kCg>(&sh->acc_full[acc]);
         }
-        if (elect_one()) mma_commit<kCg>(&sh->drain);  // what was issued is done before the end
-        __syncwarp();
+        mma_commit<kCg>(&sh->drain);  // what was issued is done before the end
         wait_quietly(&sh->drain, 0);
     } else if (warp >= 4) {
         if (kKind != kGate && kKind != kDownBwd)
