@@ -53,8 +53,9 @@ struct FfnArgs {
     uint32_t kb0, kb;                 // 64-deep slices of the first product, of both
     uint32_t tiles_m, tiles_n, tiles; // tiles = tiles_m * tiles_n * splits
     uint32_t group;                   // row tiles that are walked together
-    uint32_t kb_split;                // weight gradient: slices of one split
-    uint32_t split_rows;              // ... and rows of the workspace between splits
+    uint32_t kb_split;                // slices of one part of a split sum
+    uint32_t splits;                  // ... and its parts, where a cluster's blocks sum them
+    uint32_t split_rows;              // weight gradient: rows of the workspace between parts
     uint32_t bn, stages, a_rows, stage_bytes, load_bytes;
     uint32_t idesc, tmem_cols;
     int32_t act, half, residual, accumulate;
@@ -107,9 +108,20 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 // The address of the same shared variable in block `rank` of the cluster.
-__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
+__device__ __forceinline__ uint32_t peer_addr(uint32_t p, uint32_t rank) {
     uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(p), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
+    return peer_addr(smem_addr(p), rank);
+}
+__device__ __forceinline__ float4 ld_peer(uint32_t at) {
+    float4 r;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w)
+                 : "r"(at)
+                 : "memory");
     return r;
 }
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t bar) {
@@ -164,13 +176,6 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 template <int kCg>
-__device__ __forceinline__ void block_sync() {  // of the block, or of the pair
-    if (kCg == 1)
-        __syncthreads();
-    else
-        cluster_sync();
-}
-template <int kCg>
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {
     if (kCg == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -211,9 +216,10 @@ __device__ __forceinline__ void mma_16bit(uint32_t d, uint64_t a, uint64_t b, ui
             ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
             : "memory");
 }
-// Arrives at `bar` (of both blocks of a pair) when the products issued so far are done.
+// Arrives at `bar` (of the pair's blocks, whose bits `mask` has) when the products issued so far
+// are done.
 template <int kCg>
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+__device__ __forceinline__ void mma_commit(uint64_t* bar, uint16_t mask) {
     if (kCg == 1)
         asm volatile(
             "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
@@ -223,7 +229,7 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
         asm volatile(
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
             ".multicast::cluster.b64 [%0], %1;"
-            ::"r"(smem_addr(bar)), "h"((uint16_t)3)
+            ::"r"(smem_addr(bar)), "h"(mask)
             : "memory");
 }
 __device__ __forceinline__ void tmem_fence_before() {
@@ -368,9 +374,9 @@ __device__ __forceinline__ Tile tile_at(const FfnArgs& a, uint32_t t) {
     r.mt = first + (t - r.nt * rows);
     return r;
 }
-__device__ __forceinline__ void k_range(const FfnArgs& a, const Tile& t, uint32_t* k0,
+__device__ __forceinline__ void k_range(const FfnArgs& a, uint32_t split, uint32_t* k0,
                                         uint32_t* k1) {
-    *k0 = t.split * a.kb_split;
+    *k0 = min(a.kb, split * a.kb_split);
     *k1 = min(a.kb, *k0 + a.kb_split);
 }
 
@@ -428,21 +434,92 @@ __device__ __forceinline__ void chunk_16bit(const uint32_t (&v)[32], const uint3
     }
 }
 
+// One chunk out of registers: the epilogue's arithmetic into the set's boxes, and their stores.
+template <int kKind, int kAct>
+__device__ __forceinline__ void finish_chunk(const FfnArgs& a, const uint32_t (&v)[32],
+                                             const uint32_t (&u)[32], bool has_in, char* set,
+                                             uint32_t x, uint32_t y, uint32_t split, int lane) {
+    using E = Epilogue<kKind>;
+    auto buf = [&](int i) { return set + i * E::kBox; };
+    if (kKind == kWGrad) {
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+            *reinterpret_cast<uint4*>(buf(0) + lane * 128 + ((p ^ (lane & 7)) << 4)) =
+                make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
+    } else if (a.half) {
+        chunk_16bit<kKind, kAct, true>(v, u, has_in, buf(0), buf(E::kBufs > 1), buf(E::kBufs - 1),
+                                       lane);
+    } else {
+        chunk_16bit<kKind, kAct, false>(v, u, has_in, buf(0), buf(E::kBufs > 1), buf(E::kBufs - 1),
+                                        lane);
+    }
+    if (a.unaligned || (a.ragged && x + 32 > a.n)) {
+        // a row of up to 32 columns per step, one column a lane
+        __syncwarp();
+        const uint32_t rows = min(32u, a.m - y);
+        const int outs = kKind == kGate ? (a.residual ? 3 : 1) : E::kOut;
+        if (x + lane < a.n)
+            for (uint32_t r = 0; r < rows; ++r)
+                for (int i = 0; i < outs; ++i) {
+                    const uint64_t to = (uint64_t)(y + r) * a.ld[i] + x + lane;
+                    if (kKind == kWGrad) {
+                        const float f = *reinterpret_cast<const float*>(
+                            buf(0) + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+                        float* d = static_cast<float*>(a.out[0]) + to;
+                        *d = a.accumulate ? *d + f : f;
+                    } else {
+                        static_cast<uint16_t*>(a.out[i])[to] = *reinterpret_cast<const uint16_t*>(
+                            buf(i) + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) +
+                            (lane & 7) * 2);
+                    }
+                }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) bulk_commit();  // an empty group: the sets are counted by groups
+        return;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        if (kKind == kWGrad) {
+            if (a.accumulate)
+                tma_add(&a.out0, buf(0), x, y + split * a.split_rows);
+            else
+                tma_store(&a.out0, buf(0), x, y + split * a.split_rows);
+        } else {
+            tma_store(&a.out0, buf(0), x, y);
+            if (kKind == kDownBwd) tma_store(&a.out1, buf(1), x, y);
+            if (kKind == kGate && a.residual) {  // gate and up are wanted
+                tma_store(&a.out1, buf(1), x, y);
+                tma_store(&a.out2, buf(2), x, y);
+            }
+        }
+        bulk_commit();
+    }
+}
+
 // Warps 4-11: two for each quarter of the accumulator's rows (the quarter a warp may read is its
-// number modulo 4), taking every other chunk of 32 columns.
-template <int kKind, int kCg, int kAct>
-__device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* staging,
-                                         uint32_t tmem, uint32_t rank) {
+// number modulo 4), taking every other chunk of 32 columns. With kSplit the blocks of a cluster
+// have summed a part of the tile's products each: every block puts its accumulator into its own
+// shared memory (the stages, which are empty by then), and after a barrier each of them adds up,
+// in the order of the parts, the chunks that fall to it.
+template <int kKind, int kCg, bool kSplit, int kAct>
+__device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* parts,
+                                         char* staging, uint32_t tmem, uint32_t rank) {
     using E = Epilogue<kKind>;
     const int warp = (threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
     char* mine = staging + warp * kWarpStaging;
-    auto buf = [&](uint32_t set, int i) { return mine + (set * E::kBufs + i) * E::kBox; };
+    auto set_at = [&](uint32_t n) { return mine + (n % E::kSets) * E::kBufs * E::kBox; };
     const uint32_t out_cols = kKind == kGate ? a.bn / 2 : a.bn;  // columns of one tile's output
-    const uint32_t chunks = out_cols / 32, first_chunk = warp >> 2;
+    const uint32_t chunks = out_cols / 32;
+    const uint32_t row_rank = rank % kCg, part = rank / kCg, lead = rank - row_rank;
+    const uint32_t first_chunk = (kSplit ? 2 * part : 0) + (warp >> 2);
+    const uint32_t chunk_step = kSplit ? 2 * a.splits : 2;
     const bool has_in = E::kIn > 0 && (kKind == kDownBwd || a.residual);
-    const uint32_t first_tile = blockIdx.x / kCg, tile_step = gridDim.x / kCg;
-    const uint32_t row_in_tile = rank * kBlockM + (warp & 3) * 32;
-    const uint32_t acc_empty = kCg == 1 ? 0 : peer_addr(sh->acc_empty, 0);
+    const uint32_t first_tile = kSplit ? blockIdx.x / (a.splits * kCg) : blockIdx.x / kCg;
+    const uint32_t tile_step = kSplit ? a.tiles : gridDim.x / kCg;
+    const uint32_t row_in_tile = row_rank * kBlockM + (warp & 3) * 32;
+    const uint32_t acc_empty = kCg == 1 ? 0 : peer_addr(sh->acc_empty, lead);
 
     // The loads of one chunk's inputs; chunks outside the output have none.
     uint32_t load_tile = first_tile, load_chunk = first_chunk, load_n = 0;
@@ -456,13 +533,13 @@ __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* 
                 load_tile += tile_step;
                 continue;
             }
-            const uint32_t set = load_n % E::kSets;
-            uint64_t* bar = &sh->in_full[warp][set];
+            char* set = set_at(load_n);
+            uint64_t* bar = &sh->in_full[warp][load_n % E::kSets];
             mbar_arrive_expect_tx(bar, 2048u * E::kIn);
-            tma_load<1>(buf(set, 0), &a.in0, x, y, smem_addr(bar));
-            if (E::kIn > 1) tma_load<1>(buf(set, 1), &a.in1, x, y, smem_addr(bar));
+            tma_load<1>(set, &a.in0, x, y, smem_addr(bar));
+            if (E::kIn > 1) tma_load<1>(set + E::kBox, &a.in1, x, y, smem_addr(bar));
             ++load_n;
-            load_chunk += 2;
+            load_chunk += chunk_step;
             return;
         }
     };
@@ -472,99 +549,86 @@ __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* 
     uint32_t done = 0;  // chunks this warp has finished
     uint32_t it = 0;
     bool ok = true;
+    // Makes the set of the next chunk ready for its results (and its inputs).
+    auto ready = [&]() {
+        if (has_in) {
+            // the store before this one has left its set: the next inputs go there
+            if (lane == 0) {
+                bulk_wait_read<0>();
+                issue_load();
+            }
+            __syncwarp();
+            ok = __all_sync(kFull, wait_bar(&sh->in_full[warp][done % E::kSets],
+                                            (done / E::kSets) & 1, sh, a.status));
+        } else {
+            // the last store from this set has left it
+            if (lane == 0) bulk_wait_read<E::kSets - 1>();
+            __syncwarp();
+        }
+        return ok;
+    };
+    uint32_t v[32], u[32];
     for (uint32_t ti = first_tile; ti < a.tiles && ok; ti += tile_step, ++it) {
         const Tile t = tile_at(a, ti);
         const uint32_t acc = it & 1, y = t.mt * kBlockM * kCg + row_in_tile;
         uint32_t k0, k1;
-        k_range(a, t, &k0, &k1);
+        k_range(a, kSplit ? part : t.split, &k0, &k1);
         ok = __all_sync(kFull, wait_bar(&sh->acc_full[acc], (it >> 1) & 1, sh, a.status));
-        if (!ok) break;
         tmem_fence_after();
         const uint32_t src = tmem + acc * a.bn + ((uint32_t)((warp & 3) * 32) << 16);
+        if (kSplit) {
+            for (uint32_t c = warp >> 2; c < a.bn / 32 && ok; c += 2) {
+                tmem_load32(src + c * 32, v);
+                tmem_wait_load();
+                char* to = parts + (c * 4 + (warp & 3)) * 4096 + lane * 128;
+#pragma unroll
+                for (int p = 0; p < 8; ++p)
+                    *reinterpret_cast<uint4*>(to + ((p ^ (lane & 7)) << 4)) =
+                        k0 < k1 ? make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3])
+                                : make_uint4(0, 0, 0, 0);
+            }
+            __syncwarp();
+            cluster_sync();
+            auto sum = [&](uint32_t c, uint32_t (&r)[32]) {
+                const uint32_t at = smem_addr(parts) + (c * 4 + (warp & 3)) * 4096 + lane * 128;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) r[i] = 0;
+                for (uint32_t q = 0; q < a.splits; ++q) {
+                    const uint32_t from = peer_addr(at, q * kCg + row_rank);
+#pragma unroll
+                    for (int p = 0; p < 8; ++p) {
+                        const float4 w = ld_peer(from + ((p ^ (lane & 7)) << 4));
+                        r[4 * p] = __float_as_uint(__uint_as_float(r[4 * p]) + w.x);
+                        r[4 * p + 1] = __float_as_uint(__uint_as_float(r[4 * p + 1]) + w.y);
+                        r[4 * p + 2] = __float_as_uint(__uint_as_float(r[4 * p + 2]) + w.z);
+                        r[4 * p + 3] = __float_as_uint(__uint_as_float(r[4 * p + 3]) + w.w);
+                    }
+                }
+            };
+            for (uint32_t c = first_chunk; c < chunks && y < a.m && ok; c += chunk_step) {
+                const uint32_t x = t.nt * out_cols + c * 32;
+                if (x >= a.n) break;
+                sum(c, v);
+                if (kKind == kGate) sum(c + chunks, u);
+                if (!ready()) break;
+                finish_chunk<kKind, kAct>(a, v, u, has_in, set_at(done), x, y, 0, lane);
+                ++done;
+            }
+            break;
+        }
+        if (!ok) break;
         for (uint32_t c = first_chunk; c < chunks && y < a.m; c += 2) {
             const uint32_t x = t.nt * out_cols + c * 32;
             if (x >= a.n) break;
-            const uint32_t set = done % E::kSets;
-            uint32_t v[32], u[32];
             tmem_load32(src + c * 32, v);
             if (kKind == kGate) tmem_load32(src + out_cols + c * 32, u);
-            if (has_in) {
-                // the store before this one has left its set: the next inputs go there
-                if (lane == 0) {
-                    bulk_wait_read<0>();
-                    issue_load();
-                }
-                __syncwarp();
-                ok = __all_sync(kFull, wait_bar(&sh->in_full[warp][set], (done / E::kSets) & 1, sh,
-                                                a.status));
-                if (!ok) break;
-            } else {
-                // the last store from this set has left it
-                if (lane == 0) bulk_wait_read<E::kSets - 1>();
-                __syncwarp();
-            }
+            if (!ready()) break;
             tmem_wait_load();
             if (k0 >= k1) {  // an empty sum: the accumulator was never written
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = u[i] = 0;
             }
-            if (kKind == kWGrad) {
-#pragma unroll
-                for (int p = 0; p < 8; ++p)
-                    *reinterpret_cast<uint4*>(buf(set, 0) + lane * 128 + ((p ^ (lane & 7)) << 4)) =
-                        make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
-            } else if (a.half) {
-                chunk_16bit<kKind, kAct, true>(v, u, has_in, buf(set, 0), buf(set, E::kBufs > 1),
-                                               buf(set, E::kBufs - 1), lane);
-            } else {
-                chunk_16bit<kKind, kAct, false>(v, u, has_in, buf(set, 0), buf(set, E::kBufs > 1),
-                                                buf(set, E::kBufs - 1), lane);
-            }
-            if (a.unaligned || (a.ragged && x + 32 > a.n)) {
-                // a row of up to 32 columns per step, one column a lane
-                __syncwarp();
-                const uint32_t rows = min(32u, a.m - y);
-                const int outs = kKind == kGate ? (a.residual ? 3 : 1) : E::kOut;
-                if (x + lane < a.n)
-                    for (uint32_t r = 0; r < rows; ++r)
-                        for (int i = 0; i < outs; ++i) {
-                            const uint64_t to = (uint64_t)(y + r) * a.ld[i] + x + lane;
-                            if (kKind == kWGrad) {
-                                const float f = *reinterpret_cast<const float*>(
-                                    buf(set, 0) + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) +
-                                    (lane & 3) * 4);
-                                float* d = static_cast<float*>(a.out[0]) + to;
-                                *d = a.accumulate ? *d + f : f;
-                            } else {
-                                static_cast<uint16_t*>(a.out[i])[to] =
-                                    *reinterpret_cast<const uint16_t*>(
-                                        buf(set, i) + r * 64 +
-                                        (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
-                            }
-                        }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) bulk_commit();  // an empty group: the sets are counted by groups
-            } else {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    if (kKind == kWGrad) {
-                        if (a.accumulate)
-                            tma_add(&a.out0, buf(set, 0), x, y + t.split * a.split_rows);
-                        else
-                            tma_store(&a.out0, buf(set, 0), x, y + t.split * a.split_rows);
-                    } else {
-                        tma_store(&a.out0, buf(set, 0), x, y);
-                        if (kKind == kDownBwd) tma_store(&a.out1, buf(set, 1), x, y);
-                        if (kKind == kGate && a.residual) {  // gate and up are wanted
-                            tma_store(&a.out1, buf(set, 1), x, y);
-                            tma_store(&a.out2, buf(set, 2), x, y);
-                        }
-                    }
-                    bulk_commit();
-                }
-            }
+            finish_chunk<kKind, kAct>(a, v, u, has_in, set_at(done), x, y, t.split, lane);
             ++done;
         }
         tmem_fence_before();
@@ -585,7 +649,7 @@ __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* 
     }
 }
 
-template <int kKind, int kCg>
+template <int kKind, int kCg, bool kSplit>
 __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ FfnArgs a) {
     constexpr bool kAcrossA = kKind == kWGrad;
     constexpr bool kAcrossB = kKind == kDownBwd || kKind == kGateBwd || kKind == kWGrad;
@@ -595,8 +659,12 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
     char* base = dyn + ((1024u - (smem_addr(dyn) & 1023u)) & 1023u);
     char* staging = base + a.stages * a.stage_bytes;
     const int warp = threadIdx.x >> 5;
-    const uint32_t rank = kCg == 1 ? 0 : cluster_rank();
-    const uint32_t first_tile = blockIdx.x / kCg, tile_step = gridDim.x / kCg;
+    // A cluster is `splits` blocks or pairs: which part of the sum, and which rows of the pair's
+    // tile, are this block's. lead: the pair's first block, which issues its products.
+    const uint32_t rank = kCg == 2 || kSplit ? cluster_rank() : 0;
+    const uint32_t row_rank = rank % kCg, part = rank / kCg, lead = rank - row_rank;
+    const uint32_t first_tile = kSplit ? blockIdx.x / (a.splits * kCg) : blockIdx.x / kCg;
+    const uint32_t tile_step = kSplit ? a.tiles : gridDim.x / kCg;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
@@ -616,24 +684,24 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
     if (warp == 2) tmem_alloc<kCg>(&sh->tmem, a.tmem_cols);
     tmem_fence_before();
     __syncthreads();
-    block_sync<kCg>();
+    if (kCg == 2) cluster_sync();
     tmem_fence_after();
     const uint32_t tmem = sh->tmem;
 
     // One elected lane of warps 0 and 1 works.
     if (warp == 0 && elect_one()) {
         const uint32_t cols = a.bn / kCg;  // of B, loaded by this block
-        const uint32_t full = kCg == 1 ? smem_addr(sh->full) : peer_addr(sh->full, 0);
+        const uint32_t full = kCg == 1 ? smem_addr(sh->full) : peer_addr(sh->full, lead);
         const uint32_t stages = a.stages, stage_bytes = a.stage_bytes;
         uint32_t n = 0;  // stages filled so far
         uint32_t s = 0, phase = 1;
         bool ok = true;
         for (uint32_t ti = first_tile; ti < a.tiles && ok; ti += tile_step) {
             const Tile t = tile_at(a, ti);
-            const int32_t row = (t.mt * kCg + rank) * kBlockM;
-            const int32_t col = t.nt * a.bn + rank * cols;
+            const int32_t row = (t.mt * kCg + row_rank) * kBlockM;
+            const int32_t col = t.nt * a.bn + row_rank * cols;
             uint32_t k0, k1;
-            k_range(a, t, &k0, &k1);
+            k_range(a, kSplit ? part : t.split, &k0, &k1);
             for (uint32_t kb = k0; kb < k1; ++kb, ++n) {
                 ok = wait_bar(&sh->empty[s], phase, sh, a.status);
                 if (!ok) break;
@@ -641,7 +709,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
                     char* sa = base + s * stage_bytes;
                     char* sb = sa + kStageA;
                     const uint32_t bar = full + s * 8;
-                    if (rank == 0) mbar_arrive_expect_tx(&sh->full[s], a.load_bytes);
+                    if (row_rank == 0) mbar_arrive_expect_tx(&sh->full[s], a.load_bytes);
                     const bool second = kKind == kGateBwd && kb >= a.kb0;
                     const int32_t k = (int32_t)(second ? kb - a.kb0 : kb) * kBlockK;
                     const CUtensorMap* ma = second ? &a.a1 : &a.a0;
@@ -662,7 +730,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
                             tma_load<kCg>(sb, &a.b0, k, f, bar);
                             tma_load<kCg>(sb + a.bn / 2 * 128, &a.b1, k, f, bar);
                         } else {
-                            tma_load<kCg>(sb, rank == 0 ? &a.b0 : &a.b1, k, f, bar);
+                            tma_load<kCg>(sb, row_rank == 0 ? &a.b0 : &a.b1, k, f, bar);
                         }
                     } else {
                         tma_load<kCg>(sb, mb, k, col, bar);
@@ -673,13 +741,14 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
         }
         if (!ok || sh->abort)  // copies in flight to a block that gives up
             for (uint32_t i = n > stages ? n - stages : 0; i < n; ++i) {
-                if (rank == 0)
+                if (row_rank == 0)
                     wait_quietly(&sh->full[i % stages], (i / stages) & 1);
                 else
                     wait_quietly(&sh->empty[i % stages], (i / stages) & 1);
             }
-    } else if (warp == 1 && rank == 0 && elect_one()) {
+    } else if (warp == 1 && row_rank == 0 && elect_one()) {
         const uint32_t stages = a.stages, stage_bytes = a.stage_bytes, idesc = a.idesc;
+        const uint16_t mask = (uint16_t)(3u << lead);
         const uint64_t da0 = operand_desc<kAcrossA>(smem_addr(base));
         const uint64_t db0 = operand_desc<kAcrossB>(smem_addr(base) + kStageA);
         uint32_t s = 0, phase = 0, it = 0;
@@ -687,7 +756,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
         for (uint32_t ti = first_tile; ti < a.tiles && ok; ti += tile_step, ++it) {
             const Tile t = tile_at(a, ti);
             uint32_t k0, k1;
-            k_range(a, t, &k0, &k1);
+            k_range(a, kSplit ? part : t.split, &k0, &k1);
             const uint32_t acc = it & 1;
             ok = wait_bar<kCg == 2>(&sh->acc_empty[acc], ((it >> 1) & 1) ^ 1, sh, a.status);
             if (!ok) break;
@@ -705,33 +774,34 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
                         mma_16bit<kCg>(d, da + k * (kAcrossA ? 2048 >> 4 : 2),
                                        db + k * (kAcrossB ? 2048 >> 4 : 2), idesc,
                                        kb > k0 || k > 0);
-                    mma_commit<kCg>(&sh->empty[s]);
+                    mma_commit<kCg>(&sh->empty[s], mask);
                 }
                 if (++s == stages) s = 0, phase ^= 1;
             }
-            if (ok) mma_commit<kCg>(&sh->acc_full[acc]);
+            if (ok) mma_commit<kCg>(&sh->acc_full[acc], mask);
         }
-        mma_commit<kCg>(&sh->drain);  // what was issued is done before the end
+        mma_commit<kCg>(&sh->drain, mask);  // what was issued is done before the end
         wait_quietly(&sh->drain, 0);
     } else if (warp >= 4) {
         if (kKind != kGate && kKind != kDownBwd)
-            epilogue<kKind, kCg, DGC_ACT_RELU>(a, sh, staging, tmem, rank);
+            epilogue<kKind, kCg, kSplit, DGC_ACT_RELU>(a, sh, base, staging, tmem, rank);
         else if (a.act == DGC_ACT_SILU)
-            epilogue<kKind, kCg, DGC_ACT_SILU>(a, sh, staging, tmem, rank);
+            epilogue<kKind, kCg, kSplit, DGC_ACT_SILU>(a, sh, base, staging, tmem, rank);
         else if (a.act == DGC_ACT_GELU)
-            epilogue<kKind, kCg, DGC_ACT_GELU>(a, sh, staging, tmem, rank);
+            epilogue<kKind, kCg, kSplit, DGC_ACT_GELU>(a, sh, base, staging, tmem, rank);
         else if (a.act == DGC_ACT_GELU_TANH)
-            epilogue<kKind, kCg, DGC_ACT_GELU_TANH>(a, sh, staging, tmem, rank);
+            epilogue<kKind, kCg, kSplit, DGC_ACT_GELU_TANH>(a, sh, base, staging, tmem, rank);
         else
-            epilogue<kKind, kCg, DGC_ACT_RELU>(a, sh, staging, tmem, rank);
+            epilogue<kKind, kCg, kSplit, DGC_ACT_RELU>(a, sh, base, staging, tmem, rank);
     }
     __syncwarp();
+    if (kSplit && warp < 4) cluster_sync();  // the epilogue's warps pass theirs between their steps
     tmem_fence_before();
     __syncthreads();
     // the pair's last commit has arrived here before this block's shared memory goes
-    if (kCg == 2 && rank == 1 && threadIdx.x == 32) wait_quietly(&sh->drain, 0);
+    if (kCg == 2 && row_rank == 1 && threadIdx.x == 32) wait_quietly(&sh->drain, 0);
     __syncthreads();
-    block_sync<kCg>();
+    if (kCg == 2 || kSplit) cluster_sync();
     tmem_fence_after();
     if (warp == 2) tmem_free<kCg>(tmem, a.tmem_cols);
 }
@@ -827,23 +897,14 @@ int make_map(CUtensorMap* map, const Mat& m, uint32_t bc, uint32_t br) {
 
 uint32_t ceil_div(uint64_t a, uint64_t b) { return (uint32_t)((a + b - 1) / b); }
 
-// Output columns of a tile: the widest tile (fewest operand bytes per product) that still gives
-// every SM one, else the narrowest.
-uint32_t choose_bn(uint64_t tiles_m, uint64_t n, uint32_t out_per_bn_num, uint32_t narrowest,
-                   int sms) {
-    for (uint32_t bn = 256; bn > narrowest; bn /= 2)
-        if (tiles_m * ceil_div(n, bn / out_per_bn_num) >= (uint64_t)sms) return bn;
-    return narrowest;
-}
-
-template <int kKind, int kCg>
+template <int kKind, int kCg, bool kSplit>
 int launch_ffn(FfnArgs& a, int32_t dtype, int sms, cudaStream_t s) {
     constexpr bool kAcrossA = kKind == kWGrad;
     constexpr bool kAcrossB = kKind == kDownBwd || kKind == kGateBwd || kKind == kWGrad;
     a.stage_bytes = kStageA + a.bn / kCg * 128;
     a.stages = std::min<uint32_t>(kMaxStages, (kSmemLimit - 2048 - kEpilogueBytes) / a.stage_bytes);
     a.load_bytes = (kAcrossA ? kBlockM : a.a_rows) * 128 * kCg + a.bn * 128;
-    a.tmem_cols = std::max(32u, 2 * a.bn);
+    a.tmem_cols = 2 * a.bn;  // a power of two, 64 at least
     a.half = dtype == DGC_F16;
     const uint32_t type = dtype == DGC_F16 ? 0 : 1;
     a.idesc = (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)kAcrossA << 15) |
@@ -854,7 +915,7 @@ int launch_ffn(FfnArgs& a, int32_t dtype, int sms, cudaStream_t s) {
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 128 || !set[dev]) {
-        if (cudaFuncSetAttribute(k_ffn<kKind, kCg>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(k_ffn<kKind, kCg, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)(kSmemLimit - 1024)) != cudaSuccess) {
             cudaGetLastError();
             return DGC_ECUDA;
@@ -862,17 +923,19 @@ int launch_ffn(FfnArgs& a, int32_t dtype, int sms, cudaStream_t s) {
         if (dev >= 0 && dev < 128) set[dev] = true;
     }
     cudaLaunchConfig_t c{};
-    c.gridDim = dim3(std::min<uint32_t>(a.tiles, (uint32_t)sms / kCg) * kCg);
+    const uint32_t cluster = kSplit ? a.splits * kCg : kCg;
+    c.gridDim = dim3(kSplit ? a.tiles * cluster
+                            : std::min<uint32_t>(a.tiles, (uint32_t)sms / kCg) * kCg);
     c.blockDim = dim3(kFfnThreads);
     c.dynamicSmemBytes = smem;
     c.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = kCg;
+    at[0].val.clusterDim.x = cluster;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     c.attrs = at;
-    c.numAttrs = kCg > 1 ? 1 : 0;
-    if (cudaLaunchKernelEx(&c, k_ffn<kKind, kCg>, a) != cudaSuccess) {
+    c.numAttrs = cluster > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&c, k_ffn<kKind, kCg, kSplit>, a) != cudaSuccess) {
         cudaGetLastError();
         return DGC_ECUDA;
     }
@@ -880,9 +943,58 @@ int launch_ffn(FfnArgs& a, int32_t dtype, int sms, cudaStream_t s) {
     return DGC_OK;
 }
 
-// Pairs of blocks (256 x 256 tiles) where there are tiles enough for every pair.
-bool use_pairs(uint64_t m, uint64_t n, uint32_t halves, int sms) {
-    return m > kBlockM && (uint64_t)ceil_div(m, 2 * kBlockM) * ceil_div(n, 256 / halves) >= (uint64_t)sms / 2;
+// How a product is cut: pairs of blocks or single ones, the tile's columns, the parts of its sum.
+struct Plan {
+    bool pairs;
+    uint32_t bn, splits;
+};
+// The cheapest of the shapes that the kernel has, in SM clocks. A tile's slice of 64 costs the
+// tensor cores 2 bn, the way from L2 its operand bytes at 64 a clock and SM, the issuing loop 240:
+// the largest of the three counts. To start and end a tile takes about 2500, the epilogue of the
+// last one 8 bn; a split sum 1500 more, and 4 bn to add the parts. Clusters of 4 and 8 blocks do
+// not reach every SM of a GPU processing cluster: 18 and 15 of 19.
+Plan choose_plan(uint64_t m, uint64_t n, uint32_t kb, uint32_t halves, uint32_t narrowest,
+                 int sms) {
+    Plan best{false, 256, 1};
+    uint64_t least = ~0ull;
+    const uint64_t a_rows = std::min<uint64_t>(kBlockM, m);
+    for (int pairs = 1; pairs >= 0; --pairs) {
+        if (pairs && m <= kBlockM) continue;
+        const uint32_t cg = pairs ? 2 : 1;
+        for (uint32_t bn = 256; bn >= (pairs ? std::max(128u, narrowest) : narrowest); bn /= 2) {
+            const uint64_t slice =
+                std::max<uint64_t>({2 * bn, 240, (a_rows + bn / cg) * 128 / 64});
+            const uint64_t tiles =
+                (uint64_t)ceil_div(m, kBlockM * cg) * ceil_div(n, bn / halves);
+            for (uint32_t splits = 1; splits * cg <= 8 && (splits == 1 || splits * 4 <= kb);
+                 splits *= 2) {
+                const uint32_t cluster = splits * cg;
+                const uint64_t reach = cluster == 8 ? 15 : cluster == 4 ? 18 : 19;
+                const uint64_t slots = std::max<uint64_t>(1, sms * reach / (19 * cluster));
+                const uint64_t waves = (tiles + slots - 1) / slots;
+                const uint64_t tile = (kb + splits - 1) / splits * slice;
+                const uint64_t cost =
+                    splits > 1 ? waves * (tile + 4000 + 12 * bn)
+                               : waves * std::max<uint64_t>(tile, 6 * bn) + 2500 + 8 * bn;
+                if (cost < least) {
+                    least = cost;
+                    best = Plan{pairs != 0, bn, splits};
+                }
+            }
+        }
+    }
+    return best;
+}
+
+template <int kKind>
+int launch_plan(FfnArgs& a, const Plan& p, int32_t dtype, int sms, cudaStream_t s) {
+    a.splits = p.splits;
+    a.kb_split = ceil_div(a.kb, p.splits);
+    if (p.splits > 1)
+        return p.pairs ? launch_ffn<kKind, 2, true>(a, dtype, sms, s)
+                       : launch_ffn<kKind, 1, true>(a, dtype, sms, s);
+    return p.pairs ? launch_ffn<kKind, 2, false>(a, dtype, sms, s)
+                   : launch_ffn<kKind, 1, false>(a, dtype, sms, s);
 }
 
 // A product along rows: A [m, k] K-major, against B [n, k] K-major or [k, n] across.
@@ -901,15 +1013,15 @@ int rows_product(Product p0, const Product* p1, const Mat* b_up, const Mat* in0,
     a.m = (uint32_t)out0->rows;
     a.n = (uint32_t)out0->cols;
     constexpr uint32_t halves = kKind == kGate ? 2 : 1;
-    const bool pairs = use_pairs(a.m, a.n, halves, sms);
+    a.kb0 = ceil_div(p0.a->cols, kBlockK);
+    a.kb = a.kb0 + (p1 ? ceil_div(p1->a->cols, kBlockK) : 0);
+    const Plan plan = choose_plan(a.m, a.n, a.kb, halves, kKind == kDown ? 32 : 64, sms);
+    const bool pairs = plan.pairs;
+    a.bn = plan.bn;
     a.tiles_m = ceil_div(a.m, pairs ? 2 * kBlockM : kBlockM);
-    a.bn = pairs ? 256 : choose_bn(a.tiles_m, a.n, halves, kKind == kDown ? 32 : 64, sms);
     a.tiles_n = ceil_div(a.n, a.bn / halves);
     a.tiles = a.tiles_m * a.tiles_n;
     a.a_rows = std::min<uint32_t>(kBlockM, (a.m + 7) & ~7u);
-    a.kb0 = ceil_div(p0.a->cols, kBlockK);
-    a.kb = a.kb0 + (p1 ? ceil_div(p1->a->cols, kBlockK) : 0);
-    a.kb_split = a.kb;
     a.act = act;
     a.status = status;
     int rc = DGC_OK;
@@ -944,26 +1056,24 @@ int rows_product(Product p0, const Product* p1, const Mat* b_up, const Mat* in0,
     if (rc) return rc;
     a.residual = kKind == kGate ? out1 != nullptr : in0 != nullptr;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return pairs ? launch_ffn<kKind, 2>(a, out0->dtype, sms, s)
-                 : launch_ffn<kKind, 1>(a, out0->dtype, sms, s);
+    return launch_plan<kKind>(a, plan, out0->dtype, sms, s);
 }
 
 bool bad_act(int32_t act) { return act < DGC_ACT_SILU || act > DGC_ACT_RELU; }
 
-// Splits of a weight gradient's sum over the tokens: where the output has fewer tiles than there
-// are SMs, enough splits to fill them, each of at least 8 slices (512 tokens).
-uint32_t wgrad_splits(uint64_t tiles, uint64_t kb) {
-    constexpr uint64_t kFill = 152;
-    if (tiles == 0 || tiles >= kFill) return 1;
-    return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(kFill / tiles, kb / 8));
+// A small weight gradient over many tokens: where even clusters of 8 blocks on the narrowest tiles
+// would leave most SMs idle, the sum is cut into as many parts as fill them (152 blocks, at least
+// 8 slices each), whose results go to the workspace and are added in order by k_wgrad_join.
+uint32_t wgrad_parts(uint64_t rows, uint64_t cols, uint64_t tokens) {
+    const uint64_t tiles = (uint64_t)ceil_div(rows, kBlockM) * ceil_div(cols, 64);
+    const uint64_t kb = ceil_div(tokens, kBlockK);
+    if (tiles == 0 || tiles > 16 || kb < 64) return 1;
+    return (uint32_t)std::min<uint64_t>(152 / tiles, kb / 8);
 }
-uint32_t wgrad_bn(uint64_t cols) { return cols > 128 ? 256 : cols > 64 ? 128 : 64; }
 uint64_t wgrad_workspace(uint64_t rows, uint64_t cols, uint64_t tokens) {
-    const uint32_t bn = wgrad_bn(cols);
-    const uint64_t splits = wgrad_splits((uint64_t)ceil_div(rows, kBlockM) * ceil_div(cols, bn),
-                                         ceil_div(tokens, kBlockK));
-    if (splits < 2) return 0;
-    return splits * ceil_div(rows, kBlockM) * kBlockM * ((cols + 3) & ~3ull) * sizeof(float);
+    const uint64_t parts = wgrad_parts(rows, cols, tokens);
+    if (parts < 2) return 0;
+    return parts * ceil_div(rows, kBlockM) * kBlockM * ((cols + 3) & ~3ull) * sizeof(float);
 }
 
 }  // namespace
@@ -1096,35 +1206,35 @@ extern "C" int dgc_ffn_weight_grad(const dgc_matrix* dy, const dgc_matrix* x, in
     FfnArgs a{};
     a.m = (uint32_t)rows;
     a.n = (uint32_t)cols;
-    a.bn = wgrad_bn(cols);
-    const bool pairs = use_pairs(rows, cols, 1, sms);
-    if (pairs) a.bn = 256;
-    a.tiles_m = ceil_div(rows, pairs ? 2 * kBlockM : kBlockM);
-    a.tiles_n = ceil_div(cols, a.bn);
     a.a_rows = kBlockM;
     a.kb0 = a.kb = ceil_div(tokens, kBlockK);
-    const uint32_t want = pairs ? 1 : wgrad_splits((uint64_t)a.tiles_m * a.tiles_n, a.kb);
-    a.kb_split = ceil_div(a.kb, want);
-    const uint32_t splits = ceil_div(a.kb, a.kb_split);
-    a.tiles = a.tiles_m * a.tiles_n * splits;
     a.status = status;
     if ((rc = make_map(&a.a0, my, 64, kBlockK)) || (rc = make_map(&a.b0, mx, 64, kBlockK))) return rc;
-    if (splits > 1) {
+    const uint32_t parts = wgrad_parts(rows, cols, tokens);
+    const Plan plan = parts > 1 ? Plan{false, 64, 1}
+                                : choose_plan(rows, cols, a.kb, 1, 64, sms);
+    a.bn = plan.bn;
+    a.tiles_m = ceil_div(rows, plan.pairs ? 2 * kBlockM : kBlockM);
+    a.tiles_n = ceil_div(cols, a.bn);
+    if (parts > 1) {
+        a.kb_split = ceil_div(a.kb, parts);
+        const uint32_t used = ceil_div(a.kb, a.kb_split);
+        a.tiles = a.tiles_m * a.tiles_n * used;
         a.split_rows = a.tiles_m * kBlockM;
-        const Mat part{ws, (uint64_t)a.split_rows * splits, cols, (cols + 3) & ~3ull, DGC_F32};
+        const Mat part{ws, (uint64_t)a.split_rows * used, cols, (cols + 3) & ~3ull, DGC_F32};
         if ((rc = make_map(&a.out0, part, 32, 32))) return rc;
-        if ((rc = launch_ffn<kWGrad, 1>(a, my.dtype, sms, s))) return rc;
-        k_wgrad_join<<<grid2, 256, 0, s>>>((const float*)ws, part.ld, part.ld * a.split_rows, splits,
+        if ((rc = launch_ffn<kWGrad, 1, false>(a, my.dtype, sms, s))) return rc;
+        k_wgrad_join<<<grid2, 256, 0, s>>>((const float*)ws, part.ld, part.ld * a.split_rows, used,
                                            (float*)out.p, out.ld, (uint32_t)rows, (uint32_t)cols,
                                            accumulate != 0);
         return launched();
     }
+    a.tiles = a.tiles_m * a.tiles_n;
     a.accumulate = accumulate != 0;
     a.out[0] = out.p;
     a.ld[0] = out.ld;
     a.ragged = (cols & 3) != 0;
     a.unaligned = ((uintptr_t)out.p & 15u) || (out.ld & 3u);
     if (!a.unaligned && (rc = make_map(&a.out0, out, 32, 32))) return rc;
-    return pairs ? launch_ffn<kWGrad, 2>(a, my.dtype, sms, s)
-                 : launch_ffn<kWGrad, 1>(a, my.dtype, sms, s);
+    return launch_plan<kWGrad>(a, plan, my.dtype, sms, s);
 }
