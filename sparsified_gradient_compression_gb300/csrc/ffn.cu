@@ -37,8 +37,7 @@ constexpr int kBlockM = 128;
 constexpr int kBlockK = 64;                    // 128 bytes of 16-bit entries: the swizzle's span
 constexpr uint32_t kStageA = kBlockM * kBlockK * 2;
 constexpr int kMaxStages = 8;
-constexpr uint32_t kWarpStaging = 8192;
-constexpr uint32_t kEpilogueBytes = kWarpStaging * kEpilogueWarps;
+
 constexpr uint32_t kSmemLimit = 232448;        // 227 KB
 constexpr uint32_t kFfnWaitLimit = 1u << 23;   // probes of a wait, and its time: the longest sum
 constexpr uint64_t kFfnWaitNs = 2000000000;    // takes far less
@@ -329,7 +328,7 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
 struct FfnShared {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t acc_full[2], acc_empty[2];
-    uint64_t in_full[kEpilogueWarps][4];
+    uint64_t in_full[kEpilogueWarps][2];
     uint64_t drain;
     uint32_t tmem;
     volatile uint32_t abort;
@@ -387,8 +386,9 @@ struct Epilogue {
     static constexpr int kBufs = kOut > kIn ? kOut : kIn;       // 32 x 32 boxes of one set
     static constexpr uint32_t kBox = kKind == kWGrad ? 4096 : 2048;
     // sets: one is written while the others' stores leave and their loads arrive
-    static constexpr int kSets = kKind == kGate ? 1 : (kKind == kDownBwd || kKind == kWGrad) ? 2 : 4;
-    static_assert(kSets * kBufs * kBox <= kWarpStaging, "staging");
+    static constexpr int kSets = kKind == kGate || kKind == kWGrad ? 1 : 2;
+    static constexpr uint32_t kWarpBytes = kSets * kBufs * kBox;
+    static constexpr uint32_t kBytes = kWarpBytes * kEpilogueWarps;
 };
 
 // A chunk's 32 rows x 32 columns, a row a lane: v (and u) from the accumulator, the inputs from the
@@ -508,7 +508,7 @@ __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* 
                                          char* staging, uint32_t tmem, uint32_t rank) {
     using E = Epilogue<kKind>;
     const int warp = (threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
-    char* mine = staging + warp * kWarpStaging;
+    char* mine = staging + warp * E::kWarpBytes;
     auto set_at = [&](uint32_t n) { return mine + (n % E::kSets) * E::kBufs * E::kBox; };
     const uint32_t out_cols = kKind == kGate ? a.bn / 2 : a.bn;  // columns of one tile's output
     const uint32_t chunks = out_cols / 32;
@@ -593,6 +593,7 @@ __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* 
                 const uint32_t at = smem_addr(parts) + (c * 4 + (warp & 3)) * 4096 + lane * 128;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) r[i] = 0;
+#pragma unroll 2
                 for (uint32_t q = 0; q < a.splits; ++q) {
                     const uint32_t from = peer_addr(at, q * kCg + row_rank);
 #pragma unroll
@@ -676,7 +677,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
             mbar_init(&sh->acc_empty[i], kEpilogueWarps * kCg);
         }
         for (int w = 0; w < kEpilogueWarps; ++w)
-            for (int i = 0; i < 4; ++i) mbar_init(&sh->in_full[w][i], 1);
+            for (int i = 0; i < 2; ++i) mbar_init(&sh->in_full[w][i], 1);
         mbar_init(&sh->drain, 1);
         mbar_init_fence();
         sh->abort = 0;
@@ -902,7 +903,8 @@ int launch_ffn(FfnArgs& a, int32_t dtype, int sms, cudaStream_t s) {
     constexpr bool kAcrossA = kKind == kWGrad;
     constexpr bool kAcrossB = kKind == kDownBwd || kKind == kGateBwd || kKind == kWGrad;
     a.stage_bytes = kStageA + a.bn / kCg * 128;
-    a.stages = std::min<uint32_t>(kMaxStages, (kSmemLimit - 2048 - kEpilogueBytes) / a.stage_bytes);
+    constexpr uint32_t staging = Epilogue<kKind>::kBytes;
+    a.stages = std::min<uint32_t>(kMaxStages, (kSmemLimit - 2048 - staging) / a.stage_bytes);
     a.load_bytes = (kAcrossA ? kBlockM : a.a_rows) * 128 * kCg + a.bn * 128;
     a.tmem_cols = 2 * a.bn;  // a power of two, 64 at least
     a.half = dtype == DGC_F16;
@@ -910,7 +912,7 @@ int launch_ffn(FfnArgs& a, int32_t dtype, int sms, cudaStream_t s) {
     a.idesc = (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)kAcrossA << 15) |
               ((uint32_t)kAcrossB << 16) | ((a.bn >> 3) << 17) | ((kBlockM * kCg >> 4) << 24);
     a.group = 16 / kCg;
-    const uint32_t smem = a.stages * a.stage_bytes + kEpilogueBytes + 1024;
+    const uint32_t smem = a.stages * a.stage_bytes + staging + 1024;
     static bool set[128] = {false};
     int dev = 0;
     cudaGetDevice(&dev);
@@ -948,34 +950,40 @@ struct Plan {
     bool pairs;
     uint32_t bn, splits;
 };
-// The cheapest of the shapes that the kernel has, in SM clocks. A tile's slice of 64 costs the
-// tensor cores 2 bn, the way from L2 its operand bytes at 64 a clock and SM, the issuing loop 240:
-// the largest of the three counts. To start and end a tile takes about 2500, the epilogue of the
-// last one 8 bn; a split sum 1500 more, and 4 bn to add the parts. Clusters of 4 and 8 blocks do
-// not reach every SM of a GPU processing cluster: 18 and 15 of 19.
+// The cheapest of the shapes that the kernel has, in SM clocks, by a model that was fitted to the
+// times of every shape on 26 products (1 to 8192 rows, 512 to 11264 columns; its choices take 2%
+// longer than the best ones). A tile's slice of 64 costs the tensor cores 2.4 bn (2 bn by count),
+// the way from L2 a clock per 68 of its operand bytes, the issuing loop 240: the largest counts; a
+// pair's agreement adds 60, and a lone block's 256-column tile, whose stages are the fewest, a
+// quarter. The last tile's epilogue costs 16 bn (the others hide behind the sums, or the sums
+// behind them: the weight gradient writes 25 bn clocks' worth). A split sum pays for its cluster's
+// barriers and for moving the parts. Clusters of 4 blocks reach 18 of a processing cluster's 19
+// SMs; a split sum in more than one wave, or in clusters of 8, was never worth its start.
 Plan choose_plan(uint64_t m, uint64_t n, uint32_t kb, uint32_t halves, uint32_t narrowest,
-                 int sms) {
+                 bool wgrad, int sms) {
     Plan best{false, 256, 1};
     uint64_t least = ~0ull;
-    const uint64_t a_rows = std::min<uint64_t>(kBlockM, m);
+    const uint64_t a_rows = wgrad ? kBlockM : std::min<uint64_t>(kBlockM, m);
     for (int pairs = 1; pairs >= 0; --pairs) {
         if (pairs && m <= kBlockM) continue;
         const uint32_t cg = pairs ? 2 : 1;
         for (uint32_t bn = 256; bn >= (pairs ? std::max(128u, narrowest) : narrowest); bn /= 2) {
-            const uint64_t slice =
-                std::max<uint64_t>({2 * bn, 240, (a_rows + bn / cg) * 128 / 64});
-            const uint64_t tiles =
-                (uint64_t)ceil_div(m, kBlockM * cg) * ceil_div(n, bn / halves);
-            for (uint32_t splits = 1; splits * cg <= 8 && (splits == 1 || splits * 4 <= kb);
+            uint64_t slice =
+                std::max<uint64_t>({240, bn * 12 / 5, (a_rows + bn / cg) * 128 / 68});
+            if (pairs) slice += 60;
+            if (!pairs && bn == 256 && a_rows > 64) slice += slice / 4;
+            const uint64_t tiles = (uint64_t)ceil_div(m, kBlockM * cg) * ceil_div(n, bn / halves);
+            for (uint32_t splits = 1; splits * cg <= 4 && (splits == 1 || splits * 4 <= kb);
                  splits *= 2) {
                 const uint32_t cluster = splits * cg;
-                const uint64_t reach = cluster == 8 ? 15 : cluster == 4 ? 18 : 19;
-                const uint64_t slots = std::max<uint64_t>(1, sms * reach / (19 * cluster));
+                const uint64_t slots =
+                    std::max<uint64_t>(1, (uint64_t)sms * (cluster == 4 ? 18 : 19) / (19 * cluster));
                 const uint64_t waves = (tiles + slots - 1) / slots;
+                if (splits > 1 && waves > 1) continue;
                 const uint64_t tile = (kb + splits - 1) / splits * slice;
-                const uint64_t cost =
-                    splits > 1 ? waves * (tile + 4000 + 12 * bn)
-                               : waves * std::max<uint64_t>(tile, 6 * bn) + 2500 + 8 * bn;
+                uint64_t cost = waves * std::max<uint64_t>(tile, (wgrad ? 25 : 8) * bn) + 16 * bn;
+                if (pairs) cost += 2000;
+                if (splits > 1) cost += (cluster == 4 ? 2 : 1) * (1200 + 20 * bn);
                 if (cost < least) {
                     least = cost;
                     best = Plan{pairs != 0, bn, splits};
@@ -1015,7 +1023,7 @@ int rows_product(Product p0, const Product* p1, const Mat* b_up, const Mat* in0,
     constexpr uint32_t halves = kKind == kGate ? 2 : 1;
     a.kb0 = ceil_div(p0.a->cols, kBlockK);
     a.kb = a.kb0 + (p1 ? ceil_div(p1->a->cols, kBlockK) : 0);
-    const Plan plan = choose_plan(a.m, a.n, a.kb, halves, kKind == kDown ? 32 : 64, sms);
+    const Plan plan = choose_plan(a.m, a.n, a.kb, halves, kKind == kDown ? 32 : 64, false, sms);
     const bool pairs = plan.pairs;
     a.bn = plan.bn;
     a.tiles_m = ceil_div(a.m, pairs ? 2 * kBlockM : kBlockM);
@@ -1212,7 +1220,7 @@ extern "C" int dgc_ffn_weight_grad(const dgc_matrix* dy, const dgc_matrix* x, in
     if ((rc = make_map(&a.a0, my, 64, kBlockK)) || (rc = make_map(&a.b0, mx, 64, kBlockK))) return rc;
     const uint32_t parts = wgrad_parts(rows, cols, tokens);
     const Plan plan = parts > 1 ? Plan{false, 64, 1}
-                                : choose_plan(rows, cols, a.kb, 1, 64, sms);
+                                : choose_plan(rows, cols, a.kb, 1, 64, true, sms);
     a.bn = plan.bn;
     a.tiles_m = ceil_div(rows, plan.pairs ? 2 * kBlockM : kBlockM);
     a.tiles_n = ceil_div(cols, a.bn);
