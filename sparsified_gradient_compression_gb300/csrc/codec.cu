@@ -67,15 +67,6 @@ struct EncArgs {
     float* v;       // version 2: residual that takes back what the integers do not carry
 };
 
-// Programmatic dependent launch: a kernel launched with programmatic stream serialization may
-// start before the kernel ahead of it in the stream has finished; it waits here before it reads
-// anything that kernel writes (a no-op when it was launched the ordinary way). The kernel ahead
-// lets its dependents launch as soon as each of its blocks has started.
-__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_dep_launch() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 // version 2 layout: values of qbits/8 bytes, runs from the next even offset, nothing after them
 // (so the size fixes T: the receiver lays the messages out from their sizes)
 __host__ __device__ __forceinline__ uint64_t q_runs_offset(uint64_t T, int qbits) {

@@ -275,6 +275,15 @@ __device__ __forceinline__ void bulk_wait_all() {
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
+// Programmatic dependent launch: a kernel launched with programmatic stream serialization may
+// start before the kernel ahead of it in the stream has finished; it waits here before it reads
+// anything that kernel writes (a no-op when it was launched the ordinary way). The kernel ahead
+// lets its dependents launch as soon as each of its blocks has started.
+__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dep_launch() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Largest s in [0, n) with a[s] <= x, for a non-decreasing a with a[0] <= x (n >= 1).
 template <typename T>
 __device__ __forceinline__ int upper_bound_minus1(const T* a, int n, T x) {

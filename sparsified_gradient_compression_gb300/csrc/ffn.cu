@@ -688,6 +688,9 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
     if (kCg == 2) cluster_sync();
     tmem_fence_after();
     const uint32_t tmem = sh->tmem;
+    // a dependent launch: all of the above may run while the kernel ahead ends
+    grid_dep_wait();
+    grid_dep_launch();
 
     // One elected lane of warps 0 and 1 works.
     if (warp == 0 && elect_one()) {
@@ -931,12 +934,14 @@ int launch_ffn(FfnArgs& a, int32_t dtype, int sms, cudaStream_t s) {
     c.blockDim = dim3(kFfnThreads);
     c.dynamicSmemBytes = smem;
     c.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = cluster;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     c.attrs = at;
-    c.numAttrs = cluster > 1 ? 1 : 0;
+    c.numAttrs = cluster > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&c, k_ffn<kKind, kCg, kSplit>, a) != cudaSuccess) {
         cudaGetLastError();
         return DGC_ECUDA;

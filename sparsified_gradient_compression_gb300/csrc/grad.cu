@@ -57,13 +57,6 @@ struct GradArgs {
     float *norm, *scale;
 };
 
-__device__ __forceinline__ void pdl_wait() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-__device__ __forceinline__ void pdl_launch() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 __global__ void __launch_bounds__(256) k_grad_table(const __grid_constant__ GradTable<kTableCap> t,
                                                     int32_t n, GradEntry* entries,
                                                     uint32_t* first) {
@@ -184,8 +177,8 @@ template <int kCap>
 __global__ void __launch_bounds__(kGradThreads, kBlocksPerSm)
     k_grad_norm(const __grid_constant__ GradArgs a, const __grid_constant__ GradTable<kCap> tab) {
     __shared__ double sm[kGradWarps];
-    pdl_wait();
-    pdl_launch();
+    grid_dep_wait();
+    grid_dep_launch();
     const GradEntry* entries = a.entries ? a.entries : tab.e;
     const uint32_t* first = a.entries ? a.first : tab.first;
     uint32_t t0, t1;
@@ -226,7 +219,7 @@ __device__ __forceinline__ float join(const GradArgs& a, double* sm, bool write)
 
 __global__ void __launch_bounds__(kGradThreads) k_grad_finish(const __grid_constant__ GradArgs a) {
     __shared__ double sm[kGradWarps];
-    pdl_wait();
+    grid_dep_wait();
     join(a, sm, true);
 }
 
@@ -292,7 +285,7 @@ __global__ void __launch_bounds__(kGradThreads, kBlocksPerSm)
     __shared__ double sm[kGradWarps];
     const GradEntry* entries = a.entries ? a.entries : tab.e;
     const uint32_t* first = a.entries ? a.first : tab.first;
-    pdl_wait();
+    grid_dep_wait();
     const float f = join(a, sm, blockIdx.x == 0);
     if (a.in_place && f == 1.0f) return;
     uint32_t t0, t1;
