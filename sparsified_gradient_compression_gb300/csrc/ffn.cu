@@ -10,7 +10,7 @@
 //
 // One kernel, k_ffn, for all five. A persistent block per SM computes 128-row output tiles:
 // warp 0 brings the operands' 64-deep slices by TMA into a ring of shared-memory stages, warp 1
-// issues tcgen05.mma on them into one of two accumulators in tensor memory, warps 4-11 empty the
+// issues tcgen05.mma on them into one of two accumulators in tensor memory, warps 2-9 empty the
 // other one: tcgen05.ld, the epilogue's arithmetic in binary32, one rounding, and a TMA store
 // from shared memory. Operands whose long axis is the sum's (x, H, dy, dG, dU and the weights of
 // the forward pass) are read along it ("K-major"); the others (the weights of the backward pass,
@@ -32,11 +32,16 @@ namespace {
 enum Kind { kGate = 0, kDown = 1, kDownBwd = 2, kGateBwd = 3, kWGrad = 4 };
 
 constexpr int kEpilogueWarps = 8;
-constexpr int kFfnThreads = 128 + 32 * kEpilogueWarps;
+constexpr int kFfnThreads = 64 + 32 * kEpilogueWarps;  // 10 warps: up to 200 registers a thread
 constexpr int kBlockM = 128;
 constexpr int kBlockK = 64;                    // 128 bytes of 16-bit entries: the swizzle's span
 constexpr uint32_t kStageA = kBlockM * kBlockK * 2;
 constexpr int kMaxStages = 8;
+// The weight gradient's long sums leave the tensor cores every 8 slices (512 tokens) and are added
+// up in registers, rounded to nearest: the tensor cores' own accumulation cuts bits off, which
+// over 8192 tokens in one go took 9e-6 of the gradient's norm (a binary32 product: 1e-6), and
+// over 512 takes 6e-7.
+constexpr uint32_t kSumSlices = 12;
 
 constexpr uint32_t kSmemLimit = 232448;        // 227 KB
 constexpr uint32_t kFfnWaitLimit = 1u << 23;   // probes of a wait, and its time: the longest sum
@@ -250,6 +255,15 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
           "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr));
 }
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
 __device__ __forceinline__ void tmem_wait_load() {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -434,6 +448,37 @@ __device__ __forceinline__ void chunk_16bit(const uint32_t (&v)[32], const uint3
     }
 }
 
+// A split sum's parts: a chunk of this block's accumulator into its shared memory, a row of 128
+// bytes a lane, and the same chunk of all blocks of the cluster added up in the parts' order.
+__device__ __forceinline__ void put_part(char* parts, uint32_t chunk, const uint32_t (&v)[32],
+                                         bool empty, int lane) {
+    char* to = parts + chunk * 4096 + lane * 128;
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+        *reinterpret_cast<uint4*>(to + ((p ^ (lane & 7)) << 4)) =
+            empty ? make_uint4(0, 0, 0, 0)
+                  : make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
+}
+template <int kCg>
+__device__ __forceinline__ void add_parts(const char* parts, uint32_t chunk, uint32_t splits,
+                                          uint32_t row_rank, uint32_t (&r)[32], int lane) {
+    const uint32_t at = smem_addr(parts) + chunk * 4096 + lane * 128;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) r[i] = 0;
+#pragma unroll 2
+    for (uint32_t q = 0; q < splits; ++q) {
+        const uint32_t from = peer_addr(at, q * kCg + row_rank);
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            const float4 w = ld_peer(from + ((p ^ (lane & 7)) << 4));
+            r[4 * p] = __float_as_uint(__uint_as_float(r[4 * p]) + w.x);
+            r[4 * p + 1] = __float_as_uint(__uint_as_float(r[4 * p + 1]) + w.y);
+            r[4 * p + 2] = __float_as_uint(__uint_as_float(r[4 * p + 2]) + w.z);
+            r[4 * p + 3] = __float_as_uint(__uint_as_float(r[4 * p + 3]) + w.w);
+        }
+    }
+}
+
 // One chunk out of registers: the epilogue's arithmetic into the set's boxes, and their stores.
 template <int kKind, int kAct>
 __device__ __forceinline__ void finish_chunk(const FfnArgs& a, const uint32_t (&v)[32],
@@ -498,7 +543,7 @@ __device__ __forceinline__ void finish_chunk(const FfnArgs& a, const uint32_t (&
     }
 }
 
-// Warps 4-11: two for each quarter of the accumulator's rows (the quarter a warp may read is its
+// Warps 2-9: two for each quarter of the accumulator's rows (the quarter a warp may read is its
 // number modulo 4), taking every other chunk of 32 columns. With kSplit the blocks of a cluster
 // have summed a part of the tile's products each: every block puts its accumulator into its own
 // shared memory (the stages, which are empty by then), and after a barrier each of them adds up,
@@ -507,7 +552,8 @@ template <int kKind, int kCg, bool kSplit, int kAct>
 __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* parts,
                                          char* staging, uint32_t tmem, uint32_t rank) {
     using E = Epilogue<kKind>;
-    const int warp = (threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
+    const int warp = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31;
+    const uint32_t quarter = (threadIdx.x >> 5) & 3;
     char* mine = staging + warp * E::kWarpBytes;
     auto set_at = [&](uint32_t n) { return mine + (n % E::kSets) * E::kBufs * E::kBox; };
     const uint32_t out_cols = kKind == kGate ? a.bn / 2 : a.bn;  // columns of one tile's output
@@ -518,7 +564,7 @@ __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* 
     const bool has_in = E::kIn > 0 && (kKind == kDownBwd || a.residual);
     const uint32_t first_tile = kSplit ? blockIdx.x / (a.splits * kCg) : blockIdx.x / kCg;
     const uint32_t tile_step = kSplit ? a.tiles : gridDim.x / kCg;
-    const uint32_t row_in_tile = row_rank * kBlockM + (warp & 3) * 32;
+    const uint32_t row_in_tile = row_rank * kBlockM + quarter * 32;
     const uint32_t acc_empty = kCg == 1 ? 0 : peer_addr(sh->acc_empty, lead);
 
     // The loads of one chunk's inputs; chunks outside the output have none.
@@ -575,42 +621,21 @@ __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* 
         k_range(a, kSplit ? part : t.split, &k0, &k1);
         ok = __all_sync(kFull, wait_bar(&sh->acc_full[acc], (it >> 1) & 1, sh, a.status));
         tmem_fence_after();
-        const uint32_t src = tmem + acc * a.bn + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t src = tmem + acc * a.bn + (quarter * 32 << 16);
         if (kSplit) {
             for (uint32_t c = warp >> 2; c < a.bn / 32 && ok; c += 2) {
                 tmem_load32(src + c * 32, v);
                 tmem_wait_load();
-                char* to = parts + (c * 4 + (warp & 3)) * 4096 + lane * 128;
-#pragma unroll
-                for (int p = 0; p < 8; ++p)
-                    *reinterpret_cast<uint4*>(to + ((p ^ (lane & 7)) << 4)) =
-                        k0 < k1 ? make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3])
-                                : make_uint4(0, 0, 0, 0);
+                put_part(parts, c * 4 + quarter, v, k0 >= k1, lane);
             }
             __syncwarp();
             cluster_sync();
-            auto sum = [&](uint32_t c, uint32_t (&r)[32]) {
-                const uint32_t at = smem_addr(parts) + (c * 4 + (warp & 3)) * 4096 + lane * 128;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) r[i] = 0;
-#pragma unroll 2
-                for (uint32_t q = 0; q < a.splits; ++q) {
-                    const uint32_t from = peer_addr(at, q * kCg + row_rank);
-#pragma unroll
-                    for (int p = 0; p < 8; ++p) {
-                        const float4 w = ld_peer(from + ((p ^ (lane & 7)) << 4));
-                        r[4 * p] = __float_as_uint(__uint_as_float(r[4 * p]) + w.x);
-                        r[4 * p + 1] = __float_as_uint(__uint_as_float(r[4 * p + 1]) + w.y);
-                        r[4 * p + 2] = __float_as_uint(__uint_as_float(r[4 * p + 2]) + w.z);
-                        r[4 * p + 3] = __float_as_uint(__uint_as_float(r[4 * p + 3]) + w.w);
-                    }
-                }
-            };
             for (uint32_t c = first_chunk; c < chunks && y < a.m && ok; c += chunk_step) {
                 const uint32_t x = t.nt * out_cols + c * 32;
                 if (x >= a.n) break;
-                sum(c, v);
-                if (kKind == kGate) sum(c + chunks, u);
+                add_parts<kCg>(parts, c * 4 + quarter, a.splits, row_rank, v, lane);
+                if (kKind == kGate)
+                    add_parts<kCg>(parts, (c + chunks) * 4 + quarter, a.splits, row_rank, u, lane);
                 if (!ready()) break;
                 finish_chunk<kKind, kAct>(a, v, u, has_in, set_at(done), x, y, 0, lane);
                 ++done;
@@ -650,6 +675,92 @@ __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* 
     }
 }
 
+// The weight gradient's: every kSumSlices slices the accumulator is added to this warp's sums in
+// registers (up to four chunks), which are the tile's result at its end.
+template <int kCg, bool kSplit>
+__device__ __forceinline__ void epilogue_sums(const FfnArgs& a, FfnShared* sh, char* parts,
+                                              char* staging, uint32_t tmem, uint32_t rank) {
+    using E = Epilogue<kWGrad>;
+    const int warp = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31;
+    const uint32_t quarter = (threadIdx.x >> 5) & 3, half = warp >> 2;
+    char* box = staging + warp * E::kWarpBytes;
+    const uint32_t row_rank = rank % kCg, part = rank / kCg, lead = rank - row_rank;
+    const uint32_t chunks = a.bn / 32;
+    const uint32_t first_tile = kSplit ? blockIdx.x / (a.splits * kCg) : blockIdx.x / kCg;
+    const uint32_t tile_step = kSplit ? a.tiles : gridDim.x / kCg;
+    const uint32_t acc_empty = kCg == 1 ? 0 : peer_addr(sh->acc_empty, lead);
+    uint32_t it = 0;
+    bool ok = true;
+    auto finish = [&](const Tile& t, uint32_t c, const uint32_t (&v)[32]) {
+        const uint32_t y = (t.mt * kCg + row_rank) * kBlockM + quarter * 32;
+        const uint32_t x = t.nt * a.bn + c * 32;
+        if (y >= a.m || x >= a.n) return;
+        if (lane == 0) bulk_wait_read<0>();  // the last store has left the box
+        __syncwarp();
+        finish_chunk<kWGrad, DGC_ACT_RELU>(a, v, v, false, box, x, y, t.split, lane);
+    };
+    for (uint32_t ti = first_tile; ti < a.tiles && ok; ti += tile_step) {
+        const Tile t = tile_at(a, ti);
+        uint32_t k0, k1;
+        k_range(a, kSplit ? part : t.split, &k0, &k1);
+        uint32_t sum[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum[i][j] = 0;
+        for (uint32_t kb = k0; kb < k1; kb += kSumSlices, ++it) {
+            const uint32_t acc = it & 1;
+            ok = __all_sync(kFull, wait_bar(&sh->acc_full[acc], (it >> 1) & 1, sh, a.status));
+            if (!ok) break;
+            tmem_fence_after();
+            const uint32_t src = tmem + acc * a.bn + (quarter * 32 << 16);
+            // 16 columns at a time, the next ones on their way while these are added (128 registers
+            // hold the sums)
+            uint32_t v[2][16];
+            if (half < chunks) tmem_load16(src + half * 32, v[0]);
+#pragma unroll
+            for (int h = 0; h < 8; ++h) {
+                if (half + 2 * (h / 2) >= chunks) break;
+                tmem_wait_load();
+                const uint32_t next = half + 2 * ((h + 1) / 2);
+                if (h < 7 && next < chunks)
+                    tmem_load16(src + next * 32 + ((h + 1) & 1) * 16, v[(h + 1) & 1]);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    uint32_t& r = sum[h / 2][(h & 1) * 16 + j];
+                    r = __float_as_uint(__uint_as_float(r) + __uint_as_float(v[h & 1][j]));
+                }
+            }
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (kCg == 1)
+                    mbar_arrive(&sh->acc_empty[acc]);
+                else
+                    mbar_arrive_peer(acc_empty + acc * 8);
+            }
+        }
+        if (kSplit) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (half + 2 * i < chunks)
+                    put_part(parts, (half + 2 * i) * 4 + quarter, sum[i], false, lane);
+            __syncwarp();
+            cluster_sync();
+            for (uint32_t c = 2 * part + half; c < chunks && ok; c += 2 * a.splits) {
+                add_parts<kCg>(parts, c * 4 + quarter, a.splits, row_rank, sum[0], lane);
+                finish(t, c, sum[0]);
+            }
+            break;
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (half + 2 * i < chunks) finish(t, half + 2 * i, sum[i]);
+    }
+    if (lane == 0) bulk_wait_all();
+}
+
 template <int kKind, int kCg, bool kSplit>
 __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ FfnArgs a) {
     constexpr bool kAcrossA = kKind == kWGrad;
@@ -682,7 +793,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
         mbar_init_fence();
         sh->abort = 0;
     }
-    if (warp == 2) tmem_alloc<kCg>(&sh->tmem, a.tmem_cols);
+    if (warp == 1) tmem_alloc<kCg>(&sh->tmem, a.tmem_cols);
     tmem_fence_before();
     __syncthreads();
     if (kCg == 2) cluster_sync();
@@ -757,20 +868,22 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
         const uint64_t db0 = operand_desc<kAcrossB>(smem_addr(base) + kStageA);
         uint32_t s = 0, phase = 0, it = 0;
         bool ok = true;
-        for (uint32_t ti = first_tile; ti < a.tiles && ok; ti += tile_step, ++it) {
+        for (uint32_t ti = first_tile; ti < a.tiles && ok; ti += tile_step) {
             const Tile t = tile_at(a, ti);
-            uint32_t k0, k1;
-            k_range(a, kSplit ? part : t.split, &k0, &k1);
-            const uint32_t acc = it & 1;
-            ok = wait_bar<kCg == 2>(&sh->acc_empty[acc], ((it >> 1) & 1) ^ 1, sh, a.status);
-            if (!ok) break;
-            tmem_fence_after();
-            const uint32_t d = tmem + acc * a.bn;
-            for (uint32_t kb = k0; kb < k1; ++kb) {
-                ok = wait_bar(&sh->full[s], phase, sh, a.status);
+            uint32_t kb, k1;
+            k_range(a, kSplit ? part : t.split, &kb, &k1);
+            if (kKind == kWGrad && kb >= k1) continue;  // its epilogue waits for no empty sum
+            do {
+                const uint32_t acc = it & 1;
+                const uint32_t k0 = kb, end = kKind == kWGrad ? min(k1, kb + kSumSlices) : k1;
+                ok = wait_bar<kCg == 2>(&sh->acc_empty[acc], ((it >> 1) & 1) ^ 1, sh, a.status);
                 if (!ok) break;
                 tmem_fence_after();
-                {
+                const uint32_t d = tmem + acc * a.bn;
+                for (; kb < end; ++kb) {
+                    ok = wait_bar(&sh->full[s], phase, sh, a.status);
+                    if (!ok) break;
+                    tmem_fence_after();
                     const uint64_t da = da0 + (s * stage_bytes >> 4);
                     const uint64_t db = db0 + (s * stage_bytes >> 4);
 #pragma unroll
@@ -779,15 +892,19 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
                                        db + k * (kAcrossB ? 2048 >> 4 : 2), idesc,
                                        kb > k0 || k > 0);
                     mma_commit<kCg>(&sh->empty[s], mask);
+                    if (++s == stages) s = 0, phase ^= 1;
                 }
-                if (++s == stages) s = 0, phase ^= 1;
-            }
-            if (ok) mma_commit<kCg>(&sh->acc_full[acc], mask);
+                if (!ok) break;
+                mma_commit<kCg>(&sh->acc_full[acc], mask);
+                ++it;
+            } while (kb < k1);
         }
         mma_commit<kCg>(&sh->drain, mask);  // what was issued is done before the end
         wait_quietly(&sh->drain, 0);
-    } else if (warp >= 4) {
-        if (kKind != kGate && kKind != kDownBwd)
+    } else if (warp >= 2) {
+        if (kKind == kWGrad)
+            epilogue_sums<kCg, kSplit>(a, sh, base, staging, tmem, rank);
+        else if (kKind != kGate && kKind != kDownBwd)
             epilogue<kKind, kCg, kSplit, DGC_ACT_RELU>(a, sh, base, staging, tmem, rank);
         else if (a.act == DGC_ACT_SILU)
             epilogue<kKind, kCg, kSplit, DGC_ACT_SILU>(a, sh, base, staging, tmem, rank);
@@ -799,7 +916,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
             epilogue<kKind, kCg, kSplit, DGC_ACT_RELU>(a, sh, base, staging, tmem, rank);
     }
     __syncwarp();
-    if (kSplit && warp < 4) cluster_sync();  // the epilogue's warps pass theirs between their steps
+    if (kSplit && warp < 2) cluster_sync();  // the epilogue's warps pass theirs between their steps
     tmem_fence_before();
     __syncthreads();
     // the pair's last commit has arrived here before this block's shared memory goes
@@ -807,7 +924,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
     __syncthreads();
     if (kCg == 2 || kSplit) cluster_sync();
     tmem_fence_after();
-    if (warp == 2) tmem_free<kCg>(tmem, a.tmem_cols);
+    if (warp == 1) tmem_free<kCg>(tmem, a.tmem_cols);
 }
 
 // The splits of a weight gradient, added in order: dW = (dW +) sum over s of part_s.
