@@ -7,7 +7,7 @@
 //   k_grad_scale   joins the partial sums in every block, then dst = src * scale
 //                  (dgc_grad_clip).
 //
-// The work unit is a warp tile of 2048 entries of one tensor. Warps take contiguous ranges of
+// The work unit is a warp tile of 4 KB of one tensor. Warps take contiguous ranges of
 // tiles, so a warp looks its tensor up once and then steps through the table; no warp waits on
 // another until the block's last reduction.
 #include <cmath>
@@ -22,7 +22,10 @@ namespace {
 
 constexpr int kGradThreads = 256;
 constexpr int kGradWarps = kGradThreads / 32;
-constexpr uint32_t kWarpTile = 2048;
+// Entries of a warp tile: 4 KB of the source, 8 loads of 16 bytes a lane.
+constexpr uint32_t kTileBytes = 4096;
+template <typename T>
+constexpr uint32_t kTile = kTileBytes / sizeof(T);
 constexpr int kTableCap = 960;      // tensors in one kernel's parameters (27 KB of 32 KB)
 constexpr int kMidTable = 192;      // ... of the variants for shorter lists, whose launches
 constexpr int kSmallTable = 24;     // copy fewer bytes
@@ -118,27 +121,22 @@ __device__ __forceinline__ double squares(const Vec<T, kV> (&w)[kN]) {
     return (double)chain_sum(w, 0x1p-70f) * 0x1p140;
 }
 
-// Entries [begin, begin + 2048) of one tensor, by one warp: 16-byte loads where the address
-// allows (kV entries each), entry by entry at the ends and for unaligned tensors.
+// One tile of a tensor, from entry `begin`, by one warp: 16-byte loads where the address allows (kV
+// entries each), entry by entry at the ends and for unaligned tensors.
 template <typename T>
 __device__ __forceinline__ double tile_squares(const T* p, uint64_t n, uint64_t begin) {
     constexpr int kV = 16 / sizeof(T);
-    constexpr int kLoads = kWarpTile / 32 / kV;         // 16 or 8 loads of 16 bytes a lane
-    constexpr int kStep = kLoads < 8 ? kLoads : 8;      // in flight together
+    constexpr int kLoads = kTile<T> / 32 / kV;  // 8, in flight together
     const int lane = threadIdx.x & 31;
-    const uint32_t m = (uint32_t)umin64(kWarpTile, n - begin);
+    const uint32_t m = (uint32_t)umin64(kTile<T>, n - begin);
     const T* q = p + begin;
     double sum = 0.0;
-    if (m == kWarpTile && ((uintptr_t)q & 15u) == 0) {
-#pragma unroll 1
-        for (int h = 0; h < kLoads; h += kStep) {
-            Vec<T, kV> w[kStep];
+    if (m == kTile<T> && ((uintptr_t)q & 15u) == 0) {
+        Vec<T, kV> w[kLoads];
 #pragma unroll
-            for (int i = 0; i < kStep; ++i)
-                w[i] = *reinterpret_cast<const Vec<T, kV>*>(q + ((h + i) * 32 + lane) * kV);
-            sum += squares(w);
-        }
-        return sum;
+        for (int i = 0; i < kLoads; ++i)
+            w[i] = *reinterpret_cast<const Vec<T, kV>*>(q + (i * 32 + lane) * kV);
+        return squares(w);
     }
     for (uint32_t h = 0; h < m; h += 32 * 8) {
         Vec<T, 1> x[8];
@@ -189,13 +187,13 @@ __global__ void __launch_bounds__(kGradThreads, kBlocksPerSm)
         for (uint32_t t = t0; t < t1; ++t) {
             while (t >= first[e + 1]) ++e;
             const GradEntry g = entries[e];
-            const uint64_t begin = (uint64_t)(t - first[e]) * kWarpTile;
+            const uint64_t i = t - first[e];
             if (g.src_type() == DGC_F32)
-                sum += tile_squares((const float*)g.src, g.count(), begin);
+                sum += tile_squares((const float*)g.src, g.count(), i * kTile<float>);
             else if (g.src_type() == DGC_F16)
-                sum += tile_squares((const __half*)g.src, g.count(), begin);
+                sum += tile_squares((const __half*)g.src, g.count(), i * kTile<__half>);
             else
-                sum += tile_squares((const __nv_bfloat16*)g.src, g.count(), begin);
+                sum += tile_squares((const __nv_bfloat16*)g.src, g.count(), i * kTile<__nv_bfloat16>);
         }
     }
     sum = block_sum(sum, sm);
@@ -227,13 +225,13 @@ __global__ void __launch_bounds__(kGradThreads) k_grad_finish(const __grid_const
 template <typename S, typename D>
 __device__ __forceinline__ void tile_scale(const S* p, D* d, uint64_t n, uint64_t begin, float f) {
     constexpr int kV = (sizeof(S) == 4 || sizeof(D) == 4) ? 4 : 8;
-    constexpr int kSteps = kWarpTile / 32 / kV;
-    constexpr int kStep = 8;  // loads in flight together
+    constexpr int kSteps = kTile<S> / 32 / kV;  // 8 or 16
+    constexpr int kStep = 8;                    // loads in flight together
     const int lane = threadIdx.x & 31;
-    const uint32_t m = (uint32_t)umin64(kWarpTile, n - begin);
+    const uint32_t m = (uint32_t)umin64(kTile<S>, n - begin);
     const S* q = p + begin;
     D* o = d + begin;
-    if (m == kWarpTile && ((uintptr_t)q & (sizeof(S) * kV - 1)) == 0 &&
+    if (m == kTile<S> && ((uintptr_t)q & (sizeof(S) * kV - 1)) == 0 &&
         ((uintptr_t)o & (sizeof(D) * kV - 1)) == 0) {
 #pragma unroll 1
         for (int h = 0; h < kSteps; h += kStep) {
@@ -267,8 +265,9 @@ __device__ __forceinline__ void tile_scale(const S* p, D* d, uint64_t n, uint64_
 }
 
 template <typename S>
-__device__ __forceinline__ void tile_scale_to(const GradEntry& g, uint64_t begin, float f) {
+__device__ __forceinline__ void tile_scale_to(const GradEntry& g, uint64_t tile, float f) {
     const S* p = (const S*)g.src;
+    const uint64_t begin = tile * kTile<S>;
     if (g.dst_type() == DGC_F32)
         tile_scale(p, (float*)g.dst, g.count(), begin, f);
     else if (g.dst_type() == DGC_F16)
@@ -295,18 +294,22 @@ __global__ void __launch_bounds__(kGradThreads, kBlocksPerSm)
     for (uint32_t t = t1; t-- > t0;) {
         while (t < first[e]) --e;
         const GradEntry g = entries[e];
-        const uint64_t begin = (uint64_t)(t - first[e]) * kWarpTile;
+        const uint64_t i = t - first[e];
         if (g.src_type() == DGC_F32)
-            tile_scale_to<float>(g, begin, f);
+            tile_scale_to<float>(g, i, f);
         else if (g.src_type() == DGC_F16)
-            tile_scale_to<__half>(g, begin, f);
+            tile_scale_to<__half>(g, i, f);
         else
-            tile_scale_to<__nv_bfloat16>(g, begin, f);
+            tile_scale_to<__nv_bfloat16>(g, i, f);
     }
 }
 
 // ----------------------------------------------------------------------------------- host
 size_t type_size(int32_t t) { return t == DGC_F32 ? 4 : 2; }
+uint64_t tiles_of(const dgc_tensor& t) {
+    const uint64_t per = kTileBytes / type_size(t.dtype);
+    return ((uint64_t)t.n + per - 1) / per;
+}
 
 // Checks a list and counts its warp tiles.
 int check_list(const dgc_tensor* t, int32_t count, uint64_t* tiles) {
@@ -320,7 +323,7 @@ int check_list(const dgc_tensor* t, int32_t count, uint64_t* tiles) {
         if (t[i].n > 0 && (!t[i].data || ((uintptr_t)t[i].data & (type_size(t[i].dtype) - 1))))
             return DGC_EINVAL;
         if (t[i].n > (1ll << 42)) return DGC_EUNSUPPORTED;
-        sum += ((uint64_t)t[i].n + kWarpTile - 1) / kWarpTile;
+        sum += tiles_of(t[i]);
         if (sum > 0x7FFFFFFFull) return DGC_EUNSUPPORTED;
     }
     *tiles = sum;
@@ -374,7 +377,7 @@ void fill(GradTable<kCap>* t, const dgc_tensor* src, const dgc_tensor* dst, int3
         t->e[i].dst = d.data;
         t->e[i].n = (uint64_t)src[i].n | ((uint64_t)src[i].dtype << 56) | ((uint64_t)d.dtype << 60);
         t->first[i] = *tile;
-        *tile += (uint32_t)(((uint64_t)src[i].n + kWarpTile - 1) / kWarpTile);
+        *tile += (uint32_t)tiles_of(src[i]);
     }
     t->first[count] = *tile;
 }
