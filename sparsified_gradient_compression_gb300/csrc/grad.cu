@@ -3,13 +3,12 @@
 //   k_grad_table   writes the table of tensors into the workspace when it is too long for a
 //                  kernel's parameters (a launch per kTableCap tensors).
 //   k_grad_norm    one pass over all tensors: partial sums of squares, one binary64 per block.
-//   k_grad_finish  joins the partial sums: norm and scale (dgc_grad_norm).
-//   k_grad_scale   joins the partial sums in every block, then dst = src * scale
-//                  (dgc_grad_clip).
+//   k_grad_finish  joins the partial sums: norm and scale.
+//   k_grad_scale   dst = src * scale (dgc_grad_clip).
 //
-// The work unit is a warp tile of 4 KB of one tensor. Warps take contiguous ranges of
-// tiles, so a warp looks its tensor up once and then steps through the table; no warp waits on
-// another until the block's last reduction.
+// The work unit is a warp tile of 4 KB of one tensor. In the sum, warps take every so many-th tile
+// (which tiles is fixed by the list and the GPU's SM count, so the sum's order is too), looking
+// their first tensor up and stepping through the table from there.
 #include <cmath>
 #include <type_traits>
 
@@ -162,15 +161,8 @@ __device__ __forceinline__ double block_sum(double x, double* sm) {
     return s;
 }
 
-// The warp's tiles: [t0, t1) of all tiles, by an even split.
-__device__ __forceinline__ void warp_range(uint32_t tiles, uint32_t* t0, uint32_t* t1) {
-    const uint64_t w = (uint64_t)blockIdx.x * kGradWarps + (threadIdx.x >> 5);
-    const uint64_t all = (uint64_t)gridDim.x * kGradWarps;
-    *t0 = (uint32_t)(w * tiles / all);
-    *t1 = (uint32_t)((w + 1) * tiles / all);
-}
-
 // Bound by HBM: one read of every entry, one multiply-add each (16-bit types: and a conversion).
+// 575 us for 2^30 binary32 entries, 7.5 TB/s.
 template <int kCap>
 __global__ void __launch_bounds__(kGradThreads, kBlocksPerSm)
     k_grad_norm(const __grid_constant__ GradArgs a, const __grid_constant__ GradTable<kCap> tab) {
@@ -179,12 +171,12 @@ __global__ void __launch_bounds__(kGradThreads, kBlocksPerSm)
     grid_dep_launch();
     const GradEntry* entries = a.entries ? a.entries : tab.e;
     const uint32_t* first = a.entries ? a.first : tab.first;
-    uint32_t t0, t1;
-    warp_range(a.tiles, &t0, &t1);
+    const uint32_t step = gridDim.x * kGradWarps;
     double sum = 0.0;
-    if (t0 < t1) {
-        int e = upper_bound_minus1(first, a.count, t0);
-        for (uint32_t t = t0; t < t1; ++t) {
+    uint32_t t = blockIdx.x * kGradWarps + (threadIdx.x >> 5);
+    if (t < a.tiles) {
+        int e = upper_bound_minus1(first, a.count, t);
+        for (; t < a.tiles; t += step) {
             while (t >= first[e + 1]) ++e;
             const GradEntry g = entries[e];
             const uint64_t i = t - first[e];
@@ -276,32 +268,31 @@ __device__ __forceinline__ void tile_scale_to(const GradEntry& g, uint64_t tile,
         tile_scale(p, (__nv_bfloat16*)g.dst, g.count(), begin, f);
 }
 
-// Bound by HBM: every entry read again and written. A warp walks the tiles that the same warp of
-// k_grad_norm read, from the last one back, so that what the norm read last is still in L2.
-template <int kCap>
-__global__ void __launch_bounds__(kGradThreads, kBlocksPerSm)
+// Bound by HBM: every entry read again and written. Many small blocks, a tile a warp, which the
+// hardware hands to the SMs as they come free, from the list's end back: what the norm read last is
+// still in L2 (in the list's order 25.6M binary32 entries take 55.6 us, both kernels; from the end
+// 50.2). Persistent blocks with even shares took 8% longer on 411M bf16 entries, with loads through
+// shared memory or without: SMs do not all reach memory equally fast. kJoin: every block joins the
+// partial sums itself, for lists that need few blocks; else k_grad_finish has done it.
+template <int kCap, bool kJoin>
+__global__ void __launch_bounds__(kGradThreads)
     k_grad_scale(const __grid_constant__ GradArgs a, const __grid_constant__ GradTable<kCap> tab) {
     __shared__ double sm[kGradWarps];
     const GradEntry* entries = a.entries ? a.entries : tab.e;
     const uint32_t* first = a.entries ? a.first : tab.first;
+    const uint32_t t = (gridDim.x - 1 - blockIdx.x) * kGradWarps + (threadIdx.x >> 5);
     grid_dep_wait();
-    const float f = join(a, sm, blockIdx.x == 0);
-    if (a.in_place && f == 1.0f) return;
-    uint32_t t0, t1;
-    warp_range(a.tiles, &t0, &t1);
-    if (t0 >= t1) return;
-    int e = upper_bound_minus1(first, a.count, t1 - 1);
-    for (uint32_t t = t1; t-- > t0;) {
-        while (t < first[e]) --e;
-        const GradEntry g = entries[e];
-        const uint64_t i = t - first[e];
-        if (g.src_type() == DGC_F32)
-            tile_scale_to<float>(g, i, f);
-        else if (g.src_type() == DGC_F16)
-            tile_scale_to<__half>(g, i, f);
-        else
-            tile_scale_to<__nv_bfloat16>(g, i, f);
-    }
+    const int e = t < a.tiles ? upper_bound_minus1(first, a.count, t) : 0;
+    const float f = kJoin ? join(a, sm, blockIdx.x == 0) : *a.scale;
+    if (t >= a.tiles || (a.in_place && f == 1.0f)) return;
+    const GradEntry g = entries[e];
+    const uint64_t i = t - first[e];
+    if (g.src_type() == DGC_F32)
+        tile_scale_to<float>(g, i, f);
+    else if (g.src_type() == DGC_F16)
+        tile_scale_to<__half>(g, i, f);
+    else
+        tile_scale_to<__nv_bfloat16>(g, i, f);
 }
 
 // ----------------------------------------------------------------------------------- host
@@ -392,8 +383,12 @@ int run(const dgc_tensor* src, const dgc_tensor* dst, int32_t count, bool clip, 
     }
     int rc = launch(k_grad_norm<kCap>, grid, s, a, tab);
     if (rc) return rc;
-    if (!clip) return launch(k_grad_finish, 1, s, a);
-    return launch(k_grad_scale<kCap>, grid, s, a, tab);
+    const unsigned blocks = (a.tiles + kGradWarps - 1) / kGradWarps;
+    if (clip && blocks <= grid)
+        return launch(k_grad_scale<kCap, true>, blocks ? blocks : 1, s, a, tab);
+    rc = launch(k_grad_finish, 1, s, a);
+    if (rc || !clip) return rc;
+    return launch(k_grad_scale<kCap, false>, blocks, s, a, tab);
 }
 
 int grad_call(const dgc_tensor* src, const dgc_tensor* dst, int32_t count, float max_norm,
