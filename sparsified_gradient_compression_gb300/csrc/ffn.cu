@@ -927,6 +927,143 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
     if (warp == 1) tmem_free<kCg>(tmem, a.tmem_cols);
 }
 
+// ------------------------------------------------------------------------- a few tokens
+// The forward products of one or two tokens: the weights' bytes are all there is to it. A warp (or
+// 2, 4, 8 of a block, which split the sum) reads two weight rows -- gate: a column's gate and up
+// rows; down: two columns' rows -- with 16-byte loads, 4 in flight of each, past L1; the tokens'
+// rows stay in L1. The tensor cores would read the same bytes behind a pipeline's start, a tile's
+// barriers and a cluster's sum: one token x 1024 x 4096 5.0 + 7.0 us (gate, down; here 3.7 + 3.1),
+// x 4096 x 11264 40 + 15.6 us. From three tokens on they are ahead.
+constexpr uint32_t kFewTokens = 2;
+constexpr int kRowsWarps = 8;
+
+struct RowsArgs {
+    const uint16_t *x, *w0, *w1, *residual;
+    uint64_t ldx, ldw0, ldw1, ldr;
+    uint32_t n, k;
+    int32_t log_split, act;
+    uint16_t* out[3];
+    uint64_t ld[3];
+};
+
+__device__ __forceinline__ uint4 load_stream(const uint16_t* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+template <bool kHalf>
+__device__ __forceinline__ float dot8(uint4 a, uint4 b, float s) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 p = unpack2<kHalf>(x[i]), q = unpack2<kHalf>(y[i]);
+        s = fmaf(p.y, q.y, fmaf(p.x, q.x, s));
+    }
+    return s;
+}
+__device__ __forceinline__ float act_at(int act, float g) {
+    if (act == DGC_ACT_SILU) return act_value<DGC_ACT_SILU>(g);
+    if (act == DGC_ACT_GELU) return act_value<DGC_ACT_GELU>(g);
+    if (act == DGC_ACT_GELU_TANH) return act_value<DGC_ACT_GELU_TANH>(g);
+    return act_value<DGC_ACT_RELU>(g);
+}
+
+template <int kKind, bool kHalf, int kM>
+__global__ void __launch_bounds__(32 * kRowsWarps) k_rows(const __grid_constant__ RowsArgs a) {
+    constexpr int kW = 2;    // weight rows of a warp
+    constexpr int kFly = 4;  // loads in flight of each
+    constexpr int kCols = kKind == kGate ? 1 : 2;
+    __shared__ float part_sum[kRowsWarps][kW * kM];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t splits = 1u << a.log_split, part = warp & (splits - 1);
+    const uint32_t col = ((blockIdx.x * kRowsWarps + warp) >> a.log_split) * kCols;
+    grid_dep_wait();
+    grid_dep_launch();
+    float sum[kW][kM];
+#pragma unroll
+    for (int i = 0; i < kW; ++i)
+#pragma unroll
+        for (int m = 0; m < kM; ++m) sum[i][m] = 0.0f;
+    if (col < a.n) {
+        // down's second column, or the first again where there is none
+        const uint16_t* w[2] = {a.w0 + col * a.ldw0,
+                                kKind == kGate ? a.w1 + col * a.ldw1
+                                               : a.w0 + min(col + 1, a.n - 1) * a.ldw0};
+        const uint32_t vecs = a.k / 8;
+        const uint32_t v0 = (uint32_t)((uint64_t)vecs * part >> a.log_split);
+        const uint32_t v1 = (uint32_t)((uint64_t)vecs * (part + 1) >> a.log_split);
+        for (uint32_t v = v0 + lane; v < v1; v += 32 * kFly) {
+            uint4 q[kW][kFly];
+#pragma unroll
+            for (int u = 0; u < kFly; ++u)
+#pragma unroll
+                for (int i = 0; i < kW; ++i)
+                    q[i][u] = v + 32 * u < v1 ? load_stream(w[i] + (uint64_t)(v + 32 * u) * 8)
+                                              : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int u = 0; u < kFly; ++u) {
+                if (v + 32 * u >= v1) break;
+#pragma unroll
+                for (int m = 0; m < kM; ++m) {
+                    const uint4 t = *reinterpret_cast<const uint4*>(
+                        a.x + m * a.ldx + (uint64_t)(v + 32 * u) * 8);
+#pragma unroll
+                    for (int i = 0; i < kW; ++i) sum[i][m] = dot8<kHalf>(q[i][u], t, sum[i][m]);
+                }
+            }
+        }
+        const uint32_t at = vecs * 8 + lane;  // the last few of the sum
+        if (part == splits - 1 && at < a.k)
+#pragma unroll
+            for (int m = 0; m < kM; ++m)
+#pragma unroll
+                for (int i = 0; i < kW; ++i)
+                    sum[i][m] = fmaf(unpack2<kHalf>(w[i][at]).x,
+                                     unpack2<kHalf>(a.x[m * a.ldx + at]).x, sum[i][m]);
+    }
+#pragma unroll
+    for (int i = 0; i < kW; ++i)
+#pragma unroll
+        for (int m = 0; m < kM; ++m) sum[i][m] = warp_sum(sum[i][m]);
+    if (splits > 1) {
+        if (lane == 0)
+#pragma unroll
+            for (int i = 0; i < kW; ++i)
+#pragma unroll
+                for (int m = 0; m < kM; ++m) part_sum[warp][i * kM + m] = sum[i][m];
+        __syncthreads();
+        if (part != 0) return;
+        for (uint32_t p = 1; p < splits; ++p)
+#pragma unroll
+            for (int i = 0; i < kW; ++i)
+#pragma unroll
+                for (int m = 0; m < kM; ++m) sum[i][m] += part_sum[warp + p][i * kM + m];
+    }
+    if (col >= a.n) return;
+    auto put = [&](int i, int m, uint32_t c, float x) {
+        if (a.out[i]) a.out[i][m * a.ld[i] + c] = (uint16_t)pack2<kHalf>(x, 0.0f);
+    };
+#pragma unroll
+    for (int m = 0; m < kM; ++m) {
+        if (kKind == kGate) {
+            if (lane != m) continue;
+            put(0, m, col, act_at(a.act, sum[0][m]) * sum[1][m]);
+            put(1, m, col, sum[0][m]);
+            put(2, m, col, sum[1][m]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (lane != 2 * m + i || col + i >= a.n) continue;
+                float x = sum[i][m];
+                if (a.residual) x += unpack2<kHalf>(a.residual[m * a.ldr + col + i]).x;
+                put(0, m, col + i, x);
+            }
+        }
+    }
+}
+
 // The splits of a weight gradient, added in order: dW = (dW +) sum over s of part_s.
 __global__ void __launch_bounds__(256) k_wgrad_join(const float* part, uint64_t part_ld,
                                                     uint64_t split_stride, uint32_t splits,
@@ -1132,6 +1269,58 @@ struct Product {
     const Mat *a, *b;
 };
 
+template <int kKind, bool kHalf>
+int launch_rows(const RowsArgs& a, uint32_t m, unsigned grid, cudaStream_t s) {
+    auto kernel = m == 1 ? k_rows<kKind, kHalf, 1> : k_rows<kKind, kHalf, 2>;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(grid);
+    c.blockDim = dim3(32 * kRowsWarps);
+    c.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = at;
+    c.numAttrs = 1;
+    if (cudaLaunchKernelEx(&c, kernel, a) != cudaSuccess) {
+        cudaGetLastError();
+        return DGC_ECUDA;
+    }
+    dgc_internal_count_launches(1);
+    return DGC_OK;
+}
+
+// The products of up to kFewTokens tokens, with enough warps to a sum that the SMs have 16 each.
+template <int kKind>
+int few_tokens(const Mat& x, const Mat& w0, const Mat* w1, const Mat* residual,
+               const Mat* const (&outs)[3], int32_t act, int sms, cudaStream_t s) {
+    RowsArgs a{};
+    a.x = static_cast<const uint16_t*>(x.p);
+    a.ldx = x.ld;
+    a.w0 = static_cast<const uint16_t*>(w0.p);
+    a.ldw0 = w0.ld;
+    if (w1) {
+        a.w1 = static_cast<const uint16_t*>(w1->p);
+        a.ldw1 = w1->ld;
+    }
+    if (residual) {
+        a.residual = static_cast<const uint16_t*>(residual->p);
+        a.ldr = residual->ld;
+    }
+    for (int i = 0; i < 3; ++i)
+        if (outs[i]) {
+            a.out[i] = static_cast<uint16_t*>(outs[i]->p);
+            a.ld[i] = outs[i]->ld;
+        }
+    a.n = (uint32_t)w0.rows;
+    a.k = (uint32_t)w0.cols;
+    a.act = act;
+    const uint64_t warps = kKind == kGate ? a.n : ceil_div(a.n, 2);
+    while (a.log_split < 3 && (warps << a.log_split) < (uint64_t)sms * 16) ++a.log_split;
+    const unsigned grid = ceil_div(warps << a.log_split, kRowsWarps);
+    return x.dtype == DGC_F16 ? launch_rows<kKind, true>(a, (uint32_t)x.rows, grid, s)
+                              : launch_rows<kKind, false>(a, (uint32_t)x.rows, grid, s);
+}
+
 template <int kKind>
 int rows_product(Product p0, const Product* p1, const Mat* b_up, const Mat* in0, const Mat* in1,
                  const Mat* out0, const Mat* out1, const Mat* out2, int32_t act, int32_t* status,
@@ -1139,6 +1328,11 @@ int rows_product(Product p0, const Product* p1, const Mat* b_up, const Mat* in0,
     constexpr bool kAcrossB = kKind == kDownBwd || kKind == kGateBwd;
     const int sms = dgc_internal_sm_count();
     if (sms <= 0) return DGC_ECUDA;
+    const Mat* const outs[3] = {out0, out1, out2};
+    if constexpr (kKind == kGate || kKind == kDown)
+        if (out0->rows <= kFewTokens)
+            return few_tokens<kKind>(*p0.a, *p0.b, b_up, in0, outs, act, sms,
+                                     reinterpret_cast<cudaStream_t>(stream));
     FfnArgs a{};
     a.m = (uint32_t)out0->rows;
     a.n = (uint32_t)out0->cols;
@@ -1171,7 +1365,6 @@ int rows_product(Product p0, const Product* p1, const Mat* b_up, const Mat* in0,
         operand(&a.a1, *p1->a, kBlockK, a.a_rows);
         b_map(&a.b1, *p1->b);
     }
-    const Mat* outs[3] = {out0, out1, out2};
     for (int i = 0; i < 3; ++i)
         if (outs[i]) {
             a.out[i] = outs[i]->p;

@@ -156,6 +156,14 @@ def test_backward(m, d, f, dtype):
     backward(m, d, f, list(ACTS)[(m + f) % 4], dtype, seed=m + d + f)
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("m", [1, 2, 3])
+@pytest.mark.parametrize("d,f", [(1, 1), (7, 3), (33, 65), (264, 1000), (1027, 333), (3000, 2049)])
+def test_one_to_three_tokens(m, d, f, dtype):
+    forward(m, d, f, list(ACTS)[(d + f) % 4], dtype, seed=d, pad=8, save=m != 2,
+            residual=d % 2 == 1)
+
+
 @pytest.mark.parametrize("act", list(ACTS))
 @pytest.mark.parametrize("dtype", [F16, BF16])
 def test_activations(act, dtype):
