@@ -104,6 +104,9 @@ __device__ __forceinline__ void tma_add(const CUtensorMap* map, const void* src,
         ::"l"(map), "r"(x), "r"(y), "r"(smem_addr(src))
         : "memory");
 }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 template <int kN>
 __device__ __forceinline__ void bulk_wait_read() {
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kN) : "memory");
@@ -448,21 +451,22 @@ __device__ __forceinline__ void chunk_16bit(const uint32_t (&v)[32], const uint3
     }
 }
 
-// A split sum's parts: a chunk of this block's accumulator into its shared memory, a row of 128
-// bytes a lane, and the same chunk of all blocks of the cluster added up in the parts' order.
+// A split sum's parts: a chunk of this block's accumulator into its shared memory, and the same
+// chunk of all blocks of the cluster added up in the parts' order. Four columns of the 32 rows are
+// 512 consecutive bytes, one access of a warp here and from another block.
 __device__ __forceinline__ void put_part(char* parts, uint32_t chunk, const uint32_t (&v)[32],
                                          bool empty, int lane) {
-    char* to = parts + chunk * 4096 + lane * 128;
+    char* to = parts + chunk * 4096 + lane * 16;
 #pragma unroll
     for (int p = 0; p < 8; ++p)
-        *reinterpret_cast<uint4*>(to + ((p ^ (lane & 7)) << 4)) =
+        *reinterpret_cast<uint4*>(to + p * 512) =
             empty ? make_uint4(0, 0, 0, 0)
                   : make_uint4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
 }
 template <int kCg>
 __device__ __forceinline__ void add_parts(const char* parts, uint32_t chunk, uint32_t splits,
                                           uint32_t row_rank, uint32_t (&r)[32], int lane) {
-    const uint32_t at = smem_addr(parts) + chunk * 4096 + lane * 128;
+    const uint32_t at = smem_addr(parts) + chunk * 4096 + lane * 16;
 #pragma unroll
     for (int i = 0; i < 32; ++i) r[i] = 0;
 #pragma unroll 2
@@ -470,7 +474,7 @@ __device__ __forceinline__ void add_parts(const char* parts, uint32_t chunk, uin
         const uint32_t from = peer_addr(at, q * kCg + row_rank);
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
-            const float4 w = ld_peer(from + ((p ^ (lane & 7)) << 4));
+            const float4 w = ld_peer(from + p * 512);
             r[4 * p] = __float_as_uint(__uint_as_float(r[4 * p]) + w.x);
             r[4 * p + 1] = __float_as_uint(__uint_as_float(r[4 * p + 1]) + w.y);
             r[4 * p + 2] = __float_as_uint(__uint_as_float(r[4 * p + 2]) + w.z);
@@ -671,7 +675,7 @@ __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* 
         if (!ok && has_in)
             for (uint32_t i = done; i < load_n; ++i)
                 wait_quietly(&sh->in_full[warp][i % E::kSets], (i / E::kSets) & 1);
-        bulk_wait_all();
+        bulk_wait_read<0>();  // the block's shared memory may go
     }
 }
 
@@ -758,7 +762,7 @@ __device__ __forceinline__ void epilogue_sums(const FfnArgs& a, FfnShared* sh, c
         for (int i = 0; i < 4; ++i)
             if (half + 2 * i < chunks) finish(t, half + 2 * i, sum[i]);
     }
-    if (lane == 0) bulk_wait_all();
+    if (lane == 0) bulk_wait_read<0>();  // the block's shared memory may go
 }
 
 template <int kKind, int kCg, bool kSplit>
@@ -794,6 +798,12 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
         sh->abort = 0;
     }
     if (warp == 1) tmem_alloc<kCg>(&sh->tmem, a.tmem_cols);
+    if (threadIdx.x == 64) {
+        prefetch_map(&a.a0);
+        prefetch_map(&a.b0);
+        if (kKind == kGate || kKind == kGateBwd) prefetch_map(&a.b1);
+        if (kKind == kGateBwd) prefetch_map(&a.a1);
+    }
     tmem_fence_before();
     __syncthreads();
     if (kCg == 2) cluster_sync();
@@ -1210,27 +1220,27 @@ struct Plan {
     uint32_t bn, splits;
 };
 // The cheapest of the shapes that the kernel has, in SM clocks, by a model that was fitted to the
-// times of every shape on 26 products (1 to 8192 rows, 512 to 11264 columns; its choices take 2%
-// longer than the best ones). A tile's slice of 64 costs the tensor cores 2.4 bn (2 bn by count),
+// times of every shape on 35 products (4 to 5000 rows, 300 to 11264 columns; its choices take 1%
+// longer than the best ones). A tile's slice of 64 costs the tensor cores 2.3 bn (2 bn by count),
 // the way from L2 a clock per 68 of its operand bytes, the issuing loop 240: the largest counts; a
-// pair's agreement adds 60, and a lone block's 256-column tile, whose stages are the fewest, a
-// quarter. The last tile's epilogue costs 16 bn (the others hide behind the sums, or the sums
-// behind them: the weight gradient writes 25 bn clocks' worth). A split sum pays for its cluster's
-// barriers and for moving the parts. Clusters of 4 blocks reach 18 of a processing cluster's 19
-// SMs; a split sum in more than one wave, or in clusters of 8, was never worth its start.
+// pair's agreement adds 34, and a lone block's 256-column tile, whose stages are the fewest, a
+// tenth. A tile's epilogue costs `epilogue` bn and 1600; the last one's shows in full, the others
+// hide behind the sums, or the sums behind them. A split sum pays for its cluster's barriers and
+// for moving the parts. Clusters of 4 blocks reach 18 of a processing cluster's 19 SMs; a split sum
+// in more than one wave, or in clusters of 8, was hardly ever worth its start.
 Plan choose_plan(uint64_t m, uint64_t n, uint32_t kb, uint32_t halves, uint32_t narrowest,
-                 bool wgrad, int sms) {
+                 uint32_t a_most, uint32_t epilogue, int sms) {
     Plan best{false, 256, 1};
     uint64_t least = ~0ull;
-    const uint64_t a_rows = wgrad ? kBlockM : std::min<uint64_t>(kBlockM, m);
+    const uint64_t a_rows = std::min<uint64_t>(a_most, kBlockM);
     for (int pairs = 1; pairs >= 0; --pairs) {
         if (pairs && m <= kBlockM) continue;
         const uint32_t cg = pairs ? 2 : 1;
         for (uint32_t bn = 256; bn >= (pairs ? std::max(128u, narrowest) : narrowest); bn /= 2) {
             uint64_t slice =
-                std::max<uint64_t>({240, bn * 12 / 5, (a_rows + bn / cg) * 128 / 68});
-            if (pairs) slice += 60;
-            if (!pairs && bn == 256 && a_rows > 64) slice += slice / 4;
+                std::max<uint64_t>({240, bn * 23 / 10, (a_rows + bn / cg) * 128 / 68});
+            if (pairs) slice += 34;
+            if (!pairs && bn == 256 && a_rows > 64) slice += slice / 10;
             const uint64_t tiles = (uint64_t)ceil_div(m, kBlockM * cg) * ceil_div(n, bn / halves);
             for (uint32_t splits = 1; splits * cg <= 4 && (splits == 1 || splits * 4 <= kb);
                  splits *= 2) {
@@ -1240,9 +1250,10 @@ Plan choose_plan(uint64_t m, uint64_t n, uint32_t kb, uint32_t halves, uint32_t 
                 const uint64_t waves = (tiles + slots - 1) / slots;
                 if (splits > 1 && waves > 1) continue;
                 const uint64_t tile = (kb + splits - 1) / splits * slice;
-                uint64_t cost = waves * std::max<uint64_t>(tile, (wgrad ? 25 : 8) * bn) + 16 * bn;
-                if (pairs) cost += 2000;
-                if (splits > 1) cost += (cluster == 4 ? 2 : 1) * (1200 + 20 * bn);
+                uint64_t cost = waves * std::max<uint64_t>(tile, epilogue * bn + 1600) +
+                                epilogue * bn / splits;
+                if (pairs) cost += 1740;
+                if (splits > 1) cost += (cluster == 4 ? 2 : 1) * (1750 + 7 * bn);
                 if (cost < least) {
                     least = cost;
                     best = Plan{pairs != 0, bn, splits};
@@ -1339,7 +1350,9 @@ int rows_product(Product p0, const Product* p1, const Mat* b_up, const Mat* in0,
     constexpr uint32_t halves = kKind == kGate ? 2 : 1;
     a.kb0 = ceil_div(p0.a->cols, kBlockK);
     a.kb = a.kb0 + (p1 ? ceil_div(p1->a->cols, kBlockK) : 0);
-    const Plan plan = choose_plan(a.m, a.n, a.kb, halves, kKind == kDown ? 32 : 64, false, sms);
+    const Plan plan = choose_plan(a.m, a.n, a.kb, halves, kKind == kDown ? 32 : 64, a.m,
+                                  kKind == kDownBwd ? 32 : kKind == kGate ? 15 : kKind == kDown ? 11 : 8,
+                                  sms);
     const bool pairs = plan.pairs;
     a.bn = plan.bn;
     a.tiles_m = ceil_div(a.m, pairs ? 2 * kBlockM : kBlockM);
@@ -1535,7 +1548,7 @@ extern "C" int dgc_ffn_weight_grad(const dgc_matrix* dy, const dgc_matrix* x, in
     if ((rc = make_map(&a.a0, my, 64, kBlockK)) || (rc = make_map(&a.b0, mx, 64, kBlockK))) return rc;
     const uint32_t parts = wgrad_parts(rows, cols, tokens);
     const Plan plan = parts > 1 ? Plan{false, 64, 1}
-                                : choose_plan(rows, cols, a.kb, 1, 64, true, sms);
+                                : choose_plan(rows, cols, a.kb, 1, 64, kBlockM, 14, sms);
     a.bn = plan.bn;
     a.tiles_m = ceil_div(rows, plan.pairs ? 2 * kBlockM : kBlockM);
     a.tiles_n = ceil_div(cols, a.bn);
