@@ -366,10 +366,11 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, FfnShar
     sh->abort = 1;
     return false;
 }
-// For the way out of a block that gave up: no report, its own limit.
+// For the way out of a block that gave up, and for its last commit: no report, its own limit.
 __device__ __forceinline__ void wait_quietly(uint64_t* bar, uint32_t parity) {
-    for (uint32_t i = 0; i < (1u << 18); ++i)
-        if (mbar_try_wait(bar, parity)) return;
+    const uint64_t begin = global_ns();
+    for (uint32_t i = 0; i < (1u << 20); ++i)
+        if (mbar_test_wait(bar, parity) || global_ns() - begin > 50000000) return;
 }
 
 struct Tile {
@@ -1357,6 +1358,7 @@ int rows_product(Product p0, const Product* p1, const Mat* b_up, const Mat* in0,
     a.bn = plan.bn;
     a.tiles_m = ceil_div(a.m, pairs ? 2 * kBlockM : kBlockM);
     a.tiles_n = ceil_div(a.n, a.bn / halves);
+    if ((uint64_t)a.tiles_m * a.tiles_n > 0x3FFFFFFFull) return DGC_EUNSUPPORTED;
     a.tiles = a.tiles_m * a.tiles_n;
     a.a_rows = std::min<uint32_t>(kBlockM, (a.m + 7) & ~7u);
     a.act = act;
@@ -1552,6 +1554,7 @@ extern "C" int dgc_ffn_weight_grad(const dgc_matrix* dy, const dgc_matrix* x, in
     a.bn = plan.bn;
     a.tiles_m = ceil_div(rows, plan.pairs ? 2 * kBlockM : kBlockM);
     a.tiles_n = ceil_div(cols, a.bn);
+    if ((uint64_t)a.tiles_m * a.tiles_n > 0x3FFFFFFFull) return DGC_EUNSUPPORTED;
     if (parts > 1) {
         a.kb_split = ceil_div(a.kb, parts);
         const uint32_t used = ceil_div(a.kb, a.kb_split);
