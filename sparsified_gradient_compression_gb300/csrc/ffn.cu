@@ -1110,6 +1110,7 @@ __global__ void __launch_bounds__(256) k_wgrad_join(const float* part, uint64_t 
                                                     float* dw, uint64_t ld, uint32_t rows,
                                                     uint32_t cols, int accumulate) {
     const uint32_t x = blockIdx.x * 256 + threadIdx.x;
+    grid_dep_wait();
     if (x >= cols) return;
     for (uint32_t y = blockIdx.y; y < rows; y += gridDim.y) {
         const float* p = part + (uint64_t)y * part_ld + x;
@@ -1248,6 +1249,7 @@ int launch_ffn(FfnArgs& a, int32_t dtype, int sms, cudaStream_t s) {
 struct Plan {
     bool pairs;
     uint32_t bn, splits;
+    uint64_t cost;
 };
 // The cheapest of the shapes that the kernel has, in SM clocks, by a model that was fitted to the
 // times of every shape on 35 products (4 to 5000 rows, 300 to 11264 columns; its choices take 1%
@@ -1260,8 +1262,7 @@ struct Plan {
 // in more than one wave, or in clusters of 8, was hardly ever worth its start.
 Plan choose_plan(uint64_t m, uint64_t n, uint32_t kb, uint32_t halves, uint32_t narrowest,
                  uint32_t a_most, uint32_t epilogue, int sms) {
-    Plan best{false, 256, 1};
-    uint64_t least = ~0ull;
+    Plan best{false, 256, 1, ~0ull};
     const uint64_t a_rows = std::min<uint64_t>(a_most, kBlockM);
     for (int pairs = 1; pairs >= 0; --pairs) {
         if (pairs && m <= kBlockM) continue;
@@ -1284,10 +1285,7 @@ Plan choose_plan(uint64_t m, uint64_t n, uint32_t kb, uint32_t halves, uint32_t 
                                 epilogue * bn / splits;
                 if (pairs) cost += 1740;
                 if (splits > 1) cost += (cluster == 4 ? 2 : 1) * (1750 + 7 * bn);
-                if (cost < least) {
-                    least = cost;
-                    best = Plan{pairs != 0, bn, splits};
-                }
+                if (cost < best.cost) best = Plan{pairs != 0, bn, splits, cost};
             }
         }
     }
@@ -1428,19 +1426,38 @@ int rows_product(Product p0, const Product* p1, const Mat* b_up, const Mat* in0,
 
 bool bad_act(int32_t act) { return act < DGC_ACT_SILU || act > DGC_ACT_RELU; }
 
-// A small weight gradient over many tokens: where even clusters of 8 blocks on the narrowest tiles
-// would leave most SMs idle, the sum is cut into as many parts as fill them (152 blocks, at least
-// 8 slices each), whose results go to the workspace and are added in order by k_wgrad_join.
-uint32_t wgrad_parts(uint64_t rows, uint64_t cols, uint64_t tokens) {
-    const uint64_t tiles = (uint64_t)ceil_div(rows, kBlockM) * ceil_div(cols, 64);
-    const uint64_t kb = ceil_div(tokens, kBlockK);
-    if (tiles == 0 || tiles > 16 || kb < 64) return 1;
-    return (uint32_t)std::min<uint64_t>(152 / tiles, kb / 8);
+// A weight gradient's cut. Where the weight is small and the tokens are many, the sum is cut into
+// parts whose results go to the workspace and are added in order by k_wgrad_join: on the narrowest
+// tiles where even clusters would leave most SMs idle, or on the widest, which need the fewest
+// operand bytes, where that is cheaper than the best cut without (the join: a read and a write of
+// every part and 3000 clocks; 65536 tokens x 512 x 512 34.8 us, by clusters 52.8; 32768 x 1024 x
+// 1024 49 and 54). By sizes alone, for 152 SMs, so that the workspace can be asked for without a
+// device.
+struct WgradPlan {
+    Plan cut;
+    uint32_t parts;
+};
+WgradPlan wgrad_plan(uint64_t rows, uint64_t cols, uint64_t tokens) {
+    constexpr int kSms = 152;
+    const uint32_t kb = ceil_div(tokens, kBlockK);
+    const uint64_t narrow = (uint64_t)ceil_div(rows, kBlockM) * ceil_div(cols, 64);
+    const uint64_t wide = (uint64_t)ceil_div(rows, 256) * ceil_div(cols, 256);
+    if (narrow && narrow <= 16 && kb >= 64)
+        return {Plan{false, 64, 1, 0}, (uint32_t)std::min<uint64_t>(kSms / narrow, kb / 8)};
+    WgradPlan best{choose_plan(rows, cols, kb, 1, 64, kBlockM, 14, kSms), 1};
+    for (uint32_t parts = 2; wide && rows > kBlockM && wide * parts <= kSms / 2 && parts * 32 <= kb;
+         ++parts) {
+        const uint64_t cost = (uint64_t)ceil_div(kb, parts) * 622 + 14 * 256 + 1740 + 3000 +
+                              rows * cols * 8 * (parts + 1) / 2600;
+        if (cost < best.cut.cost) best = {Plan{true, 256, 1, cost}, parts};
+    }
+    return best;
 }
 uint64_t wgrad_workspace(uint64_t rows, uint64_t cols, uint64_t tokens) {
-    const uint64_t parts = wgrad_parts(rows, cols, tokens);
-    if (parts < 2) return 0;
-    return parts * ceil_div(rows, kBlockM) * kBlockM * ((cols + 3) & ~3ull) * sizeof(float);
+    const WgradPlan p = wgrad_plan(rows, cols, tokens);
+    if (p.parts < 2) return 0;
+    const uint64_t tile = p.cut.pairs ? 2 * kBlockM : kBlockM;
+    return p.parts * (rows + tile - 1) / tile * tile * ((cols + 3) & ~3ull) * sizeof(float);
 }
 
 }  // namespace
@@ -1577,24 +1594,35 @@ extern "C" int dgc_ffn_weight_grad(const dgc_matrix* dy, const dgc_matrix* x, in
     a.kb0 = a.kb = ceil_div(tokens, kBlockK);
     a.status = status;
     if ((rc = make_map(&a.a0, my, 64, kBlockK)) || (rc = make_map(&a.b0, mx, 64, kBlockK))) return rc;
-    const uint32_t parts = wgrad_parts(rows, cols, tokens);
-    const Plan plan = parts > 1 ? Plan{false, 64, 1}
-                                : choose_plan(rows, cols, a.kb, 1, 64, kBlockM, 14, sms);
+    const WgradPlan wp = wgrad_plan(rows, cols, tokens);
+    const Plan plan = wp.cut;
+    const uint32_t parts = wp.parts;
     a.bn = plan.bn;
-    a.tiles_m = ceil_div(rows, plan.pairs ? 2 * kBlockM : kBlockM);
+    const uint32_t tile_rows = plan.pairs ? 2 * kBlockM : kBlockM;
+    a.tiles_m = ceil_div(rows, tile_rows);
     a.tiles_n = ceil_div(cols, a.bn);
     if ((uint64_t)a.tiles_m * a.tiles_n > 0x3FFFFFFFull) return DGC_EUNSUPPORTED;
     if (parts > 1) {
         a.kb_split = ceil_div(a.kb, parts);
         const uint32_t used = ceil_div(a.kb, a.kb_split);
         a.tiles = a.tiles_m * a.tiles_n * used;
-        a.split_rows = a.tiles_m * kBlockM;
+        a.split_rows = a.tiles_m * tile_rows;
         const Mat part{ws, (uint64_t)a.split_rows * used, cols, (cols + 3) & ~3ull, DGC_F32};
         if ((rc = make_map(&a.out0, part, 32, 32))) return rc;
-        if ((rc = launch_ffn<kWGrad, 1, false>(a, my.dtype, sms, s))) return rc;
-        k_wgrad_join<<<grid2, 256, 0, s>>>((const float*)ws, part.ld, part.ld * a.split_rows, used,
-                                           (float*)out.p, out.ld, (uint32_t)rows, (uint32_t)cols,
-                                           accumulate != 0);
+        rc = plan.pairs ? launch_ffn<kWGrad, 2, false>(a, my.dtype, sms, s)
+                        : launch_ffn<kWGrad, 1, false>(a, my.dtype, sms, s);
+        if (rc) return rc;
+        cudaLaunchConfig_t c{};
+        c.gridDim = grid2;
+        c.blockDim = dim3(256);
+        c.stream = s;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        c.attrs = at;
+        c.numAttrs = 1;
+        cudaLaunchKernelEx(&c, k_wgrad_join, (const float*)ws, part.ld, part.ld * a.split_rows, used,
+                           (float*)out.p, out.ld, (uint32_t)rows, (uint32_t)cols, (int)accumulate);
         return launched();
     }
     a.tiles = a.tiles_m * a.tiles_n;

@@ -180,6 +180,14 @@ def test_weight_grad(tokens, rows, cols, accumulate, dtype):
     weight_grad(tokens, rows, cols, dtype, accumulate, seed=tokens)
 
 
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("tokens,rows,cols", [(65536, 264, 260), (40001, 500, 301)])
+def test_weight_grad_in_parts_of_wide_tiles(tokens, rows, cols, accumulate):
+    """Sums long enough that the parts go to the workspace from 256 x 256 tiles."""
+    assert dgc.dgc_ffn_weight_grad_workspace(rows, cols, tokens) > 0
+    weight_grad(tokens, rows, cols, BF16, accumulate, seed=1, pad=8)
+
+
 @pytest.mark.parametrize("shift,extra", [(1, 0), (4, 1), (3, 3), (0, 4), (8, 2)])
 @pytest.mark.parametrize("accumulate", [False, True])
 @pytest.mark.parametrize("tokens", [100, 3000])
