@@ -181,7 +181,7 @@ def test_weight_grad(tokens, rows, cols, accumulate, dtype):
 
 
 @pytest.mark.parametrize("accumulate", [False, True])
-@pytest.mark.parametrize("tokens,rows,cols", [(65536, 264, 260), (40001, 500, 301)])
+@pytest.mark.parametrize("tokens,rows,cols", [(65536, 300, 390), (40001, 500, 301)])
 def test_weight_grad_in_parts_of_wide_tiles(tokens, rows, cols, accumulate):
     """Sums long enough that the parts go to the workspace from 256 x 256 tiles."""
     assert dgc.dgc_ffn_weight_grad_workspace(rows, cols, tokens) > 0
