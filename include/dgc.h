@@ -471,6 +471,14 @@ void dgc_profile_stream_pass(dgc_event_t begin, dgc_event_t end);
  * back with *status = DGC_ETIMEOUT. Returns the launch status. */
 int dgc_selftest_wait_timeout(int32_t* status, uint32_t spin_limit, dgc_stream_t stream);
 
+/* Self-test of the feed-forward kernel's bounded waits: dgc_ffn_down without a residual, as a copy
+ * that never arrives would leave it (the second 64 columns of hidden and w_down are not loaded).
+ * The waits give up after about wait_ms (1 to 1000), the kernel must come back with
+ * *status = DGC_ETIMEOUT, and y is invalid. hidden must have more than 64 columns. */
+int dgc_selftest_ffn_timeout(const dgc_matrix* hidden, const dgc_matrix* w_down,
+                             const dgc_matrix* y, int32_t* status, uint32_t wait_ms,
+                             dgc_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -28,6 +28,7 @@ __all__ = [
     "dgc_ffn_gate", "dgc_ffn_down", "dgc_ffn_down_backward", "dgc_ffn_gate_backward",
     "dgc_ffn_weight_grad_workspace", "dgc_ffn_weight_grad",
     "dgc_read_status", "dgc_status_string", "dgc_launch_count", "dgc_selftest_wait_timeout",
+    "dgc_selftest_ffn_timeout",
     "dgc_set_l2_fetch_granularity",
     "dgc_profile_stream_pass",
     "SELECT_EXACT", "SELECT_SAMPLED", "SELECT_ADACOMP", "FLAG_MASK_MOMENTUM",
@@ -155,6 +156,7 @@ def lib():
         L.dgc_set_l2_fetch_granularity.argtypes = [i32]
         L.dgc_set_l2_fetch_granularity.restype = ctypes.c_int
         L.dgc_selftest_wait_timeout.argtypes = [vp, u32, vp]
+        L.dgc_selftest_ffn_timeout.argtypes = [vp, vp, vp, vp, u32, vp]
         L.dgc_profile_stream_pass.argtypes = [vp, vp]
         L.dgc_profile_stream_pass.restype = None
         for f in ("dgc_compress_workspace", "dgc_compress_max_out", "dgc_compress",
@@ -171,7 +173,7 @@ def lib():
                   "dgc_ffn_gate_backward", "dgc_ffn_weight_grad_workspace",
                   "dgc_ffn_weight_grad",
                   "dgc_read_status",
-                  "dgc_selftest_wait_timeout"):
+                  "dgc_selftest_wait_timeout", "dgc_selftest_ffn_timeout"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -598,3 +600,9 @@ def dgc_profile_stream_pass(begin, end) -> None:
 def dgc_selftest_wait_timeout(status, spin_limit: int, stream=None) -> int:
     return _check(lib().dgc_selftest_wait_timeout(_ptr(status), int(spin_limit), _stream(stream)),
                   "dgc_selftest_wait_timeout")
+
+
+def dgc_selftest_ffn_timeout(hidden, w_down, y, status, wait_ms: int, stream=None) -> int:
+    return _check(lib().dgc_selftest_ffn_timeout(_mat(hidden), _mat(w_down), _mat(y), _ptr(status),
+                                                 int(wait_ms), _stream(stream)),
+                  "dgc_selftest_ffn_timeout")

@@ -69,6 +69,8 @@ struct FfnArgs {
     void* out[3];
     uint64_t ld[3];
     int32_t ragged, unaligned;
+    uint32_t lost;                    // self-test: a slice whose copies are left out
+    uint64_t wait_ns;
     int32_t* status;
 };
 
@@ -380,18 +382,18 @@ struct FfnShared {
     volatile uint32_t abort;
 };
 
-// At most kFfnWaitLimit probes and about kFfnWaitNs.
+// At most kFfnWaitLimit probes and about a.wait_ns.
 template <bool kCluster = false>
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, FfnShared* sh,
-                                         int32_t* status) {
+                                         const FfnArgs& a) {
     if (mbar_sleep_wait<kCluster>(bar, parity, kSleepNs)) return true;
     const uint64_t begin = global_ns();
     for (uint32_t i = 0; i < kFfnWaitLimit; ++i) {
         if (mbar_sleep_wait<kCluster>(bar, parity, kSleepNs)) return true;
         if (sh->abort) return false;
-        if (global_ns() - begin > kFfnWaitNs) break;
+        if (global_ns() - begin > a.wait_ns) break;
     }
-    report(status, DGC_ETIMEOUT);
+    report(a.status, DGC_ETIMEOUT);
     sh->abort = 1;
     return false;
 }
@@ -639,7 +641,7 @@ __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* 
             }
             __syncwarp();
             ok = __all_sync(kFull, wait_bar(&sh->in_full[warp][done % E::kSets],
-                                            (done / E::kSets) & 1, sh, a.status));
+                                            (done / E::kSets) & 1, sh, a));
         } else {
             // the last store from this set has left it
             if (lane == 0) bulk_wait_read<E::kSets - 1>();
@@ -653,7 +655,7 @@ __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* 
         const uint32_t acc = it & 1, y = t.mt * kBlockM * kCg + row_in_tile;
         uint32_t k0, k1;
         k_range(a, kSplit ? part : t.split, &k0, &k1);
-        ok = __all_sync(kFull, wait_bar(&sh->acc_full[acc], (it >> 1) & 1, sh, a.status));
+        ok = __all_sync(kFull, wait_bar(&sh->acc_full[acc], (it >> 1) & 1, sh, a));
         tmem_fence_after();
         const uint32_t src = tmem + acc * a.bn + (quarter * 32 << 16);
         if (kSplit) {
@@ -744,7 +746,7 @@ __device__ __forceinline__ void epilogue_sums(const FfnArgs& a, FfnShared* sh, c
             for (int j = 0; j < 32; ++j) sum[i][j] = 0;
         for (uint32_t kb = k0; kb < k1; kb += kSumSlices, ++it) {
             const uint32_t acc = it & 1;
-            ok = __all_sync(kFull, wait_bar(&sh->acc_full[acc], (it >> 1) & 1, sh, a.status));
+            ok = __all_sync(kFull, wait_bar(&sh->acc_full[acc], (it >> 1) & 1, sh, a));
             if (!ok) break;
             tmem_fence_after();
             const uint32_t src = tmem + acc * a.bn + (quarter * 32 << 16);
@@ -858,9 +860,9 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
             uint32_t k0, k1;
             k_range(a, kSplit ? part : t.split, &k0, &k1);
             for (uint32_t kb = k0; kb < k1; ++kb, ++n) {
-                ok = wait_bar(&sh->empty[s], phase, sh, a.status);
+                ok = wait_bar(&sh->empty[s], phase, sh, a);
                 if (!ok) break;
-                {
+                if (kb != a.lost) {
                     char* sa = base + s * stage_bytes;
                     char* sb = sa + kStageA;
                     const uint32_t bar = full + s * 8;
@@ -916,12 +918,12 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
             do {
                 const uint32_t acc = it & 1;
                 const uint32_t k0 = kb, end = kKind == kWGrad ? min(k1, kb + kSumSlices) : k1;
-                ok = wait_bar<kCg == 2>(&sh->acc_empty[acc], ((it >> 1) & 1) ^ 1, sh, a.status);
+                ok = wait_bar<kCg == 2>(&sh->acc_empty[acc], ((it >> 1) & 1) ^ 1, sh, a);
                 if (!ok) break;
                 tmem_fence_after();
                 const uint32_t d = tmem + acc * a.bn;
                 for (; kb < end; ++kb) {
-                    ok = wait_bar(&sh->full[s], phase, sh, a.status);
+                    ok = wait_bar(&sh->full[s], phase, sh, a);
                     if (!ok) break;
                     tmem_fence_after();
                     const uint64_t da = da0 + (s * stage_bytes >> 4);
@@ -1198,6 +1200,10 @@ uint32_t ceil_div(uint64_t a, uint64_t b) { return (uint32_t)((a + b - 1) / b); 
 
 template <int kKind, int kCg, bool kSplit>
 int launch_ffn(FfnArgs& a, int32_t dtype, int sms, cudaStream_t s) {
+    if (a.wait_ns == 0) {
+        a.wait_ns = kFfnWaitNs;
+        a.lost = ~0u;
+    }
     constexpr bool kAcrossA = kKind == kWGrad;
     constexpr bool kAcrossB = kKind == kDownBwd || kKind == kGateBwd || kKind == kWGrad;
     a.stage_bytes = kStageA + a.bn / kCg * 128;
@@ -1363,16 +1369,20 @@ int few_tokens(const Mat& x, const Mat& w0, const Mat* w1, const Mat* residual,
 template <int kKind>
 int rows_product(Product p0, const Product* p1, const Mat* b_up, const Mat* in0, const Mat* in1,
                  const Mat* out0, const Mat* out1, const Mat* out2, int32_t act, int32_t* status,
-                 dgc_stream_t stream) {
+                 dgc_stream_t stream, uint32_t test_wait_ms = 0) {
     constexpr bool kAcrossB = kKind == kDownBwd || kKind == kGateBwd;
     const int sms = dgc_internal_sm_count();
     if (sms <= 0) return DGC_ECUDA;
     const Mat* const outs[3] = {out0, out1, out2};
     if constexpr (kKind == kGate || kKind == kDown)
-        if (out0->rows <= kFewTokens)
+        if (out0->rows <= kFewTokens && !test_wait_ms)
             return few_tokens<kKind>(*p0.a, *p0.b, b_up, in0, outs, act, sms,
                                      reinterpret_cast<cudaStream_t>(stream));
     FfnArgs a{};
+    if (test_wait_ms) {  // the self-test: the second slice never arrives
+        a.wait_ns = test_wait_ms * 1000000ull;
+        a.lost = 1;
+    }
     a.m = (uint32_t)out0->rows;
     a.n = (uint32_t)out0->cols;
     constexpr uint32_t halves = kKind == kGate ? 2 : 1;
@@ -1484,9 +1494,9 @@ extern "C" int dgc_ffn_gate(const dgc_matrix* x, const dgc_matrix* w_gate, const
                                gate ? &og : nullptr, gate ? &ou : nullptr, act, status, stream);
 }
 
-extern "C" int dgc_ffn_down(const dgc_matrix* hidden, const dgc_matrix* w_down,
-                            const dgc_matrix* residual, const dgc_matrix* y, int32_t* status,
-                            dgc_stream_t stream) {
+static int ffn_down(const dgc_matrix* hidden, const dgc_matrix* w_down, const dgc_matrix* residual,
+                    const dgc_matrix* y, int32_t* status, dgc_stream_t stream,
+                    uint32_t test_wait_ms) {
     Mat mh, mw, mr, my;
     int rc;
     if (!hidden || !status) return DGC_EINVAL;
@@ -1499,7 +1509,20 @@ extern "C" int dgc_ffn_down(const dgc_matrix* hidden, const dgc_matrix* w_down,
     if (residual && !shaped(mr, m, d)) return DGC_EINVAL;
     if (m == 0 || d == 0) return DGC_OK;
     return rows_product<kDown>({&mh, &mw}, nullptr, nullptr, residual ? &mr : nullptr, nullptr, &my,
-                               nullptr, nullptr, 0, status, stream);
+                               nullptr, nullptr, 0, status, stream, test_wait_ms);
+}
+
+extern "C" int dgc_ffn_down(const dgc_matrix* hidden, const dgc_matrix* w_down,
+                            const dgc_matrix* residual, const dgc_matrix* y, int32_t* status,
+                            dgc_stream_t stream) {
+    return ffn_down(hidden, w_down, residual, y, status, stream, 0);
+}
+
+extern "C" int dgc_selftest_ffn_timeout(const dgc_matrix* hidden, const dgc_matrix* w_down,
+                                        const dgc_matrix* y, int32_t* status, uint32_t wait_ms,
+                                        dgc_stream_t stream) {
+    if (wait_ms == 0 || wait_ms > 1000) return DGC_EINVAL;
+    return ffn_down(hidden, w_down, nullptr, y, status, stream, wait_ms);
 }
 
 extern "C" int dgc_ffn_down_backward(const dgc_matrix* dy, const dgc_matrix* w_down,

@@ -117,3 +117,11 @@ def test_binding_checks():
         dgc.matrix(torch.zeros(4, 8, dtype=torch.int16))
     m = dgc.matrix(torch.zeros(4, 16, dtype=torch.float16)[:, :5])
     assert (m.rows, m.cols, m.ld, m.dtype) == (4, 5, 16, dgc.F16)
+
+
+def test_selftest_rejects_on_host(L):
+    t = L.dgc_selftest_ffn_timeout
+    args = (mat(M, F), mat(D, F), mat(M, D))
+    assert t(*args, FAKE, 0, None) == dgc.EINVAL and t(*args, FAKE, 1001, None) == dgc.EINVAL
+    assert t(*args, None, 20, None) == dgc.EINVAL
+    assert t(None, args[1], args[2], FAKE, 20, None) == dgc.EINVAL

@@ -391,3 +391,22 @@ def test_graph_replays():
     got = y.clone()
     step()
     assert torch.equal(got, y) and dgc.dgc_read_status(st) == 0
+
+
+@pytest.mark.parametrize("m,n,k", [
+    (100, 512, 200),      # single blocks, each a whole sum
+    (100, 1024, 4096),    # a cluster's blocks, a part of the sum each
+    (4096, 4096, 256),    # pairs of blocks, several tiles each
+    (512, 2048, 8192)])   # few tiles of long sums
+def test_a_copy_that_never_arrives(m, n, k):
+    """The waits give up, the status says so, and the next call finds everything in order."""
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    h, w, y = rand(gen, m, k, BF16), rand(gen, n, k, BF16, k ** -0.5), padded(m, n, BF16)
+    st = status_word()
+    dgc.dgc_selftest_ffn_timeout(h, w, y, st, 20)
+    assert dgc.dgc_read_status(st) == dgc.ETIMEOUT
+    st.zero_()
+    dgc.dgc_ffn_down(h, w, None, y, st)
+    p, pe = product(h.double(), w.double().t())
+    near(y, p, pe, BF16)
+    assert dgc.dgc_read_status(st) == 0
