@@ -357,8 +357,8 @@ int dgc_grad_workspace(const dgc_tensor* src, int32_t count, size_t* bytes);
  *   norm  = sqrt(sum over all tensors and entries of g^2)
  *   scale = max_norm / norm where norm > max_norm, else 1
  * Squares are summed in binary32 over at most 64 entries of a thread and in binary64 from there
- * on, in an order that depends on the sizes alone: the same inputs give the same bits on every
- * run. Magnitudes whose squares leave the binary32 range are summed scaled, so the norm is right
+ * on, in an order that depends on the sizes and the GPU's SM count alone: the same inputs give
+ * the same bits on every run. Magnitudes whose squares leave the binary32 range are summed scaled, so the norm is right
  * for every finite input whose norm is. A NaN entry makes norm NaN (scale 1, as in
  * dgc_compress), else an infinite one makes it +inf (scale 0).
  *   src       host array of count tensors (0 allowed: norm 0, scale 1); read only
@@ -374,7 +374,7 @@ int dgc_grad_norm(const dgc_tensor* src, int32_t count, float max_norm, float* n
  *        own addresses and types: in place (then nothing is written where scale is 1). Tensors
  *        of dst may be consecutive pieces of one binary32 array: the clipped gradient is then
  *        in the flat bucket that dgc_compress takes. Apart from equal addresses, dst must not
- *        overlap src. */
+ *        overlap src, nor two tensors of dst one another. */
 int dgc_grad_clip(const dgc_tensor* src, const dgc_tensor* dst, int32_t count, float max_norm,
                   float* norm, float* scale, void* ws, size_t ws_bytes, dgc_stream_t stream);
 
@@ -403,8 +403,9 @@ enum { DGC_ACT_SILU = 0, DGC_ACT_GELU = 1, DGC_ACT_GELU_TANH = 2, DGC_ACT_RELU =
  * read in its place: y the residual, d_gate the gate, d_up the up, dx the residual.
  * Any extent may be 0: no rows or columns of the result, nothing is done; an empty sum gives 0.
  * Entries that are not finite go through the sums as they do in IEEE arithmetic. Extents above
- * 2^24 return DGC_EUNSUPPORTED. Every result is deterministic. One ordinary call of each kind
- * on the device must precede its stream capture. */
+ * 2^24 return DGC_EUNSUPPORTED. Every result is deterministic. The calls enqueue kernels only
+ * (programmatic dependent launches) and can be captured into a CUDA graph after one ordinary call
+ * of any of them on the device. */
 
 /* hidden = act(x w_gate^T) o (x w_up^T), M x F, in one kernel; gate and up (both or neither,
  * NULL): x w_gate^T and x w_up^T, for the backward pass. */

@@ -1199,6 +1199,32 @@ int make_map(CUtensorMap* map, const Mat& m, uint32_t bc, uint32_t br) {
 uint32_t ceil_div(uint64_t a, uint64_t b) { return (uint32_t)((a + b - 1) / b); }
 
 template <int kKind, int kCg, bool kSplit>
+bool raise_smem() {
+    return cudaFuncSetAttribute(k_ffn<kKind, kCg, kSplit>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)(kSmemLimit - 1024)) == cudaSuccess;
+}
+template <int kKind>
+bool raise_smem_all() {
+    return raise_smem<kKind, 1, false>() && raise_smem<kKind, 1, true>() &&
+           raise_smem<kKind, 2, false>() && raise_smem<kKind, 2, true>();
+}
+// The shared-memory limit of every form of the kernel, once per device.
+int set_ffn_attributes() {
+    static bool set[128] = {false};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 128 && set[dev]) return DGC_OK;
+    if (!raise_smem_all<kGate>() || !raise_smem_all<kDown>() || !raise_smem_all<kDownBwd>() ||
+        !raise_smem_all<kGateBwd>() || !raise_smem_all<kWGrad>()) {
+        cudaGetLastError();
+        return DGC_ECUDA;
+    }
+    if (dev >= 0 && dev < 128) set[dev] = true;
+    return DGC_OK;
+}
+
+template <int kKind, int kCg, bool kSplit>
 int launch_ffn(FfnArgs& a, int32_t dtype, int sms, cudaStream_t s) {
     if (a.wait_ns == 0) {
         a.wait_ns = kFfnWaitNs;
@@ -1217,19 +1243,10 @@ int launch_ffn(FfnArgs& a, int32_t dtype, int sms, cudaStream_t s) {
               ((uint32_t)kAcrossB << 16) | ((a.bn >> 3) << 17) | ((kBlockM * kCg >> 4) << 24);
     a.group = 16 / kCg;
     const uint32_t smem = a.stages * a.stage_bytes + staging + 1024;
-    static bool set[128] = {false};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 128 || !set[dev]) {
-        if (cudaFuncSetAttribute(k_ffn<kKind, kCg, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)(kSmemLimit - 1024)) != cudaSuccess) {
-            cudaGetLastError();
-            return DGC_ECUDA;
-        }
-        if (dev >= 0 && dev < 128) set[dev] = true;
-    }
-    cudaLaunchConfig_t c{};
+    const int rc = set_ffn_attributes();
+    if (rc) return rc;
     const uint32_t cluster = kSplit ? a.splits * kCg : kCg;
+    cudaLaunchConfig_t c{};
     c.gridDim = dim3(kSplit ? a.tiles * cluster
                             : std::min<uint32_t>(a.tiles, (uint32_t)sms / kCg) * kCg);
     c.blockDim = dim3(kFfnThreads);

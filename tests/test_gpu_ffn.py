@@ -393,6 +393,33 @@ def test_graph_replays():
     assert torch.equal(got, y) and dgc.dgc_read_status(st) == 0
 
 
+@pytest.mark.slow
+def test_offsets_past_32_bits():
+    """Results and operands of more than 2^32 entries, their last rows against binary64."""
+    m, d, f = 530_000, 64, 8200
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x, wg, wu = rand(gen, m, d, BF16), rand(gen, f, d, BF16, 0.1), rand(gen, f, d, BF16, 0.1)
+    hidden, st = torch.empty(m, f, dtype=BF16, device="cuda"), status_word()
+    assert hidden.numel() > 1 << 32
+    dgc.dgc_ffn_gate(x, wg, wu, dgc.ACT_RELU, hidden, None, None, st)
+    last = slice(m - 300, m)
+    g, ge = product(x[last].double(), wg.double().t())
+    u, ue = product(x[last].double(), wu.double().t())
+    near(hidden[last], torch.relu(g) * u, ge * u.abs() + g.abs() * ue + ge * ue, BF16)
+    wd, y = rand(gen, 40, f, BF16, 0.01), torch.empty(m, 40, dtype=BF16, device="cuda")
+    dgc.dgc_ffn_down(hidden, wd, None, y, st)
+    p, pe = product(hidden[last].double(), wd.double().t())
+    near(y[last], p, pe, BF16)
+    del y
+    # a weight gradient of more than 2^32 entries, from rows of the same big matrix
+    dy = rand(gen, 8, 530_000, BF16)
+    dw = torch.empty(530_000, f, device="cuda")
+    dgc.dgc_ffn_weight_grad(dy, hidden[:8], dw, False, st, None)
+    p, pe = product(dy[:, last].double().t(), hidden[:8].double())
+    assert ((dw[last].double() - p).abs() <= pe + 2.0 ** -22 * p.abs() + 1e-40).all()
+    assert dgc.dgc_read_status(st) == 0
+
+
 @pytest.mark.parametrize("m,n,k", [
     (100, 512, 200),      # single blocks, each a whole sum
     (100, 1024, 4096),    # a cluster's blocks, a part of the sum each
