@@ -201,12 +201,24 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
-def _stream(stream) -> int | None:
-    if stream is None:
+_get_raw_stream = None
+
+
+def _raw_stream():
+    """The current stream's handle for a device index (-1: the current device). The handle alone:
+    torch.cuda.current_stream() builds a stream object, 3 us a call."""
+    global _get_raw_stream
+    if _get_raw_stream is None:
         import torch
 
-        # the handle alone: torch.cuda.current_stream() builds a stream object, 3 us a call
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        torch.cuda.current_device()  # the context, before the first call
+        _get_raw_stream = torch._C._cuda_getCurrentRawStream
+    return _get_raw_stream
+
+
+def _stream(stream) -> int | None:
+    if stream is None:
+        return _raw_stream()(-1)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -504,16 +516,24 @@ def dgc_grad_clip(src: TensorList, dst: TensorList | None, max_norm: float, norm
 
 
 # ------------------------------------------------------------- gated feed-forward block
-def matrix(t) -> dgc_matrix:
+class Matrix(dgc_matrix):
+    """A dgc_matrix that keeps its tensor alive and knows its own address."""
+
+
+def matrix(t) -> Matrix:
     """The C view of a two-dimensional tensor whose rows are contiguous. The calls below build it
-    from the tensors they get; a program with fixed buffers builds it once (and keeps the tensor
-    alive, which the view does not)."""
+    from the tensors they get; a program with fixed buffers builds it once."""
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise DGCError(EINVAL, "matrix: a two-dimensional tensor with contiguous rows is wanted")
-    return dgc_matrix(t.data_ptr(), t.shape[0], t.shape[1], t.stride(0), _dtype_code(t), 0)
+    m = Matrix(t.data_ptr(), t.shape[0], t.shape[1], t.stride(0), _dtype_code(t), 0)
+    m.tensor = t
+    m.address = ctypes.addressof(m)
+    return m
 
 
 def _mat(m):
+    if type(m) is Matrix:
+        return m.address
     if m is None:
         return None
     return ctypes.byref(m if isinstance(m, dgc_matrix) else matrix(m))
