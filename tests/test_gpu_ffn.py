@@ -369,6 +369,46 @@ def test_runs_agree_bitwise_on_a_side_stream():
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[1], outs[2])
 
 
+def test_calls_on_several_streams_at_once():
+    """Two streams of this library's calls and one of library products, all using the tensor cores:
+    the same bits as one after the other."""
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    sets, st = [], status_word()
+    for m, d, f in ((700, 256, 1000), (1500, 512, 520)):
+        x, dy = rand(gen, m, d, BF16), rand(gen, m, d, BF16)
+        w = [rand(gen, f, d, BF16, 0.05) for _ in range(2)] + [rand(gen, d, f, BF16, 0.05)]
+        sets.append((x, dy, w, [padded(m, f, BF16) for _ in range(5)],
+                     [padded(m, d, BF16) for _ in range(2)], torch.empty(f, d, device="cuda")))
+
+    def run(s):
+        x, dy, (wg, wu, wd), (hidden, gate, up, dg, du), (y, dx), dw = s
+        dgc.dgc_ffn_gate(x, wg, wu, dgc.ACT_GELU_TANH, hidden, gate, up, st)
+        dgc.dgc_ffn_down(hidden, wd, x, y, st)
+        dgc.dgc_ffn_down_backward(dy, wd, gate, up, dgc.ACT_GELU_TANH, dg, du, st)
+        dgc.dgc_ffn_gate_backward(dg, du, wg, wu, dy, dx, st)
+        dgc.dgc_ffn_weight_grad(dg, x, dw, False, st, None)
+        return [hidden, gate, up, dg, du, y, dx, dw]
+
+    want = [[t.clone() for t in run(s)] for s in sets]
+    a = rand(gen, 2048, 2048, BF16)
+    product_alone = a @ a
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(20):
+        for s, stream in zip(sets, streams):
+            with torch.cuda.stream(stream):
+                run(s)
+        with torch.cuda.stream(streams[2]):
+            b = a @ a
+    torch.cuda.synchronize()
+    assert dgc.dgc_read_status(st) == 0
+    assert torch.equal(b, product_alone)
+    for s, w in zip(sets, want):
+        x, dy, _, inner, outer, dw = s
+        for got, ref in zip([*inner, *outer, dw], w):
+            assert torch.equal(got, ref)
+
+
 def test_graph_replays():
     gen = torch.Generator(device="cuda").manual_seed(3)
     m, d, f = 200, 136, 264
