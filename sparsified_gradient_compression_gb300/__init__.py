@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from ._build import LIB, build
 
@@ -459,13 +460,18 @@ def dgc_sum_shared(vals, count, max_count: int, out, status, ws, ws_bytes: int |
 
 
 # ------------------------------------------------------- gradient tensors: norm and clipping
-def _dtype_code(t) -> int:
-    import torch
+_dtype_codes = {}
 
-    codes = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
-    if t.dtype not in codes:
+
+def _dtype_code(t) -> int:
+    if not _dtype_codes:
+        import torch
+
+        _dtype_codes.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
         raise DGCError(EINVAL, f"tensor of type {t.dtype}")
-    return codes[t.dtype]
+    return code
 
 
 class TensorList:
@@ -476,10 +482,12 @@ class TensorList:
     def __init__(self, tensors):
         self.tensors = list(tensors)
         self.array = (dgc_tensor * max(len(self.tensors), 1))()
+        size = ctypes.sizeof(dgc_tensor)
         for i, t in enumerate(self.tensors):
             if not t.is_contiguous():
                 raise DGCError(EINVAL, f"TensorList: tensor {i} is not contiguous")
-            self.array[i] = dgc_tensor(t.data_ptr(), t.numel(), _dtype_code(t), 0)
+            struct.pack_into("=Qqii", self.array, i * size, t.data_ptr(), t.numel(),
+                             _dtype_code(t), 0)
         self.address = ctypes.addressof(self.array)
 
     def __len__(self):
