@@ -1216,18 +1216,43 @@ bool raise_smem_all() {
     return raise_smem<kKind, 1, false>() && raise_smem<kKind, 1, true>() &&
            raise_smem<kKind, 2, false>() && raise_smem<kKind, 2, true>();
 }
-// The shared-memory limit of every form of the kernel, once per device.
-int set_ffn_attributes() {
-    static bool set[128] = {false};
+// How many clusters of so many blocks the GPU holds at once, by the cluster's size. Those of a GPU
+// with all its 152 SMs are what a plan goes by where it must not depend on the device.
+struct Slots {
+    int of[9];
+};
+constexpr Slots kFullSlots = {{0, 152, 76, 46, 36, 28, 23, 15, 15}};
+
+// The shared-memory limit of every form of the kernel, and the slots, once per device.
+int ffn_device(const Slots** slots) {
+    static bool known[128] = {false};
+    static Slots table[128];
     int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev >= 0 && dev < 128 && set[dev]) return DGC_OK;
-    if (!raise_smem_all<kGate>() || !raise_smem_all<kDown>() || !raise_smem_all<kDownBwd>() ||
-        !raise_smem_all<kGateBwd>() || !raise_smem_all<kWGrad>()) {
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return DGC_ECUDA;
+    *slots = &table[dev];
+    if (known[dev]) return DGC_OK;
+    bool ok = raise_smem_all<kGate>() && raise_smem_all<kDown>() && raise_smem_all<kDownBwd>() &&
+              raise_smem_all<kGateBwd>() && raise_smem_all<kWGrad>();
+    for (unsigned size = 1; ok && size <= 8; ++size) {
+        cudaLaunchConfig_t c{};
+        c.gridDim = dim3(size * 256);
+        c.blockDim = dim3(kFfnThreads);
+        c.dynamicSmemBytes = kSmemLimit - 2048;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = size;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        c.attrs = at;
+        c.numAttrs = 1;
+        ok = cudaOccupancyMaxActiveClusters(&table[dev].of[size], k_ffn<kDown, 1, true>, &c) ==
+                 cudaSuccess &&
+             table[dev].of[1] > 0;
+    }
+    if (!ok) {
         cudaGetLastError();
         return DGC_ECUDA;
     }
-    if (dev >= 0 && dev < 128) set[dev] = true;
+    known[dev] = true;
     return DGC_OK;
 }
 
@@ -1250,8 +1275,6 @@ int launch_ffn(FfnArgs& a, int32_t dtype, int sms, cudaStream_t s) {
               ((uint32_t)kAcrossB << 16) | ((a.bn >> 3) << 17) | ((kBlockM * kCg >> 4) << 24);
     a.group = 16 / kCg;
     const uint32_t smem = a.stages * a.stage_bytes + staging + 1024;
-    const int rc = set_ffn_attributes();
-    if (rc) return rc;
     const uint32_t cluster = kSplit ? a.splits * kCg : kCg;
     cudaLaunchConfig_t c{};
     c.gridDim = dim3(kSplit ? a.tiles * cluster
@@ -1281,40 +1304,48 @@ struct Plan {
     uint32_t bn, splits;
     uint64_t cost;
 };
+// A product as the model below sees it.
+struct Shape {
+    uint64_t m, n;
+    uint32_t kb, halves, narrowest;
+    uint32_t a_rows;    // rows of A that a tile loads
+    uint32_t epilogue;  // clocks per column of a tile
+};
 // The cheapest of the shapes that the kernel has, in SM clocks, by a model that was fitted to the
-// times of every shape on 35 products (4 to 5000 rows, 300 to 11264 columns; its choices take 1%
-// longer than the best ones). A tile's slice of 64 costs the tensor cores 2.3 bn (2 bn by count),
-// the way from L2 a clock per 68 of its operand bytes, the issuing loop 240: the largest counts; a
-// pair's agreement adds 34, and a lone block's 256-column tile, whose stages are the fewest, a
-// tenth. A tile's epilogue costs `epilogue` bn and 1600; the last one's shows in full, the others
-// hide behind the sums, or the sums behind them. A split sum pays for its cluster's barriers and
-// for moving the parts. Clusters of 4 blocks reach 18 of a processing cluster's 19 SMs; a split sum
-// in more than one wave, or in clusters of 8, was hardly ever worth its start.
-Plan choose_plan(uint64_t m, uint64_t n, uint32_t kb, uint32_t halves, uint32_t narrowest,
-                 uint32_t a_most, uint32_t epilogue, int sms) {
+// times of every shape on 279 products (3 to 8192 rows, 64 to 11264 columns, more than half of them
+// odd; its choices take 0.9% longer than the best ones). A tile's slice of 64 costs the tensor
+// cores 2.2 bn (2 bn by count), the way from L2 a clock per 68 of its operand bytes, the issuing
+// loop 300: the largest counts; a pair's agreement adds 22, and a lone block's 256-column tile,
+// whose stages are the fewest, a quarter. A tile's epilogue costs `epilogue` bn and 1200; the last
+// one's shows in full, the others hide behind the sums, or the sums behind them. A split sum pays
+// for its cluster's start and barriers, and for moving the parts; in more than one wave it was
+// never worth that.
+uint64_t slice_cost(const Shape& p, uint32_t bn, uint32_t cg) {
+    const uint64_t bytes = (p.a_rows + bn / cg) * 128;
+    uint64_t cost = std::max<uint64_t>({300, bn * 11 / 5, bytes / 68});
+    if (cg == 2) return cost + 22;
+    return bn == 256 && p.a_rows > 64 ? cost + cost / 4 : cost;
+}
+Plan choose_plan(const Shape& p, const Slots& slots) {
+    constexpr uint32_t kCluster[9] = {0, 0, 10, 19, 15, 0, 23, 0, 24};  // tenths of a pair's start
     Plan best{false, 256, 1, ~0ull};
-    const uint64_t a_rows = std::min<uint64_t>(a_most, kBlockM);
     for (int pairs = 1; pairs >= 0; --pairs) {
-        if (pairs && m <= kBlockM) continue;
+        if (pairs && p.m <= kBlockM) continue;
         const uint32_t cg = pairs ? 2 : 1;
-        for (uint32_t bn = 256; bn >= (pairs ? std::max(128u, narrowest) : narrowest); bn /= 2) {
-            uint64_t slice =
-                std::max<uint64_t>({240, bn * 23 / 10, (a_rows + bn / cg) * 128 / 68});
-            if (pairs) slice += 34;
-            if (!pairs && bn == 256 && a_rows > 64) slice += slice / 10;
-            const uint64_t tiles = (uint64_t)ceil_div(m, kBlockM * cg) * ceil_div(n, bn / halves);
-            for (uint32_t splits = 1; splits * cg <= 4 && (splits == 1 || splits * 4 <= kb);
-                 splits *= 2) {
+        for (uint32_t bn = 256; bn >= (pairs ? std::max(128u, p.narrowest) : p.narrowest); bn /= 2) {
+            const uint64_t slice = slice_cost(p, bn, cg);
+            const uint64_t tiles =
+                (uint64_t)ceil_div(p.m, kBlockM * cg) * ceil_div(p.n, bn / p.halves);
+            for (uint32_t splits = 1; splits <= 4 && (splits == 1 || splits * 4 <= p.kb); ++splits) {
                 const uint32_t cluster = splits * cg;
-                const uint64_t slots =
-                    std::max<uint64_t>(1, (uint64_t)sms * (cluster == 4 ? 18 : 19) / (19 * cluster));
-                const uint64_t waves = (tiles + slots - 1) / slots;
+                const uint64_t held = (uint64_t)std::max(1, slots.of[cluster]);
+                const uint64_t waves = (tiles + held - 1) / held;
                 if (splits > 1 && waves > 1) continue;
-                const uint64_t tile = (kb + splits - 1) / splits * slice;
-                uint64_t cost = waves * std::max<uint64_t>(tile, epilogue * bn + 1600) +
-                                epilogue * bn / splits;
-                if (pairs) cost += 1740;
-                if (splits > 1) cost += (cluster == 4 ? 2 : 1) * (1750 + 7 * bn);
+                const uint64_t tile = (p.kb + splits - 1) / splits * slice;
+                uint64_t cost = waves * std::max<uint64_t>(tile, p.epilogue * bn + 1200) +
+                                p.epilogue * bn / splits;
+                if (pairs) cost += 770;
+                if (splits > 1) cost += kCluster[cluster] * (3100 + bn * 6 / 5) / 10;
                 if (cost < best.cost) best = Plan{pairs != 0, bn, splits, cost};
             }
         }
@@ -1402,6 +1433,9 @@ int rows_product(Product p0, const Product* p1, const Mat* b_up, const Mat* in0,
         if (out0->rows <= kFewTokens && !test_wait_ms)
             return few_tokens<kKind>(*p0.a, *p0.b, b_up, in0, outs, act, sms,
                                      reinterpret_cast<cudaStream_t>(stream));
+    const Slots* slots;
+    int rc = ffn_device(&slots);
+    if (rc) return rc;
     FfnArgs a{};
     if (test_wait_ms) {  // the self-test: the second slice never arrives
         a.wait_ns = test_wait_ms * 1000000ull;
@@ -1412,22 +1446,19 @@ int rows_product(Product p0, const Product* p1, const Mat* b_up, const Mat* in0,
     constexpr uint32_t halves = kKind == kGate ? 2 : 1;
     a.kb0 = ceil_div(p0.a->cols, kBlockK);
     a.kb = a.kb0 + (p1 ? ceil_div(p1->a->cols, kBlockK) : 0);
-    const Plan plan = choose_plan(a.m, a.n, a.kb, halves, kKind == kDown ? 32 : 64, a.m,
-                                  kKind == kDownBwd ? 32
-                                  : kKind == kGate  ? 15
-                                  : kKind == kDown  ? 11
-                                                    : 8,
-                                  sms);
+    a.a_rows = std::min<uint32_t>(kBlockM, (a.m + 7) & ~7u);
+    const Plan plan = choose_plan(
+        Shape{a.m, a.n, a.kb, halves, kKind == kDown ? 32u : 64u, a.a_rows,
+              kKind == kDownBwd ? 23u : kKind == kGate ? 17u : kKind == kDown ? 14u : 12u},
+        *slots);
     const bool pairs = plan.pairs;
     a.bn = plan.bn;
     a.tiles_m = ceil_div(a.m, pairs ? 2 * kBlockM : kBlockM);
     a.tiles_n = ceil_div(a.n, a.bn / halves);
     if ((uint64_t)a.tiles_m * a.tiles_n > 0x3FFFFFFFull) return DGC_EUNSUPPORTED;
     a.tiles = a.tiles_m * a.tiles_n;
-    a.a_rows = std::min<uint32_t>(kBlockM, (a.m + 7) & ~7u);
     a.act = act;
     a.status = status;
-    int rc = DGC_OK;
     auto operand = [&](CUtensorMap* map, const Mat& m, uint32_t bc, uint32_t br) {
         if (!rc && m.rows && m.cols) rc = make_map(map, m, bc, br);
     };
@@ -1475,16 +1506,17 @@ struct WgradPlan {
     uint32_t parts;
 };
 WgradPlan wgrad_plan(uint64_t rows, uint64_t cols, uint64_t tokens) {
-    constexpr int kSms = 152;
+    const uint64_t sms = kFullSlots.of[1], pairs = kFullSlots.of[2];
     const uint32_t kb = ceil_div(tokens, kBlockK);
     const uint64_t narrow = (uint64_t)ceil_div(rows, kBlockM) * ceil_div(cols, 64);
     const uint64_t wide = (uint64_t)ceil_div(rows, 256) * ceil_div(cols, 256);
     if (narrow && narrow <= 16 && kb >= 64)
-        return {Plan{false, 64, 1, 0}, (uint32_t)std::min<uint64_t>(kSms / narrow, kb / 8)};
-    WgradPlan best{choose_plan(rows, cols, kb, 1, 64, kBlockM, 14, kSms), 1};
-    for (uint32_t parts = 2; wide && rows > kBlockM && wide * parts <= kSms / 2 && parts * 32 <= kb;
+        return {Plan{false, 64, 1, 0}, (uint32_t)std::min<uint64_t>(sms / narrow, kb / 8)};
+    const Shape shape{rows, cols, kb, 1, 64, kBlockM, 15};
+    WgradPlan best{choose_plan(shape, kFullSlots), 1};
+    for (uint32_t parts = 2; wide && rows > kBlockM && wide * parts <= pairs && parts * 32 <= kb;
          ++parts) {
-        const uint64_t cost = (uint64_t)ceil_div(kb, parts) * 622 + 14 * 256 + 1740 + 3000 +
+        const uint64_t cost = ceil_div(kb, parts) * slice_cost(shape, 256, 2) + 15 * 256 + 770 + 3000 +
                               rows * cols * 8 * (parts + 1) / 2600;
         if (cost < best.cut.cost) best = {Plan{true, 256, 1, cost}, parts};
     }
@@ -1644,6 +1676,8 @@ extern "C" int dgc_ffn_weight_grad(const dgc_matrix* dy, const dgc_matrix* x, in
     a.kb0 = a.kb = ceil_div(tokens, kBlockK);
     a.status = status;
     if ((rc = make_map(&a.a0, my, 64, kBlockK)) || (rc = make_map(&a.b0, mx, 64, kBlockK))) return rc;
+    const Slots* slots;  // the plan does not go by them
+    if ((rc = ffn_device(&slots))) return rc;
     const WgradPlan wp = wgrad_plan(rows, cols, tokens);
     const Plan plan = wp.cut;
     const uint32_t parts = wp.parts;
