@@ -380,12 +380,14 @@ int dgc_grad_clip(const dgc_tensor* src, const dgc_tensor* dst, int32_t count, f
 
 /* --------------------------------------------------------- gated feed-forward block */
 
-/* A matrix of rows x cols entries, row r at data + r * ld entries. */
+/* A matrix of rows x cols entries, row r at data + r * ld entries. Operands and inputs whose rows
+ * start on 16-byte boundaries (data 16-byte aligned, ld a multiple of 8 for 16-bit types) go to the
+ * tensor cores; a call with any that do not is computed on the ordinary cores, some forty times
+ * slower on large products. Results may lie anywhere. */
 typedef struct {
-    void* data;       /* device; 16-byte aligned (the weight gradient: 4-byte aligned) */
+    void* data;       /* device, aligned to the element size */
     int64_t rows, cols;
-    int64_t ld;       /* entries from a row to the next, >= cols; a multiple of 8 for 16-bit types
-                         (any for the weight gradient; not read where rows is 1) */
+    int64_t ld;       /* entries from a row to the next, >= cols (not read where rows is 1) */
     int32_t dtype;    /* DGC_F16 or DGC_BF16; the weight gradient DGC_F32 */
     int32_t reserved; /* 0 */
 } dgc_matrix;
@@ -475,7 +477,8 @@ int dgc_selftest_wait_timeout(int32_t* status, uint32_t spin_limit, dgc_stream_t
 /* Self-test of the feed-forward kernel's bounded waits: dgc_ffn_down without a residual, as a copy
  * that never arrives would leave it (the second 64 columns of hidden and w_down are not loaded).
  * The waits give up after about wait_ms (1 to 1000), the kernel must come back with
- * *status = DGC_ETIMEOUT, and y is invalid. hidden must have more than 64 columns. */
+ * *status = DGC_ETIMEOUT, and y is invalid. hidden must have more than 64 columns, and rows on
+ * 16-byte boundaries, as w_down. */
 int dgc_selftest_ffn_timeout(const dgc_matrix* hidden, const dgc_matrix* w_down,
                              const dgc_matrix* y, int32_t* status, uint32_t wait_ms,
                              dgc_stream_t stream);

@@ -980,8 +980,10 @@ __global__ void __launch_bounds__(kFfnThreads, 1) k_ffn(const __grid_constant__ 
 // 2, 4, 8 of a block, which split the sum) reads two weight rows -- gate: a column's gate and up
 // rows; down: two columns' rows -- with 16-byte loads, 4 in flight of each, past L1; the tokens'
 // rows stay in L1. The tensor cores would read the same bytes behind a pipeline's start, a tile's
-// barriers and a cluster's sum: one token x 1024 x 4096 5.0 + 7.0 us (gate, down; here 3.7 + 3.1),
-// x 4096 x 11264 40 + 15.6 us. From three tokens on they are ahead.
+// barriers and a cluster's sum: one token x 1024 x 4096 5.0 + 7.0 us (gate, down; here 3.7 + 2.8),
+// x 4096 x 11264 40 + 15.6 us (here 29.1 + 13.9, the weights at the copy rate 27.6 + 13.8). From
+// three tokens on they are ahead. Rows off 16-byte boundaries are read entry by entry (1023 x 4095:
+// 22 + 14 us).
 constexpr uint32_t kFewTokens = 2;
 constexpr int kRowsWarps = 8;
 
@@ -1018,7 +1020,14 @@ __device__ __forceinline__ float act_at(int act, float g) {
     return act_value<DGC_ACT_RELU>(g);
 }
 
-template <int kKind, bool kHalf, int kM>
+__device__ __forceinline__ ActValue act_both_at(int act, float g) {
+    if (act == DGC_ACT_SILU) return act_both<DGC_ACT_SILU>(g);
+    if (act == DGC_ACT_GELU) return act_both<DGC_ACT_GELU>(g);
+    if (act == DGC_ACT_GELU_TANH) return act_both<DGC_ACT_GELU_TANH>(g);
+    return act_both<DGC_ACT_RELU>(g);
+}
+
+template <int kKind, bool kHalf, int kM, bool kAligned>
 __global__ void __launch_bounds__(32 * kRowsWarps) k_rows(const __grid_constant__ RowsArgs a) {
     constexpr int kW = 2;    // weight rows of a warp
     constexpr int kFly = 4;  // loads in flight of each
@@ -1039,7 +1048,28 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_rows(const __grid_constant_
         const uint16_t* w[2] = {a.w0 + col * a.ldw0,
                                 kKind == kGate ? a.w1 + col * a.ldw1
                                                : a.w0 + min(col + 1, a.n - 1) * a.ldw0};
-        const uint32_t vecs = a.k / 8;
+        // rows off 16-byte boundaries: entry by entry
+        const uint32_t first = (uint32_t)((uint64_t)a.k * part >> a.log_split);
+        const uint32_t end = (uint32_t)((uint64_t)a.k * (part + 1) >> a.log_split);
+        for (uint32_t k = first + lane; !kAligned && k < end; k += 32 * 2 * kFly) {
+            uint16_t q[kW][2 * kFly];
+#pragma unroll
+            for (int u = 0; u < 2 * kFly; ++u)
+#pragma unroll
+                for (int i = 0; i < kW; ++i) q[i][u] = k + 32 * u < end ? w[i][k + 32 * u] : 0;
+#pragma unroll
+            for (int u = 0; u < 2 * kFly; ++u) {
+                if (k + 32 * u >= end) break;
+#pragma unroll
+                for (int m = 0; m < kM; ++m) {
+                    const float t = unpack2<kHalf>(a.x[m * a.ldx + k + 32 * u]).x;
+#pragma unroll
+                    for (int i = 0; i < kW; ++i)
+                        sum[i][m] = fmaf(unpack2<kHalf>(q[i][u]).x, t, sum[i][m]);
+                }
+            }
+        }
+        const uint32_t vecs = kAligned ? a.k / 8 : 0;
         const uint32_t v0 = (uint32_t)((uint64_t)vecs * part >> a.log_split);
         const uint32_t v1 = (uint32_t)((uint64_t)vecs * (part + 1) >> a.log_split);
         for (uint32_t v = v0 + lane; v < v1; v += 32 * kFly) {
@@ -1063,7 +1093,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_rows(const __grid_constant_
             }
         }
         const uint32_t at = vecs * 8 + lane;  // the last few of the sum
-        if (part == splits - 1 && at < a.k)
+        if (kAligned && part == splits - 1 && at < a.k)
 #pragma unroll
             for (int m = 0; m < kM; ++m)
 #pragma unroll
@@ -1107,6 +1137,156 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_rows(const __grid_constant_
                 float x = sum[i][m];
                 if (a.residual) x += unpack2<kHalf>(a.residual[m * a.ldr + col + i]).x;
                 put(0, m, col + i, x);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- rows off 16-byte boundaries
+// The five products for operands that neither TMA nor 16-byte loads can address (an odd number of
+// contiguous columns, a slice that starts anywhere): tiles of 128 x 128 (gate: 128 x 64, twice) in
+// binary32 on the ordinary cores, 8 x 8 results a thread, 16 of the sum at a time through shared
+// memory, in partial sums of 768 as above. Bound by the multiply-adds, 20-30 TFLOP/s.
+struct AnyArgs {
+    const uint16_t *a[2], *b[2], *b_up;
+    uint64_t lda[2], ldb[2], ldb_up;
+    uint32_t k[2];
+    uint32_t m, n;
+    int32_t act, residual, accumulate;
+    const uint16_t *in0, *in1;
+    uint64_t ld_in0, ld_in1;
+    void* out[3];
+    uint64_t ld[3];
+};
+constexpr int kAnyM = 128, kAnyK = 16, kAnyPad = 4;
+template <int kKind>
+constexpr int kAnyN = kKind == kGate ? 64 : 128;
+
+template <int kKind, bool kHalf>
+__global__ void __launch_bounds__(256) k_any(const __grid_constant__ AnyArgs a) {
+    constexpr bool kAcrossA = kKind == kWGrad;
+    constexpr bool kAcrossB = kKind == kDownBwd || kKind == kGateBwd || kKind == kWGrad;
+    constexpr int kN = kAnyN<kKind>, kTn = kN / 16, kSets = kKind == kGate ? 2 : 1;
+    constexpr int kProducts = kKind == kGateBwd ? 2 : 1;
+    __shared__ __align__(16) float sa[kAnyK][kAnyM + kAnyPad];
+    __shared__ __align__(16) float sb[kSets][kAnyK][kN + kAnyPad];
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    grid_dep_wait();
+    grid_dep_launch();
+    const uint32_t col0 = blockIdx.x * kN;
+    for (uint32_t tile = blockIdx.y; tile * kAnyM < a.m; tile += gridDim.y) {
+        const uint32_t row0 = tile * kAnyM;
+        float sum[kSets][8][kTn], part[kSets][8][kTn];
+#pragma unroll
+        for (int s = 0; s < kSets; ++s)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int j = 0; j < kTn; ++j) sum[s][i][j] = part[s][i][j] = 0.0f;
+        // entry (own, k) of an operand, 0 outside of it
+        auto at = [](const uint16_t* p, uint64_t ld, bool across, uint32_t own, uint32_t owns,
+                     uint32_t k, uint32_t ks) {
+            return own < owns && k < ks ? p[across ? k * ld + own : own * ld + k] : (uint16_t)0;
+        };
+        constexpr int kLa = kAnyM * kAnyK / 256, kLb = kN * kAnyK / 256;  // a thread's loads
+        uint16_t ra[kLa], rb[kSets][kLb];
+        // neighbouring threads take neighbouring entries in memory
+        auto load = [&](int q, uint32_t k0) {
+#pragma unroll
+            for (int i = 0; i < kLa; ++i) {
+                const int e = tid + 256 * i;
+                ra[i] = at(a.a[q], a.lda[q], kAcrossA, row0 + (kAcrossA ? e % kAnyM : e / kAnyK), a.m,
+                           k0 + (kAcrossA ? e / kAnyM : e % kAnyK), a.k[q]);
+            }
+#pragma unroll
+            for (int i = 0; i < kLb; ++i) {
+                const int e = tid + 256 * i;
+                const uint32_t n = col0 + (kAcrossB ? e % kN : e / kAnyK);
+                const uint32_t k = k0 + (kAcrossB ? e / kN : e % kAnyK);
+                rb[0][i] = at(a.b[q], a.ldb[q], kAcrossB, n, a.n, k, a.k[q]);
+                if (kKind == kGate) rb[kSets - 1][i] = at(a.b_up, a.ldb_up, false, n, a.n, k, a.k[q]);
+            }
+        };
+        for (int q = 0; q < kProducts; ++q) {
+            load(q, 0);
+            for (uint32_t k0 = 0; k0 < a.k[q]; k0 += kAnyK) {
+#pragma unroll
+                for (int i = 0; i < kLa; ++i) {
+                    const int e = tid + 256 * i;
+                    sa[kAcrossA ? e / kAnyM : e % kAnyK][kAcrossA ? e % kAnyM : e / kAnyK] =
+                        unpack2<kHalf>(ra[i]).x;
+                }
+#pragma unroll
+                for (int i = 0; i < kLb; ++i) {
+                    const int e = tid + 256 * i;
+#pragma unroll
+                    for (int s = 0; s < kSets; ++s)
+                        sb[s][kAcrossB ? e / kN : e % kAnyK][kAcrossB ? e % kN : e / kAnyK] =
+                            unpack2<kHalf>(rb[s][i]).x;
+                }
+                __syncthreads();
+                if (k0 + kAnyK < a.k[q]) load(q, k0 + kAnyK);  // on their way during the products
+#pragma unroll
+                for (int k = 0; k < kAnyK; ++k) {
+                    float x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = sa[k][ty * 8 + i];
+#pragma unroll
+                    for (int s = 0; s < kSets; ++s)
+#pragma unroll
+                        for (int j = 0; j < kTn; ++j) {
+                            const float y = sb[s][k][tx * kTn + j];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                part[s][i][j] = fmaf(x[i], y, part[s][i][j]);
+                        }
+                }
+                __syncthreads();
+                if (k0 / kAnyK % (kSumSlices * kBlockK / kAnyK) ==
+                        kSumSlices * kBlockK / kAnyK - 1 || k0 + kAnyK >= a.k[q]) {
+#pragma unroll
+                    for (int s = 0; s < kSets; ++s)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+#pragma unroll
+                            for (int j = 0; j < kTn; ++j) {
+                                sum[s][i][j] += part[s][i][j];
+                                part[s][i][j] = 0.0f;
+                            }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t y = row0 + ty * 8 + i;
+            if (y >= a.m) continue;
+#pragma unroll
+            for (int j = 0; j < kTn; ++j) {
+                const uint32_t x = col0 + tx * kTn + j;
+                if (x >= a.n) continue;
+                const float v = sum[0][i][j];
+                auto put = [&](int o, float f) {
+                    if (a.out[o])
+                        static_cast<uint16_t*>(a.out[o])[y * a.ld[o] + x] =
+                            (uint16_t)pack2<kHalf>(f, 0.0f);
+                };
+                if (kKind == kWGrad) {
+                    float* d = static_cast<float*>(a.out[0]) + y * a.ld[0] + x;
+                    *d = a.accumulate ? *d + v : v;
+                } else if (kKind == kGate) {
+                    const float u = sum[kSets - 1][i][j];
+                    put(0, act_at(a.act, v) * u);
+                    put(1, v);
+                    put(2, u);
+                } else if (kKind == kDownBwd) {
+                    const float g = unpack2<kHalf>(a.in0[y * a.ld_in0 + x]).x;
+                    const float u = unpack2<kHalf>(a.in1[y * a.ld_in1 + x]).x;
+                    const ActValue f = act_both_at(a.act, g);
+                    put(0, v * u * f.slope);
+                    put(1, v * f.value);
+                } else {
+                    put(0, a.residual ? v + unpack2<kHalf>(a.in0[y * a.ld_in0 + x]).x : v);
+                }
             }
         }
     }
@@ -1163,9 +1343,14 @@ struct Mat {  // a checked matrix
     void* p;
     uint64_t rows, cols, ld;
     int32_t dtype;
+    // whether TMA can address its rows
+    bool aligned() const {
+        return rows == 0 || cols == 0 || (((uintptr_t)p & 15u) == 0 && (ld & 7) == 0);
+    }
 };
+bool aligned(const Mat* m) { return !m || m->aligned(); }
 
-// A matrix argument of 16-bit entries whose rows TMA can address.
+// A matrix argument of 16-bit entries.
 int check_matrix(const dgc_matrix* m, Mat* out, int32_t dtype) {
     if (!m || m->rows < 0 || m->cols < 0 || m->reserved != 0) return DGC_EINVAL;
     if (m->dtype != DGC_F16 && m->dtype != DGC_BF16) return DGC_EINVAL;
@@ -1173,12 +1358,12 @@ int check_matrix(const dgc_matrix* m, Mat* out, int32_t dtype) {
     if (m->rows > kMaxExtent || m->cols > kMaxExtent) return DGC_EUNSUPPORTED;
     *out = Mat{m->data, (uint64_t)m->rows, (uint64_t)m->cols, (uint64_t)m->ld, m->dtype};
     if (m->rows == 0 || m->cols == 0) return DGC_OK;
-    if (!m->data || ((uintptr_t)m->data & 15u)) return DGC_EINVAL;
+    if (!m->data || ((uintptr_t)m->data & 1u)) return DGC_EINVAL;
     if (m->rows == 1) {
         out->ld = ((uint64_t)m->cols + 7) & ~7ull;
         return DGC_OK;
     }
-    if (m->ld < m->cols || (m->ld & 7)) return DGC_EINVAL;
+    if (m->ld < m->cols) return DGC_EINVAL;
     if (m->ld > (1ll << 36)) return DGC_EUNSUPPORTED;
     return DGC_OK;
 }
@@ -1369,9 +1554,9 @@ struct Product {
     const Mat *a, *b;
 };
 
-template <int kKind, bool kHalf>
+template <int kKind, bool kHalf, bool kAligned>
 int launch_rows(const RowsArgs& a, uint32_t m, unsigned grid, cudaStream_t s) {
-    auto kernel = m == 1 ? k_rows<kKind, kHalf, 1> : k_rows<kKind, kHalf, 2>;
+    auto kernel = m == 1 ? k_rows<kKind, kHalf, 1, kAligned> : k_rows<kKind, kHalf, 2, kAligned>;
     cudaLaunchConfig_t c{};
     c.gridDim = dim3(grid);
     c.blockDim = dim3(32 * kRowsWarps);
@@ -1382,6 +1567,28 @@ int launch_rows(const RowsArgs& a, uint32_t m, unsigned grid, cudaStream_t s) {
     c.attrs = at;
     c.numAttrs = 1;
     if (cudaLaunchKernelEx(&c, kernel, a) != cudaSuccess) {
+        cudaGetLastError();
+        return DGC_ECUDA;
+    }
+    dgc_internal_count_launches(1);
+    return DGC_OK;
+}
+
+template <int kKind>
+int launch_any(const AnyArgs& a, int32_t dtype, cudaStream_t s) {
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(ceil_div(a.n, kAnyN<kKind>),
+                     std::min<uint32_t>(ceil_div(a.m, kAnyM), 65535));
+    c.blockDim = dim3(256);
+    c.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = at;
+    c.numAttrs = 1;
+    const cudaError_t e = dtype == DGC_F16 ? cudaLaunchKernelEx(&c, k_any<kKind, true>, a)
+                                           : cudaLaunchKernelEx(&c, k_any<kKind, false>, a);
+    if (e != cudaSuccess) {
         cudaGetLastError();
         return DGC_ECUDA;
     }
@@ -1417,8 +1624,12 @@ int few_tokens(const Mat& x, const Mat& w0, const Mat* w1, const Mat* residual,
     const uint64_t warps = kKind == kGate ? a.n : ceil_div(a.n, 2);
     while (a.log_split < 3 && (warps << a.log_split) < (uint64_t)sms * 16) ++a.log_split;
     const unsigned grid = ceil_div(warps << a.log_split, kRowsWarps);
-    return x.dtype == DGC_F16 ? launch_rows<kKind, true>(a, (uint32_t)x.rows, grid, s)
-                              : launch_rows<kKind, false>(a, (uint32_t)x.rows, grid, s);
+    const uint32_t m = (uint32_t)x.rows;
+    if (x.aligned() && w0.aligned() && aligned(w1))
+        return x.dtype == DGC_F16 ? launch_rows<kKind, true, true>(a, m, grid, s)
+                                  : launch_rows<kKind, false, true>(a, m, grid, s);
+    return x.dtype == DGC_F16 ? launch_rows<kKind, true, false>(a, m, grid, s)
+                              : launch_rows<kKind, false, false>(a, m, grid, s);
 }
 
 template <int kKind>
@@ -1433,6 +1644,40 @@ int rows_product(Product p0, const Product* p1, const Mat* b_up, const Mat* in0,
         if (out0->rows <= kFewTokens && !test_wait_ms)
             return few_tokens<kKind>(*p0.a, *p0.b, b_up, in0, outs, act, sms,
                                      reinterpret_cast<cudaStream_t>(stream));
+    if (!p0.a->aligned() || !p0.b->aligned() || !aligned(b_up) || !aligned(in0) || !aligned(in1) ||
+        (p1 && (!p1->a->aligned() || !p1->b->aligned()))) {
+        AnyArgs a{};
+        const Product* products[2] = {&p0, p1};
+        for (int i = 0; i < (p1 ? 2 : 1); ++i) {
+            a.a[i] = static_cast<const uint16_t*>(products[i]->a->p);
+            a.lda[i] = products[i]->a->ld;
+            a.b[i] = static_cast<const uint16_t*>(products[i]->b->p);
+            a.ldb[i] = products[i]->b->ld;
+            a.k[i] = (uint32_t)products[i]->a->cols;
+        }
+        if (b_up) {
+            a.b_up = static_cast<const uint16_t*>(b_up->p);
+            a.ldb_up = b_up->ld;
+        }
+        if (in0) {
+            a.in0 = static_cast<const uint16_t*>(in0->p);
+            a.ld_in0 = in0->ld;
+        }
+        if (in1) {
+            a.in1 = static_cast<const uint16_t*>(in1->p);
+            a.ld_in1 = in1->ld;
+        }
+        for (int i = 0; i < 3; ++i)
+            if (outs[i]) {
+                a.out[i] = outs[i]->p;
+                a.ld[i] = outs[i]->ld;
+            }
+        a.m = (uint32_t)out0->rows;
+        a.n = (uint32_t)out0->cols;
+        a.act = act;
+        a.residual = in0 != nullptr;
+        return launch_any<kKind>(a, out0->dtype, reinterpret_cast<cudaStream_t>(stream));
+    }
     const Slots* slots;
     int rc = ffn_device(&slots);
     if (rc) return rc;
@@ -1481,9 +1726,12 @@ int rows_product(Product p0, const Product* p1, const Mat* b_up, const Mat* in0,
             a.ld[i] = outs[i]->ld;
         }
     a.ragged = (a.n & 7) != 0;
-    operand(&a.out0, *out0, 32, 32);
-    if (out1) operand(&a.out1, *out1, 32, 32);
-    if (out2) operand(&a.out2, *out2, 32, 32);
+    a.unaligned = !out0->aligned() || !aligned(out1) || !aligned(out2);
+    if (!a.unaligned) {
+        operand(&a.out0, *out0, 32, 32);
+        if (out1) operand(&a.out1, *out1, 32, 32);
+        if (out2) operand(&a.out2, *out2, 32, 32);
+    }
     if (in0) operand(&a.in0, *in0, 32, 32);
     if (in1) operand(&a.in1, *in1, 32, 32);
     if (rc) return rc;
@@ -1668,6 +1916,20 @@ extern "C" int dgc_ffn_weight_grad(const dgc_matrix* dy, const dgc_matrix* x, in
         if (accumulate) return DGC_OK;
         k_wgrad_zero<<<grid2, 256, 0, s>>>((float*)out.p, out.ld, (uint32_t)rows, (uint32_t)cols);
         return launched();
+    }
+    if (!my.aligned() || !mx.aligned()) {
+        AnyArgs a{};
+        a.a[0] = static_cast<const uint16_t*>(my.p);
+        a.lda[0] = my.ld;
+        a.b[0] = static_cast<const uint16_t*>(mx.p);
+        a.ldb[0] = mx.ld;
+        a.k[0] = (uint32_t)tokens;
+        a.m = (uint32_t)rows;
+        a.n = (uint32_t)cols;
+        a.accumulate = accumulate != 0;
+        a.out[0] = out.p;
+        a.ld[0] = out.ld;
+        return launch_any<kWGrad>(a, my.dtype, s);
     }
     FfnArgs a{};
     a.m = (uint32_t)rows;

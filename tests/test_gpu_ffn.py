@@ -29,7 +29,12 @@ def _lib():
 
 
 def padded(rows, cols, dtype, pad=0, fill=float("nan")):
-    """A view whose rows start on 16-byte boundaries, in a buffer filled with NaN."""
+    """A view whose rows start on 16-byte boundaries, in a buffer filled with NaN; pad "odd": an odd
+    number of entries from row to row, the first one off every boundary."""
+    if pad == "odd":
+        ld = cols | 1
+        flat = torch.full((rows * ld + 2,), fill, dtype=dtype, device="cuda")
+        return flat[1:1 + rows * ld].view(rows, ld)[:, :cols]
     ld = -(-cols // 8) * 8 + pad
     return torch.full((max(rows, 1), max(ld, 8)), fill, dtype=dtype, device="cuda")[:rows, :cols]
 
@@ -162,6 +167,55 @@ def test_backward(m, d, f, dtype):
 def test_one_to_three_tokens(m, d, f, dtype):
     forward(m, d, f, list(ACTS)[(d + f) % 4], dtype, seed=d, pad=8, save=m != 2,
             residual=d % 2 == 1)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("m,d,f", [(1, 1, 1), (2, 9, 5), (7, 33, 64), (130, 65, 129), (300, 129, 257),
+                                   (65, 1001, 333), (1000, 70, 900)])
+def test_rows_off_16_byte_boundaries(m, d, f, dtype):
+    act = list(ACTS)[(m + d) % 4]
+    forward(m, d, f, act, dtype, m, "odd", m % 2 == 0, m != 7)
+    backward(m, d, f, act, dtype, m, "odd", m != 7)
+    for accumulate in (False, True):
+        weight_grad(m, d, f, dtype, accumulate, m, "odd", 1, 2)
+
+
+def test_long_sum_off_16_byte_boundaries():
+    weight_grad(9000, 65, 130, BF16, True, 3, "odd")
+
+
+@pytest.mark.parametrize("which", range(8))
+def test_one_matrix_off_16_byte_boundaries(which):
+    """Each operand, input and result in turn: the same values as with all of them on."""
+    gen = torch.Generator(device="cuda").manual_seed(which)
+    m, d, f = 200, 72, 136
+    x, dy = rand(gen, m, d, BF16), rand(gen, m, d, BF16)
+    wg, wu, wd = rand(gen, f, d, BF16, 0.1), rand(gen, f, d, BF16, 0.1), rand(gen, d, f, BF16, 0.1)
+
+    def run(off):
+        def moved(t, i):
+            if i != off:
+                return t
+            o = padded(*t.shape, t.dtype, "odd")
+            o.copy_(t)
+            return o
+
+        out = [moved(padded(m, f, BF16), 4 if i == 0 else 5 if i == 1 else -2) for i in range(5)]
+        hidden, gate, up, dg, du = out
+        y, dx = moved(padded(m, d, BF16), 6), moved(padded(m, d, BF16), 7)
+        st = status_word()
+        X, D, G, W = moved(x, 0), moved(dy, 1), moved(wg, 2), moved(wd, 3)
+        dgc.dgc_ffn_gate(X, G, wu, dgc.ACT_SILU, hidden, gate, up, st)
+        dgc.dgc_ffn_down(hidden, W, X, y, st)
+        dgc.dgc_ffn_down_backward(D, W, gate, up, dgc.ACT_SILU, dg, du, st)
+        dgc.dgc_ffn_gate_backward(dg, du, G, wu, D, dx, st)
+        dw = torch.empty(f, d, device="cuda")
+        dgc.dgc_ffn_weight_grad(dg, X, dw, False, st, None)
+        assert dgc.dgc_read_status(st) == 0
+        return [t.double() for t in (hidden, gate, up, dg, du, y, dx, dw)]
+
+    for got, want in zip(run(which), run(-1)):  # two orders of sums and one or two roundings each
+        assert (got - want).norm() <= 2.0 ** -7 * want.norm()
 
 
 @pytest.mark.parametrize("act", list(ACTS))
