@@ -346,7 +346,9 @@ __device__ __forceinline__ ActValue act_both(float g) {
         r.value = g * p;
         r.slope = fmaf(g * 0.3989422804014327f, exp_fast(-0.5f * g * g), p);
     } else if (kAct == DGC_ACT_GELU_TANH) {
-        const float g2 = g * g;
+        // Beyond 16 the sigmoid is 0 or 1 to the last bit: a square held there keeps the slope's
+        // polynomial finite, where 0 * inf would make a NaN of gates from 1.9e19 on.
+        const float g2 = fminf(g * g, 256.0f);
         const float s = sigmoid(2.0f * kGeluC * g * fmaf(kGeluA, g2, 1.0f));
         r.value = g * s;
         r.slope = fmaf(r.value * (1.0f - s), 2.0f * kGeluC * fmaf(3.0f * kGeluA, g2, 1.0f), s);

@@ -1,0 +1,75 @@
+"""The feed-forward calls at the ends of their ranges, on the GPU: gates of every magnitude on every
+route of the products."""
+import math
+
+import pytest
+import torch
+
+import sparsified_gradient_compression_gb300 as dgc
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+ACTS = {"silu": dgc.ACT_SILU, "gelu": dgc.ACT_GELU, "gelu_tanh": dgc.ACT_GELU_TANH,
+        "relu": dgc.ACT_RELU}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    dgc.build()
+    dgc.lib()
+
+
+def status_word():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def rows(t, odd):
+    """t's entries in rows on 16-byte boundaries, or off them."""
+    r, c = t.shape
+    if not odd:
+        o = torch.zeros(r, -(-c // 8) * 8, dtype=t.dtype, device="cuda")[:, :c]
+    else:
+        ld = c | 1
+        o = torch.zeros(r * ld + 1, dtype=t.dtype, device="cuda")[1:].view(r, ld)[:, :c]
+    o.copy_(t)
+    return o
+
+
+def block_of_gates(act, terms, m, odd):
+    """What the two calls that evaluate the activation make of gates that are given as sums of
+    bfloat16 terms (len(terms[0]) of them each), with up, dh = 1: hidden, and from the gates' first
+    terms alone d_gate and d_up, of m equal rows. Every sum but the gate's is exact."""
+    f, k = len(terms), len(terms[0])
+    t = torch.tensor(terms, dtype=torch.float64, device="cuda").to(BF16)
+    x = rows(torch.ones(m, k, dtype=BF16, device="cuda"), odd)
+    wu = torch.zeros(f, k, dtype=BF16, device="cuda")
+    wu[:, 0] = 1.0
+    hidden = rows(torch.full((m, f), 7.0, dtype=BF16, device="cuda"), odd)
+    st = status_word()
+    dgc.dgc_ffn_gate(x, rows(t, odd), rows(wu, odd), ACTS[act], hidden, None, None, st)
+    gate = rows(t[:, 0].repeat(m, 1), odd)
+    up = rows(torch.ones_like(gate), odd)
+    dg, du = rows(torch.full_like(gate, 7.0), odd), rows(torch.full_like(gate, 7.0), odd)
+    dy, wd = torch.zeros(m, 8, dtype=BF16, device="cuda"), torch.zeros(8, f, dtype=BF16,
+                                                                       device="cuda")
+    dy[:, 0], wd[0] = 1.0, 1.0
+    dgc.dgc_ffn_down_backward(rows(dy, odd), rows(wd, odd), gate, up, ACTS[act], dg, du, st)
+    assert dgc.dgc_read_status(st) == 0
+    return t.double(), hidden, dg, du
+
+
+ROUTES = [(1, False), (2, True), (3, False), (3, True), (200, False), (300, True)]
+
+
+@pytest.mark.parametrize("m,odd", ROUTES)
+@pytest.mark.parametrize("act", list(ACTS))
+def test_gates_up_to_the_largest(act, m, odd):
+    """From 1e4 on the activations are the identity and 0, their slopes 1 and 0, to the last bit."""
+    g = [s * v for v in (1e4, 1e10, 1.8e19, 1.9e19, 2e19, 1e20, 1e30, 3e38) for s in (1, -1)]
+    t, hidden, dg, du = block_of_gates(act, [[v] for v in g], m, odd)
+    value = t[:, 0].clamp_min(0.0).to(BF16).expand(m, -1)
+    slope = (t[:, 0] > 0).to(BF16).expand(m, -1)
+    assert torch.equal(hidden, value)
+    assert torch.equal(du, value)
+    assert torch.equal(dg, slope)
