@@ -301,13 +301,19 @@ __device__ __forceinline__ float reciprocal(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ float sigmoid(float x) { return reciprocal(1.0f + exp_fast(-x)); }
+// The reciprocal flushes what is below 2^-126, which a sigmoid is from x = -87.3 on while g times it
+// is not: it is taken 2^8 times larger. Below -88.7, where e^-x leaves binary32, the result is 0
+// (g times it would be under 2.7e-37).
+__device__ __forceinline__ float sigmoid(float x) {
+    return 0x1p-8f * reciprocal(fmaf(exp_fast(-x), 0x1p-8f, 0x1p-8f));
+}
 
 // The normal distribution function: erfc(z) = t exp(-z^2 + p(t)), t = 1 / (1 + z/2), z >= 0, with
 // the Chebyshev fit p of Press, Flannery, Teukolsky and Vetterling (Numerical Recipes, section 6.2:
 // relative error below 1.2e-7 everywhere; in binary32 4e-6 up to |g| = 6, from the exponent's
 // rounding). 1 + erf would lose its digits where it cancels, 1e-3 of the value already at -4; the
-// library's normcdff took 2 us more of a call over 777 x 1001 x 2721.
+// library's normcdff took 2 us more of a call over 777 x 1001 x 2721. 0 below g = -12.9, where the
+// exponential leaves the normal range (g times it would be under 1.5e-38).
 __device__ __forceinline__ float normal_cdf(float g) {
     const float z = fabsf(g) * 0.7071067811865476f, t = reciprocal(fmaf(0.5f, z, 1.0f));
     float p = fmaf(t, 0.17087277f, -0.82215223f);

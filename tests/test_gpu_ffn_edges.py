@@ -73,3 +73,33 @@ def test_gates_up_to_the_largest(act, m, odd):
     assert torch.equal(hidden, value)
     assert torch.equal(du, value)
     assert torch.equal(dg, slope)
+
+
+def off_by(got, want):
+    return ((got.double() - want).abs() / want.abs()).max().item()
+
+
+@pytest.mark.parametrize("m,odd", ROUTES)
+def test_silu_where_the_sigmoid_is_subnormal(m, odd):
+    """Gates from -87.3 down to -88.7: the sigmoid is below 2^-126, its product with the gate is not.
+    Error: bfloat16's rounding (2^-8), and the exponent's in binary32 (up to 128 * 2^-24 * ln 2)
+    with the instructions' 2^-22: below 2^-16 in all."""
+    t, hidden, dg, du = block_of_gates("silu", [[-g] for g in (88.5, 88.0, 87.5, 87.0, 80.0)], m,
+                                       odd)
+    g = t[:, 0]
+    s = torch.exp(g) / (1 + torch.exp(g))
+    tol = 2.0 ** -8 + 2.0 ** -16
+    assert off_by(hidden, g * s) <= tol
+    assert off_by(du, g * s) <= tol
+    assert off_by(dg, s * (1 + g * (1 - s))) <= tol
+
+
+@pytest.mark.parametrize("m,odd", ROUTES)
+def test_tanh_gelu_where_the_sigmoid_is_subnormal(m, odd):
+    """The same of the sigmoid in tanh GELU, between two bfloat16 gates: -10 - 1/32 and their like.
+    The argument, about 88, takes five roundings more: 2^-14 in all."""
+    terms = [[-10.0, -1 / 32], [-10.0, -3 / 64], [-10.0, 1 / 32]]
+    t, hidden, _, _ = block_of_gates("gelu_tanh", terms, m, odd)
+    g = t.sum(1)
+    z = math.sqrt(8 / math.pi) * (g + 0.044715 * g ** 3)
+    assert off_by(hidden, g * torch.exp(z) / (1 + torch.exp(z))) <= 2.0 ** -8 + 2.0 ** -14
