@@ -91,9 +91,11 @@ struct alignas(sizeof(T) * kN) Vec {
 };
 
 // Priorities in L2. When the list is read twice (clipping), the first pass reads the entries before
-// the last 48 MB so that they are the first to leave, and those so that they stay for the second
-// pass, which starts with them and lets them go, and whose results leave before them: 411M bf16
-// entries 495 -> 482 us, 25.6M binary32 entries 53.1 -> 52.0 (32 and 64 MB: within 1%).
+// the last 48 MB so that they are the first to leave, and those at the normal priority; the second
+// pass starts with them, and reads everything for the last time. No line is kept above the normal
+// priority (evict_last): nothing takes that back, and the work behind the call would find so much
+// less of L2 (six passes over 90 MB: 145 us for 112), for 0.4 to 2 us of the call's own. Against one
+// priority for all: 411M bf16 entries 493 -> 483 us, 25.6M binary32 entries 49.9 -> 48.0.
 constexpr uint32_t kKeepTiles = (48u << 20) / kTileBytes;
 
 __device__ __forceinline__ uint64_t l2_first() {
@@ -104,11 +106,6 @@ __device__ __forceinline__ uint64_t l2_first() {
 __device__ __forceinline__ uint64_t l2_normal() {
     uint64_t p;
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
-    return p;
-}
-__device__ __forceinline__ uint64_t l2_last() {
-    uint64_t p;
-    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
     return p;
 }
 template <typename T, int kN>
@@ -230,7 +227,7 @@ __global__ void __launch_bounds__(kGradThreads, kBlocksPerSm)
     const uint32_t* first = a.entries ? a.first : tab.first;
     const uint32_t step = gridDim.x * kGradWarps;
     const uint32_t leave = a.twice && a.tiles > kKeepTiles ? a.tiles - kKeepTiles : 0;
-    const uint64_t early = l2_first(), late = a.twice ? l2_last() : l2_normal();
+    const uint64_t early = l2_first(), late = l2_normal();
     double sum = 0.0;
     uint32_t t = blockIdx.x * kGradWarps + (threadIdx.x >> 5);
     if (t < a.tiles) {
