@@ -1782,7 +1782,7 @@ uint64_t wgrad_workspace(uint64_t rows, uint64_t cols, uint64_t tokens) {
     const WgradPlan p = wgrad_plan(rows, cols, tokens);
     if (p.parts < 2) return 0;
     const uint64_t tile = p.cut.pairs ? 2 * kBlockM : kBlockM;
-    return p.parts * (rows + tile - 1) / tile * tile * ((cols + 3) & ~3ull) * sizeof(float);
+    return p.parts * (ceil_div(rows, tile) * tile) * ((cols + 3) & ~3ull) * sizeof(float);
 }
 
 }  // namespace
