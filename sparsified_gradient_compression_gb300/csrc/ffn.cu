@@ -1903,7 +1903,7 @@ extern "C" int dgc_ffn_weight_grad(const dgc_matrix* dy, const dgc_matrix* x, in
     if (dw->rows == 0 || dw->cols == 0) return DGC_OK;
     if (!dw->data || ((uintptr_t)dw->data & 3u) || (dw->rows > 1 && dw->ld < dw->cols))
         return DGC_EINVAL;
-    if (dw->ld > (1ll << 36)) return DGC_EUNSUPPORTED;
+    if (dw->rows > 1 && dw->ld > (1ll << 36)) return DGC_EUNSUPPORTED;
     const uint64_t rows = my.cols, cols = mx.cols, tokens = my.rows;
     const uint64_t need = wgrad_workspace(rows, cols, tokens);
     if (ws_bytes < need || (need && (!ws || ((uintptr_t)ws & 255u)))) return DGC_EINVAL;

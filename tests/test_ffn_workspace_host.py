@@ -37,3 +37,13 @@ def test_wide_parts_ask_for_their_tiles_alone(L, rows):
     part = 512 * cols * 4
     need = dgc.dgc_ffn_weight_grad_workspace(rows, cols, tokens)
     assert need % part == 0 and 2 <= need // part <= tokens // 2048
+
+
+@pytest.mark.parametrize("ld", [0, -5, 24, 2**37, 2**62])
+def test_a_single_row_has_no_row_to_row_distance(L, ld):
+    """dw's ld is not read where it has one row: what is missing is the workspace alone."""
+    tokens, cols = 1 << 16, 24
+    assert dgc.dgc_ffn_weight_grad_workspace(1, cols, tokens) > 0
+    rc = L.dgc_ffn_weight_grad(mat(tokens, 1), mat(tokens, cols), 0, mat(1, cols, ld, dgc.F32),
+                               FAKE, None, 0, None)
+    assert rc == dgc.EINVAL

@@ -103,3 +103,14 @@ def test_tanh_gelu_where_the_sigmoid_is_subnormal(m, odd):
     g = t.sum(1)
     z = math.sqrt(8 / math.pi) * (g + 0.044715 * g ** 3)
     assert off_by(hidden, g * torch.exp(z) / (1 + torch.exp(z))) <= 2.0 ** -8 + 2.0 ** -14
+
+
+@pytest.mark.parametrize("ld", [0, 2**62])
+def test_a_weight_gradient_of_one_row(ld):
+    dy = torch.full((3, 8), 2.0, dtype=BF16, device="cuda")[:, :1]
+    x = torch.arange(72, device="cuda").view(3, 24).to(BF16)
+    flat, st = torch.full((32,), 7.0, device="cuda"), status_word()
+    dgc.dgc_ffn_weight_grad(dy, x, dgc.dgc_matrix(flat.data_ptr(), 1, 24, ld, dgc.F32, 0), False,
+                            st, None)
+    assert torch.equal(flat[:24], 2 * x.float().sum(0)) and flat[24:].eq(7.0).all()
+    assert dgc.dgc_read_status(st) == 0
