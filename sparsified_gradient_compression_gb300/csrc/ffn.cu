@@ -1388,11 +1388,19 @@ int make_map(CUtensorMap* map, const Mat& m, uint32_t bc, uint32_t br) {
     const CUtensorMapDataType type = m.dtype == DGC_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                      : m.dtype == DGC_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                           : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    const CUresult r = fn(map, type, 2, m.p, dims, strides, box, step,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          bc * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    auto encode = [&] {
+        return fn(map, type, 2, m.p, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  bc * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = encode();
+    if (r == CUDA_ERROR_INVALID_CONTEXT) {
+        // A driver call, in a thread whose first CUDA call this is: the runtime makes the device's
+        // context the thread's own at the first of its calls that needs one.
+        cudaFuncAttributes at;
+        if (cudaFuncGetAttributes(&at, k_wgrad_zero) != cudaSuccess) cudaGetLastError();
+        r = encode();
+    }
     return r == CUDA_SUCCESS ? DGC_OK : DGC_ECUDA;
 }
 

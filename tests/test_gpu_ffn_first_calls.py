@@ -1,0 +1,81 @@
+"""The feed-forward calls' first use of a device, each case in a process of its own."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+import sparsified_gradient_compression_gb300 as dgc
+
+pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+SETUP = """
+import sys
+sys.path.insert(0, sys.argv[1])
+import torch
+import sparsified_gradient_compression_gb300 as dgc
+
+dgc.lib()
+gen = torch.Generator(device="cuda").manual_seed(1)
+
+def rand(r, c, s=1.0):
+    return (torch.randn(r, c, generator=gen, device="cuda") * s).bfloat16()
+
+def status_word():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+"""
+
+OTHER_THREAD = SETUP + """
+import threading
+
+def calls():
+    st, out = status_word(), []
+    for m in (1, 3, 300):
+        x, dy = rand(m, 64), rand(m, 64)
+        wg, wu, wd = rand(128, 64), rand(128, 64), rand(64, 128)
+        hidden, gate, up, dg, du = (rand(m, 128) for _ in range(5))
+        y, dx, dw = torch.empty_like(x), torch.empty_like(x), torch.empty(128, 64, device="cuda")
+        a = dict(gate=(dgc.dgc_ffn_gate, x, wg, wu, dgc.ACT_SILU, hidden, gate, up, st),
+                 down=(dgc.dgc_ffn_down, hidden, wd, x, y, st),
+                 down_backward=(dgc.dgc_ffn_down_backward, dy, wd, gate, up, dgc.ACT_SILU, dg, du,
+                                st),
+                 gate_backward=(dgc.dgc_ffn_gate_backward, dg, du, wg, wu, dy, dx, st),
+                 weight_grad=(dgc.dgc_ffn_weight_grad, dg, x, dw, False, st, None))
+        out += [(m, name, *call) for name, call in a.items()]
+    return out, st
+
+todo, st = calls()
+if WARM:
+    for _, _, f, *args in todo:
+        f(*args)
+torch.cuda.synchronize()
+errors = []
+
+def call(m, name, f, *args):
+    try:
+        f(*args)
+    except Exception as e:
+        errors.append((m, name, str(e)))
+
+for t in todo:  # a new thread for every call
+    thread = threading.Thread(target=call, args=t)
+    thread.start()
+    thread.join()
+torch.cuda.synchronize()
+assert not errors, errors
+assert dgc.dgc_read_status(st) == 0
+"""
+
+
+def run(code):
+    dgc.build()
+    r = subprocess.run([sys.executable, "-c", code, ROOT], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("warm", [False, True])
+def test_calls_from_threads_that_made_no_cuda_call_before(warm):
+    run(OTHER_THREAD.replace("WARM", str(warm)))
