@@ -23,6 +23,8 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
+#include <mutex>
 
 #include "dgc_device.cuh"
 
@@ -1424,14 +1426,18 @@ struct Slots {
 };
 constexpr Slots kFullSlots = {{0, 152, 76, 46, 36, 28, 23, 15, 15}};
 
-// The shared-memory limit of every form of the kernel, and the slots, once per device.
+// The shared-memory limit of every form of the kernel, and the slots, once per device; the first
+// calls may come from several threads.
 int ffn_device(const Slots** slots) {
-    static bool known[128] = {false};
+    static std::atomic<bool> known[128];
+    static std::mutex first;
     static Slots table[128];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return DGC_ECUDA;
     *slots = &table[dev];
-    if (known[dev]) return DGC_OK;
+    if (known[dev].load(std::memory_order_acquire)) return DGC_OK;
+    std::lock_guard<std::mutex> lock(first);
+    if (known[dev].load(std::memory_order_relaxed)) return DGC_OK;
     bool ok = raise_smem_all<kGate>() && raise_smem_all<kDown>() && raise_smem_all<kDownBwd>() &&
               raise_smem_all<kGateBwd>() && raise_smem_all<kWGrad>();
     for (unsigned size = 1; ok && size <= 8; ++size) {
@@ -1453,7 +1459,7 @@ int ffn_device(const Slots** slots) {
         cudaGetLastError();
         return DGC_ECUDA;
     }
-    known[dev] = true;
+    known[dev].store(true, std::memory_order_release);
     return DGC_OK;
 }
 

@@ -69,6 +69,42 @@ assert dgc.dgc_read_status(st) == 0
 """
 
 
+THREADS = SETUP + """
+import threading
+
+# shapes that the cost model cuts into clusters by what the device holds of them
+sets = []
+for m, n, k in ((100, 1024, 4096), (40, 512, 8192), (700, 1024, 4096), (256, 2048, 2048)) * 3:
+    sets.append((rand(m, k), rand(n, k, k ** -0.5), torch.empty(m, n, dtype=torch.bfloat16,
+                                                                device="cuda"),
+                 torch.cuda.Stream(), status_word()))
+torch.cuda.synchronize()
+gate = threading.Barrier(len(sets))
+errors = []
+
+def first_call(s):
+    try:
+        with torch.cuda.stream(s[3]):
+            gate.wait()
+            dgc.dgc_ffn_down(s[0], s[1], None, s[2], s[4])
+    except Exception as e:
+        errors.append(e)
+
+threads = [threading.Thread(target=first_call, args=(s,)) for s in sets]
+for t in threads:
+    t.start()
+for t in threads:
+    t.join()
+torch.cuda.synchronize()
+assert not errors, errors
+for h, w, y, _, st in sets:
+    again = torch.empty_like(y)
+    dgc.dgc_ffn_down(h, w, None, again, st)
+    assert dgc.dgc_read_status(st) == 0
+    assert torch.equal(y, again)
+"""
+
+
 def run(code):
     dgc.build()
     r = subprocess.run([sys.executable, "-c", code, ROOT], capture_output=True, text=True,
@@ -79,3 +115,8 @@ def run(code):
 @pytest.mark.parametrize("warm", [False, True])
 def test_calls_from_threads_that_made_no_cuda_call_before(warm):
     run(OTHER_THREAD.replace("WARM", str(warm)))
+
+
+def test_first_calls_from_several_threads():
+    """The same bits as from calls one after the other, later."""
+    run(THREADS)
