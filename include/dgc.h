@@ -407,7 +407,7 @@ enum { DGC_ACT_SILU = 0, DGC_ACT_GELU = 1, DGC_ACT_GELU_TANH = 2, DGC_ACT_RELU =
  * Entries that are not finite go through the sums as they do in IEEE arithmetic. Extents above
  * 2^24 return DGC_EUNSUPPORTED. Every result is deterministic. The calls enqueue kernels only
  * (programmatic dependent launches) and can be captured into a CUDA graph after one ordinary call
- * of any of them on the device. */
+ * of any of them on the device that had something to do. */
 
 /* hidden = act(x w_gate^T) o (x w_up^T), M x F, in one kernel; gate and up (both or neither,
  * NULL): x w_gate^T and x w_up^T, for the backward pass. */

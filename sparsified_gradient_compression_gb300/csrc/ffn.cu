@@ -1426,8 +1426,9 @@ struct Slots {
 };
 constexpr Slots kFullSlots = {{0, 152, 76, 46, 36, 28, 23, 15, 15}};
 
-// The shared-memory limit of every form of the kernel, and the slots, once per device; the first
-// calls may come from several threads.
+// The shared-memory limit of every form of the kernel, the slots and the driver's entry point, once
+// per device, by the first call that has work, whichever route it takes: the header promises that a
+// capture after it only enqueues. First calls may come from several threads.
 int ffn_device(const Slots** slots) {
     static std::atomic<bool> known[128];
     static std::mutex first;
@@ -1438,6 +1439,7 @@ int ffn_device(const Slots** slots) {
     if (known[dev].load(std::memory_order_acquire)) return DGC_OK;
     std::lock_guard<std::mutex> lock(first);
     if (known[dev].load(std::memory_order_relaxed)) return DGC_OK;
+    encode_fn();
     bool ok = raise_smem_all<kGate>() && raise_smem_all<kDown>() && raise_smem_all<kDownBwd>() &&
               raise_smem_all<kGateBwd>() && raise_smem_all<kWGrad>();
     for (unsigned size = 1; ok && size <= 8; ++size) {
@@ -1661,6 +1663,9 @@ int rows_product(Product p0, const Product* p1, const Mat* b_up, const Mat* in0,
     constexpr bool kAcrossB = kKind == kDownBwd || kKind == kGateBwd;
     const int sms = dgc_internal_sm_count();
     if (sms <= 0) return DGC_ECUDA;
+    const Slots* slots;
+    int rc = ffn_device(&slots);
+    if (rc) return rc;
     const Mat* const outs[3] = {out0, out1, out2};
     if constexpr (kKind == kGate || kKind == kDown)
         if (out0->rows <= kFewTokens && !test_wait_ms)
@@ -1700,9 +1705,6 @@ int rows_product(Product p0, const Product* p1, const Mat* b_up, const Mat* in0,
         a.residual = in0 != nullptr;
         return launch_any<kKind>(a, out0->dtype, reinterpret_cast<cudaStream_t>(stream));
     }
-    const Slots* slots;
-    int rc = ffn_device(&slots);
-    if (rc) return rc;
     FfnArgs a{};
     if (test_wait_ms) {  // the self-test: the second slice never arrives
         a.wait_ns = test_wait_ms * 1000000ull;
@@ -1923,6 +1925,8 @@ extern "C" int dgc_ffn_weight_grad(const dgc_matrix* dy, const dgc_matrix* x, in
     if (ws_bytes < need || (need && (!ws || ((uintptr_t)ws & 255u)))) return DGC_EINVAL;
     const int sms = dgc_internal_sm_count();
     if (sms <= 0) return DGC_ECUDA;
+    const Slots* slots;  // the plan does not go by them
+    if ((rc = ffn_device(&slots))) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     auto launched = [] {
         if (cudaPeekAtLastError() != cudaSuccess) {
@@ -1960,8 +1964,6 @@ extern "C" int dgc_ffn_weight_grad(const dgc_matrix* dy, const dgc_matrix* x, in
     a.kb0 = a.kb = ceil_div(tokens, kBlockK);
     a.status = status;
     if ((rc = make_map(&a.a0, my, 64, kBlockK)) || (rc = make_map(&a.b0, mx, 64, kBlockK))) return rc;
-    const Slots* slots;  // the plan does not go by them
-    if ((rc = ffn_device(&slots))) return rc;
     const WgradPlan wp = wgrad_plan(rows, cols, tokens);
     const Plan plan = wp.cut;
     const uint32_t parts = wp.parts;

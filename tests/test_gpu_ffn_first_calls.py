@@ -105,6 +105,53 @@ for h, w, y, _, st in sets:
 """
 
 
+CAPTURE = SETUP + """
+st = status_word()
+x, wg, wu, wd = rand(300, 64), rand(128, 64, 0.1), rand(128, 64, 0.1), rand(64, 128, 0.1)
+hidden, gate, up, dg, du = (rand(300, 128) for _ in range(5))
+y, dx, dw = torch.empty_like(x), torch.empty_like(x), torch.empty(128, 64, device="cuda")
+odd = torch.zeros(300, 65, device="cuda").bfloat16()[:, :64]
+odd.copy_(x)
+long = rand(65536, 32)
+ws = torch.empty(dgc.dgc_ffn_weight_grad_workspace(32, 32, 65536), dtype=torch.uint8, device="cuda")
+assert ws.numel() > 0
+dw2, one = torch.empty(32, 32, device="cuda"), torch.empty(1, 128, device="cuda").bfloat16()
+nothing = torch.empty(0, 128, device="cuda").bfloat16()
+first = {
+    "one token": lambda: dgc.dgc_ffn_gate(x[:1], wg, wu, 0, one, None, None, st),
+    "odd rows": lambda: dgc.dgc_ffn_gate(odd, wg, wu, 0, hidden, None, None, st),
+    "odd weight gradient": lambda: dgc.dgc_ffn_weight_grad(dg, odd, dw, False, st, None),
+    "no tokens": lambda: dgc.dgc_ffn_weight_grad(nothing, x[:0], dw, False, st, None),
+}[FIRST]
+torch.cuda.synchronize()
+first()
+torch.cuda.synchronize()
+
+def step():
+    dgc.dgc_ffn_gate(x, wg, wu, dgc.ACT_GELU, hidden, gate, up, st)
+    dgc.dgc_ffn_down(hidden, wd, x, y, st)
+    dgc.dgc_ffn_down_backward(x, wd, gate, up, dgc.ACT_GELU, dg, du, st)
+    dgc.dgc_ffn_gate_backward(dg, du, wg, wu, x, dx, st)
+    dgc.dgc_ffn_weight_grad(dg, x, dw, False, st, None)
+    dgc.dgc_ffn_weight_grad(long, long, dw2, False, st, ws)
+    return hidden, gate, up, y, dg, du, dx, dw, dw2
+
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    outs = step()
+for t in outs:
+    t.fill_(7.0)
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in outs]
+for t in outs:
+    t.fill_(7.0)
+step()
+assert all(torch.equal(a, b) for a, b in zip(got, outs))
+assert dgc.dgc_read_status(st) == 0
+"""
+
+
 def run(code):
     dgc.build()
     r = subprocess.run([sys.executable, "-c", code, ROOT], capture_output=True, text=True,
@@ -120,3 +167,8 @@ def test_calls_from_threads_that_made_no_cuda_call_before(warm):
 def test_first_calls_from_several_threads():
     """The same bits as from calls one after the other, later."""
     run(THREADS)
+
+
+@pytest.mark.parametrize("first", ["one token", "odd rows", "odd weight gradient", "no tokens"])
+def test_capture_after_one_call_of_another_form(first):
+    run(CAPTURE.replace("FIRST", repr(first)))
