@@ -202,6 +202,24 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+def _on_host(t) -> bool:
+    """Whether t, which is not a CUDA tensor, has entries that no kernel may be sent to."""
+    return t.numel() != 0 and not t.is_pinned()
+
+
+def _refuse_host(what: str):
+    raise DGCError(EINVAL, f"host tensor as {what}")
+
+
+def _gpu(t, what: str) -> int | None:
+    """_ptr of what the caller says is on the GPU."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_cuda and _on_host(t):
+        _refuse_host(what)
+    return t.data_ptr()
+
+
 _get_raw_stream = None
 
 
@@ -483,12 +501,23 @@ class TensorList:
         self.tensors = list(tensors)
         self.array = (dgc_tensor * max(len(self.tensors), 1))()
         size = ctypes.sizeof(dgc_tensor)
+        host = None
         for i, t in enumerate(self.tensors):
             if not t.is_contiguous():
                 raise DGCError(EINVAL, f"TensorList: tensor {i} is not contiguous")
             struct.pack_into("=Qqii", self.array, i * size, t.data_ptr(), t.numel(),
                              _dtype_code(t), 0)
-        self.address = ctypes.addressof(self.array)
+            if not t.is_cuda and _on_host(t):
+                host = i
+        if host is None:
+            self.address = ctypes.addressof(self.array)
+        else:
+            self.host = host
+
+    def __getattr__(self, name):  # what is not set: a list with a host tensor has no address
+        if name == "address" and "host" in self.__dict__:
+            _refuse_host(f"entry {self.host} of a list")
+        raise AttributeError(name)
 
     def __len__(self):
         return len(self.tensors)
@@ -496,7 +525,7 @@ class TensorList:
 
 def dgc_grad_workspace(src: TensorList) -> int:
     out = ctypes.c_size_t(0)
-    _check(lib().dgc_grad_workspace(src.address, len(src), ctypes.byref(out)),
+    _check(lib().dgc_grad_workspace(ctypes.addressof(src.array), len(src), ctypes.byref(out)),
            "dgc_grad_workspace")
     return out.value
 
@@ -505,22 +534,23 @@ def dgc_grad_norm(src: TensorList, max_norm: float, norm, scale, ws, ws_bytes: i
                   stream=None) -> int:
     """norm, scale: float32 CUDA tensors (1): the global L2 norm of src's tensors, and the factor
     that clips them to max_norm."""
-    ws_bytes = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
-    return _check(lib().dgc_grad_norm(src.address, len(src), float(max_norm), _ptr(norm),
-                                      _ptr(scale), _ptr(ws), int(ws_bytes), _stream(stream)),
-                  "dgc_grad_norm")
+    ws_bytes = ws.nbytes if ws_bytes is None else ws_bytes
+    return _check(lib().dgc_grad_norm(src.address, len(src), float(max_norm), _gpu(norm, "norm"),
+                                      _gpu(scale, "scale"), _gpu(ws, "ws"), int(ws_bytes),
+                                      _stream(stream)), "dgc_grad_norm")
 
 
 def dgc_grad_clip(src: TensorList, dst: TensorList | None, max_norm: float, norm, scale, ws,
                   ws_bytes: int | None = None, stream=None) -> int:
     """dgc_grad_norm, then dst = src * scale (dst None: in place). With dst the pieces of a flat
     float32 buffer, the clipped gradients land where dgc_compress reads them."""
-    ws_bytes = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    ws_bytes = ws.nbytes if ws_bytes is None else ws_bytes
     if dst is not None and len(dst) != len(src):
         raise DGCError(EINVAL, "dgc_grad_clip: lists of different lengths")
     return _check(lib().dgc_grad_clip(src.address, None if dst is None else dst.address, len(src),
-                                      float(max_norm), _ptr(norm), _ptr(scale), _ptr(ws),
-                                      int(ws_bytes), _stream(stream)), "dgc_grad_clip")
+                                      float(max_norm), _gpu(norm, "norm"), _gpu(scale, "scale"),
+                                      _gpu(ws, "ws"), int(ws_bytes), _stream(stream)),
+                  "dgc_grad_clip")
 
 
 # ------------------------------------------------------------- gated feed-forward block
@@ -528,12 +558,17 @@ class Matrix(dgc_matrix):
     """A dgc_matrix that keeps its tensor alive and knows its own address."""
 
 
+class _HostMatrix(dgc_matrix):
+    """The view of a tensor that is not on the GPU; the calls refuse it."""
+
+
 def matrix(t) -> Matrix:
     """The C view of a two-dimensional tensor whose rows are contiguous. The calls below build it
     from the tensors they get; a program with fixed buffers builds it once."""
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise DGCError(EINVAL, "matrix: a two-dimensional tensor with contiguous rows is wanted")
-    m = Matrix(t.data_ptr(), t.shape[0], t.shape[1], t.stride(0), _dtype_code(t), 0)
+    kind = Matrix if t.is_cuda or not _on_host(t) else _HostMatrix
+    m = kind(t.data_ptr(), t.shape[0], t.shape[1], t.stride(0), _dtype_code(t), 0)
     m.tensor = t
     m.address = ctypes.addressof(m)
     return m
@@ -544,35 +579,40 @@ def _mat(m):
         return m.address
     if m is None:
         return None
-    return ctypes.byref(m if isinstance(m, dgc_matrix) else matrix(m))
+    if not isinstance(m, dgc_matrix):
+        m = matrix(m)
+    if type(m) is _HostMatrix:
+        _refuse_host("a matrix")
+    return ctypes.byref(m)
 
 
 def dgc_ffn_gate(x, w_gate, w_up, act: int, hidden, gate, up, status, stream=None) -> int:
     """hidden = act(x w_gate^T) o (x w_up^T); gate, up: the two products, or None. Every matrix:
     a float16 or bfloat16 CUDA tensor, or its matrix() view."""
     return _check(lib().dgc_ffn_gate(_mat(x), _mat(w_gate), _mat(w_up), int(act), _mat(hidden),
-                                     _mat(gate), _mat(up), _ptr(status), _stream(stream)),
-                  "dgc_ffn_gate")
+                                     _mat(gate), _mat(up), _gpu(status, "status"),
+                                     _stream(stream)), "dgc_ffn_gate")
 
 
 def dgc_ffn_down(hidden, w_down, residual, y, status, stream=None) -> int:
     """y = hidden w_down^T + residual (or None)."""
     return _check(lib().dgc_ffn_down(_mat(hidden), _mat(w_down), _mat(residual), _mat(y),
-                                     _ptr(status), _stream(stream)), "dgc_ffn_down")
+                                     _gpu(status, "status"), _stream(stream)), "dgc_ffn_down")
 
 
 def dgc_ffn_down_backward(dy, w_down, gate, up, act: int, d_gate, d_up, status,
                           stream=None) -> int:
     """d_gate, d_up: the gradients of gate and up, from dy."""
     return _check(lib().dgc_ffn_down_backward(_mat(dy), _mat(w_down), _mat(gate), _mat(up),
-                                              int(act), _mat(d_gate), _mat(d_up), _ptr(status),
-                                              _stream(stream)), "dgc_ffn_down_backward")
+                                              int(act), _mat(d_gate), _mat(d_up),
+                                              _gpu(status, "status"), _stream(stream)),
+                  "dgc_ffn_down_backward")
 
 
 def dgc_ffn_gate_backward(d_gate, d_up, w_gate, w_up, residual, dx, status, stream=None) -> int:
     """dx = d_gate w_gate + d_up w_up + residual (or None)."""
     return _check(lib().dgc_ffn_gate_backward(_mat(d_gate), _mat(d_up), _mat(w_gate), _mat(w_up),
-                                              _mat(residual), _mat(dx), _ptr(status),
+                                              _mat(residual), _mat(dx), _gpu(status, "status"),
                                               _stream(stream)), "dgc_ffn_gate_backward")
 
 
@@ -588,9 +628,9 @@ def dgc_ffn_weight_grad(dy, x, dw, accumulate: bool, status, ws, ws_bytes: int |
                         stream=None) -> int:
     """dw (float32) = dy^T x, or dw + dy^T x; ws may be None where the workspace query says 0."""
     if ws_bytes is None:
-        ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+        ws_bytes = 0 if ws is None else ws.nbytes
     return _check(lib().dgc_ffn_weight_grad(_mat(dy), _mat(x), int(bool(accumulate)), _mat(dw),
-                                            _ptr(status), _ptr(ws), int(ws_bytes),
+                                            _gpu(status, "status"), _gpu(ws, "ws"), int(ws_bytes),
                                             _stream(stream)), "dgc_ffn_weight_grad")
 
 
@@ -631,6 +671,7 @@ def dgc_selftest_wait_timeout(status, spin_limit: int, stream=None) -> int:
 
 
 def dgc_selftest_ffn_timeout(hidden, w_down, y, status, wait_ms: int, stream=None) -> int:
-    return _check(lib().dgc_selftest_ffn_timeout(_mat(hidden), _mat(w_down), _mat(y), _ptr(status),
-                                                 int(wait_ms), _stream(stream)),
+    return _check(lib().dgc_selftest_ffn_timeout(_mat(hidden), _mat(w_down), _mat(y),
+                                                 _gpu(status, "status"), int(wait_ms),
+                                                 _stream(stream)),
                   "dgc_selftest_ffn_timeout")
