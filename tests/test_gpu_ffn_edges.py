@@ -114,3 +114,38 @@ def test_a_weight_gradient_of_one_row(ld):
                             st, None)
     assert torch.equal(flat[:24], 2 * x.float().sum(0)) and flat[24:].eq(7.0).all()
     assert dgc.dgc_read_status(st) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, BF16])
+@pytest.mark.parametrize("m", [1, 2])
+@pytest.mark.parametrize("d,f", [(65, 300), (257, 511), (1027, 333), (3000, 2049), (4095, 70),
+                                 (4901, 2603)])
+def test_one_and_two_tokens_off_16_byte_boundaries(d, f, m, dtype):
+    """Long sums read entry by entry: steps of 256 entries with a short last one, a sum in eight parts
+    and, from 2432 rows of weights on (4864 of the down projection's), in one."""
+    from test_gpu_ffn import ACTS as names, forward
+
+    forward(m, d, f, list(names)[(d + f) % 4], dtype, d, "odd", m == 2, d % 2 == 1)
+
+
+@pytest.mark.parametrize("m", [1, 2])
+@pytest.mark.parametrize("which", range(3))
+def test_one_operand_of_few_tokens_off_16_byte_boundaries(which, m):
+    """x, the gate's and the up projection's weights in turn, within the roundings of the sums of
+    those that all lie on them."""
+    gen = torch.Generator(device="cuda").manual_seed(which)
+    k, f = 1999, 301
+    t = [(torch.randn(r, k, generator=gen, device="cuda") * s).to(BF16)
+         for r, s in ((m, 1.0), (f, k ** -0.5), (f, k ** -0.5))]
+    st, outs = status_word(), []
+    for off in (which, None):
+        x, wg, wu = (rows(a, i == off) for i, a in enumerate(t))
+        out = [torch.empty(m, f, dtype=BF16, device="cuda") for _ in range(3)]
+        dgc.dgc_ffn_gate(x, wg, wu, dgc.ACT_RELU, *out, st)
+        outs.append([o.double() for o in out])
+    assert dgc.dgc_read_status(st) == 0
+    x, wg, wu = (a.double() for a in t)
+    for i, w in ((1, wg), (2, wu)):  # two binary32 sums, each rounded: K 2^-23 of the terms, a unit
+        terms = x.abs() @ w.abs().t()
+        assert ((outs[0][i] - outs[1][i]).abs()
+                <= 2 * k * 2.0 ** -23 * terms + 2.0 ** -7 * outs[1][i].abs()).all()
