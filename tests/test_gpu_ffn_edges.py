@@ -149,3 +149,24 @@ def test_one_operand_of_few_tokens_off_16_byte_boundaries(which, m):
         terms = x.abs() @ w.abs().t()
         assert ((outs[0][i] - outs[1][i]).abs()
                 <= 2 * k * 2.0 ** -23 * terms + 2.0 ** -7 * outs[1][i].abs()).all()
+
+
+@pytest.mark.parametrize("tokens,cols,shift,odd", [
+    (8, 64, 0, False),       # added by the bulk reduction
+    (8, 61, 0, False),       # its last columns one by one
+    (8, 64, 1, False),       # every column
+    (8, 64, 0, True),        # on the ordinary cores
+    (1 << 16, 64, 0, False)])  # by the parts' join
+def test_subnormal_sums_are_kept(tokens, cols, shift, odd):
+    """dw = 2^-130 + 2^-130 and 1.5 * 2^-126 - 2^-126, exact on every route of the addition."""
+    for start, left, right, want in ((2.0 ** -130, 2.0 ** -65, 2.0 ** -65, 2.0 ** -129),
+                                     (1.5 * 2.0 ** -126, -2.0 ** -63, 2.0 ** -63, 2.0 ** -127)):
+        dy, x = torch.zeros(tokens, 64, dtype=BF16), torch.zeros(tokens, cols, dtype=BF16)
+        dy[tokens // 2], x[tokens // 2] = left, right
+        flat = torch.full((64 * 64 + 8,), start, device="cuda")
+        dw, st = flat[shift:shift + 64 * 64].view(64, 64)[:, :cols], status_word()
+        ws = torch.empty(max(1, dgc.dgc_ffn_weight_grad_workspace(64, cols, tokens)),
+                         dtype=torch.uint8, device="cuda")
+        dgc.dgc_ffn_weight_grad(rows(dy, odd), rows(x, odd), dw, True, st, ws)
+        assert dgc.dgc_read_status(st) == 0
+        assert torch.equal(dw.double().cpu(), torch.full((64, cols), want, dtype=torch.float64))
