@@ -8,7 +8,11 @@
 //   gate_backward dx = dG Wg + dU Wu + r                     one sum over both products
 //   weight_grad   dW = dy^T x, binary32, or dW += dy^T x
 //
-// One kernel, k_ffn, for all five. A persistent block per SM computes 128-row output tiles:
+// Three routes. Forward products of one or two tokens are read by warps that stream the weights
+// (k_rows); products with an operand, or an input of the epilogue, whose rows lie off 16-byte
+// boundaries go to the ordinary cores (k_any); all others, of each of the five kinds, are k_ffn's.
+//
+// k_ffn: a persistent block per SM computes 128-row output tiles:
 // warp 0 brings the operands' 64-deep slices by TMA into a ring of shared-memory stages, warp 1
 // issues tcgen05.mma on them into one of two accumulators in tensor memory, warps 2-9 empty the
 // other one: tcgen05.ld, the epilogue's arithmetic in binary32, one rounding, and a TMA store
@@ -41,8 +45,10 @@ constexpr uint32_t kStageA = kBlockM * kBlockK * 2;
 constexpr int kMaxStages = 8;
 // The weight gradient's long sums leave the tensor cores every 12 slices (768 tokens) and are added
 // up in registers, rounded to nearest: the tensor cores' own accumulation cuts bits off, which
-// over 8192 tokens in one go took 9e-6 of the gradient's norm (a product in binary32: 1e-6), and
-// over 768 takes at most 9.5e-7, however many follow. Costs 2% at 8192 tokens x 11264 x 4096.
+// over 8192 tokens in one go took 9e-6 of the gradient's norm. Measured so, as a share of its norm:
+// 7.3e-7 over 768 tokens, 7.2e-7 over 8192, 1.0e-6 over 2^20 (products of one sign: 1.5e-6; the
+// additions' own share grows as the root of the tokens, 2.6e-6 at 2^24). A product in binary32 took
+// 2e-7 over 768 tokens and 1.4e-6 over 2^20. Costs 2% at 8192 tokens x 11264 x 4096.
 constexpr uint32_t kSumSlices = 12;
 
 constexpr uint32_t kSmemLimit = 232448;        // 227 KB
@@ -722,7 +728,8 @@ __device__ __forceinline__ void epilogue(const FfnArgs& a, FfnShared* sh, char* 
 }
 
 // The weight gradient's: every kSumSlices slices the accumulator is added to this warp's sums in
-// registers (up to four chunks), which are the tile's result at its end.
+// registers (up to four chunks), which are the tile's result at its end. 128 of the 168 registers
+// hold sums; 20 to 36 bytes a thread are spilled.
 template <int kCg, bool kSplit>
 __device__ __forceinline__ void epilogue_sums(const FfnArgs& a, FfnShared* sh, char* parts,
                                               char* staging, uint32_t tmem, uint32_t rank) {
@@ -808,7 +815,7 @@ __device__ __forceinline__ void epilogue_sums(const FfnArgs& a, FfnShared* sh, c
 }
 
 // The product of one kind. Bound by the tensor cores where the tiles are 256 x 256 and fill the
-// GPU: 8192 x 4096 x 11264 bf16 gate 850-870 us (1.74-1.78 PFLOP/s), down and gate backward 1.7,
+// GPU: 8192 x 4096 x 11264 bf16 gate 850-880 us (1.72-1.78 PFLOP/s), down and gate backward 1.7,
 // weight gradient 1.62, at the 1.4 kW cap and 1.55-1.6 GHz, where the vendor's library takes 839 us
 // for the gate's products alone. Below that by the operands' way from L2 (about 68 bytes a clock and
 // SM) and, under about 20 us, by the start, the first loads and the last epilogue (1 + 1 + 2-4 us).
@@ -1156,7 +1163,8 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_rows(const __grid_constant_
 // The five products for operands that neither TMA nor 16-byte loads can address (an odd number of
 // contiguous columns, a slice that starts anywhere): tiles of 128 x 128 (gate: 128 x 64, twice) in
 // binary32 on the ordinary cores, 8 x 8 results a thread, 16 of the sum at a time through shared
-// memory, in partial sums of 768 as above. Bound by the multiply-adds, 20-30 TFLOP/s.
+// memory, in partial sums of 768 as above. Bound by the multiply-adds: 31-44 TFLOP/s at 4096 x 2047 x
+// 4095, the five kinds.
 struct AnyArgs {
     const uint16_t *a[2], *b[2], *b_up;
     uint64_t lda[2], ldb[2], ldb_up;

@@ -94,7 +94,7 @@ struct alignas(sizeof(T) * kN) Vec {
 // the last 48 MB so that they are the first to leave, and those at the normal priority; the second
 // pass starts with them, and reads everything for the last time. No line is kept above the normal
 // priority (evict_last): nothing takes that back, and the work behind the call would find so much
-// less of L2 (six passes over 90 MB: 145 us for 112), for 0.4 to 2 us of the call's own. Against one
+// less of L2 (six passes over 90 MB: 145 us for 112), for 0.4 to 2.5 us of the call's own. Against one
 // priority for all: 411M bf16 entries 493 -> 483 us, 25.6M binary32 entries 49.9 -> 48.0.
 constexpr uint32_t kKeepTiles = (48u << 20) / kTileBytes;
 
@@ -144,9 +144,10 @@ __device__ __forceinline__ void store_vec(T* p, const Vec<T, kN>& v) {
 
 // ------------------------------------------------------------------------------- the sum
 // A lane's squares of up to 64 entries, as one binary64 number. The squares are summed in
-// binary32 (four chains of at most 16 fused multiply-adds; all terms are positive, so the chains
-// lose at most 16 * 2^-24 of their sum) and the chains joined in binary64: binary64 for every
-// entry would be bound by its arithmetic, 1/64 of binary32's rate. A sum outside [2^-90, 2^126]
+// binary32: four chains of at most 16 fused multiply-adds and two additions that join them, all of
+// positive terms, so that at most 18 * 2^-24 of the sum is lost, and half of that, 5.4e-7, of the
+// norm. From there on sums are binary64: for every entry it would be bound by its arithmetic, 1/64
+// of binary32's rate. A sum outside [2^-90, 2^126]
 // may have lost squares to underflow or overflow: it is taken again with the entries scaled by
 // 2^90 or 2^-70, where neither can happen to any finite entry (below the first limit every entry
 // is under 2^-45, and the least subnormal's square becomes 2^-118; above the second limit the
