@@ -338,14 +338,14 @@ int dgc_sum_shared(const float* const* vals, int32_t W, const int64_t* count, in
 
 /* ------------------------------------------------- gradient tensors: norm and clipping */
 
-/* Element types of the calls below. */
-enum { DGC_F32 = 0, DGC_F16 = 1, DGC_BF16 = 2 };
+/* Element types of the calls below; the last two are tokens'. */
+enum { DGC_F32 = 0, DGC_F16 = 1, DGC_BF16 = 2, DGC_I32 = 3, DGC_I64 = 4 };
 
 /* One tensor as a run of n entries in memory. */
 typedef struct {
     void* data;       /* device, aligned to the element size (16-byte alignment is faster) */
     int64_t n;        /* entries; 0 allowed (data may then be NULL) */
-    int32_t dtype;    /* DGC_F32, DGC_F16 or DGC_BF16 */
+    int32_t dtype;    /* DGC_F32, DGC_F16 or DGC_BF16; tokens DGC_I32 or DGC_I64 */
     int32_t reserved; /* 0 */
 } dgc_tensor;
 
@@ -388,7 +388,8 @@ typedef struct {
     void* data;       /* device, aligned to the element size */
     int64_t rows, cols;
     int64_t ld;       /* entries from a row to the next, >= cols (not read where rows is 1) */
-    int32_t dtype;    /* DGC_F16 or DGC_BF16; the weight gradient DGC_F32 */
+    int32_t dtype;    /* DGC_F16 or DGC_BF16; the weight gradient DGC_F32. The operators around the
+                         block (embedding, norm, dropout, recurrence) take all three. */
     int32_t reserved; /* 0 */
 } dgc_matrix;
 
@@ -445,6 +446,118 @@ int dgc_ffn_weight_grad(const dgc_matrix* dy, const dgc_matrix* x, int32_t accum
                         const dgc_matrix* dw, int32_t* status, void* ws, size_t ws_bytes,
                         dgc_stream_t stream);
 
+/* ------------------------------------------------ around the block: embedding */
+
+/* What the calls from here to the utilities have in common. Matrices are of any of the three types
+ * (states and gradients of weights: binary32) and of any strides and alignment to their entries;
+ * rows on 16-byte boundaries (the recurrence: on two entries) are faster. Arithmetic is binary32, and
+ * every result is rounded once. Results are deterministic. A result may be an operand of the same
+ * shape and type (its rows then at the same addresses) where the call says so, else results overlap
+ * nothing. Any extent may be 0. Extents above 2^24 return DGC_EUNSUPPORTED. The calls enqueue
+ * kernels only (programmatic dependent launches) and can be captured into a CUDA graph; pointers
+ * belong to the current device. */
+
+/* out[t] = scale * table[tokens[t]], for tokens t = 0 .. n-1 of type DGC_I32 or DGC_I64 (device);
+ * table: vocabulary x D, out: n x D, their types independent. A token outside the vocabulary sets
+ * *status = DGC_EINVAL and its row of out to zeros. */
+int dgc_embed(const dgc_matrix* table, const dgc_tensor* tokens, float scale,
+              const dgc_matrix* out, int32_t* status, dgc_stream_t stream);
+
+/* Bytes of workspace of dgc_embed_backward. */
+int dgc_embed_backward_workspace(int64_t tokens, int64_t vocabulary, int64_t dim, size_t* bytes);
+
+/* dtable[w] = scale * (sum of dy[t] over the t with tokens[t] = w) for every word w (zeros for words
+ * that are not met), or (accumulate not 0) dtable[w] + that, for the words that are met alone.
+ * dtable is binary32 and may be any 4-byte aligned piece of the bucket. The tokens are sorted (equal
+ * ones stay in order) and sums are taken in that order, over at most 32 tokens and then over these
+ * sums, with no atomic additions.
+ *   padding  a word whose tokens are left out; -1: none
+ * A token outside the vocabulary sets *status = DGC_EINVAL and is left out. */
+int dgc_embed_backward(const dgc_tensor* tokens, const dgc_matrix* dy, float scale,
+                       int64_t padding, int32_t accumulate, const dgc_matrix* dtable,
+                       int32_t* status, void* ws, size_t ws_bytes, dgc_stream_t stream);
+
+/* ----------------------------------------------------------------------- layer norm */
+
+/* y = (x - mean) * rstd * gamma + beta, with mean the average of a row and rstd = 1 / sqrt(variance
+ * + eps), x and y M x D of one type.
+ *   gamma, beta  D binary32; beta NULL: none
+ *   eps          above 0, finite
+ *   mean, rstd   device, M binary32 each, for the backward pass; both or neither NULL
+ * The variance is taken around the mean, and the mean's rounding is taken out of it and of y. y may
+ * be x. */
+int dgc_layer_norm(const dgc_matrix* x, const dgc_tensor* gamma, const dgc_tensor* beta, float eps,
+                   const dgc_matrix* y, float* mean, float* rstd, dgc_stream_t stream);
+
+/* Bytes of workspace of dgc_layer_norm_backward. */
+int dgc_layer_norm_backward_workspace(int64_t rows, int64_t cols, size_t* bytes);
+
+/* With xhat = (x - mean) rstd and g = dy gamma: dx = rstd (g - avg(g) - xhat avg(g xhat)) + residual,
+ * dgamma = sum over the rows of dy xhat, dbeta = sum over the rows of dy (accumulate not 0: added to
+ * what is there).
+ *   mean, rstd     of the forward pass
+ *   residual       NULL: none; the gradient that goes around the normed branch
+ *   dgamma, dbeta  D binary32 each, any 4-byte aligned pieces of the bucket; NULL: not wanted
+ * dx may be dy, x or the residual. */
+int dgc_layer_norm_backward(const dgc_matrix* dy, const dgc_matrix* x, const dgc_tensor* gamma,
+                            const float* mean, const float* rstd, const dgc_matrix* residual,
+                            const dgc_matrix* dx, const dgc_tensor* dgamma,
+                            const dgc_tensor* dbeta, int32_t accumulate, void* ws, size_t ws_bytes,
+                            dgc_stream_t stream);
+
+/* -------------------------------------------------------------------------- dropout */
+
+/* out = residual (NULL: none) + (kept ? x * 65536 / (65536 - T) : 0), T = floor(65536 p + 1/2): p is
+ * taken to 16 bits, and the factor goes by what is taken. An entry is kept if its 16 bits of the
+ * counter-based generator are T or more:
+ *   key = mix(seed + G (1 + *step)),  word = mix(key + G (row * ceil(cols / 4) + col / 4 + 1)),
+ *   bits 16 (col mod 4) to 16 (col mod 4) + 15 of the word
+ * with SplitMix64's output function as mix and its increment 0x9E3779B97F4A7C15 as G, all modulo
+ * 2^64. No mask is stored, and none depends on strides, types or the launch: the backward pass is the
+ * same call, with the same seed and step, on the gradient.
+ *   p     in [0, 1]; 1 drops everything
+ *   step  device; NULL: 0. A captured graph draws a new mask at each replay if it advances it.
+ * What is dropped is dropped whatever its value. out may be x or the residual. */
+int dgc_dropout(const dgc_matrix* x, const dgc_matrix* residual, double p, uint64_t seed,
+                const uint64_t* step, const dgc_matrix* out, dgc_stream_t stream);
+
+/* ----------------------------------------------------------- gated linear recurrence */
+
+/* Bytes of workspace of the two calls below (0: none needed). */
+int dgc_recurrence_workspace(int64_t rows, int64_t cols, size_t* bytes);
+
+/* Rows of the saved states of a training step: a state ahead of every 64th row. */
+int dgc_recurrence_saved_rows(int64_t rows, int64_t* saved_rows);
+
+/* h_t = a_t h_{t-1} + (1 - a_t) x_t with a = 1 / (1 + e^-gate), y_t = h_t, in every column, over
+ * nseq sequences packed one behind the other: sequence q has the rows offsets[q] to offsets[q+1] - 1
+ * of x, gate and y (rows x cols, one type). Its first row's h_{t-1} is h0[q]. States are binary32.
+ *   offsets  device, nseq + 1 int64: 0 <= offsets[0], never falling, offsets[nseq] <= rows; else
+ *            *status = DGC_EINVAL and the results are invalid
+ *   h0       nseq x cols; NULL: zeros
+ *   h_last   nseq x cols, the state behind each sequence (h0 of an empty one); NULL: not wanted. It
+ *            may be h0, whose states are then lost to a backward pass.
+ *   saved    dgc_recurrence_saved_rows(rows) x cols, for the backward pass; NULL: not wanted
+ * Rows of no sequence are left as they are, and nothing in them reaches a result. y may be x or gate.
+ * One row a sequence is the step of a model that answers. Non-finite entries make their sequence's
+ * column non-finite from there on. */
+int dgc_recurrence(const dgc_matrix* x, const dgc_matrix* gate, const int64_t* offsets,
+                   int32_t nseq, const dgc_matrix* h0, const dgc_matrix* y,
+                   const dgc_matrix* h_last, const dgc_matrix* saved, int32_t* status, void* ws,
+                   size_t ws_bytes, dgc_stream_t stream);
+
+/* With G_t the gradient of h_t in all, G_t = dy_t + a_{t+1} G_{t+1} (+ d_last[q] at a last row):
+ * dx_t = G_t (1 - a_t), dgate_t = G_t (h_{t-1} - x_t) a_t (1 - a_t), d_h0[q] = a_t G_t at the first
+ * row (d_last[q] of an empty sequence).
+ *   x, gate, offsets, h0, saved  as in, or from, the forward pass
+ *   d_last, d_h0                 nseq x cols, binary32; NULL: zeros, not wanted. d_h0 may be d_last.
+ * dx and dgate may be x, gate or dy (not both the same). */
+int dgc_recurrence_backward(const dgc_matrix* dy, const dgc_matrix* x, const dgc_matrix* gate,
+                            const int64_t* offsets, int32_t nseq, const dgc_matrix* h0,
+                            const dgc_matrix* saved, const dgc_matrix* d_last,
+                            const dgc_matrix* dx, const dgc_matrix* dgate, const dgc_matrix* d_h0,
+                            int32_t* status, void* ws, size_t ws_bytes, dgc_stream_t stream);
+
 /* -------------------------------------------------------------------------- utilities */
 
 /* Synchronize `stream`, then return the int32 at status_dev (or DGC_ECUDA). */
@@ -485,6 +598,14 @@ int dgc_selftest_wait_timeout(int32_t* status, uint32_t spin_limit, dgc_stream_t
 int dgc_selftest_ffn_timeout(const dgc_matrix* hidden, const dgc_matrix* w_down,
                              const dgc_matrix* y, int32_t* status, uint32_t wait_ms,
                              dgc_stream_t stream);
+
+/* Self-test of the recurrence's bounded waits: dgc_recurrence over more than 128 rows whose first
+ * chunk never publishes its map. The waits give up after spin_limit polls, the call must come back
+ * with *status = DGC_ETIMEOUT, and y is invalid. */
+int dgc_selftest_recurrence_timeout(const dgc_matrix* x, const dgc_matrix* gate,
+                                    const int64_t* offsets, int32_t nseq, const dgc_matrix* y,
+                                    int32_t* status, void* ws, size_t ws_bytes,
+                                    uint32_t spin_limit, dgc_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -28,8 +28,12 @@ __all__ = [
     "ACT_SILU", "ACT_GELU", "ACT_GELU_TANH", "ACT_RELU", "dgc_matrix", "matrix",
     "dgc_ffn_gate", "dgc_ffn_down", "dgc_ffn_down_backward", "dgc_ffn_gate_backward",
     "dgc_ffn_weight_grad_workspace", "dgc_ffn_weight_grad",
+    "I32", "I64", "vector", "dgc_embed", "dgc_embed_backward_workspace", "dgc_embed_backward",
+    "dgc_layer_norm", "dgc_layer_norm_backward_workspace", "dgc_layer_norm_backward",
+    "dgc_dropout", "dgc_recurrence_workspace", "dgc_recurrence_saved_rows", "dgc_recurrence",
+    "dgc_recurrence_backward",
     "dgc_read_status", "dgc_status_string", "dgc_launch_count", "dgc_selftest_wait_timeout",
-    "dgc_selftest_ffn_timeout",
+    "dgc_selftest_ffn_timeout", "dgc_selftest_recurrence_timeout",
     "dgc_set_l2_fetch_granularity",
     "dgc_profile_stream_pass",
     "SELECT_EXACT", "SELECT_SAMPLED", "SELECT_ADACOMP", "FLAG_MASK_MOMENTUM",
@@ -38,7 +42,7 @@ __all__ = [
 OK, EINVAL, ECAPACITY, ECUDA, ETIMEOUT, ECORRUPT, EUNSUPPORTED = 0, -1, -2, -3, -4, -5, -6
 SELECT_EXACT, SELECT_SAMPLED, SELECT_ADACOMP = 0, 1, 2
 FLAG_MASK_MOMENTUM = 1
-F32, F16, BF16 = 0, 1, 2
+F32, F16, BF16, I32, I64 = 0, 1, 2, 3, 4
 ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU = 0, 1, 2, 3
 
 
@@ -149,6 +153,20 @@ def lib():
         L.dgc_ffn_gate_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp]
         L.dgc_ffn_weight_grad_workspace.argtypes = [i64, i64, i64, P(sz)]
         L.dgc_ffn_weight_grad.argtypes = [vp, vp, i32, vp, vp, vp, sz, vp]
+        f32, f64 = ctypes.c_float, ctypes.c_double
+        L.dgc_embed.argtypes = [vp, vp, f32, vp, vp, vp]
+        L.dgc_embed_backward_workspace.argtypes = [i64, i64, i64, P(sz)]
+        L.dgc_embed_backward.argtypes = [vp, vp, f32, i64, i32, vp, vp, vp, sz, vp]
+        L.dgc_layer_norm.argtypes = [vp, vp, vp, f32, vp, vp, vp, vp]
+        L.dgc_layer_norm_backward_workspace.argtypes = [i64, i64, P(sz)]
+        L.dgc_layer_norm_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp]
+        L.dgc_dropout.argtypes = [vp, vp, f64, u64, vp, vp, vp]
+        L.dgc_recurrence_workspace.argtypes = [i64, i64, P(sz)]
+        L.dgc_recurrence_saved_rows.argtypes = [i64, P(i64)]
+        L.dgc_recurrence.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.dgc_recurrence_backward.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp,
+                                              sz, vp]
+        L.dgc_selftest_recurrence_timeout.argtypes = [vp, vp, vp, i32, vp, vp, vp, sz, u32, vp]
         L.dgc_read_status.argtypes = [vp, vp]
         L.dgc_status_string.argtypes = [ctypes.c_int]
         L.dgc_status_string.restype = ctypes.c_char_p
@@ -173,7 +191,11 @@ def lib():
                   "dgc_ffn_gate", "dgc_ffn_down", "dgc_ffn_down_backward",
                   "dgc_ffn_gate_backward", "dgc_ffn_weight_grad_workspace",
                   "dgc_ffn_weight_grad",
-                  "dgc_read_status",
+                  "dgc_embed", "dgc_embed_backward_workspace", "dgc_embed_backward",
+                  "dgc_layer_norm", "dgc_layer_norm_backward_workspace",
+                  "dgc_layer_norm_backward", "dgc_dropout", "dgc_recurrence_workspace",
+                  "dgc_recurrence_saved_rows", "dgc_recurrence", "dgc_recurrence_backward",
+                  "dgc_read_status", "dgc_selftest_recurrence_timeout",
                   "dgc_selftest_wait_timeout", "dgc_selftest_ffn_timeout"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
@@ -634,6 +656,182 @@ def dgc_ffn_weight_grad(dy, x, dw, accumulate: bool, status, ws, ws_bytes: int |
                                             _stream(stream)), "dgc_ffn_weight_grad")
 
 
+# --------------------------------------------- around the block: embedding, norm, dropout
+class Vector(dgc_tensor):
+    """A dgc_tensor that keeps its tensor alive and knows its own address."""
+
+
+class _HostVector(dgc_tensor):
+    """The view of a tensor that is not on the GPU; the calls refuse it."""
+
+
+def vector(t) -> Vector:
+    """The C view of a contiguous tensor as a run of entries: tokens (int32 or int64; a batch of them
+    may keep its shape), a norm's weights and their gradients. The calls below build it from the
+    tensors they get; a program with fixed buffers builds it once."""
+    import torch
+
+    if not t.is_contiguous():
+        raise DGCError(EINVAL, "vector: a contiguous tensor is wanted")
+    code = I32 if t.dtype == torch.int32 else I64 if t.dtype == torch.int64 else _dtype_code(t)
+    kind = Vector if t.is_cuda or not _on_host(t) else _HostVector
+    v = kind(t.data_ptr(), t.numel(), code, 0)
+    v.tensor = t
+    v.address = ctypes.addressof(v)
+    return v
+
+
+def _vec(v):
+    if type(v) is Vector:
+        return v.address
+    if v is None:
+        return None
+    if not isinstance(v, dgc_tensor):
+        v = vector(v)
+    if type(v) is _HostVector:
+        _refuse_host("a vector")
+    return ctypes.byref(v)
+
+
+def _size(ws, ws_bytes) -> int:
+    if ws_bytes is not None:
+        return int(ws_bytes)
+    return 0 if ws is None else ws.nbytes
+
+
+def _float32():
+    import torch
+
+    return torch.float32
+
+
+def _int64():
+    import torch
+
+    return torch.int64
+
+
+def _row_count(m) -> int:
+    return m.rows if isinstance(m, dgc_matrix) else m.shape[0]
+
+
+def _typed(t, dtype, n, what: str) -> int | None:
+    """The address of a tensor that must have this type and at least n entries in one run."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype != dtype or not t.is_contiguous() or (n is not None and t.numel() < n):
+        raise DGCError(EINVAL, f"{what}: a contiguous {dtype} tensor of {n} entries is wanted")
+    return _gpu(t, what)
+
+
+def dgc_embed(table, tokens, scale: float, out, status, stream=None) -> int:
+    """out[t] = scale * table[tokens[t]]. table, out: CUDA tensors of any of the three types, or their
+    matrix() views; tokens: int32 or int64, or their vector() view."""
+    return _check(lib().dgc_embed(_mat(table), _vec(tokens), float(scale), _mat(out),
+                                  _gpu(status, "status"), _stream(stream)), "dgc_embed")
+
+
+def dgc_embed_backward_workspace(tokens: int, vocabulary: int, dim: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().dgc_embed_backward_workspace(int(tokens), int(vocabulary), int(dim),
+                                              ctypes.byref(out)), "dgc_embed_backward_workspace")
+    return out.value
+
+
+def dgc_embed_backward(tokens, dy, scale: float, padding: int | None, dtable, accumulate: bool,
+                       status, ws, ws_bytes: int | None = None, stream=None) -> int:
+    """dtable (float32)[w] = scale * the sum of dy over w's tokens, or dtable + that; padding: a word
+    whose tokens are left out, or None."""
+    if padding is None:
+        padding = -1
+    elif padding < 0:
+        raise DGCError(EINVAL, "dgc_embed_backward: a negative padding word")
+    return _check(lib().dgc_embed_backward(_vec(tokens), _mat(dy), float(scale), int(padding),
+                                           int(bool(accumulate)), _mat(dtable),
+                                           _gpu(status, "status"), _gpu(ws, "ws"),
+                                           _size(ws, ws_bytes), _stream(stream)),
+                  "dgc_embed_backward")
+
+
+def dgc_layer_norm(x, gamma, beta, eps: float, y, mean, rstd, stream=None) -> int:
+    """y = (x - mean) * rstd * gamma + beta (or None); mean, rstd: float32, one a row, or None."""
+    f32, rows = _float32(), _row_count(x)
+    return _check(lib().dgc_layer_norm(_mat(x), _vec(gamma), _vec(beta), float(eps), _mat(y),
+                                       _typed(mean, f32, rows, "mean"),
+                                       _typed(rstd, f32, rows, "rstd"), _stream(stream)),
+                  "dgc_layer_norm")
+
+
+def dgc_layer_norm_backward_workspace(rows: int, cols: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().dgc_layer_norm_backward_workspace(int(rows), int(cols), ctypes.byref(out)),
+           "dgc_layer_norm_backward_workspace")
+    return out.value
+
+
+def dgc_layer_norm_backward(dy, x, gamma, mean, rstd, residual, dx, dgamma, dbeta,
+                            accumulate: bool, ws, ws_bytes: int | None = None, stream=None) -> int:
+    """dx (plus residual, or None), and dgamma and dbeta (float32, or None), written or added."""
+    f32, rows = _float32(), _row_count(dy)
+    return _check(lib().dgc_layer_norm_backward(
+        _mat(dy), _mat(x), _vec(gamma), _typed(mean, f32, rows, "mean"),
+        _typed(rstd, f32, rows, "rstd"), _mat(residual), _mat(dx), _vec(dgamma), _vec(dbeta),
+        int(bool(accumulate)), _gpu(ws, "ws"), _size(ws, ws_bytes), _stream(stream)),
+        "dgc_layer_norm_backward")
+
+
+def dgc_dropout(x, residual, p: float, seed: int, step, out, stream=None) -> int:
+    """out = residual (or None) + what is kept of x, scaled. step: a device int64 (or uint64) word
+    that numbers the draws, or None. The backward pass is the same call on the gradient."""
+    if step is not None and not isinstance(step, int):
+        if step.element_size() != 8 or step.is_floating_point() or step.numel() < 1:
+            raise DGCError(EINVAL, "dgc_dropout: step is one 64-bit word")
+        step = _gpu(step, "step")
+    return _check(lib().dgc_dropout(_mat(x), _mat(residual), float(p), int(seed) & (2**64 - 1),
+                                    step, _mat(out), _stream(stream)), "dgc_dropout")
+
+
+# --------------------------------------------------------------- gated linear recurrence
+def dgc_recurrence_workspace(rows: int, cols: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().dgc_recurrence_workspace(int(rows), int(cols), ctypes.byref(out)),
+           "dgc_recurrence_workspace")
+    return out.value
+
+
+def dgc_recurrence_saved_rows(rows: int) -> int:
+    out = ctypes.c_int64(0)
+    _check(lib().dgc_recurrence_saved_rows(int(rows), ctypes.byref(out)),
+           "dgc_recurrence_saved_rows")
+    return out.value
+
+
+def dgc_recurrence(x, gate, offsets, h0, y, h_last, saved, status, ws, nseq: int | None = None,
+                   ws_bytes: int | None = None, stream=None) -> int:
+    """y_t = h_t = a h_{t-1} + (1 - a) x_t, a = sigmoid(gate), over the sequences whose rows begin at
+    offsets (int64 CUDA tensor, one more than sequences). h0, h_last (float32, a row a sequence), saved
+    (float32, for the backward pass): or None. ws may be None where the workspace query says 0."""
+    nseq = offsets.numel() - 1 if nseq is None else nseq
+    return _check(lib().dgc_recurrence(_mat(x), _mat(gate),
+                                       _typed(offsets, _int64(), nseq + 1, "offsets"), int(nseq),
+                                       _mat(h0), _mat(y), _mat(h_last), _mat(saved),
+                                       _gpu(status, "status"), _gpu(ws, "ws"),
+                                       _size(ws, ws_bytes), _stream(stream)), "dgc_recurrence")
+
+
+def dgc_recurrence_backward(dy, x, gate, offsets, h0, saved, d_last, dx, dgate, d_h0, status, ws,
+                            nseq: int | None = None, ws_bytes: int | None = None,
+                            stream=None) -> int:
+    """dx, dgate and d_h0 (or None) from dy and d_last (or None); x, gate, offsets, h0, saved: of the
+    forward pass."""
+    nseq = offsets.numel() - 1 if nseq is None else nseq
+    return _check(lib().dgc_recurrence_backward(
+        _mat(dy), _mat(x), _mat(gate), _typed(offsets, _int64(), nseq + 1, "offsets"), int(nseq),
+        _mat(h0), _mat(saved), _mat(d_last), _mat(dx), _mat(dgate), _mat(d_h0),
+        _gpu(status, "status"), _gpu(ws, "ws"), _size(ws, ws_bytes), _stream(stream)),
+        "dgc_recurrence_backward")
+
+
 # ----------------------------------------------------------------------------- utilities
 def dgc_read_status(status, stream=None) -> int:
     return int(lib().dgc_read_status(_ptr(status), _stream(stream)))
@@ -675,3 +873,11 @@ def dgc_selftest_ffn_timeout(hidden, w_down, y, status, wait_ms: int, stream=Non
                                                  _gpu(status, "status"), int(wait_ms),
                                                  _stream(stream)),
                   "dgc_selftest_ffn_timeout")
+
+
+def dgc_selftest_recurrence_timeout(x, gate, offsets, y, status, ws, spin_limit: int,
+                                    stream=None) -> int:
+    return _check(lib().dgc_selftest_recurrence_timeout(
+        _mat(x), _mat(gate), _typed(offsets, _int64(), 1, "offsets"), offsets.numel() - 1, _mat(y),
+        _gpu(status, "status"), _gpu(ws, "ws"), _size(ws, None), int(spin_limit),
+        _stream(stream)), "dgc_selftest_recurrence_timeout")

@@ -1,0 +1,360 @@
+"""The gated linear recurrence and its backward pass on the GPU against the definition, row by row in
+64 bits (the bounds are derived with it, in layer_helpers)."""
+import numpy as np
+import pytest
+import torch
+
+import sparsified_gradient_compression_gb300 as dgc
+from layer_helpers import (BF16, E, F16, F32, bits, buffer, generator, near, normal,
+                           outside_is_untouched, scan64, scan64_backward, status_word, workspace)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    dgc.build()
+    dgc.lib()
+
+
+def numpy64(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def inside(rows, ends):
+    m = torch.zeros(rows, dtype=torch.bool)
+    m[ends[0]:ends[-1]] = True
+    return m
+
+
+def run(rows, cols, ends, type_, state=True, pad=0, gate_mean=1.5, gate_sigma=2.0, alias=False,
+        outside=float("nan"), backward=True, seed=0, state_pad="packed"):
+    """Forward and backward; the rows of no sequence hold `outside` in every operand."""
+    gen = generator(seed + rows + cols)
+    n = len(ends) - 1
+    x, dy = normal(gen, rows, cols, type_, pad=pad), normal(gen, rows, cols, type_, 0.5, pad=pad)
+    gate = normal(gen, rows, cols, type_, gate_sigma, gate_mean, pad)
+    ok = inside(rows, ends)
+    for t in (x, gate, dy):
+        t[~ok.cuda()] = outside
+    h0, d_last = (normal(gen, n, cols, F32, pad=state_pad) if state else None for _ in range(2))
+    off = torch.tensor(ends, dtype=torch.int64, device="cuda")
+    X, G, DY, H0, DL = (numpy64(t) for t in (x, gate, dy, h0, d_last))
+    y = buffer(rows, cols, type_, pad)
+    h_last = buffer(n, cols, F32, state_pad)
+    saved = torch.full((dgc.dgc_recurrence_saved_rows(rows), cols), float("nan"), device="cuda")
+    st, ws = status_word(), workspace(dgc.dgc_recurrence_workspace(rows, cols))
+    dgc.dgc_recurrence(x, gate, off, h0, y, h_last, saved, st, ws)
+    h, _, err, last, last_err = scan64(X, G, ends, H0)
+    T = torch.from_numpy
+    near(y.cpu()[ok], T(h)[ok], T(err)[ok])
+    assert torch.isnan(y.cpu()[~ok]).all()  # the buffer's fill
+    near(h_last.cpu(), T(last), T(last_err))
+    outside_is_untouched(y)
+    outside_is_untouched(h_last)
+    if backward:
+        if alias:
+            dx, dgate, d_h0 = dy, gate, d_last
+        else:
+            dx, dgate = buffer(rows, cols, type_, pad), buffer(rows, cols, type_, pad)
+            d_h0 = buffer(n, cols, F32, state_pad) if state else None
+        dgc.dgc_recurrence_backward(dy, x, gate, off, h0, saved, d_last, dx, dgate, d_h0, st, ws)
+        (wx, ex), (wg, eg), (wh, eh) = scan64_backward(X, G, ends, H0, DY, DL)
+        near(dx.cpu()[ok], T(wx)[ok], T(ex)[ok])
+        near(dgate.cpu()[ok], T(wg)[ok], T(eg)[ok])
+        if state:
+            near(d_h0.cpu(), T(wh), T(eh))
+        if not alias:
+            assert torch.isnan(dx.cpu()[~ok]).all() and torch.isnan(dgate.cpu()[~ok]).all()
+            outside_is_untouched(dx)
+            outside_is_untouched(dgate)
+    assert dgc.dgc_read_status(st) == 0
+
+
+@pytest.mark.parametrize("type_", [F32, F16, BF16])
+@pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 300])
+def test_one_sequence(rows, type_):
+    for cols in (1, 2, 64, 67):
+        run(rows, cols, [0, rows], type_)
+    run(rows, 130, [0, rows], type_, state=False)
+
+
+@pytest.mark.parametrize("type_", [F32, BF16])
+def test_long_sequences(type_):
+    """Several groups of chunks in both directions."""
+    run(4229, 66, [0, 4229], type_, gate_mean=5.0)
+    run(9000, 3, [0, 9000], type_, gate_mean=8.0, gate_sigma=0.5)
+    run(8192, 65, [0, 100, 4096, 4097, 8192], type_)
+    run(6000, 2, [17, 17, 5000, 5000, 5990], type_, gate_mean=4.0)
+
+
+TABLES = [
+    [0, 64], [0, 1, 2, 3], [0, 0, 0, 5], [0, 5, 5, 5], [3, 3], [3, 9], [0, 63, 64, 65, 130],
+    [0, 128, 256], [1, 127, 129, 255, 256], [0, 127, 128, 129], [5, 64, 128, 190, 192, 192, 300],
+    list(range(0, 200)), list(range(0, 400, 2)), [0] * 70 + [40] * 70 + [90] * 40 + [91],
+]
+
+
+@pytest.mark.parametrize("type_", [F32, BF16])
+@pytest.mark.parametrize("i", range(len(TABLES)))
+def test_packed_sequences(i, type_):
+    ends = TABLES[i]
+    for rows in (ends[-1], ends[-1] + 1, ends[-1] + 77):
+        run(rows, 70, ends, type_, seed=i)
+        run(rows, 5, ends, type_, seed=i, state=False, outside=float("inf"))
+
+
+@pytest.mark.parametrize("alias", [False, True])
+@pytest.mark.parametrize("pad", [1, "odd", "packed"])
+@pytest.mark.parametrize("type_", [F32, F16, BF16])
+def test_strides(type_, pad, alias):
+    for cols in (1, 31, 65, 100):
+        run(150, cols, [2, 70, 70, 150], type_, pad=pad, alias=alias, state_pad=pad)
+
+
+@pytest.mark.parametrize("type_", [F32, F16, BF16])
+def test_gates_at_their_ends(type_):
+    """Gates of +-30, +-100 and the infinities: open, closed, and nothing in between is lost."""
+    rows, cols = 90, 8
+    gen = generator(3)
+    x, dy = normal(gen, rows, cols, type_), normal(gen, rows, cols, type_)
+    gate = buffer(rows, cols, type_, fill=0.0)
+    ends = [0, 40, rows]
+    values = [30.0, -30.0, 100.0, -100.0, float("inf"), -float("inf"), 0.0, 88.0]
+    for c, v in enumerate(values):
+        gate[:, c] = v
+    gate[20], gate[60] = -float("inf"), float("inf")
+    h0, d_last = normal(gen, 2, cols, F32), normal(gen, 2, cols, F32)
+    off = torch.tensor(ends, device="cuda")
+    y, dx, dgate = (buffer(rows, cols, type_) for _ in range(3))
+    h_last, d_h0 = buffer(2, cols, F32), buffer(2, cols, F32)
+    saved, st = torch.empty(2, cols, device="cuda"), status_word()
+    ws = workspace(dgc.dgc_recurrence_workspace(rows, cols))
+    dgc.dgc_recurrence(x, gate, off, h0, y, h_last, saved, st, ws)
+    dgc.dgc_recurrence_backward(dy, x, gate, off, h0, saved, d_last, dx, dgate, d_h0, st, ws)
+    args = [numpy64(t) for t in (x, gate)] + [ends, numpy64(h0)]
+    h, _, err, last, last_err = scan64(*args)
+    (wx, ex), (wg, eg), (wh, eh) = scan64_backward(*args, numpy64(dy), numpy64(d_last))
+    T = torch.from_numpy
+    near(y.cpu(), T(h), T(err))
+    near(h_last.cpu(), T(last), T(last_err))
+    # factors below 2^-126 are zero here: 1e-37 of the terms, whose magnitudes are below 1000
+    near(dx.cpu(), T(wx), T(ex) + 1e-34)
+    near(dgate.cpu(), T(wg), T(eg) + 1e-34)
+    near(d_h0.cpu(), T(wh), T(eh) + 1e-34)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_what_is_not_finite_stays_in_its_sequence(bad):
+    rows, cols, ends = 700, 66, [0, 300, 301, 500, 700]
+    gen = generator(8)
+    x, gate, dy = (normal(gen, rows, cols, BF16) for _ in range(3))
+    x[120, 7], dy[420, 9] = bad, bad
+    off, st = torch.tensor(ends, device="cuda"), status_word()
+    y, dx, dgate = (buffer(rows, cols, BF16) for _ in range(3))
+    h_last, d_h0 = buffer(4, cols, F32), buffer(4, cols, F32)
+    h0 = normal(gen, 4, cols, F32)
+    h0[2, 11] = bad
+    saved = torch.empty(dgc.dgc_recurrence_saved_rows(rows), cols, device="cuda")
+    ws = workspace(dgc.dgc_recurrence_workspace(rows, cols))
+    dgc.dgc_recurrence(x, gate, off, h0, y, h_last, saved, st, ws)
+    dgc.dgc_recurrence_backward(dy, x, gate, off, h0, saved, None, dx, dgate, d_h0, st, ws)
+    good = torch.ones(rows, cols, dtype=torch.bool, device="cuda")
+    good[120:300, 7] = False
+    good[301:500, 11] = False
+    assert torch.isfinite(y[good]).all() and not torch.isfinite(y[~good]).any()
+    back = torch.ones_like(good)
+    back[301:421, 9] = False
+    assert torch.isfinite(dx[back]).all() and not torch.isfinite(dx[~back]).any()
+    back[120:300, 7] = False
+    back[301:500, 11] = False
+    assert torch.isfinite(dgate[back]).all()
+    assert dgc.dgc_read_status(st) == 0
+
+
+def test_steps_of_a_model_that_answers():
+    """One row a sequence, state in place, against the whole sequences at once: each step's state
+    passes on in binary32."""
+    n, cols, steps = 9, 200, 40
+    gen = generator(5)
+    x, gate = normal(gen, n * steps, cols, BF16), normal(gen, n * steps, cols, BF16)
+    off = torch.arange(0, n * steps + 1, steps, device="cuda")
+    y, h_last, st = buffer(n * steps, cols, BF16), buffer(n, cols, F32), status_word()
+    ws = workspace(dgc.dgc_recurrence_workspace(n * steps, cols))
+    dgc.dgc_recurrence(x, gate, off, None, y, h_last, None, st, ws)
+    state, out = torch.zeros(n, cols, device="cuda"), buffer(n, cols, BF16)
+    one = torch.arange(n + 1, device="cuda")
+    X, G = x.view(n, steps, cols), gate.view(n, steps, cols)
+    ends = [steps * i for i in range(n + 1)]
+    h, _, err, last, last_err = scan64(numpy64(x), numpy64(gate), ends, None)
+    ws1 = workspace(dgc.dgc_recurrence_workspace(n, cols))
+    for t in range(steps):
+        dgc.dgc_recurrence(X[:, t], G[:, t], one, state, out, state, None, st, ws1)
+        near(out.cpu(), torch.from_numpy(h.reshape(n, steps, cols)[:, t]),
+             torch.from_numpy(err.reshape(n, steps, cols)[:, t]))
+    near(state.cpu(), torch.from_numpy(last), torch.from_numpy(last_err))
+    assert dgc.dgc_read_status(st) == 0
+
+
+def test_in_place_over_many_rows():
+    rows, cols, ends = 5000, 70, [0, 900, 900, 4999]
+    gen = generator(6)
+    x, gate, h0 = normal(gen, rows, cols, BF16), normal(gen, rows, cols, BF16), normal(gen, 3, cols,
+                                                                                       F32)
+    off, st = torch.tensor(ends, device="cuda"), status_word()
+    ws = workspace(dgc.dgc_recurrence_workspace(rows, cols))
+    y, last = buffer(rows, cols, BF16), buffer(3, cols, F32)
+    dgc.dgc_recurrence(x, gate, off, h0, y, last, None, st, ws)
+    for out in ("x", "gate"):
+        a, b, h = x.clone(), gate.clone(), h0.clone()
+        dgc.dgc_recurrence(a, b, off, h, a if out == "x" else b, h, None, st, ws)
+        assert torch.equal(bits((a if out == "x" else b)[:4999]), bits(y[:4999].contiguous()))
+        assert torch.equal((a if out == "x" else b)[4999], (x if out == "x" else gate)[4999])
+        assert torch.equal(h, last)
+    assert dgc.dgc_read_status(st) == 0
+
+
+def test_deterministic_and_shares_its_workspace():
+    rows, cols = 20000, 130
+    gen = generator(7)
+    x, gate, dy = (normal(gen, rows, cols, BF16, mean=m) for m in (0.0, 4.0, 0.0))
+    off, st = torch.tensor([0, rows], device="cuda"), status_word()
+    ws = workspace(dgc.dgc_recurrence_workspace(rows, cols))
+    saved = torch.empty(dgc.dgc_recurrence_saved_rows(rows), cols, device="cuda")
+    runs = []
+    for _ in range(4):
+        y, dx, dgate = (buffer(rows, cols, BF16, "packed") for _ in range(3))
+        dgc.dgc_recurrence(x, gate, off, None, y, None, saved, st, ws)
+        dgc.dgc_recurrence_backward(dy, x, gate, off, None, saved, None, dx, dgate, None, st, ws)
+        runs.append((y, dx, dgate))
+    for r in runs[1:]:
+        assert all(torch.equal(bits(a), bits(b)) for a, b in zip(runs[0], r))
+    assert dgc.dgc_read_status(st) == 0
+
+
+@pytest.mark.parametrize("ends", [[-1, 5], [0, 6, 5], [0, 201], [0, 2**40], [-2**63, 200],
+                                  [200, 0], [0, 500, 3, 200]])
+@pytest.mark.parametrize("rows", [200])
+def test_bad_tables_are_reported(rows, ends):
+    x, gate = (normal(generator(1), rows, 70, BF16) for _ in range(2))
+    y, st = buffer(rows, 70, BF16), status_word()
+    n = len(ends) - 1
+    h0, saved = torch.zeros(n, 70, device="cuda"), torch.zeros(4, 70, device="cuda")
+    off = torch.tensor(ends, device="cuda")
+    ws = workspace(dgc.dgc_recurrence_workspace(rows, 70))
+    dgc.dgc_recurrence(x, gate, off, h0, y, h0, saved, st, ws)
+    assert dgc.dgc_read_status(st) == dgc.EINVAL
+    st.zero_()
+    dgc.dgc_recurrence_backward(x, x, gate, off, h0, saved, h0, y, y, h0, st, ws)
+    assert dgc.dgc_read_status(st) == dgc.EINVAL
+
+
+def test_nothing_to_scan():
+    st = status_word()
+    h0 = torch.ones(2, 9, device="cuda")
+    last, d_h0 = torch.zeros_like(h0), torch.zeros_like(h0)
+    none, off = buffer(0, 9, BF16), torch.zeros(3, dtype=torch.int64, device="cuda")
+    saved = torch.empty(0, 9, device="cuda")
+    dgc.dgc_recurrence(none, none, off, h0, none, last, saved, st, None)
+    assert torch.equal(last, h0)
+    dgc.dgc_recurrence_backward(none, none, none, off, h0, saved, h0, none, none, d_h0, st, None)
+    assert torch.equal(d_h0, h0)
+    x, y = normal(generator(1), 5, 9, BF16), buffer(5, 9, BF16)
+    dgc.dgc_recurrence(x, x, off[:1], None, y, None, None, st, None)  # no sequence
+    assert torch.isnan(y).all() and dgc.dgc_read_status(st) == 0
+
+
+def test_gradient_against_differences():
+    """Of sum(w y) + sum(c h_last) along a direction, by central differences of the definition in 64
+    bits (the step's error: its square, 1e-8, times third derivatives of order one)."""
+    rows, cols, ends = 150, 20, [0, 60, 60, 150]
+    gen = generator(12)
+    x, gate, w = (normal(gen, rows, cols, F32, pad="packed") for _ in range(3))
+    h0, c = normal(gen, 3, cols, F32, pad="packed"), normal(gen, 3, cols, F32, pad="packed")
+    vx, vg, vh = (numpy64(torch.randn(t.shape, generator=gen, device="cuda")) for t in (x, gate, h0))
+    X, G, W, H, C = (numpy64(t) for t in (x, gate, w, h0, c))
+
+    def loss(t):
+        h, _, _, last, _ = scan64(X + t * vx, G + t * vg, ends, H + t * vh)
+        return (h * W).sum() + (last * C).sum()
+
+    slope = (loss(1e-4) - loss(-1e-4)) / 2e-4
+    off, st = torch.tensor(ends, device="cuda"), status_word()
+    y, dx, dgate, d_h0 = (torch.empty_like(t) for t in (x, x, x, h0))
+    saved = torch.empty(3, cols, device="cuda")
+    ws = workspace(dgc.dgc_recurrence_workspace(rows, cols))
+    dgc.dgc_recurrence(x, gate, off, h0, y, None, saved, st, ws)
+    dgc.dgc_recurrence_backward(w, x, gate, off, h0, saved, c, dx, dgate, d_h0, st, ws)
+    parts = [numpy64(a) * b for a, b in ((dx, vx), (dgate, vg), (d_h0, vh))]
+    got, terms = sum(p.sum() for p in parts), sum(np.abs(p).sum() for p in parts)
+    assert abs(got - slope) <= 1e-5 * terms
+    assert dgc.dgc_read_status(st) == 0
+
+
+def test_a_wait_that_runs_out():
+    """The first chunk's map never arrives: the status says so, and the next call is right."""
+    rows, cols = 700, 130
+    gen = generator(13)
+    x, gate = normal(gen, rows, cols, BF16), normal(gen, rows, cols, BF16)
+    off, st, y = torch.tensor([0, rows], device="cuda"), status_word(), buffer(rows, cols, BF16)
+    ws = workspace(dgc.dgc_recurrence_workspace(rows, cols))
+    dgc.dgc_selftest_recurrence_timeout(x, gate, off, y, st, ws, 2000)
+    assert dgc.dgc_read_status(st) == dgc.ETIMEOUT
+    run(rows, cols, [0, rows], BF16)
+
+
+def test_captured_calls_on_their_own_streams():
+    """Two graphs with their own workspaces, replayed on two streams at once, and the bits of plain
+    calls."""
+    rows, cols = 3000, 64
+    sets = []
+    for i in range(2):
+        gen = generator(20 + i)
+        x, gate, dy = (normal(gen, rows, cols, F16) for _ in range(3))
+        off = torch.tensor([0, 1000 * (i + 1), rows], device="cuda")
+        y, dx, dgate = (buffer(rows, cols, F16) for _ in range(3))
+        saved = torch.empty(dgc.dgc_recurrence_saved_rows(rows), cols, device="cuda")
+        st, ws = status_word(), workspace(dgc.dgc_recurrence_workspace(rows, cols))
+
+        def step(x=x, gate=gate, dy=dy, off=off, y=y, dx=dx, dgate=dgate, saved=saved, st=st, ws=ws):
+            dgc.dgc_recurrence(x, gate, off, None, y, None, saved, st, ws)
+            dgc.dgc_recurrence_backward(dy, x, gate, off, None, saved, None, dx, dgate, None, st, ws)
+
+        step()
+        want = [t.clone() for t in (y, dx, dgate)]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        sets.append((graph, (y, dx, dgate), want, torch.cuda.Stream(), st, step))  # step: its inputs
+    for _ in range(3):
+        for _, outs, *_ in sets:
+            for t in outs:
+                t.fill_(1.0)
+        torch.cuda.synchronize()
+        for graph, _, _, stream, *_ in sets:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for _, outs, want, _, st, _ in sets:
+            assert all(torch.equal(a, b) for a, b in zip(outs, want))
+            assert dgc.dgc_read_status(st) == 0
+
+
+def test_rows_past_two_to_the_32():
+    """Long rows far apart: the last rows lie behind 2^32 entries."""
+    rows, cols, ld = 400, 70, 1 << 24
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    flat = torch.empty(rows * ld, dtype=BF16, device="cuda")
+    x = flat.view(rows, ld)[:, :cols]
+    gate = flat.view(rows, ld)[:, 4096:4096 + cols]
+    y = flat.view(rows, ld)[:, 8192:8192 + cols]
+    gen = generator(30)
+    x.copy_(torch.randn(rows, cols, generator=gen, device="cuda"))
+    gate.copy_(torch.randn(rows, cols, generator=gen, device="cuda"))
+    off, st = torch.tensor([0, rows], device="cuda"), status_word()
+    ws = workspace(dgc.dgc_recurrence_workspace(rows, cols))
+    dgc.dgc_recurrence(x, gate, off, None, y, None, None, st, ws)
+    h, _, err, _, _ = scan64(numpy64(x), numpy64(gate), [0, rows], None)
+    near(y.cpu(), torch.from_numpy(h), torch.from_numpy(err))
+    assert dgc.dgc_read_status(st) == 0 and E > 0
