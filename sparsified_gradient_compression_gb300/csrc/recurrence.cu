@@ -5,18 +5,22 @@
 //   dgate_t = G_t (h_{t-1} - x_t) a_t (1 - a_t)
 //
 // Columns are independent; rows are a scan. A step, and any run of steps, is an affine map of the
-// state, h -> A h + B, so a run's map is known before the state that enters it. A block takes 64
-// columns of a chunk of rows, each of its 8 warps kS rows of it, two columns a lane, all in
-// registers:
-//   1. each warp composes its rows' map; the first warp composes the warps' and publishes the
+// state, h -> A h + B, so a run's map is known before the state that enters it. A block takes tiles
+// of 64 columns by a chunk of rows, each of its 8 warps kS rows, two columns a lane:
+//   1. each warp composes its rows' map; the last warp composes the warps' and publishes the
 //      chunk's (A, B);
-//   2. 32 chunks are a group: the first warp takes the state that enters the group, which the last
-//      chunk of the group ahead publishes, and applies the maps of the chunks before its own, in
-//      order. (Which maps are joined is fixed, so the rounding is too: results are the same bits on
-//      every run. A chain from chunk to chunk would cost its latency 32 times.)
+//   2. 32 chunks are a group: the warps collect the maps of the chunks ahead of this one in its
+//      group, four each, and the state that enters the group, which the last chunk of the group
+//      ahead publishes. (Which maps are joined, and how, is fixed, so the rounding is too: results
+//      are the same bits on every run. A chain from chunk to chunk would cost its latency 32 times.)
 //   3. each warp walks its rows again from the state it enters with, and writes.
-// The data is read once. Blocks take their chunks by a ticket, in order, so a block only waits for
-// blocks that run; waits are bounded all the same.
+// The data is read once. Blocks stay, and the next tiles are on their way to shared memory while one
+// is computed: a tile's latency is that of two barriers and a round trip to L2. (One block a tile,
+// with its loads at its beginning, took 279 us for 32768 x 2048.) Tiles go by a ticket, in order, so
+// a block only waits for tiles that running blocks hold; waits are bounded all the same.
+//
+// Maps and states are published without flags: the workspace is filled with a bit pattern that no
+// result has, and a reader waits until it has gone.
 //
 // A sequence's first row has no predecessor: its map is h -> B with B = a h0 + (1 - a) x, kept as
 // A = kReset, so that nothing of what is ahead, infinities and NaNs among it, comes through.
@@ -33,10 +37,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCols = 64;        // of a block
+constexpr int kCols = 64;        // of a tile
 constexpr uint32_t kGroup = 32;  // chunks
 constexpr uint32_t kPiece = 64;  // rows between two saved states
 constexpr float kReset = -1.0f;  // no run of steps has a negative A
+constexpr uint32_t kNotYet = 0xFFFFFFFFu;  // a NaN that no arithmetic makes
 
 struct ScanArgs {
     const void *x, *gate, *dy;
@@ -47,38 +52,16 @@ struct ScanArgs {
     uint64_t ldh0, ldd_last, ldh_last, ldd_h0, lds;
     const int64_t* offsets;
     uint32_t nseq, rows, cols, tiles, chunks;
-    // the workspace: a ticket, whether a wait gave up, a flag of every chunk and of every group of a column tile, their
-    // maps {A, A, B, B} and states of a lane's two columns. ticket null: one chunk, nothing shared.
-    uint32_t *ticket, *abort, *chunk_flag, *group_flag;
-    float4* maps;
-    float2* states;
+    // the workspace: a ticket, whether a wait gave up, the chunks' maps {A, A, B, B} and the groups'
+    // entering states of a lane's two columns. ticket null: one chunk, nothing is shared.
+    uint32_t *ticket, *abort;
+    uint4* maps;
+    uint2* states;
     uint32_t spin_limit, lost;  // lost: self-test, a chunk that publishes nothing
     int32_t* status;
 };
 
-__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
-    uint32_t v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
-}
-__device__ __forceinline__ void st_release(uint32_t* p, uint32_t v) {
-    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
-}
-
 // Two columns of a row: kPair whole, where the address allows it and both are there.
-template <typename T>
-struct Two {
-    Packed<T, 2> p;
-    template <bool kPair>
-    __device__ static Two load(const void* m, uint64_t ld, uint64_t row, uint32_t col, uint32_t n) {
-        return {load_piece<kPair, T, 2>(static_cast<const T*>(m) + row * ld + col, n)};
-    }
-    __device__ float2 up() const {
-        float f[2];
-        unpack<T, 2>(p, f);
-        return {f[0], f[1]};
-    }
-};
 template <typename T, bool kPair>
 __device__ __forceinline__ void store_two(void* m, uint64_t ld, uint64_t row, uint32_t col,
                                           uint32_t n, float2 v) {
@@ -97,23 +80,45 @@ __device__ __forceinline__ void store_state(float* m, uint64_t ld, uint64_t row,
     if (n > 1) p[1] = v.y;
 }
 
-// a = 1 / (1 + e^-g) and 1 - a = e^-g / (1 + e^-g), neither by a subtraction. e^-g is held below
-// 2^126, where the reciprocal is still a normal number; a gate of -infinity closes the state off.
-__device__ __forceinline__ void sigmoid2(float g, float& a, float& keep) {
-    const float e = expf(-g);
-    const float r = __fdividef(1.0f, 1.0f + fminf(e, 0x1p125f));
-    a = e < INFINITY ? r : 0.0f;
-    keep = e < 0x1p125f ? e * r : 1.0f;
-    if (g != g) a = keep = g;
+// a = 1 / (1 + e^-g) and 1 - a = e^-g / (1 + e^-g), neither by a subtraction; each is off by some
+// 4 * 2^-24 of itself. The hardware's 2^p takes p = -g / ln 2 rounded; what that lost, r, is put back
+// as e (1 + r). Gates are taken to [-86, 104]: 2^124 has a normal reciprocal, and 1 - a is 0 from
+// 87.4 on. A NaN stays one.
+__device__ __forceinline__ void sigmoids(float2 g, float2& a, float2& keep) {
+    float2 v, e;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(v.x) : "f"(-g.x), "f"(-104.0f));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(v.y) : "f"(-g.y), "f"(-104.0f));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(v.x) : "f"(v.x), "f"(86.0f));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(v.y) : "f"(v.y), "f"(86.0f));
+    const float2 p = mul2(v, both(1.44269504f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(p.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(p.y));
+    e = fma2(e, fma2(p, both(-0.69314718f), v), e);
+    const float2 d = add2(both(1.0f), e);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a.x) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a.y) : "f"(d.y));
+    keep = mul2(e, a);
 }
 
 // h -> A h + B, two columns.
 struct Map {
-    float4 m;  // A, A, B, B
+    float2 A, B;
     __device__ float2 operator()(float2 h) const {
-        return {m.x < 0.0f ? m.z : fmaf(m.x, h.x, m.z), m.y < 0.0f ? m.w : fmaf(m.y, h.y, m.w)};
+        const float2 r = fma2(A, h, B);
+        return {A.x < 0.0f ? B.x : r.x, A.y < 0.0f ? B.y : r.y};
     }
+    // this one first, then q
+    __device__ Map then(const Map& q) const {
+        const float2 p = mul2(q.A, A);
+        return {{fminf(q.A.x, A.x) < 0.0f ? kReset : p.x, fminf(q.A.y, A.y) < 0.0f ? kReset : p.y},
+                q(B)};
+    }
+    // the same where neither has a reset
+    __device__ Map plain_then(const Map& q) const { return {mul2(q.A, A), fma2(q.A, B, q.B)}; }
+    __device__ float4 packed() const { return {A.x, A.y, B.x, B.y}; }
 };
+__device__ __forceinline__ Map map_of(const float4& v) { return {{v.x, v.y}, {v.z, v.w}}; }
+__device__ __forceinline__ Map identity() { return {both(1.0f), both(0.0f)}; }
 
 // The first index i in [0, n) with off[i] >= key, n if there is none. All lanes of a warp; any
 // contents (where they do not rise, any index).
@@ -134,25 +139,41 @@ __device__ __forceinline__ uint32_t first_from(const int64_t* off, uint32_t n, i
     return lo;
 }
 
-// Marks the rows of a chunk where a sequence starts or ends. starts, ends: the sequence, or -1.
-template <int kRows>
-__device__ __forceinline__ void mark_rows(const ScanArgs& a, uint32_t row0, int32_t* starts,
-                                          int32_t* ends) {
-    const int lane = threadIdx.x & 31;
-    for (int i = lane; i < kRows; i += 32) starts[i] = ends[i] = -1;
-    __syncwarp();
-    const uint32_t n = a.nseq + 1;
-    for (uint32_t i0 = first_from(a.offsets, n, row0);; i0 += 32) {
-        const uint32_t i = i0 + lane;
-        const int64_t off = i < n ? a.offsets[i] : INT64_MAX;
-        if (off >= (int64_t)row0 && off <= (int64_t)row0 + kRows) {
-            const int r = (int)(off - row0);
-            if (r < kRows && i + 1 < n && a.offsets[i + 1] > off) starts[r] = (int32_t)i;
-            if (r > 0 && i > 0 && a.offsets[i - 1] < off) ends[r - 1] = (int32_t)i - 1;
+// Where sequences start and end in a warp's kS rows: bits, and the sequences in the arrays (the
+// warp's own). mine: the lane's entry of a table of at most 32.
+template <int kS>
+struct Marks {
+    uint32_t start, end;
+    __device__ Marks(const ScanArgs& a, uint32_t first, int64_t mine, int32_t* starts,
+                     int32_t* ends) {
+        const uint32_t lane = threadIdx.x & 31, n = a.nseq + 1;
+        const int64_t begin = first, stop = begin + kS;
+        start = end = 0;
+        __syncwarp();  // the arrays' readers of the tile before
+        for (uint32_t i0 = n <= 32 ? 0 : first_from(a.offsets, n, begin);; i0 += 32) {
+            const uint32_t i = i0 + lane;
+            const int64_t off = n <= 32 ? mine : i < n ? a.offsets[i] : INT64_MAX;
+            if (__any_sync(kFull, off >= begin && off <= stop)) {
+                uint32_t s = 0, e = 0;
+                if (off >= begin && off <= stop) {
+                    const int r = (int)(off - begin);
+                    if (r < kS && i + 1 < n && a.offsets[i + 1] > off) {
+                        starts[r] = (int32_t)i;
+                        s = 1u << r;
+                    }
+                    if (r > 0 && i > 0 && a.offsets[i - 1] < off) {
+                        ends[r - 1] = (int32_t)i - 1;
+                        e = 1u << (r - 1);
+                    }
+                }
+                start |= __reduce_or_sync(kFull, s);
+                end |= __reduce_or_sync(kFull, e);
+            }
+            if (n <= 32 || !__all_sync(kFull, off <= stop)) break;
         }
-        if (!__all_sync(kFull, off <= (int64_t)row0 + kRows)) break;
+        __syncwarp();
     }
-}
+};
 
 // What has no row: sequences of length 0 pass their state on; and the table's check. By the first
 // chunk's blocks.
@@ -175,339 +196,522 @@ __device__ __forceinline__ void empty_sequences(const ScanArgs& a, uint32_t tile
     if (tile == 0 && bad) report(a.status, DGC_EINVAL);
 }
 
-// The chunk and the column tile of this block.
-__device__ __forceinline__ uint32_t take_ticket(const ScanArgs& a, uint32_t* slot) {
-    if (!a.ticket) return blockIdx.x;
-    if (threadIdx.x == 0) *slot = atomicAdd(a.ticket, 1u);
-    __syncthreads();
-    return *slot;
+// A tile: its chunk's place in the scan's direction, and its columns. order of chunks on: none.
+struct Tile {
+    uint32_t order, tile;
+};
+// A block's tiles. The first one is computed, the others, kAhead, have their copies under way (the
+// last one's begin with the first one's computation).
+template <int kAhead>
+struct Tiles {
+    Tile held[kAhead + 1];
+    __device__ Tiles(const ScanArgs& a, uint32_t* slot) {
+        if (!a.ticket) {
+            held[0] = {0, blockIdx.x};
+#pragma unroll
+            for (int i = 1; i <= kAhead; ++i) held[i] = {a.chunks, 0};
+            return;
+        }
+        // One by one: neighbouring tickets belong to blocks that work at the same time. (Taken
+        // together, each block's second tile kept others waiting for its first: 630 us for 279.)
+#pragma unroll
+        for (int i = 0; i <= kAhead; ++i) {
+            if (threadIdx.x == 0) *slot = atomicAdd(a.ticket, 1u);
+            __syncthreads();
+            held[i] = {*slot / a.tiles, *slot % a.tiles};
+            __syncthreads();
+        }
+    }
+    __device__ void step(const ScanArgs& a, uint32_t ticket) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) held[i] = held[i + 1];
+        held[kAhead] = {ticket / a.tiles, ticket % a.tiles};
+    }
+};
+
+// What the warps of a block tell one another about a tile. A tile has two barriers: what is written
+// ahead of the first one is read between the two, what is written between them is read behind the
+// second one and ahead of the next tile's first.
+struct Board {
+    float4 map[kWarps][32];    // the warps' maps, in the scan's direction
+    float4 ahead[kWarps][32];  // the chunks' ahead of this one, four to an entry
+    float2 state[32];          // that enters the group
+    uint32_t next;             // ticket
+    uint32_t fresh;            // a sequence begins with the chunk: nothing enters
+};
+
+__device__ __forceinline__ uint32_t not_kept(float f) {  // the bits, never kNotYet
+    const uint32_t b = __float_as_uint(f);
+    return b == kNotYet ? 0x7FFFFFFFu : b;
+}
+__device__ __forceinline__ void publish(uint4* p, const Map& m) {
+    asm volatile("st.relaxed.gpu.global.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p),
+                 "r"(not_kept(m.A.x)), "r"(not_kept(m.A.y)), "r"(not_kept(m.B.x)),
+                 "r"(not_kept(m.B.y))
+                 : "memory");
+}
+__device__ __forceinline__ void publish(uint2* p, float2 h) {
+    asm volatile("st.relaxed.gpu.global.v2.u32 [%0], {%1, %2};" ::"l"(p), "r"(not_kept(h.x)),
+                 "r"(not_kept(h.y))
+                 : "memory");
+}
+__device__ __forceinline__ uint4 look(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.relaxed.gpu.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 look(const uint2* p) {
+    uint2 v;
+    asm volatile("ld.relaxed.gpu.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ bool there(const uint4& v) {
+    return v.x != kNotYet && v.y != kNotYet && v.z != kNotYet && v.w != kNotYet;
+}
+__device__ __forceinline__ bool there(const uint2& v) { return v.x != kNotYet && v.y != kNotYet; }
+
+// Whether a wait goes on, after so many polls. When one gives up, the others do too.
+__device__ __forceinline__ bool wait_on(const ScanArgs& a, uint32_t polls) {
+    if (polls <= a.spin_limit && ((polls & 63) != 63 || ld_relaxed_u32(a.abort) == 0)) {
+        __nanosleep(20);
+        return true;
+    }
+    if ((threadIdx.x & 31) == 0) {
+        report(a.status, DGC_ETIMEOUT);
+        atomicExch(a.abort, 1u);
+    }
+    return false;
 }
 
-// By the first warp: publishes the chunk's map, if the last of a group the state behind it too, and
-// returns the state that enters the chunk. order: the chunk's place in the scan's direction.
-// no_carry: nothing enters (a sequence begins with the chunk).
-__device__ __forceinline__ void publish_map(const ScanArgs& a, uint32_t order, uint32_t tile,
-                                            const Map& m) {
-    const int lane = threadIdx.x & 31;
-    if (!a.ticket || order == a.lost) return;
-    a.maps[((uint64_t)order * a.tiles + tile) * 32 + lane] = m.m;
-    __threadfence();
-    __syncwarp();
-    if (lane == 0) st_release(&a.chunk_flag[(uint64_t)tile * a.chunks + order], 1);
+// Step 2 by all warps: `w` is the warp's place in the scan's direction, m its map (on the board),
+// `order` the chunk's place, resets: whether a sequence begins in it. Returns the map of the warps ahead of this one; a barrier has to follow.
+__device__ __forceinline__ Map collect(const ScanArgs& a, Board& b, uint32_t order, uint32_t tile,
+                                       int w, const Map& m, bool fresh, bool resets) {
+    const uint32_t lane = threadIdx.x & 31, group = order / kGroup, k = order % kGroup;
+    Map before = identity();
+    if (resets)
+        for (int i = 0; i < w; ++i) before = before.then(map_of(b.map[i][lane]));
+    else
+#pragma unroll
+        for (int i = 0; i < kWarps - 1; ++i)
+            if (i < w) before = before.plain_then(map_of(b.map[i][lane]));
+    if (!a.ticket) return before;
+    if (w == kWarps - 1 && order != a.lost)
+        publish(&a.maps[((uint64_t)order * a.tiles + tile) * 32 + lane], before.then(m));
+    if (fresh) return before;
+    const uint32_t from = 4 * (uint32_t)w, count = k > from ? min(4u, k - from) : 0;
+    if (count) {
+        const uint4* p = a.maps + (((uint64_t)group * kGroup + from) * a.tiles + tile) * 32 + lane;
+        const uint64_t step = (uint64_t)a.tiles * 32;
+        uint4 v[4];
+        for (uint32_t polls = 0;; ++polls) {
+            bool ready = true;
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i)
+                if (i < count) {
+                    v[i] = look(p + i * step);
+                    ready = ready && there(v[i]);
+                }
+            if (__all_sync(kFull, ready) || !wait_on(a, polls)) break;
+        }
+        Map all = identity();
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i)
+            if (i < count)
+                all = all.then({{__uint_as_float(v[i].x), __uint_as_float(v[i].y)},
+                                {__uint_as_float(v[i].z), __uint_as_float(v[i].w)}});
+        b.ahead[w][lane] = all.packed();
+    }
+    if (w == 0) {
+        float2 h = {0.0f, 0.0f};
+        if (group > 0) {
+            const uint2* p = &a.states[((uint64_t)group * a.tiles + tile) * 32 + lane];
+            uint2 v;
+            for (uint32_t polls = 0;; ++polls) {
+                v = look(p);
+                if (__all_sync(kFull, there(v)) || !wait_on(a, polls)) break;
+            }
+            h = {__uint_as_float(v.x), __uint_as_float(v.y)};
+        }
+        b.state[lane] = h;
+    }
+    return before;
 }
-__device__ __forceinline__ float2 enter_chunk(const ScanArgs& a, uint32_t order, uint32_t tile,
-                                              const Map& m, bool no_carry) {
-    const uint32_t lane = threadIdx.x & 31;
-    const uint32_t group = order / kGroup, k = order % kGroup;
-    const uint32_t groups = (a.chunks + kGroup - 1) / kGroup;
+
+// After the barrier: the state that enters the chunk. The last warp passes a group's on.
+__device__ __forceinline__ float2 enter(const ScanArgs& a, const Board& b, uint32_t order,
+                                        uint32_t tile, int w, const Map& before, const Map& m,
+                                        bool fresh) {
+    const uint32_t lane = threadIdx.x & 31, group = order / kGroup, k = order % kGroup;
     float2 h = {0.0f, 0.0f};
     if (!a.ticket) return h;
-    if (!no_carry) {
-        const uint32_t* flag = nullptr;
-        if (lane < k)
-            flag = &a.chunk_flag[(uint64_t)tile * a.chunks + group * kGroup + lane];
-        else if (lane == 31 && group > 0)
-            flag = &a.group_flag[(uint64_t)tile * groups + group];
-        bool ready = flag == nullptr;
-        for (uint32_t spins = 0;; ++spins) {
-            if (!ready) ready = ld_acquire(flag) != 0;
-            if (__all_sync(kFull, ready)) break;
-            if (spins > a.spin_limit || ((spins & 63) == 63 && ld_acquire(a.abort) != 0)) {
-                if (lane == 0) {
-                    report(a.status, DGC_ETIMEOUT);
-                    atomicExch(a.abort, 1u);
-                }
-                break;
-            }
-            __nanosleep(20);
-        }
-        __threadfence();
-        if (group > 0) h = __ldcg(&a.states[((uint64_t)group * a.tiles + tile) * 32 + lane]);
-        const float4* maps = a.maps + ((uint64_t)group * kGroup * a.tiles + tile) * 32 + lane;
-        const uint64_t step = (uint64_t)a.tiles * 32;
-        for (uint32_t i = 0; i < k; i += 8) {
-            Map p[8];
-#pragma unroll
-            for (uint32_t j = 0; j < 8; ++j)
-                if (i + j < k) p[j].m = __ldcg(maps + (i + j) * step);
-#pragma unroll
-            for (uint32_t j = 0; j < 8; ++j)
-                if (i + j < k) h = p[j](h);
-        }
+    if (!fresh) {
+        h = b.state[lane];
+        for (uint32_t i = 0; 4 * i < k; ++i) h = map_of(b.ahead[i][lane])(h);
     }
-    if (k == kGroup - 1 && group + 1 < groups && order != a.lost) {
-        a.states[((uint64_t)(group + 1) * a.tiles + tile) * 32 + lane] = m(h);
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) st_release(&a.group_flag[(uint64_t)tile * groups + group + 1], 1);
-    }
+    if (w == kWarps - 1 && k == kGroup - 1 && order + 1 < a.chunks && order != a.lost)
+        publish(&a.states[((uint64_t)(group + 1) * a.tiles + tile) * 32 + lane], m(before(h)));
     return h;
 }
 
-// Composes the maps of the warps before (or, from the end, behind) one.
-struct WarpMaps {
-    float4 m[kWarps][32];
-};
-
-__global__ void __launch_bounds__(256) k_scan_clear(uint32_t* words, uint64_t n) {
+__global__ void __launch_bounds__(256)
+    k_scan_clear(uint32_t* control, uint4* words, uint64_t n) {
     grid_dep_wait();
     grid_dep_launch();
+    if (blockIdx.x == 0 && threadIdx.x < 2) control[threadIdx.x] = 0;
     for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (uint64_t)gridDim.x * 256)
-        words[i] = 0;
+        words[i] = make_uint4(kNotYet, kNotYet, kNotYet, kNotYet);
 }
 
+// The operands' tiles in shared memory, each warp's rows for itself, by copies of kUnit bytes: 16
+// where every operand's rows allow it, two entries, or (0) by loads and stores of single ones.
+template <typename T, int kUnit, int kS, int kOperands>
+struct Landing {
+    using Word = std::conditional_t<sizeof(T) == 4, uint2, uint32_t>;  // a lane's two columns
+    static constexpr uint32_t kRow = kCols * sizeof(T);
+    static constexpr uint32_t kStageBytes = kOperands * kWarps * kS * kRow;
+    Word* words;
+    __device__ explicit Landing(void* ring) : words(static_cast<Word*>(ring)) {}
+    __device__ Word* rows(int stage, int q) const {
+        return words + ((stage * kOperands + q) * kWarps + (threadIdx.x >> 5)) * kS * 32;
+    }
+    // rows `first` to first + kS - 1 of m, of which `left` are there, columns from col on
+    __device__ void fetch(int stage, int q, const void* m, uint64_t ld, uint64_t first,
+                          uint32_t left, uint32_t col, uint32_t cols) const {
+        const uint32_t lane = threadIdx.x & 31;
+        const T* p = static_cast<const T*>(m) + first * ld + col;
+        Word* to = rows(stage, q);
+        if constexpr (kUnit == 16) {
+            constexpr uint32_t kLanes = kRow / 16, kStep = 32 / kLanes;  // of a row; rows a turn
+            const uint32_t r = lane / kLanes, c = lane % kLanes * (16 / sizeof(T));
+            const T* src = p + r * ld + c;
+            uint4* dst = reinterpret_cast<uint4*>(to) + lane;
+            const uint32_t n = cols - col > c ? min(cols - col - c, 16u / (uint32_t)sizeof(T)) : 0;
+            if (left >= kS && cols - col >= kCols) {
+#pragma unroll
+                for (int i = 0; i < kS / (int)kStep; ++i, src += kStep * ld)
+                    copy_async<16>(dst + i * 32, src, 16);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kS / (int)kStep; ++i, src += kStep * ld) {
+                    const uint32_t here = r + i * kStep < left ? n : 0;
+                    copy_async<16>(dst + i * 32, here ? src : m, here * sizeof(T));
+                }
+            }
+        } else {
+            p += 2 * lane;
+            to += lane;
+            const uint32_t n = cols - col > 2 * lane ? min(cols - col - 2 * lane, 2u) : 0;
+            if constexpr (kUnit != 0) {
+#pragma unroll
+                for (int s = 0; s < kS; ++s) {
+                    const uint32_t here = s < left ? n : 0;
+                    copy_async<sizeof(Word)>(to + s * 32, here ? p + s * ld : m, here * sizeof(T));
+                }
+            } else {
+                Packed<T, 2> v[kS];
+#pragma unroll
+                for (int s = 0; s < kS; ++s) v[s] = load_some<T, 2>(p + s * ld, s < left ? n : 0);
+#pragma unroll
+                for (int s = 0; s < kS; ++s) to[s * 32] = *reinterpret_cast<Word*>(v[s].w);
+            }
+        }
+    }
+    __device__ float2 get(int stage, int q, int s) const {
+        Packed<T, 2> p;
+        *reinterpret_cast<Word*>(p.w) = rows(stage, q)[s * 32 + (threadIdx.x & 31)];
+        return pair_of<T, 2>(p, 0);
+    }
+};
+
+// What a warp has of a tile: its rows, how many of them there are, and its lane's columns.
+struct Spot {
+    uint32_t first, left, col, lane_col, n;
+    __device__ Spot(const ScanArgs& a, uint32_t chunk, uint32_t tile, uint32_t rows, uint32_t s) {
+        first = chunk * rows + (threadIdx.x >> 5) * s;
+        left = first < a.rows ? a.rows - first : 0;
+        col = tile * kCols;
+        lane_col = col + 2 * (threadIdx.x & 31);
+        n = lane_col < a.cols ? min(2u, a.cols - lane_col) : 0;
+    }
+};
+
 // --------------------------------------------------------------------------------- forward
-// Bound by HBM: x and gate read once, y written once.
-template <typename T, bool kPair, int kS>
-__global__ void __launch_bounds__(kThreads) k_scan(const __grid_constant__ ScanArgs a) {
-    constexpr int kRows = kWarps * kS;
-    __shared__ int32_t starts[kRows], ends[kRows];
-    __shared__ WarpMaps maps;
-    __shared__ float2 enter[32];
-    __shared__ uint32_t slot;
+// Bound by HBM: x and gate read once, y written once. Rows with no border among them and whole
+// columns take a way without tests.
+template <typename T, int kUnit, int kS, int kStages>
+__global__ void __launch_bounds__(kThreads, 2) k_scan(const __grid_constant__ ScanArgs a) {
+    constexpr int kRows = kWarps * kS, kAhead = kStages - 1;
+    constexpr bool kPair = kUnit != 0;
+    extern __shared__ uint4 ring[];
+    __shared__ Board board;
+    __shared__ int32_t starts_of[kWarps][kS], ends_of[kWarps][kS];
+    const Landing<T, kUnit, kS, 2> land(ring);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int32_t *starts = starts_of[warp], *ends = ends_of[warp];
     grid_dep_wait();
     grid_dep_launch();
-    const uint32_t ticket = take_ticket(a, &slot);
-    const uint32_t chunk = ticket / a.tiles, tile = ticket % a.tiles;
-    const uint32_t row0 = chunk * kRows, first = row0 + warp * kS;
-    const uint32_t col = tile * kCols + 2 * lane, n = col < a.cols ? min(2u, a.cols - col) : 0;
-    Two<T> px[kS], pg[kS];
+    Tiles<kAhead> tiles(a, &board.next);
+    auto fetch = [&](int stage, const Tile& t) {
+        if (t.order < a.chunks) {
+            const Spot at(a, t.order, t.tile, kRows, kS);
+            land.fetch(stage, 0, a.gate, a.ldg, at.first, at.left, at.col, a.cols);
+            land.fetch(stage, 1, a.x, a.ldx, at.first, at.left, at.col, a.cols);
+        }
+        copy_commit();
+    };
 #pragma unroll
-    for (int s = 0; s < kS; ++s) {
-        const uint32_t here = first + s < a.rows ? n : 0;
-        pg[s] = Two<T>::template load<kPair>(a.gate, a.ldg, first + s, col, here);
-        px[s] = Two<T>::template load<kPair>(a.x, a.ldx, first + s, col, here);
-    }
-    const int64_t valid0 = a.offsets[0], valid1 = a.offsets[a.nseq];
-    if (warp == kWarps - 1) mark_rows<kRows>(a, row0, starts, ends);
-    if (chunk == 0) empty_sequences(a, tile, a.h0, a.ldh0, a.h_last, a.ldh_last);
-    __syncthreads();
-    uint32_t start_bits = 0, end_bits = 0;
-    {
-        const int r = warp * kS + (lane < kS ? lane : 0);
-        start_bits = __ballot_sync(kFull, lane < kS && starts[r] >= 0);
-        end_bits = __ballot_sync(kFull, lane < kS && ends[r] >= 0);
-    }
-    // rows as h -> A h + B
-    float2 A[kS], B[kS];
+    for (int i = 0; i < kAhead; ++i) fetch(i, tiles.held[i]);
+    const int64_t valid0 = a.offsets[0], valid1 = min((int64_t)a.rows, a.offsets[a.nseq]);
+    const int64_t mine = lane <= a.nseq ? a.offsets[lane] : INT64_MAX;
+    for (int stage = 0; tiles.held[0].order < a.chunks;) {
+        uint32_t more = 0xFFFFFFFFu;  // the ticket behind those that are held
+        if (a.ticket && threadIdx.x == 0) more = atomicAdd(a.ticket, 1u);
+        fetch(stage == 0 ? kStages - 1 : stage - 1, tiles.held[kAhead]);
+        const uint32_t chunk = tiles.held[0].order, tile = tiles.held[0].tile;
+        const Spot at(a, chunk, tile, kRows, kS);
+        if (chunk == 0) empty_sequences(a, tile, a.h0, a.ldh0, a.h_last, a.ldh_last);
+        const Marks<kS> marks(a, at.first, mine, starts, ends);
+        copy_wait<kAhead>();
+        __syncwarp();
+        // rows as h -> A h + B
+        float2 A[kS], B[kS];
 #pragma unroll
-    for (int s = 0; s < kS; ++s) {
-        const float2 g = pg[s].up(), x = px[s].up();
-        float2 keep;
-        sigmoid2(g.x, A[s].x, keep.x);
-        sigmoid2(g.y, A[s].y, keep.y);
-        B[s] = {keep.x * x.x, keep.y * x.y};
-    }
-    if (start_bits && a.h0) {
-        float2 h[kS];
+        for (int s = 0; s < kS; ++s) {
+            float2 keep;
+            sigmoids(land.get(stage, 0, s), A[s], keep);
+            B[s] = mul2(keep, land.get(stage, 1, s));
+        }
+        Map m = identity();
+        if (marks.start) {
+            if (a.h0) {
+                float2 h[kS];
 #pragma unroll
-        for (int s = 0; s < kS; ++s)
-            h[s] = load_state(a.h0, a.ldh0, start_bits >> s & 1 ? starts[warp * kS + s] : 0, col,
-                              start_bits >> s & 1 ? n : 0);
+                for (int s = 0; s < kS; ++s) {
+                    const bool here = marks.start >> s & 1;
+                    h[s] = load_state(a.h0, a.ldh0, here ? starts[s] : 0, at.lane_col,
+                                      here ? at.n : 0);
+                }
 #pragma unroll
-        for (int s = 0; s < kS; ++s)
-            if (start_bits >> s & 1) {
-                B[s].x = fmaf(A[s].x, h[s].x, B[s].x);
-                B[s].y = fmaf(A[s].y, h[s].y, B[s].y);
+                for (int s = 0; s < kS; ++s)
+                    if (marks.start >> s & 1) B[s] = fma2(A[s], h[s], B[s]);
             }
-    }
-    Map m{{1.0f, 1.0f, 0.0f, 0.0f}};
 #pragma unroll
-    for (int s = 0; s < kS; ++s) {
-        if (start_bits >> s & 1) {
-            m.m = {kReset, kReset, B[s].x, B[s].y};
+            for (int s = 0; s < kS; ++s)
+                m = marks.start >> s & 1 ? Map{both(kReset), B[s]} : m.then({A[s], B[s]});
         } else {
-            m.m.z = fmaf(A[s].x, m.m.z, B[s].x);
-            m.m.w = fmaf(A[s].y, m.m.w, B[s].y);
-            m.m.x = m.m.x < 0.0f ? kReset : m.m.x * A[s].x;
-            m.m.y = m.m.y < 0.0f ? kReset : m.m.y * A[s].y;
-        }
-    }
-    maps.m[warp][lane] = m.m;
-    __syncthreads();
-    if (warp == 0) {
-        Map all = m;
-        for (int w = 1; w < kWarps; ++w) {
-            const Map q{maps.m[w][lane]};
-            const float2 b = q({all.m.z, all.m.w});
-            all.m = {q.m.x < 0.0f || all.m.x < 0.0f ? kReset : q.m.x * all.m.x,
-                     q.m.y < 0.0f || all.m.y < 0.0f ? kReset : q.m.y * all.m.y, b.x, b.y};
-        }
-        publish_map(a, chunk, tile, all);
-        enter[lane] = enter_chunk(a, chunk, tile, all, starts[0] >= 0);
-    }
-    __syncthreads();
-    float2 h = enter[lane];
-    for (int w = 0; w < warp; ++w) h = Map{maps.m[w][lane]}(h);
-    if (a.saved && first % kPiece == 0 && first < a.rows)
-        store_state(a.saved, a.lds, first / kPiece, col, n, h);
 #pragma unroll
-    for (int s = 0; s < kS; ++s) {
-        const uint32_t row = first + s;
-        if (start_bits >> s & 1) {
-            h = B[s];
-        } else {
-            h.x = fmaf(A[s].x, h.x, B[s].x);
-            h.y = fmaf(A[s].y, h.y, B[s].y);
+            for (int s = 0; s < kS; ++s) m = m.plain_then({A[s], B[s]});
         }
-        if (row < a.rows && row >= valid0 && row < valid1)
-            store_two<T, kPair>(a.y, a.ldy, row, col, n, h);
-        if (a.h_last && (end_bits >> s & 1) && row < a.rows)
-            store_state(a.h_last, a.ldh_last, ends[warp * kS + s], col, n, h);
+        board.map[warp][lane] = m.packed();
+        if (threadIdx.x == 0) {
+            board.fresh = marks.start & 1;
+            board.next = more;
+        }
+        const bool resets = __syncthreads_or(marks.start != 0);
+        const uint32_t next = board.next;
+        const bool fresh = board.fresh;
+        const Map before = collect(a, board, chunk, tile, warp, m, fresh, resets);
+        __syncthreads();
+        float2 h = before(enter(a, board, chunk, tile, warp, before, m, fresh));
+        if (a.saved && at.first % kPiece == 0 && at.left)
+            store_state(a.saved, a.lds, at.first / kPiece, at.lane_col, at.n, h);
+        if (kPair && !(marks.start | marks.end) && at.first >= valid0 && at.first + kS <= valid1 &&
+            at.col + kCols <= a.cols) {
+            T* y = static_cast<T*>(a.y) + at.first * a.ldy + at.lane_col;
+#pragma unroll
+            for (int s = 0; s < kS; ++s, y += a.ldy) {
+                h = fma2(A[s], h, B[s]);
+                Packed<T, 2> p;
+                set_pair<T, 2>(p, 0, h);
+                store_packed<T, 2>(y, p);
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < kS; ++s) {
+                const int64_t row = at.first + s;
+                h = marks.start >> s & 1 ? B[s] : fma2(A[s], h, B[s]);
+                if (row >= valid0 && row < valid1)
+                    store_two<T, kPair>(a.y, a.ldy, row, at.lane_col, at.n, h);
+                if (a.h_last && (marks.end >> s & 1) && s < at.left)
+                    store_state(a.h_last, a.ldh_last, ends[s], at.lane_col, at.n, h);
+            }
+        }
+        tiles.step(a, next);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
     }
+    copy_wait<0>();
 }
 
 // -------------------------------------------------------------------------------- backward
 // Bound by HBM: x, gate and dy read once, dx and dgate written once, the states of every 64th row.
-template <typename T, bool kPair, int kS>
-__global__ void __launch_bounds__(kThreads) k_scan_back(const __grid_constant__ ScanArgs a) {
-    constexpr int kRows = kWarps * kS;
-    static_assert(kRows % kPiece == 0 && kPiece % kS == 0, "a chunk begins at a saved state");
-    __shared__ int32_t starts[kRows], ends[kRows];
-    __shared__ WarpMaps maps, back;
-    __shared__ float2 enter[32];
-    __shared__ uint32_t slot;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+template <typename T, int kUnit, int kS, int kStages>
+__global__ void __launch_bounds__(kThreads, 2) k_scan_back(const __grid_constant__ ScanArgs a) {
+    constexpr int kRows = kWarps * kS, kAhead = kStages - 1;
+    constexpr bool kPair = kUnit != 0;
+    static_assert(kRows == kPiece, "a chunk begins at its saved state");
+    extern __shared__ uint4 ring[];
+    __shared__ Board board;
+    __shared__ float4 maps[kWarps][32];  // of h, as the board's are of u
+    __shared__ int32_t starts_of[kWarps][kS], ends_of[kWarps][kS];
+    const Landing<T, kUnit, kS, 3> land(ring);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, place = kWarps - 1 - warp;
+    int32_t *starts = starts_of[warp], *ends = ends_of[warp];
     grid_dep_wait();
     grid_dep_launch();
-    const uint32_t ticket = take_ticket(a, &slot);
-    const uint32_t order = ticket / a.tiles, tile = ticket % a.tiles;
-    const uint32_t chunk = a.chunks - 1 - order;
-    const uint32_t row0 = chunk * kRows, first = row0 + warp * kS;
-    const uint32_t col = tile * kCols + 2 * lane, n = col < a.cols ? min(2u, a.cols - col) : 0;
-    Two<T> px[kS], pg[kS], pd[kS];
+    Tiles<kAhead> tiles(a, &board.next);
+    auto fetch = [&](int stage, const Tile& t) {
+        if (t.order < a.chunks) {
+            const Spot at(a, a.chunks - 1 - t.order, t.tile, kRows, kS);
+            land.fetch(stage, 0, a.gate, a.ldg, at.first, at.left, at.col, a.cols);
+            land.fetch(stage, 1, a.x, a.ldx, at.first, at.left, at.col, a.cols);
+            land.fetch(stage, 2, a.dy, a.lddy, at.first, at.left, at.col, a.cols);
+        }
+        copy_commit();
+    };
 #pragma unroll
-    for (int s = 0; s < kS; ++s) {
-        const uint32_t here = first + s < a.rows ? n : 0;
-        pg[s] = Two<T>::template load<kPair>(a.gate, a.ldg, first + s, col, here);
-        px[s] = Two<T>::template load<kPair>(a.x, a.ldx, first + s, col, here);
-        pd[s] = Two<T>::template load<kPair>(a.dy, a.lddy, first + s, col, here);
-    }
-    float2 h = row0 < a.rows ? load_state(a.saved, a.lds, row0 / kPiece, col, n)
-                             : make_float2(0.0f, 0.0f);
-    const int64_t valid0 = a.offsets[0], valid1 = a.offsets[a.nseq];
-    if (warp == kWarps - 1) mark_rows<kRows>(a, row0, starts, ends);
-    if (chunk == 0) empty_sequences(a, tile, a.d_last, a.ldd_last, a.d_h0, a.ldd_h0);
-    __syncthreads();
-    uint32_t start_bits = 0, end_bits = 0;
-    {
-        const int r = warp * kS + (lane < kS ? lane : 0);
-        start_bits = __ballot_sync(kFull, lane < kS && starts[r] >= 0);
-        end_bits = __ballot_sync(kFull, lane < kS && ends[r] >= 0);
-    }
-    float2 A[kS], keep[kS], q[kS], G[kS];  // q: x, then (h_{t-1} - x) a (1 - a)
+    for (int i = 0; i < kAhead; ++i) fetch(i, tiles.held[i]);
+    const int64_t valid0 = a.offsets[0], valid1 = min((int64_t)a.rows, a.offsets[a.nseq]);
+    const int64_t mine = lane <= a.nseq ? a.offsets[lane] : INT64_MAX;
+    for (int stage = 0; tiles.held[0].order < a.chunks;) {
+        uint32_t more = 0xFFFFFFFFu;
+        if (a.ticket && threadIdx.x == 0) more = atomicAdd(a.ticket, 1u);
+        fetch(stage == 0 ? kStages - 1 : stage - 1, tiles.held[kAhead]);
+        const uint32_t order = tiles.held[0].order, tile = tiles.held[0].tile;
+        const uint32_t chunk = a.chunks - 1 - order;
+        const Spot at(a, chunk, tile, kRows, kS);
+        float2 h = both(0.0f);
+        if (chunk * kRows < a.rows) h = load_state(a.saved, a.lds, chunk, at.lane_col, at.n);
+        if (chunk == 0) empty_sequences(a, tile, a.d_last, a.ldd_last, a.d_h0, a.ldd_h0);
+        const Marks<kS> marks(a, at.first, mine, starts, ends);
+        copy_wait<kAhead>();
+        __syncwarp();
+        float2 A[kS], keep[kS], q[kS], G[kS];  // q: (1-a) x, then (h_{t-1} - x) a (1 - a)
 #pragma unroll
-    for (int s = 0; s < kS; ++s) {
-        const float2 g = pg[s].up();
-        q[s] = px[s].up();
-        G[s] = pd[s].up();
-        sigmoid2(g.x, A[s].x, keep[s].x);
-        sigmoid2(g.y, A[s].y, keep[s].y);
-    }
-    if (end_bits && a.d_last)
+        for (int s = 0; s < kS; ++s) {
+            sigmoids(land.get(stage, 0, s), A[s], keep[s]);
+            q[s] = mul2(keep[s], land.get(stage, 1, s));
+            G[s] = land.get(stage, 2, s);
+        }
+        if (marks.end && a.d_last)
 #pragma unroll
-        for (int s = 0; s < kS; ++s)
-            if (end_bits >> s & 1) {
-                const float2 d = load_state(a.d_last, a.ldd_last, ends[warp * kS + s], col, n);
-                G[s].x += d.x;
-                G[s].y += d.y;
+            for (int s = 0; s < kS; ++s)
+                if (marks.end >> s & 1)
+                    G[s] = add2(G[s], load_state(a.d_last, a.ldd_last, ends[s], at.lane_col, at.n));
+        // the rows' map of h, and from the end that of u
+        Map m = identity(), u = identity();
+        auto first_state = [&](int s) {
+            return a.h0 ? load_state(a.h0, a.ldh0, starts[s], at.lane_col, at.n) : both(0.0f);
+        };
+        if (marks.start | marks.end) {
+#pragma unroll
+            for (int s = 0; s < kS; ++s)
+                m = marks.start >> s & 1 ? Map{both(kReset), fma2(A[s], first_state(s), q[s])}
+                                         : m.then({A[s], q[s]});
+#pragma unroll
+            for (int s = kS - 1; s >= 0; --s) {
+                const Map row{A[s], mul2(A[s], G[s])};
+                u = marks.end >> s & 1 ? Map{both(kReset), row.B} : u.then(row);
             }
-    // the rows' map of h, and from the end that of u
-    Map m{{1.0f, 1.0f, 0.0f, 0.0f}}, u{{1.0f, 1.0f, 0.0f, 0.0f}};
-    float2 first_h[kS];  // a sequence's first state where one starts
-#pragma unroll
-    for (int s = 0; s < kS; ++s) {
-        first_h[s] = {0.0f, 0.0f};
-        if ((start_bits >> s & 1) && a.h0)
-            first_h[s] = load_state(a.h0, a.ldh0, starts[warp * kS + s], col, n);
-        const float2 b = {keep[s].x * q[s].x, keep[s].y * q[s].y};
-        if (start_bits >> s & 1) {
-            m.m = {kReset, kReset, fmaf(A[s].x, first_h[s].x, b.x), fmaf(A[s].y, first_h[s].y, b.y)};
         } else {
-            m.m.z = fmaf(A[s].x, m.m.z, b.x);
-            m.m.w = fmaf(A[s].y, m.m.w, b.y);
-            m.m.x = m.m.x < 0.0f ? kReset : m.m.x * A[s].x;
-            m.m.y = m.m.y < 0.0f ? kReset : m.m.y * A[s].y;
-        }
-    }
 #pragma unroll
-    for (int s = kS - 1; s >= 0; --s) {
-        if (end_bits >> s & 1) {
-            u.m = {kReset, kReset, A[s].x * G[s].x, A[s].y * G[s].y};
+            for (int s = 0; s < kS; ++s) m = m.plain_then({A[s], q[s]});
+#pragma unroll
+            for (int s = kS - 1; s >= 0; --s) u.B = mul2(A[s], add2(G[s], u.B));
+            u.A = m.A;
+        }
+        maps[warp][lane] = m.packed();
+        board.map[place][lane] = u.packed();
+        if (threadIdx.x == kThreads - 1) board.fresh = marks.end >> (kS - 1) & 1;
+        if (threadIdx.x == 0) board.next = more;
+        const bool resets = __syncthreads_or((marks.start | marks.end) != 0);
+        const uint32_t next = board.next;
+        const bool fresh = board.fresh;
+        const Map behind = collect(a, board, order, tile, place, u, fresh, resets);
+        if (resets)
+            for (int w = 0; w < warp; ++w) h = map_of(maps[w][lane])(h);
+        else
+#pragma unroll
+            for (int w = 0; w < kWarps - 1; ++w)
+                if (w < warp) {
+                    const Map p = map_of(maps[w][lane]);
+                    h = fma2(p.A, h, p.B);
+                }
+#pragma unroll
+        for (int s = 0; s < kS; ++s) {
+            if (marks.start >> s & 1) h = first_state(s);
+            const float2 x = land.get(stage, 1, s), b = q[s];
+            q[s] = mul2(mul2(A[s], keep[s]), add2(h, {-x.x, -x.y}));
+            h = fma2(A[s], h, b);
+        }
+        __syncthreads();
+        // u of the row behind
+        float2 v = behind(enter(a, board, order, tile, place, behind, u, fresh));
+        if (kPair && !(marks.start | marks.end) && at.first >= valid0 && at.first + kS <= valid1 &&
+            at.col + kCols <= a.cols) {
+            T* dx = static_cast<T*>(a.dx) + (at.first + kS - 1) * a.lddx + at.lane_col;
+            T* dgate = static_cast<T*>(a.dgate) + (at.first + kS - 1) * a.lddg + at.lane_col;
+#pragma unroll
+            for (int s = kS - 1; s >= 0; --s, dx -= a.lddx, dgate -= a.lddg) {
+                const float2 g = add2(G[s], v);
+                Packed<T, 2> p, r;
+                set_pair<T, 2>(p, 0, mul2(g, keep[s]));
+                set_pair<T, 2>(r, 0, mul2(g, q[s]));
+                store_packed<T, 2>(dx, p);
+                store_packed<T, 2>(dgate, r);
+                v = mul2(A[s], g);
+            }
         } else {
-            u.m.z = A[s].x * (G[s].x + u.m.z);
-            u.m.w = A[s].y * (G[s].y + u.m.w);
-            u.m.x = u.m.x < 0.0f ? kReset : u.m.x * A[s].x;
-            u.m.y = u.m.y < 0.0f ? kReset : u.m.y * A[s].y;
-        }
-    }
-    maps.m[warp][lane] = m.m;
-    back.m[warp][lane] = u.m;
-    __syncthreads();
-    Map all = u;  // of the last warp, which is the first one from the end
-    if (warp == kWarps - 1) {
-        for (int w = kWarps - 2; w >= 0; --w) {
-            const Map p{back.m[w][lane]};
-            const float2 b = p({all.m.z, all.m.w});
-            all.m = {p.m.x < 0.0f || all.m.x < 0.0f ? kReset : p.m.x * all.m.x,
-                     p.m.y < 0.0f || all.m.y < 0.0f ? kReset : p.m.y * all.m.y, b.x, b.y};
-        }
-        publish_map(a, order, tile, all);
-    }
-    for (int w = 0; w < warp; ++w) h = Map{maps.m[w][lane]}(h);
 #pragma unroll
-    for (int s = 0; s < kS; ++s) {
-        if (start_bits >> s & 1) h = first_h[s];
-        const float2 x = q[s];
-        q[s] = {(h.x - x.x) * A[s].x * keep[s].x, (h.y - x.y) * A[s].y * keep[s].y};
-        h.x = fmaf(A[s].x, h.x, keep[s].x * x.x);
-        h.y = fmaf(A[s].y, h.y, keep[s].y * x.y);
-    }
-    if (warp == kWarps - 1)
-        enter[lane] = enter_chunk(a, order, tile, all, ends[kRows - 1] >= 0);
-    __syncthreads();
-    float2 v = enter[lane];  // u of the row behind
-    for (int w = kWarps - 1; w > warp; --w) v = Map{back.m[w][lane]}(v);
-#pragma unroll
-    for (int s = kS - 1; s >= 0; --s) {
-        const uint32_t row = first + s;
-        if (end_bits >> s & 1) v = {0.0f, 0.0f};
-        const float2 g = {G[s].x + v.x, G[s].y + v.y};
-        if (row < a.rows && row >= valid0 && row < valid1) {
-            store_two<T, kPair>(a.dx, a.lddx, row, col, n, {g.x * keep[s].x, g.y * keep[s].y});
-            store_two<T, kPair>(a.dgate, a.lddg, row, col, n, {g.x * q[s].x, g.y * q[s].y});
+            for (int s = kS - 1; s >= 0; --s) {
+                const int64_t row = at.first + s;
+                if (marks.end >> s & 1) v = both(0.0f);
+                const float2 g = add2(G[s], v);
+                if (row >= valid0 && row < valid1) {
+                    store_two<T, kPair>(a.dx, a.lddx, row, at.lane_col, at.n, mul2(g, keep[s]));
+                    store_two<T, kPair>(a.dgate, a.lddg, row, at.lane_col, at.n, mul2(g, q[s]));
+                }
+                v = mul2(A[s], g);
+                if (a.d_h0 && (marks.start >> s & 1) && s < at.left)
+                    store_state(a.d_h0, a.ldd_h0, starts[s], at.lane_col, at.n, v);
+            }
         }
-        v = {A[s].x * g.x, A[s].y * g.y};
-        if (a.d_h0 && (start_bits >> s & 1) && row < a.rows)
-            store_state(a.d_h0, a.ldd_h0, starts[warp * kS + s], col, n, v);
+        tiles.step(a, next);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
     }
+    copy_wait<0>();
 }
 
 // ----------------------------------------------------------------------------------- host
-constexpr uint32_t kBackRows = 64;     // of a chunk of the backward pass
-constexpr uint32_t kForwardRows = 128; // of the forward pass
+// Rows of a warp, and stages of the ring: 96 KB of it a block, two blocks an SM.
+template <typename T>
+struct Form {
+    static constexpr int kS = sizeof(T) == 2 ? 16 : 8, kStages = 3;
+    static constexpr int kBackS = kPiece / kWarps, kBackStages = sizeof(T) == 2 ? 4 : 2;
+};
 
 struct ScanLayout {
-    size_t flags, flag_words, maps, states, total;
+    size_t maps, states, total;
     uint32_t chunks, groups, tiles;
 };
 ScanLayout scan_layout(uint64_t rows, uint64_t cols, uint32_t chunk_rows) {
-    auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
     ScanLayout L{};
     L.chunks = (uint32_t)std::max<uint64_t>(1, (rows + chunk_rows - 1) / chunk_rows);
     L.groups = (L.chunks + kGroup - 1) / kGroup;
     L.tiles = (uint32_t)((cols + kCols - 1) / kCols);
     if (L.chunks == 1) return L;
-    L.flag_words = 2 + (size_t)L.tiles * (L.chunks + L.groups);
-    L.maps = up(L.flag_words * 4);
-    L.states = L.maps + (size_t)L.chunks * L.tiles * 32 * sizeof(float4);
-    L.total = up(L.states + (size_t)L.groups * L.tiles * 32 * sizeof(float2));
+    L.maps = 256;
+    L.states = L.maps + (size_t)L.chunks * L.tiles * 32 * sizeof(uint4);
+    L.total = (L.states + (size_t)L.groups * L.tiles * 32 * sizeof(uint2) + 255) & ~(size_t)255;
     return L;
 }
+// For the shortest chunks that the calls use.
 size_t scan_workspace(uint64_t rows, uint64_t cols) {
-    return std::max(scan_layout(rows, cols, kForwardRows).total,
-                    scan_layout(rows, cols, kBackRows).total);
+    return scan_layout(rows, cols, kPiece).total;
 }
 
 // A state of binary32, one row a sequence; may be missing.
@@ -522,24 +726,32 @@ int check_state(const dgc_matrix* m, uint64_t nseq, uint64_t cols, const float**
     return DGC_OK;
 }
 
-int start_scan(ScanArgs& a, const ScanLayout& L, void* ws, cudaStream_t s) {
+template <typename T, int kUnit, int kS, int kOperands, int kStages>
+int launch_scan(void (*kernel)(ScanArgs), ScanArgs a, void* ws, int sms, cudaStream_t s) {
+    const ScanLayout L = scan_layout(a.rows, a.cols, kWarps * kS);
+    if ((uint64_t)L.tiles * L.chunks > 0x7FFFFFFFull) return DGC_EUNSUPPORTED;
     a.tiles = L.tiles;
     a.chunks = L.chunks;
     if (!a.spin_limit) {
         a.spin_limit = kDefaultSpinLimit;
         a.lost = ~0u;
     }
-    if (L.chunks == 1) return DGC_OK;
-    char* w = static_cast<char*>(ws);
-    a.ticket = reinterpret_cast<uint32_t*>(w);
-    a.abort = a.ticket + 1;
-    a.chunk_flag = a.ticket + 2;
-    a.group_flag = a.chunk_flag + (size_t)L.tiles * L.chunks;
-    a.maps = reinterpret_cast<float4*>(w + L.maps);
-    a.states = reinterpret_cast<float2*>(w + L.states);
-    const unsigned blocks = (unsigned)std::min<size_t>(1024, (L.flag_words + 1023) / 1024);
-    return launch_rows_kernel(k_scan_clear, dim3(blocks), 256, s, a.ticket,
-                              (uint64_t)L.flag_words);
+    uint32_t blocks = L.tiles;
+    if (L.chunks > 1) {
+        char* w = static_cast<char*>(ws);
+        a.ticket = reinterpret_cast<uint32_t*>(w);
+        a.abort = a.ticket + 1;
+        a.maps = reinterpret_cast<uint4*>(w + L.maps);
+        a.states = reinterpret_cast<uint2*>(w + L.states);
+        const uint64_t words = (L.total - L.maps) / sizeof(uint4);
+        const int rc = launch_rows_kernel(k_scan_clear,
+                                          dim3((unsigned)umin64((words + 1023) / 1024, 1024)), 256,
+                                          s, a.ticket, a.maps, words);
+        if (rc) return rc;
+        blocks = (uint32_t)umin64((uint64_t)L.tiles * L.chunks, (uint64_t)sms * 2);
+    }
+    return launch_shared_kernel(kernel, dim3(blocks), kThreads,
+                                kStages * Landing<T, kUnit, kS, kOperands>::kStageBytes, s, a);
 }
 
 int check_common(const dgc_matrix* x, const dgc_matrix* gate, const int64_t* offsets, int32_t nseq,
@@ -586,17 +798,21 @@ int recurrence(const dgc_matrix* x, const dgc_matrix* gate, const int64_t* offse
     a.cols = (uint32_t)mx.cols;
     a.status = status;
     if (test_spins) a.spin_limit = test_spins;
+    const int sms = dgc_internal_sm_count();
+    if (sms <= 0) return DGC_ECUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const ScanLayout L = scan_layout(mx.rows, mx.cols, kForwardRows);
-    if ((uint64_t)L.tiles * L.chunks > 0x7FFFFFFFull) return DGC_EUNSUPPORTED;
-    if ((rc = start_scan(a, L, ws, s))) return rc;
-    const bool pair = mx.on(2 * mx.entry()) && mg.on(2 * mx.entry()) && my.on(2 * mx.entry());
-    const dim3 grid(L.tiles * L.chunks);
+    const size_t two = 2 * mx.entry();
+    const bool pair = mx.on(two) && mg.on(two) && my.on(two);
+    const bool wide = pair && mx.on(16) && mg.on(16);
     return with_type(mx.dtype, [&](auto t) {
         using T = decltype(t);
-        return launch_rows_kernel(pair ? k_scan<T, true, kForwardRows / kWarps>
-                                       : k_scan<T, false, kForwardRows / kWarps>,
-                                  grid, kThreads, s, a);
+        constexpr int kS = Form<T>::kS, kStages = Form<T>::kStages, kTwo = 2 * sizeof(T);
+        if (wide)
+            return launch_scan<T, 16, kS, 2, kStages>(k_scan<T, 16, kS, kStages>, a, ws, sms, s);
+        if (pair)
+            return launch_scan<T, kTwo, kS, 2, kStages>(k_scan<T, kTwo, kS, kStages>, a, ws, sms,
+                                                        s);
+        return launch_scan<T, 0, kS, 2, kStages>(k_scan<T, 0, kS, kStages>, a, ws, sms, s);
     });
 }
 
@@ -679,17 +895,21 @@ extern "C" int dgc_recurrence_backward(const dgc_matrix* dy, const dgc_matrix* x
     a.rows = (uint32_t)mx.rows;
     a.cols = (uint32_t)mx.cols;
     a.status = status;
+    const int sms = dgc_internal_sm_count();
+    if (sms <= 0) return DGC_ECUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const ScanLayout L = scan_layout(mx.rows, mx.cols, kBackRows);
-    if ((uint64_t)L.tiles * L.chunks > 0x7FFFFFFFull) return DGC_EUNSUPPORTED;
-    if ((rc = start_scan(a, L, ws, s))) return rc;
     const size_t two = 2 * mx.entry();
     const bool pair = mx.on(two) && mg.on(two) && my.on(two) && md.on(two) && me.on(two);
-    const dim3 grid(L.tiles * L.chunks);
+    const bool wide = pair && mx.on(16) && mg.on(16) && my.on(16);
     return with_type(mx.dtype, [&](auto t) {
         using T = decltype(t);
-        return launch_rows_kernel(pair ? k_scan_back<T, true, kBackRows / kWarps>
-                                       : k_scan_back<T, false, kBackRows / kWarps>,
-                                  grid, kThreads, s, a);
+        constexpr int kS = Form<T>::kBackS, kStages = Form<T>::kBackStages, kTwo = 2 * sizeof(T);
+        if (wide)
+            return launch_scan<T, 16, kS, 3, kStages>(k_scan_back<T, 16, kS, kStages>, a, ws, sms,
+                                                      s);
+        if (pair)
+            return launch_scan<T, kTwo, kS, 3, kStages>(k_scan_back<T, kTwo, kS, kStages>, a, ws,
+                                                        sms, s);
+        return launch_scan<T, 0, kS, 3, kStages>(k_scan_back<T, 0, kS, kStages>, a, ws, sms, s);
     });
 }

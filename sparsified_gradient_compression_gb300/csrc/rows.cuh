@@ -126,6 +126,24 @@ __device__ __forceinline__ void unpack(const Packed<T, kN>& p, float (&f)[kN]) {
     }
 }
 
+// Entries 2 i and 2 i + 1.
+template <typename T, int kN>
+__device__ __forceinline__ float2 pair_of(const Packed<T, kN>& p, int i) {
+    if constexpr (sizeof(T) == 4)
+        return {__uint_as_float(p.w[2 * i]), __uint_as_float(p.w[2 * i + 1])};
+    else
+        return Num<T>::up2(p.w[i]);
+}
+template <typename T, int kN>
+__device__ __forceinline__ void set_pair(Packed<T, kN>& p, int i, float2 v) {
+    if constexpr (sizeof(T) == 4) {
+        p.w[2 * i] = __float_as_uint(v.x);
+        p.w[2 * i + 1] = __float_as_uint(v.y);
+    } else {
+        p.w[i] = Num<T>::down2(v.x, v.y);
+    }
+}
+
 template <typename T, int kN>
 __device__ __forceinline__ Packed<T, kN> pack(const float (&f)[kN]) {
     Packed<T, kN> r;
@@ -183,6 +201,54 @@ __device__ __forceinline__ void store_piece(T* p, const Packed<T, kN>& r, uint32
         store_packed<T, kN>(p, r);
     else
         store_some<T, kN>(p, r, n);
+}
+
+// Two binary32 numbers in one instruction, each rounded as alone.
+__device__ __forceinline__ uint64_t bits2(float2 a) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+    return r;
+}
+__device__ __forceinline__ float2 floats2(uint64_t r) {
+    float2 a;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(r));
+    return a;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return floats2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return floats2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return floats2(r);
+}
+__device__ __forceinline__ float2 both(float a) { return {a, a}; }
+
+// Copies to shared memory that run behind the thread's back: kBytes (4, 8 or 16) of which the first
+// `n` are read and the rest become zeros. Every thread reads what it copied itself, after
+// copy_wait<k>: all but its last k groups of copies have arrived (the hardware's wait, no loop).
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void* smem, const void* p, uint32_t n) {
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(smem)), "l"(p),
+                     "r"(n)
+                     : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_addr(smem)), "l"(p),
+                     "n"(kBytes), "r"(n)
+                     : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
 // The pieces of a matrix, `per_row` to a row, walked by blocks of kThreads threads that take kSteps
@@ -260,12 +326,20 @@ inline int check_vector(const dgc_tensor* t, uint64_t n, int32_t dtype) {
 // A launch that may start while the kernel ahead of it ends (every kernel waits before it reads or
 // writes).
 template <typename... A>
-int launch_rows_kernel(void (*kernel)(A...), dim3 grid, unsigned threads, cudaStream_t s,
-                       const std::decay_t<A>&... args) {
+int launch_shared_kernel(void (*kernel)(A...), dim3 grid, unsigned threads, size_t smem,
+                         cudaStream_t s, const std::decay_t<A>&... args) {
     void* ptrs[] = {const_cast<void*>(static_cast<const void*>(&args))...};
+    if (smem > 32 * 1024 &&  // 48 KB with the static part need no leave
+        cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)smem) != cudaSuccess) {
+        cudaGetLastError();
+        return DGC_ECUDA;
+    }
     cudaLaunchConfig_t c{};
     c.gridDim = grid;
     c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
     c.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -278,6 +352,12 @@ int launch_rows_kernel(void (*kernel)(A...), dim3 grid, unsigned threads, cudaSt
     }
     dgc_internal_count_launches(1);
     return DGC_OK;
+}
+
+template <typename... A>
+int launch_rows_kernel(void (*kernel)(A...), dim3 grid, unsigned threads, cudaStream_t s,
+                       const std::decay_t<A>&... args) {
+    return launch_shared_kernel(kernel, grid, threads, 0, s, args...);
 }
 
 // f with the type of the entries: f(T{}).
