@@ -4,11 +4,12 @@
 //   dtable[w] = scale sum of dy[t] over the t with token[t] = w, in the order of t; or added
 //
 //   k_embed        the lookup.
-//   k_sort_count   how often a block's tokens have each value of a digit of up to 9 bits;
-//   k_sort_move    puts (token, position) in the digit's order, equal ones in theirs: a stable
-//                  radix sort, lowest digit first, two launches a digit (one for few tokens).
-//   k_embed_sum    a warp sums the rows of 32 sorted tokens over 32 pieces of columns, and writes
-//                  each word's sum once; other blocks zero the rows of words that are not met.
+//   k_sort         a stable radix sort of (token, position), lowest digit first, digits of up to 9
+//                  bits, by one cluster: up to 32768 tokens.
+//   k_sort_count   for more: how often a block's tokens have each value of a digit;
+//   k_sort_move    puts them in the digit's order, equal ones in theirs.
+//   k_embed_sum    a warp sums the rows of 32 sorted tokens over some columns, and writes each
+//                  word's sum once; other blocks zero the rows of words that are not met.
 //   k_embed_join   joins the sums of words that are met more than 32 times, in order.
 //
 // No sum is made by atomic additions: the order of the additions is that of the positions within
@@ -94,107 +95,190 @@ __global__ void __launch_bounds__(kThreads) k_embed(const __grid_constant__ Embe
 // ----------------------------------------------------------------------------------- sort
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kDigits = 512;          // of up to 9 bits
-constexpr uint32_t kSortMost = 256;   // blocks
-constexpr uint32_t kSortLeast = 4096; // tokens up to which one block sorts alone
+constexpr int kSortRows = 8;                                  // tokens of a lane
+constexpr uint32_t kSortTile = kSortThreads * kSortRows;      // of a block
+constexpr int kDigits = 512;                                  // of up to 9 bits
+constexpr uint32_t kSortCluster = 8;                          // blocks
+constexpr uint32_t kSortMost = 256;                           // blocks of the launches for more
 
 struct SortArgs {
     Tokens tokens;                 // the first pass's source
-    const uint32_t *key, *pos;     // the others'
-    uint32_t *key_out, *pos_out;
+    uint32_t *key[2], *pos[2];     // pass p reads [p & 1] (but for the first) and writes the other
     uint32_t* counts;              // [block][digit]
-    uint32_t n, per_block;         // per_block: a multiple of kSortThreads
-    uint32_t vocab, shift, mask;
+    uint32_t n, per_block;         // per_block: a multiple of kSortTile
+    uint32_t vocab, digit_bits, passes;
     int64_t padding;
     uint32_t* list_count;          // zeroed for k_embed_sum
-    int32_t first;
     int32_t* status;
 };
 
 // The key of token i: its word; `vocab` (behind all words) for those without a gradient.
-__device__ __forceinline__ uint32_t sort_key(const SortArgs& a, uint32_t i, bool check) {
-    if (!a.first) return a.key[i];
+__device__ __forceinline__ uint32_t sort_key(const SortArgs& a, uint32_t pass, uint32_t i) {
+    if (pass != 0) return __ldcg(&a.key[pass & 1][i]);  // of other blocks of this launch
     const int64_t w = a.tokens[i];
     const bool known = w >= 0 && w < (int64_t)a.vocab;
-    if (check && !known) report(a.status, DGC_EINVAL);
+    if (!known) report(a.status, DGC_EINVAL);
     return known && w != a.padding ? (uint32_t)w : a.vocab;
 }
 
-__global__ void __launch_bounds__(kSortThreads) k_sort_count(const __grid_constant__ SortArgs a) {
+// A block's tile of tokens in shared memory, a warp's kSortRows * 32 of them in a row. (Short loops:
+// with the tile in registers, and so everything unrolled, a pass took 12 us, most of it the SMs'
+// wait for instructions that run once.)
+struct SortTile {
+    uint32_t key[kSortTile], pos[kSortTile];
+    uint16_t rank[kSortTile];
+
+    __device__ void load(const SortArgs& a, uint32_t pass, uint32_t first, uint32_t end) {
+#pragma unroll 4
+        for (int i = 0; i < kSortRows; ++i) {
+            const uint32_t s = i * kSortThreads + threadIdx.x, at = first + s;
+            if (at < end) {
+                key[s] = sort_key(a, pass, at);
+                pos[s] = pass == 0 ? at : __ldcg(&a.pos[pass & 1][at]);
+            } else {
+                key[s] = 0xFFFFFFFFu;  // none
+            }
+        }
+    }
+    // Each token's place among its equals in the warp; count: how many of each digit it has.
+    __device__ void ranks(uint32_t shift, uint32_t mask, uint32_t* count) {
+        const uint32_t lane = threadIdx.x & 31, below = (1u << lane) - 1;
+        const uint32_t begin = (threadIdx.x >> 5) * (32 * kSortRows) + lane;
+#pragma unroll 1
+        for (uint32_t s = begin; s < begin + 32 * kSortRows; s += 32) {
+            const uint32_t k = key[s], d = k == 0xFFFFFFFFu ? kDigits : (k >> shift) & mask;
+            const unsigned same = __match_any_sync(kFull, d);
+            const uint32_t r = d < kDigits ? count[d] : 0;
+            __syncwarp();
+            if (d < kDigits && (same & below) == 0) count[d] = r + __popc(same);
+            rank[s] = (uint16_t)(r + __popc(same & below));
+            __syncwarp();
+        }
+    }
+    __device__ void store(const SortArgs& a, uint32_t pass, uint32_t shift, uint32_t mask,
+                          const uint32_t* place) const {
+        const uint32_t begin = (threadIdx.x >> 5) * (32 * kSortRows) + (threadIdx.x & 31);
+#pragma unroll 2
+        for (uint32_t s = begin; s < begin + 32 * kSortRows; s += 32) {
+            const uint32_t k = key[s];
+            if (k != 0xFFFFFFFFu) {
+                const uint32_t to = place[(k >> shift) & mask] + rank[s];
+                a.key[~pass & 1][to] = k;
+                a.pos[~pass & 1][to] = pos[s];
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ void clear_places(uint32_t (*place)[kDigits]) {
+#pragma unroll 4
+    for (int w = 0; w < kSortWarps; ++w) place[w][threadIdx.x] = 0;
+}
+// Where the thread's digit begins in the order: behind all smaller ones and those of the blocks
+// before this one. counts of `blocks` blocks; own: this block's.
+__device__ __forceinline__ uint32_t digit_begin(const uint32_t* counts, uint32_t blocks,
+                                                uint32_t block, uint32_t own, uint32_t* scan) {
+    uint32_t before = 0, all = own;
+    if (blocks > 1) {
+        all = 0;
+#pragma unroll 8
+        for (uint32_t b = 0; b < blocks; ++b) {
+            const uint32_t c = __ldcg(&counts[b * kDigits + threadIdx.x]);
+            all += c;
+            if (b < block) before += c;
+        }
+    }
+    uint32_t total;
+    return block_excl_scan<kSortThreads>(all, scan, &total) + before;
+}
+// The thread's digit in each warp: counts become places, from `at` on. Returns the end.
+__device__ __forceinline__ uint32_t warp_places(uint32_t (*place)[kDigits], uint32_t at) {
+#pragma unroll 4
+    for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t c = place[w][threadIdx.x];
+        place[w][threadIdx.x] = at;
+        at += c;
+    }
+    return at;
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// All passes by one cluster of up to 8 blocks, a tile each. The blocks' counts and the tokens go
+// through global memory (L2).
+__global__ void __launch_bounds__(kSortThreads) k_sort(const __grid_constant__ SortArgs a) {
+    extern __shared__ uint4 shared[];
+    SortTile& tile = *reinterpret_cast<SortTile*>(shared);
+    __shared__ uint32_t place[kSortWarps][kDigits];
+    __shared__ uint32_t scan[33];
+    const int warp = threadIdx.x >> 5;
+    grid_dep_wait();
+    grid_dep_launch();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.list_count = 0;
+    for (uint32_t pass = 0; pass < a.passes; ++pass) {
+        const uint32_t shift = pass * a.digit_bits, mask = (1u << a.digit_bits) - 1;
+        tile.load(a, pass, blockIdx.x * kSortTile, a.n);
+        clear_places(place);
+        __syncthreads();
+        tile.ranks(shift, mask, place[warp]);
+        __syncthreads();
+        uint32_t own = 0;
+#pragma unroll 4
+        for (int w = 0; w < kSortWarps; ++w) own += place[w][threadIdx.x];
+        if (gridDim.x > 1) {
+            __stcg(&a.counts[blockIdx.x * kDigits + threadIdx.x], own);
+            cluster_barrier();
+        }
+        warp_places(place, digit_begin(a.counts, gridDim.x, blockIdx.x, own, scan));
+        __syncthreads();
+        tile.store(a, pass, shift, mask, place[warp]);
+        if (gridDim.x > 1) cluster_barrier();
+        __syncthreads();
+    }
+}
+
+__global__ void __launch_bounds__(kSortThreads)
+    k_sort_count(const __grid_constant__ SortArgs a, uint32_t pass) {
     __shared__ uint32_t count[kDigits];
     grid_dep_wait();
     grid_dep_launch();
     count[threadIdx.x] = 0;
     __syncthreads();
+    const uint32_t shift = pass * a.digit_bits, mask = (1u << a.digit_bits) - 1;
     const uint32_t begin = blockIdx.x * a.per_block, end = min(a.n, begin + a.per_block);
     for (uint32_t i = begin + threadIdx.x; i < end; i += kSortThreads)
-        atomicAdd(&count[(sort_key(a, i, false) >> a.shift) & a.mask], 1u);
+        atomicAdd(&count[(sort_key(a, pass, i) >> shift) & mask], 1u);
     __syncthreads();
     a.counts[blockIdx.x * kDigits + threadIdx.x] = count[threadIdx.x];
 }
 
-// A warp owns a run of the block's tokens. Counted once by warp and digit, summed up to where each
-// warp's tokens of a digit begin, then walked again, 32 tokens at a time: a token's place among
-// its equals is that of its lane.
-__global__ void __launch_bounds__(kSortThreads) k_sort_move(const __grid_constant__ SortArgs a) {
+// A block's tiles one behind the other.
+__global__ void __launch_bounds__(kSortThreads)
+    k_sort_move(const __grid_constant__ SortArgs a, uint32_t pass) {
+    extern __shared__ uint4 shared[];
+    SortTile& tile = *reinterpret_cast<SortTile*>(shared);
     __shared__ uint32_t place[kSortWarps][kDigits];
     __shared__ uint32_t scan[33];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int warp = threadIdx.x >> 5;
     grid_dep_wait();
     grid_dep_launch();
-    if (a.list_count && blockIdx.x == 0 && threadIdx.x == 0) *a.list_count = 0;
-#pragma unroll
-    for (int w = 0; w < kSortWarps; ++w) place[w][threadIdx.x] = 0;
-    __syncthreads();
-    const uint32_t per_warp = a.per_block / kSortWarps;
-    const uint32_t begin = min(a.n, blockIdx.x * a.per_block + warp * per_warp);
-    const uint32_t end = min(a.n, begin + per_warp);
-    for (uint32_t i = begin + lane; i < end; i += 32)
-        atomicAdd(&place[warp][(sort_key(a, i, true) >> a.shift) & a.mask], 1u);
-    __syncthreads();
-    {
-        const uint32_t d = threadIdx.x;
-        uint32_t before = 0, own = 0, all = 0;  // in earlier blocks, in this one, everywhere
-#pragma unroll
-        for (int w = 0; w < kSortWarps; ++w) own += place[w][d];
-        if (gridDim.x == 1) {
-            all = own;
-        } else {
-#pragma unroll 8
-            for (uint32_t b = 0; b < gridDim.x; ++b) {
-                const uint32_t c = a.counts[b * kDigits + d];
-                all += c;
-                if (b < blockIdx.x) before += c;
-            }
-        }
-        uint32_t total;
-        uint32_t at = block_excl_scan<kSortThreads>(all, scan, &total) + before;
-#pragma unroll
-        for (int w = 0; w < kSortWarps; ++w) {
-            const uint32_t c = place[w][d];
-            place[w][d] = at;
-            at += c;
-        }
-    }
-    __syncthreads();
-    for (uint32_t i0 = begin; i0 < end; i0 += 32) {
-        const uint32_t i = i0 + lane;
-        const bool in = i < end;
-        const uint32_t key = in ? sort_key(a, i, false) : 0;
-        const uint32_t d = in ? (key >> a.shift) & a.mask : kDigits;
-        const unsigned same = __match_any_sync(kFull, d);
-        const int leader = __ffs(same) - 1;
-        uint32_t to = 0;
-        if (in && lane == leader) {
-            to = place[warp][d];
-            place[warp][d] = to + __popc(same);
-        }
-        to = __shfl_sync(kFull, to, leader) + __popc(same & ((1u << lane) - 1));
-        if (in) {
-            a.key_out[to] = key;
-            a.pos_out[to] = a.first ? i : a.pos[i];
-        }
-        __syncwarp();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.list_count = 0;
+    const uint32_t shift = pass * a.digit_bits, mask = (1u << a.digit_bits) - 1;
+    const uint32_t begin = blockIdx.x * a.per_block, end = min(a.n, begin + a.per_block);
+    uint32_t at = digit_begin(a.counts, gridDim.x, blockIdx.x,
+                              a.counts[blockIdx.x * kDigits + threadIdx.x], scan);
+    for (uint32_t first = begin; first < end; first += kSortTile) {
+        tile.load(a, pass, first, end);
+        clear_places(place);
+        __syncthreads();
+        tile.ranks(shift, mask, place[warp]);
+        __syncthreads();
+        at = warp_places(place, at);
+        __syncthreads();
+        tile.store(a, pass, shift, mask, place[warp]);
+        __syncthreads();
     }
 }
 
@@ -210,7 +294,7 @@ struct SumArgs {
     uint64_t ldt;
     float scale;
     int32_t accumulate;
-    uint32_t tiles;              // of columns, a warp's 32 pieces each
+    uint32_t tiles;              // of columns: a warp's
     uint32_t sum_blocks;         // the others zero
     float* part;                 // [chunk][2][ldp]: of words met more than 32 times, the sum in a
     uint64_t ldp;                // chunk that goes on from the last one, and in one that starts it
@@ -243,23 +327,57 @@ struct Chunk {
     }
 };
 
-// One row of sums to the table, or (scaled later) to a part.
-template <bool kWide, bool kAdd, int kN>
-__device__ __forceinline__ void write_sums(float* p, const float (&acc)[kN], float scale,
-                                           const float (&old)[kN], uint32_t left) {
-    float f[kN];
+// A lane's kN columns of a row. kWide: neighbours, all of them in the row or none, on a 16-byte
+// boundary (8 for four 16-bit entries); else 32 apart. Columns behind the row's end are read as the
+// last one's and not written, so that no load waits for a test.
+template <int kN, bool kWide>
+struct Cols {
+    uint32_t at[kWide ? 1 : kN];
+    uint32_t n;  // how many are the row's
+    __device__ Cols(uint32_t tile, uint32_t cols) {
+        const uint32_t lane = threadIdx.x & 31, first = tile * 32 * kN + (kWide ? lane * kN : lane);
+        n = 0;
 #pragma unroll
-    for (int j = 0; j < kN; ++j) f[j] = kAdd ? fmaf(acc[j], scale, old[j]) : acc[j] * scale;
-    store_piece<kWide, float, kN>(p, pack<float, kN>(f), left);
-}
+        for (int i = 0; i < (kWide ? 1 : kN); ++i) {
+            n += first + 32 * i < cols;
+            at[i] = min(first + 32 * i, cols - (kWide ? kN : 1));
+        }
+        if (kWide) n *= kN;
+    }
+    template <typename T>
+    __device__ Packed<T, kN> load(const T* row) const {
+        if constexpr (kWide) {
+            return load_packed<T, kN>(row + at[0]);
+        } else {
+            Packed<T, kN> r;
+#pragma unroll
+            for (int i = 0; i < Packed<T, kN>::kWords; ++i) r.w[i] = 0;
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                const uint32_t one = load_packed<T, 1>(row + at[i]).w[0];
+                if constexpr (sizeof(T) == 4) r.w[i] = one;
+                else r.w[i / 2] |= one << (16 * (i & 1));
+            }
+            return r;
+        }
+    }
+    __device__ void store(float* row, const float (&f)[kN]) const {
+        if constexpr (kWide) {
+            if (n) store_packed<float, kN>(row + at[0], pack<float, kN>(f));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+                if ((uint32_t)i < n) __stcs(row + at[i], f[i]);
+        }
+    }
+};
 
 // Bound by HBM: dy read once, the table written once (read and written where it is added to).
 // A word met up to 32 times is summed by the warp in whose chunk it starts; a longer run is cut at
-// the chunks' borders.
-template <typename T, bool kWide, bool kWideTable, bool kAdd>
-__global__ void __launch_bounds__(kThreads) k_embed_sum(const __grid_constant__ SumArgs a) {
-    constexpr int kN = 16 / sizeof(T);
-    constexpr int kBatch = kAdd ? 4 : 8;  // rows in flight (and as many rows of the table)
+// the chunks' borders. kN: a lane's columns.
+template <typename T, int kN, bool kWide, bool kAdd>
+__global__ void __launch_bounds__(kThreads, 2) k_embed_sum(const __grid_constant__ SumArgs a) {
+    constexpr int kBatch = 4;  // rows in flight (and as many of the table's)
     const int lane = threadIdx.x & 31;
     grid_dep_wait();
     grid_dep_launch();
@@ -268,21 +386,22 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(const __grid_constant__ 
         const uint64_t units = (uint64_t)((a.vocab + kZeroRows - 1) / kZeroRows) * col_units;
         for (uint64_t u = blockIdx.x - a.sum_blocks; u < units; u += gridDim.x - a.sum_blocks) {
             const uint32_t row0 = (uint32_t)(u / col_units) * kZeroRows;
-            const uint32_t col = (uint32_t)(u % col_units) * kZeroCols + threadIdx.x * 4;
-            const uint32_t left = col < a.cols ? a.cols - col : 0;
-            // is this lane's row met?
+            const uint32_t tile = (uint32_t)(u % col_units) * (kThreads / 32) + (threadIdx.x >> 5);
+            const Cols<4, kWide> cols(tile, a.cols);
+            // is this lane's row met? The rows' stretch of the list first, then a row's
             const uint32_t row = row0 + lane;
-            uint32_t lo = 0, hi = a.n;
+            const uint32_t from = first_from(a.key, 0, a.n, row0);
+            uint32_t lo = from, hi = from + first_from(a.key + from, 0, a.n - from, row0 + kZeroRows);
+            const uint32_t stop = hi;
             while (lo < hi) {
                 const uint32_t mid = (lo + hi) >> 1;
                 if (a.key[mid] < row) lo = mid + 1; else hi = mid;
             }
-            const bool met = lo < a.n && a.key[lo] == row;
+            const bool met = lo < stop && a.key[lo] == row;
             uint32_t todo = __ballot_sync(kFull, !met && row < a.vocab);
             const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             for (; todo; todo &= todo - 1)
-                store_piece<kWideTable, float, 4>(
-                    a.dtable + (row0 + __ffs(todo) - 1) * a.ldt + col, pack<float, 4>(zero), left);
+                cols.store(a.dtable + (row0 + __ffs(todo) - 1) * a.ldt, zero);
         }
         return;
     }
@@ -292,8 +411,8 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(const __grid_constant__ 
     for (uint64_t u = (uint64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < units;
          u += (uint64_t)a.sum_blocks * (kThreads / 32)) {
         const uint32_t chunk = (uint32_t)(u / a.tiles), tile = (uint32_t)(u % a.tiles);
-        const uint32_t base = chunk * 32, col = (tile * 32 + lane) * kN;
-        const uint32_t left = col < a.cols ? a.cols - col : 0;
+        const uint32_t base = chunk * 32;
+        const Cols<kN, kWide> cols(tile, a.cols);
         const Chunk c(a, base);
         const uint32_t pos = base + lane < a.n ? a.pos[base + lane] : 0;
         const uint32_t pos_next = base + 32 + lane < a.n ? a.pos[base + 32 + lane] : 0;
@@ -313,50 +432,49 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(const __grid_constant__ 
         if (valid < 32) end = min(end, valid);  // words without a gradient are the last ones
         if (long_tail && valid == 32 && tile == 0 && lane == 0)
             a.list[atomicAdd(a.list_count, 1u)] = chunk;
-        const uint64_t next_starts = ~(((uint64_t)c.e2 << 32 | c.e1) >> 1);  // bit 63: 1
+        // which tokens end a run, and which of those runs are whole: from head on, ahead of last
+        const uint64_t ends = ~(((uint64_t)c.e2 << 32 | c.e1) >> 1);  // bit 63: 1
+        const uint32_t whole_from = long_head ? head : 0, whole_to = long_tail ? last : 64;
         float acc[kN];
 #pragma unroll
         for (int j = 0; j < kN; ++j) acc[j] = 0.0f;
+#pragma unroll 1
         for (uint32_t e0 = begin; e0 < end; e0 += kBatch) {
             Packed<T, kN> p[kBatch];
             Packed<float, kN> old[kAdd ? kBatch : 1];
-            uint32_t word[kBatch];
-            uint32_t flush = 0;
+            float* row[kBatch];  // where the run's sum goes, at its end
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                const uint32_t e = e0 + i;
+                const uint32_t e = min(e0 + i, end - 1);
                 const uint32_t t = __shfl_sync(kFull, e < 32 ? pos : pos_next, e & 31);
-                word[i] = __shfl_sync(kFull, e < 32 ? c.key : c.key_next, e & 31);
-                const bool in = e < end;
-                p[i] = load_piece<kWide, T, kN>(dy + (uint64_t)t * a.ldy + col, in ? left : 0);
-                const bool ends = in && ((next_starts >> e & 1) || e + 1 == end);
-                if (ends) flush |= 1u << i;
-                if (kAdd) {
-                    const bool whole = ends && !(long_head && e < head) &&
-                                       !(long_tail && (int)e >= last);
-                    old[i] = load_piece<kWideTable, float, kN>(
-                        a.dtable + (uint64_t)word[i] * a.ldt + col, whole ? left : 0);
+                const uint32_t word = __shfl_sync(kFull, e < 32 ? c.key : c.key_next, e & 31);
+                p[i] = cols.load(dy + (uint64_t)t * a.ldy);
+                row[i] = nullptr;
+                if (e0 + i < end && ((ends >> e & 1) || e + 1 == end)) {
+                    const bool whole = e >= whole_from && e < whole_to;
+                    row[i] = whole ? a.dtable + (uint64_t)word * a.ldt
+                                   : a.part + ((uint64_t)chunk * 2 + (e >= whole_from)) * a.ldp;
+                    if (kAdd && whole) old[i] = cols.load(row[i]);
                 }
             }
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 const uint32_t e = e0 + i;
-                if (e >= end) break;
-                float f[kN];
-                unpack<T, kN>(p[i], f);
+                if (e < end) {
+                    float f[kN];
+                    unpack<T, kN>(p[i], f);
 #pragma unroll
-                for (int j = 0; j < kN; ++j) acc[j] += f[j];
-                if (flush >> i & 1) {
-                    float was[kN];
-                    const bool to_head = long_head && e < head;
-                    if (to_head || (long_tail && (int)e >= last)) {
-                        float* q = a.part + ((uint64_t)chunk * 2 + (to_head ? 0 : 1)) * a.ldp + col;
-                        store_piece<true, float, kN>(q, pack<float, kN>(acc), left);
-                    } else {
+                    for (int j = 0; j < kN; ++j) acc[j] += f[j];
+                }
+                if (row[i]) {
+                    if (e >= whole_from && e < whole_to) {
+                        float was[kN];
                         if (kAdd) unpack<float, kN>(old[kAdd ? i : 0], was);
-                        write_sums<kWideTable, kAdd, kN>(a.dtable + (uint64_t)word[i] * a.ldt + col,
-                                                         acc, a.scale, was, left);
+#pragma unroll
+                        for (int j = 0; j < kN; ++j)
+                            acc[j] = kAdd ? fmaf(acc[j], a.scale, was[j]) : acc[j] * a.scale;
                     }
+                    cols.store(row[i], acc);
 #pragma unroll
                     for (int j = 0; j < kN; ++j) acc[j] = 0.0f;
                 }
@@ -366,8 +484,8 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(const __grid_constant__ 
 }
 
 // The parts of a long run, 128 columns by a block: each warp sums an eighth of them in order, the
-// first warp adds the eight.
-template <bool kWideTable, bool kAdd>
+// first warp adds the eight. Lanes' columns as in k_embed_sum.
+template <bool kWide, bool kAdd>
 __global__ void __launch_bounds__(kThreads) k_embed_join(const __grid_constant__ SumArgs a) {
     constexpr int kWarps = kThreads / 32;
     __shared__ float4 sm[kWarps][32];
@@ -377,33 +495,26 @@ __global__ void __launch_bounds__(kThreads) k_embed_join(const __grid_constant__
     const uint32_t count = *a.list_count;
     const uint32_t tiles = (a.cols + 127) / 128;
     for (uint64_t u = blockIdx.x; u < (uint64_t)count * tiles; u += gridDim.x) {
-        const uint32_t chunk = a.list[u / tiles], col = (uint32_t)(u % tiles) * 128 + lane * 4;
-        const uint32_t left = col < a.cols ? a.cols - col : 0;
-        const uint32_t word = a.key[chunk * 32 + 31];
-        uint32_t lo = chunk * 32 + 32, hi = a.n;  // the run's end
-        while (lo < hi) {
-            const uint32_t mid = (lo + hi) >> 1;
-            if (a.key[mid] <= word) lo = mid + 1; else hi = mid;
-        }
-        const uint32_t parts = (lo - 1) / 32 - chunk + 1, share = (parts + kWarps - 1) / kWarps;
+        const uint32_t chunk = a.list[u / tiles], next = chunk * 32 + 32;
+        const Cols<4, kWide> cols((uint32_t)(u % tiles), a.cols);
+        const uint32_t word = a.key[next - 1];
+        float* out = a.dtable + (uint64_t)word * a.ldt;
+        Packed<float, 4> old{};
+        if (kAdd && warp == 0) old = cols.load(out);
+        const uint32_t end = first_from(a.key, next, a.n - next, word + 1);
+        const uint32_t parts = (end - 1) / 32 - chunk + 1, share = (parts + kWarps - 1) / kWarps;
         float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         const uint32_t from = min(parts, warp * share), to = min(parts, from + share);
-        if (left)
 #pragma unroll 8
-            for (uint32_t i = from; i < to; ++i) {  // the first part starts the run
-                const float4 v = __ldcs(reinterpret_cast<const float4*>(
-                    a.part + ((uint64_t)(chunk + i) * 2 + (i == 0)) * a.ldp + col));
-                s[0] += v.x;
-                s[1] += v.y;
-                s[2] += v.z;
-                s[3] += v.w;
-            }
+        for (uint32_t i = from; i < to; ++i) {  // the first part starts the run
+            float v[4];
+            unpack<float, 4>(cols.load(a.part + ((uint64_t)(chunk + i) * 2 + (i == 0)) * a.ldp), v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j] += v[j];
+        }
         sm[warp][lane] = make_float4(s[0], s[1], s[2], s[3]);
         __syncthreads();
         if (warp == 0) {
-            float old[4];
-            float* out = a.dtable + (uint64_t)word * a.ldt + col;
-            if (kAdd) unpack<float, 4>(load_piece<kWideTable, float, 4>(out, left), old);
             for (int w = 1; w < kWarps; ++w) {
                 const float4 v = sm[w][lane];
                 s[0] += v.x;
@@ -411,7 +522,11 @@ __global__ void __launch_bounds__(kThreads) k_embed_join(const __grid_constant__
                 s[2] += v.z;
                 s[3] += v.w;
             }
-            write_sums<kWideTable, kAdd, 4>(out, s, a.scale, old, left);
+            float was[4];
+            unpack<float, 4>(old, was);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j] = kAdd ? fmaf(s[j], a.scale, was[j]) : s[j] * a.scale;
+            cols.store(out, s);
         }
         __syncthreads();
     }
@@ -419,7 +534,7 @@ __global__ void __launch_bounds__(kThreads) k_embed_join(const __grid_constant__
 
 // ----------------------------------------------------------------------------------- host
 struct BackwardLayout {
-    uint32_t blocks, per_block, passes, digit_bits;
+    uint32_t blocks, per_block, passes, digit_bits;  // of the sort
     size_t key[2], pos[2], counts, list, part, total;
     uint64_t ldp;
 };
@@ -430,11 +545,11 @@ BackwardLayout backward_layout(uint64_t n, uint64_t vocab, uint64_t dim) {
     while ((vocab >> bits) != 0) ++bits;  // keys 0 to vocab
     L.passes = (bits + 8) / 9;
     L.digit_bits = (bits + L.passes - 1) / L.passes;
-    const uint64_t blocks =
-        n <= kSortLeast ? 1 : std::min<uint64_t>(kSortMost, (n + 2047) / 2048);
-    L.per_block = (uint32_t)(((n + blocks - 1) / blocks + kSortThreads - 1) / kSortThreads *
-                             kSortThreads);
-    L.blocks = L.per_block ? (uint32_t)((n + L.per_block - 1) / L.per_block) : 0;
+    // a tile a block where a cluster sorts, else whole tiles, as many as it takes
+    const uint64_t tiles = (n + kSortTile - 1) / kSortTile;
+    const uint64_t each = tiles <= kSortCluster ? 1 : (tiles + kSortMost - 1) / kSortMost;
+    L.per_block = (uint32_t)(each * kSortTile);
+    L.blocks = (uint32_t)((tiles + each - 1) / each);
     size_t at = 0;
     for (int i = 0; i < 2; ++i) {
         L.key[i] = at;
@@ -454,25 +569,69 @@ BackwardLayout backward_layout(uint64_t n, uint64_t vocab, uint64_t dim) {
     return L;
 }
 
-template <typename T>
-int launch_sums(const SumArgs& a, bool wide, bool wide_table, unsigned zero_blocks, unsigned join,
-                cudaStream_t s) {
-    auto pick = [&](auto w, auto wt, auto add) {
-        return k_embed_sum<T, decltype(w)::value, decltype(wt)::value, decltype(add)::value>;
+template <typename T, int kN>
+int launch_sums(SumArgs a, bool wide, int sms, cudaStream_t s) {
+    a.tiles = (a.cols + 32 * kN - 1) / (32 * kN);
+    const uint64_t chunks = (a.n + 31) / 32;
+    a.sum_blocks = (uint32_t)umin64((chunks * a.tiles + 7) / 8, 1u << 24);
+    const uint64_t zeros = a.accumulate ? 0
+                                        : ((uint64_t)a.vocab + kZeroRows - 1) / kZeroRows *
+                                              ((a.cols + kZeroCols - 1) / kZeroCols);
+    const dim3 grid(a.sum_blocks + (unsigned)umin64(zeros, 1u << 24));
+    if (grid.x == 0) return DGC_OK;
+    auto pick = [&] {
+        if constexpr (kN == 8)  // wide
+            return a.accumulate ? k_embed_sum<T, kN, true, true> : k_embed_sum<T, kN, true, false>;
+        else
+            return a.accumulate
+                       ? (wide ? k_embed_sum<T, kN, true, true> : k_embed_sum<T, kN, false, true>)
+                       : (wide ? k_embed_sum<T, kN, true, false> : k_embed_sum<T, kN, false, false>);
     };
-    using Y = std::true_type;
-    using N = std::false_type;
-    auto kernel = a.accumulate
-                      ? (wide ? (wide_table ? pick(Y{}, Y{}, Y{}) : pick(Y{}, N{}, Y{}))
-                              : (wide_table ? pick(N{}, Y{}, Y{}) : pick(N{}, N{}, Y{})))
-                      : (wide ? (wide_table ? pick(Y{}, Y{}, N{}) : pick(Y{}, N{}, N{}))
-                              : (wide_table ? pick(N{}, Y{}, N{}) : pick(N{}, N{}, N{})));
-    const int rc = launch_rows_kernel(kernel, dim3(a.sum_blocks + zero_blocks), kThreads, s, a);
-    if (rc || !join) return rc;
-    auto joiner = a.accumulate ? (wide_table ? k_embed_join<true, true> : k_embed_join<false, true>)
-                               : (wide_table ? k_embed_join<true, false>
-                                             : k_embed_join<false, false>);
-    return launch_rows_kernel(joiner, dim3(join), kThreads, s, a);
+    auto kernel = pick();
+    const int rc = launch_rows_kernel(kernel, grid, kThreads, s, a);
+    // only a list of more than 32 tokens can hold a word more than 32 times
+    if (rc || a.n <= 32) return rc;
+    auto joiner = a.accumulate ? (wide ? k_embed_join<true, true> : k_embed_join<false, true>)
+                               : (wide ? k_embed_join<true, false> : k_embed_join<false, false>);
+    const uint64_t blocks = umin64((uint64_t)sms * 4, chunks * ((a.cols + 127) / 128));
+    return launch_rows_kernel(joiner, dim3((unsigned)blocks), kThreads, s, a);
+}
+
+int launch_sort(const SortArgs& a, const BackwardLayout& L, cudaStream_t s) {
+    if (L.blocks <= kSortCluster) {
+        cudaLaunchConfig_t c{};
+        c.gridDim = dim3(L.blocks);
+        c.blockDim = dim3(kSortThreads);
+        c.dynamicSmemBytes = sizeof(SortTile);
+        c.stream = s;
+        if (cudaFuncSetAttribute(k_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 sizeof(SortTile)) != cudaSuccess) {
+            cudaGetLastError();
+            return DGC_ECUDA;
+        }
+        cudaLaunchAttribute at[2];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim.x = L.blocks;
+        at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+        c.attrs = at;
+        c.numAttrs = L.blocks > 1 ? 2 : 1;
+        if (cudaLaunchKernelEx(&c, k_sort, a) != cudaSuccess) {
+            cudaGetLastError();
+            return DGC_ECUDA;
+        }
+        dgc_internal_count_launches(1);
+        return DGC_OK;
+    }
+    for (uint32_t pass = 0; pass < a.passes; ++pass) {
+        int rc = launch_rows_kernel(k_sort_count, dim3(L.blocks), kSortThreads, s, a, pass);
+        if (rc) return rc;
+        rc = launch_shared_kernel(k_sort_move, dim3(L.blocks), kSortThreads, sizeof(SortTile), s, a,
+                                  pass);
+        if (rc) return rc;
+    }
+    return DGC_OK;
 }
 
 int check_tokens(const dgc_tensor* t, Tokens* out) {
@@ -566,23 +725,16 @@ extern "C" int dgc_embed_backward(const dgc_tensor* tokens, const dgc_matrix* dy
         a.padding = padding;
         a.counts = words(L.counts);
         a.status = status;
-        for (uint32_t pass = 0; pass < L.passes; ++pass) {
-            a.first = pass == 0;
-            a.key = words(L.key[pass & 1]);
-            a.pos = words(L.pos[pass & 1]);
-            a.key_out = words(L.key[~pass & 1]);
-            a.pos_out = words(L.pos[~pass & 1]);
-            a.shift = pass * L.digit_bits;
-            a.mask = (1u << L.digit_bits) - 1;
-            a.list_count = pass + 1 == L.passes ? sum.list_count : nullptr;
-            if (L.blocks > 1 &&
-                (rc = launch_rows_kernel(k_sort_count, dim3(L.blocks), kSortThreads, s, a)))
-                return rc;
-            if ((rc = launch_rows_kernel(k_sort_move, dim3(L.blocks), kSortThreads, s, a)))
-                return rc;
+        a.digit_bits = L.digit_bits;
+        a.passes = L.passes;
+        a.list_count = sum.list_count;
+        for (int i = 0; i < 2; ++i) {
+            a.key[i] = words(L.key[i]);
+            a.pos[i] = words(L.pos[i]);
         }
-        sum.key = a.key_out;
-        sum.pos = a.pos_out;
+        if ((rc = launch_sort(a, L, s))) return rc;
+        sum.key = a.key[L.passes & 1];
+        sum.pos = a.pos[L.passes & 1];
     }
     sum.n = n;
     sum.vocab = (uint32_t)mt.rows;
@@ -595,21 +747,14 @@ extern "C" int dgc_embed_backward(const dgc_tensor* tokens, const dgc_matrix* dy
     sum.accumulate = accumulate != 0;
     sum.part = reinterpret_cast<float*>(w + L.part);
     sum.ldp = L.ldp;
-    const uint32_t span = 32 * (uint32_t)(16 / my.entry());  // a warp's columns
-    sum.tiles = (sum.cols + span - 1) / span;
-    const uint64_t units = (uint64_t)((n + 31) / 32) * sum.tiles;
-    sum.sum_blocks = (uint32_t)umin64((units + 7) / 8, 1u << 24);
-    const uint64_t zeros = accumulate ? 0
-                                      : ((mt.rows + kZeroRows - 1) / kZeroRows) *
-                                            ((mt.cols + kZeroCols - 1) / kZeroCols);
-    const unsigned zero_blocks = (unsigned)umin64(zeros, 1u << 24);
-    // only a list of more than 32 tokens can hold a word more than 32 times
-    const unsigned join = n > 32 ? (unsigned)umin64((uint64_t)sms * 2, (uint64_t)((n + 31) / 32) *
-                                                                           ((mt.cols + 127) / 128))
-                                 : 0;
-    const bool wide = my.on(16), wide_table = mt.on(16);
-    if (sum.sum_blocks + zero_blocks == 0) return DGC_OK;
+    const bool wide = my.on(16) && mt.on(16) && mt.cols % 4 == 0;
+    // eight columns a lane where that leaves the SMs 16 warps each: 16-byte loads of 16-bit entries
+    const bool eight = my.dtype != DGC_F32 && wide && mt.cols % 8 == 0 &&
+                       (uint64_t)((n + 31) / 32) * ((mt.cols + 255) / 256) >= (uint64_t)sms * 16;
     return with_type(my.dtype, [&](auto t) {
-        return launch_sums<decltype(t)>(sum, wide, wide_table, zero_blocks, join, s);
+        using T = decltype(t);
+        if constexpr (sizeof(T) == 2)
+            if (eight) return launch_sums<T, 8>(sum, wide, sms, s);
+        return launch_sums<T, 4>(sum, wide, sms, s);
     });
 }

@@ -14,10 +14,12 @@
 //      ahead publishes. (Which maps are joined, and how, is fixed, so the rounding is too: results
 //      are the same bits on every run. A chain from chunk to chunk would cost its latency 32 times.)
 //   3. each warp walks its rows again from the state it enters with, and writes.
-// The data is read once. Blocks stay, and the next tiles are on their way to shared memory while one
-// is computed: a tile's latency is that of two barriers and a round trip to L2. (One block a tile,
-// with its loads at its beginning, took 279 us for 32768 x 2048.) Tiles go by a ticket, in order, so
-// a block only waits for tiles that running blocks hold; waits are bounded all the same.
+// The data is read once. Blocks stay: the next tile is on its way to shared memory as soon as the
+// rows of this one are in registers, while the maps are exchanged and the results written. (One block
+// a tile, with its loads at its beginning, took 279 us for 32768 x 2048.) Tiles go by a ticket, in
+// order, so a block only waits for tiles that running blocks hold; waits are bounded all the same.
+// A ticket is taken late: the further ahead, the less tiles are begun in the order in which they
+// wait for one another (two tiles ahead 149 us).
 //
 // Maps and states are published without flags: the workspace is filled with a bit pattern that no
 // result has, and a reader waits until it has gone.
@@ -39,6 +41,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCols = 64;        // of a tile
 constexpr uint32_t kGroup = 32;  // chunks
+constexpr uint32_t kEach = kGroup / kWarps;  // of them for a warp to collect
 constexpr uint32_t kPiece = 64;  // rows between two saved states
 constexpr float kReset = -1.0f;  // no run of steps has a negative A
 constexpr uint32_t kNotYet = 0xFFFFFFFFu;  // a NaN that no arithmetic makes
@@ -51,7 +54,7 @@ struct ScanArgs {
     float *h_last, *d_h0, *saved;
     uint64_t ldh0, ldd_last, ldh_last, ldd_h0, lds;
     const int64_t* offsets;
-    uint32_t nseq, rows, cols, tiles, chunks;
+    uint32_t nseq, rows, cols, tiles, tiles_inverse, chunks;
     // the workspace: a ticket, whether a wait gave up, the chunks' maps {A, A, B, B} and the groups'
     // entering states of a lane's two columns. ticket null: one chunk, nothing is shared.
     uint32_t *ticket, *abort;
@@ -120,25 +123,6 @@ struct Map {
 __device__ __forceinline__ Map map_of(const float4& v) { return {{v.x, v.y}, {v.z, v.w}}; }
 __device__ __forceinline__ Map identity() { return {both(1.0f), both(0.0f)}; }
 
-// The first index i in [0, n) with off[i] >= key, n if there is none. All lanes of a warp; any
-// contents (where they do not rise, any index).
-__device__ __forceinline__ uint32_t first_from(const int64_t* off, uint32_t n, int64_t key) {
-    const uint32_t lane = threadIdx.x & 31;
-    uint32_t lo = 0, len = n;
-    while (len > 0) {
-        const uint32_t step = (len + 31) / 32;
-        const uint32_t i = lo + min((lane + 1) * step, len) - 1;
-        const uint32_t not_less = ~__ballot_sync(kFull, off[i] < key);
-        if (not_less == 0) return lo + len;
-        const uint32_t less = __ffs(not_less) - 1;
-        lo += less * step;
-        if (step == 1) return lo;
-        len = min(step, len - less * step) - 1;  // its last one is known not to be less
-        if (len == 0) return lo;
-    }
-    return lo;
-}
-
 // Where sequences start and end in a warp's kS rows: bits, and the sequences in the arrays (the
 // warp's own). mine: the lane's entry of a table of at most 32.
 template <int kS>
@@ -150,7 +134,7 @@ struct Marks {
         const int64_t begin = first, stop = begin + kS;
         start = end = 0;
         __syncwarp();  // the arrays' readers of the tile before
-        for (uint32_t i0 = n <= 32 ? 0 : first_from(a.offsets, n, begin);; i0 += 32) {
+        for (uint32_t i0 = n <= 32 ? 0 : first_from(a.offsets, 0, n, begin);; i0 += 32) {
             const uint32_t i = i0 + lane;
             const int64_t off = n <= 32 ? mine : i < n ? a.offsets[i] : INT64_MAX;
             if (__any_sync(kFull, off >= begin && off <= stop)) {
@@ -200,41 +184,27 @@ __device__ __forceinline__ void empty_sequences(const ScanArgs& a, uint32_t tile
 struct Tile {
     uint32_t order, tile;
 };
-// A block's tiles. The first one is computed, the others, kAhead, have their copies under way (the
-// last one's begin with the first one's computation).
-template <int kAhead>
-struct Tiles {
-    Tile held[kAhead + 1];
-    __device__ Tiles(const ScanArgs& a, uint32_t* slot) {
-        if (!a.ticket) {
-            held[0] = {0, blockIdx.x};
-#pragma unroll
-            for (int i = 1; i <= kAhead; ++i) held[i] = {a.chunks, 0};
-            return;
-        }
-        // One by one: neighbouring tickets belong to blocks that work at the same time. (Taken
-        // together, each block's second tile kept others waiting for its first: 630 us for 279.)
-#pragma unroll
-        for (int i = 0; i <= kAhead; ++i) {
-            if (threadIdx.x == 0) *slot = atomicAdd(a.ticket, 1u);
-            __syncthreads();
-            held[i] = {*slot / a.tiles, *slot % a.tiles};
-            __syncthreads();
-        }
-    }
-    __device__ void step(const ScanArgs& a, uint32_t ticket) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) held[i] = held[i + 1];
-        held[kAhead] = {ticket / a.tiles, ticket % a.tiles};
-    }
-};
+__device__ __forceinline__ Tile tile_of(const ScanArgs& a, uint32_t ticket) {
+    // ticket / tiles, by the reciprocal rounded down: at most one short
+    uint32_t order = __umulhi(ticket, a.tiles_inverse);
+    if (ticket - order * a.tiles >= a.tiles) ++order;
+    return {order, ticket - order * a.tiles};
+}
+__device__ __forceinline__ Tile first_tile(const ScanArgs& a, uint32_t* slot) {
+    if (!a.ticket) return {0, blockIdx.x};
+    if (threadIdx.x == 0) *slot = atomicAdd(a.ticket, 1u);
+    __syncthreads();
+    const Tile t = tile_of(a, *slot);
+    __syncthreads();
+    return t;
+}
 
 // What the warps of a block tell one another about a tile. A tile has two barriers: what is written
 // ahead of the first one is read between the two, what is written between them is read behind the
 // second one and ahead of the next tile's first.
 struct Board {
     float4 map[kWarps][32];    // the warps' maps, in the scan's direction
-    float4 ahead[kWarps][32];  // the chunks' ahead of this one, four to an entry
+    float4 ahead[kWarps][32];  // the chunks' ahead of this one, kEach to an entry
     float2 state[32];          // that enters the group
     uint32_t next;             // ticket
     uint32_t fresh;            // a sequence begins with the chunk: nothing enters
@@ -276,10 +246,7 @@ __device__ __forceinline__ bool there(const uint2& v) { return v.x != kNotYet &&
 
 // Whether a wait goes on, after so many polls. When one gives up, the others do too.
 __device__ __forceinline__ bool wait_on(const ScanArgs& a, uint32_t polls) {
-    if (polls <= a.spin_limit && ((polls & 63) != 63 || ld_relaxed_u32(a.abort) == 0)) {
-        __nanosleep(20);
-        return true;
-    }
+    if (polls <= a.spin_limit && ((polls & 63) != 63 || ld_relaxed_u32(a.abort) == 0)) return true;
     if ((threadIdx.x & 31) == 0) {
         report(a.status, DGC_ETIMEOUT);
         atomicExch(a.abort, 1u);
@@ -287,11 +254,12 @@ __device__ __forceinline__ bool wait_on(const ScanArgs& a, uint32_t polls) {
     return false;
 }
 
-// Step 2 by all warps: `w` is the warp's place in the scan's direction, m its map (on the board),
-// `order` the chunk's place, resets: whether a sequence begins in it. Returns the map of the warps ahead of this one; a barrier has to follow.
-__device__ __forceinline__ Map collect(const ScanArgs& a, Board& b, uint32_t order, uint32_t tile,
-                                       int w, const Map& m, bool fresh, bool resets) {
-    const uint32_t lane = threadIdx.x & 31, group = order / kGroup, k = order % kGroup;
+// Step 1's end, by all warps: `w` is the warp's place in the scan's direction, m its map (on the
+// board), `order` the chunk's place, resets: whether a sequence begins in it. Returns the map of the
+// warps ahead of this one; the last one publishes the chunk's.
+__device__ __forceinline__ Map compose(const ScanArgs& a, const Board& b, uint32_t order,
+                                       uint32_t tile, int w, const Map& m, bool resets) {
+    const uint32_t lane = threadIdx.x & 31;
     Map before = identity();
     if (resets)
         for (int i = 0; i < w; ++i) before = before.then(map_of(b.map[i][lane]));
@@ -299,48 +267,62 @@ __device__ __forceinline__ Map collect(const ScanArgs& a, Board& b, uint32_t ord
 #pragma unroll
         for (int i = 0; i < kWarps - 1; ++i)
             if (i < w) before = before.plain_then(map_of(b.map[i][lane]));
-    if (!a.ticket) return before;
-    if (w == kWarps - 1 && order != a.lost)
+    if (a.ticket && w == kWarps - 1 && order != a.lost)
         publish(&a.maps[((uint64_t)order * a.tiles + tile) * 32 + lane], before.then(m));
-    if (fresh) return before;
-    const uint32_t from = 4 * (uint32_t)w, count = k > from ? min(4u, k - from) : 0;
-    if (count) {
-        const uint4* p = a.maps + (((uint64_t)group * kGroup + from) * a.tiles + tile) * 32 + lane;
-        const uint64_t step = (uint64_t)a.tiles * 32;
-        uint4 v[4];
-        for (uint32_t polls = 0;; ++polls) {
-            bool ready = true;
+    return before;
+}
+
+// Step 2: a warp collects the maps of kEach chunks, the last one also the state that enters the group
+// (it has the fewest chunks to wait for). The first look is taken ahead of the next tile's copies, or
+// it would queue behind them (2500 clocks for 900).
+struct LookBack {
+    const uint4* maps;
+    const uint2* state;
+    uint64_t step;
+    uint32_t count;
+    uint4 v[kEach];
+    uint2 h;
+    __device__ LookBack(const ScanArgs& a, uint32_t order, uint32_t tile, int w, bool fresh) {
+        const uint32_t lane = threadIdx.x & 31, group = order / kGroup, k = order % kGroup;
+        const uint32_t from = kEach * (uint32_t)w;
+        count = 0;
+        state = nullptr;
+        h = make_uint2(0, 0);
+        if (!a.ticket || fresh) return;
+        if (k > from) count = min(kEach, k - from);
+        step = (uint64_t)a.tiles * 32;
+        maps = a.maps + ((uint64_t)group * kGroup + from) * step + tile * 32 + lane;
+        if (w == kWarps - 1 && group > 0) state = a.states + group * step + tile * 32 + lane;
+        look_again();
+    }
+    __device__ void look_again() {
 #pragma unroll
-            for (uint32_t i = 0; i < 4; ++i)
-                if (i < count) {
-                    v[i] = look(p + i * step);
-                    ready = ready && there(v[i]);
-                }
+        for (uint32_t i = 0; i < kEach; ++i)
+            if (i < count) v[i] = look(maps + i * step);
+        if (state) h = look(state);
+    }
+    // A barrier has to follow.
+    __device__ void finish(const ScanArgs& a, Board& b, int w) {
+        const uint32_t lane = threadIdx.x & 31;
+        for (uint32_t polls = 0;; ++polls) {
+            bool ready = !state || there(h);
+#pragma unroll
+            for (uint32_t i = 0; i < kEach; ++i)
+                if (i < count) ready = ready && there(v[i]);
             if (__all_sync(kFull, ready) || !wait_on(a, polls)) break;
+            look_again();
         }
         Map all = identity();
 #pragma unroll
-        for (uint32_t i = 0; i < 4; ++i)
+        for (uint32_t i = 0; i < kEach; ++i)
             if (i < count)
                 all = all.then({{__uint_as_float(v[i].x), __uint_as_float(v[i].y)},
                                 {__uint_as_float(v[i].z), __uint_as_float(v[i].w)}});
-        b.ahead[w][lane] = all.packed();
+        b.ahead[w][lane] = all.packed();  // without any: the identity
+        if (w == kWarps - 1)
+            b.state[lane] = {__uint_as_float(h.x), __uint_as_float(h.y)};
     }
-    if (w == 0) {
-        float2 h = {0.0f, 0.0f};
-        if (group > 0) {
-            const uint2* p = &a.states[((uint64_t)group * a.tiles + tile) * 32 + lane];
-            uint2 v;
-            for (uint32_t polls = 0;; ++polls) {
-                v = look(p);
-                if (__all_sync(kFull, there(v)) || !wait_on(a, polls)) break;
-            }
-            h = {__uint_as_float(v.x), __uint_as_float(v.y)};
-        }
-        b.state[lane] = h;
-    }
-    return before;
-}
+};
 
 // After the barrier: the state that enters the chunk. The last warp passes a group's on.
 __device__ __forceinline__ float2 enter(const ScanArgs& a, const Board& b, uint32_t order,
@@ -351,7 +333,9 @@ __device__ __forceinline__ float2 enter(const ScanArgs& a, const Board& b, uint3
     if (!a.ticket) return h;
     if (!fresh) {
         h = b.state[lane];
-        for (uint32_t i = 0; 4 * i < k; ++i) h = map_of(b.ahead[i][lane])(h);
+#pragma unroll
+        for (uint32_t i = 0; i < kWarps; ++i)
+            if (kEach * i < k) h = map_of(b.ahead[i][lane])(h);
     }
     if (w == kWarps - 1 && k == kGroup - 1 && order + 1 < a.chunks && order != a.lost)
         publish(&a.states[((uint64_t)(group + 1) * a.tiles + tile) * 32 + lane], m(before(h)));
@@ -373,18 +357,18 @@ template <typename T, int kUnit, int kS, int kOperands>
 struct Landing {
     using Word = std::conditional_t<sizeof(T) == 4, uint2, uint32_t>;  // a lane's two columns
     static constexpr uint32_t kRow = kCols * sizeof(T);
-    static constexpr uint32_t kStageBytes = kOperands * kWarps * kS * kRow;
+    static constexpr uint32_t kBytes = kOperands * kWarps * kS * kRow;
     Word* words;
     __device__ explicit Landing(void* ring) : words(static_cast<Word*>(ring)) {}
-    __device__ Word* rows(int stage, int q) const {
-        return words + ((stage * kOperands + q) * kWarps + (threadIdx.x >> 5)) * kS * 32;
+    __device__ Word* rows(int q) const {
+        return words + (q * kWarps + (threadIdx.x >> 5)) * kS * 32;
     }
     // rows `first` to first + kS - 1 of m, of which `left` are there, columns from col on
-    __device__ void fetch(int stage, int q, const void* m, uint64_t ld, uint64_t first,
-                          uint32_t left, uint32_t col, uint32_t cols) const {
+    __device__ void fetch(int q, const void* m, uint64_t ld, uint64_t first, uint32_t left,
+                          uint32_t col, uint32_t cols) const {
         const uint32_t lane = threadIdx.x & 31;
         const T* p = static_cast<const T*>(m) + first * ld + col;
-        Word* to = rows(stage, q);
+        Word* to = rows(q);
         if constexpr (kUnit == 16) {
             constexpr uint32_t kLanes = kRow / 16, kStep = 32 / kLanes;  // of a row; rows a turn
             const uint32_t r = lane / kLanes, c = lane % kLanes * (16 / sizeof(T));
@@ -421,9 +405,9 @@ struct Landing {
             }
         }
     }
-    __device__ float2 get(int stage, int q, int s) const {
+    __device__ float2 get(int q, int s) const {
         Packed<T, 2> p;
-        *reinterpret_cast<Word*>(p.w) = rows(stage, q)[s * 32 + (threadIdx.x & 31)];
+        *reinterpret_cast<Word*>(p.w) = rows(q)[s * 32 + (threadIdx.x & 31)];
         return pair_of<T, 2>(p, 0);
     }
 };
@@ -443,9 +427,9 @@ struct Spot {
 // --------------------------------------------------------------------------------- forward
 // Bound by HBM: x and gate read once, y written once. Rows with no border among them and whole
 // columns take a way without tests.
-template <typename T, int kUnit, int kS, int kStages>
-__global__ void __launch_bounds__(kThreads, 2) k_scan(const __grid_constant__ ScanArgs a) {
-    constexpr int kRows = kWarps * kS, kAhead = kStages - 1;
+template <typename T, int kUnit, int kS, int kBlocks>
+__global__ void __launch_bounds__(kThreads, kBlocks) k_scan(const __grid_constant__ ScanArgs a) {
+    constexpr int kRows = kWarps * kS;
     constexpr bool kPair = kUnit != 0;
     extern __shared__ uint4 ring[];
     __shared__ Board board;
@@ -455,36 +439,35 @@ __global__ void __launch_bounds__(kThreads, 2) k_scan(const __grid_constant__ Sc
     int32_t *starts = starts_of[warp], *ends = ends_of[warp];
     grid_dep_wait();
     grid_dep_launch();
-    Tiles<kAhead> tiles(a, &board.next);
-    auto fetch = [&](int stage, const Tile& t) {
+    Tile t = first_tile(a, &board.next);
+    auto fetch = [&] {
         if (t.order < a.chunks) {
             const Spot at(a, t.order, t.tile, kRows, kS);
-            land.fetch(stage, 0, a.gate, a.ldg, at.first, at.left, at.col, a.cols);
-            land.fetch(stage, 1, a.x, a.ldx, at.first, at.left, at.col, a.cols);
+            land.fetch(0, a.gate, a.ldg, at.first, at.left, at.col, a.cols);
+            land.fetch(1, a.x, a.ldx, at.first, at.left, at.col, a.cols);
         }
         copy_commit();
     };
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) fetch(i, tiles.held[i]);
+    fetch();
     const int64_t valid0 = a.offsets[0], valid1 = min((int64_t)a.rows, a.offsets[a.nseq]);
     const int64_t mine = lane <= a.nseq ? a.offsets[lane] : INT64_MAX;
-    for (int stage = 0; tiles.held[0].order < a.chunks;) {
-        uint32_t more = 0xFFFFFFFFu;  // the ticket behind those that are held
-        if (a.ticket && threadIdx.x == 0) more = atomicAdd(a.ticket, 1u);
-        fetch(stage == 0 ? kStages - 1 : stage - 1, tiles.held[kAhead]);
-        const uint32_t chunk = tiles.held[0].order, tile = tiles.held[0].tile;
+    while (t.order < a.chunks) {
+        const uint32_t chunk = t.order, tile = t.tile;
         const Spot at(a, chunk, tile, kRows, kS);
         if (chunk == 0) empty_sequences(a, tile, a.h0, a.ldh0, a.h_last, a.ldh_last);
         const Marks<kS> marks(a, at.first, mine, starts, ends);
-        copy_wait<kAhead>();
+        copy_wait<0>();
         __syncwarp();
+        // the next ticket; not ahead of the wait, which would wait for it too
+        uint32_t more = 0xFFFFFFFFu;
+        if (a.ticket && threadIdx.x == 0) more = atomicAdd(a.ticket, 1u);
         // rows as h -> A h + B
         float2 A[kS], B[kS];
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
             float2 keep;
-            sigmoids(land.get(stage, 0, s), A[s], keep);
-            B[s] = mul2(keep, land.get(stage, 1, s));
+            sigmoids(land.get(0, s), A[s], keep);
+            B[s] = mul2(keep, land.get(1, s));
         }
         Map m = identity();
         if (marks.start) {
@@ -513,9 +496,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_scan(const __grid_constant__ Sc
             board.next = more;
         }
         const bool resets = __syncthreads_or(marks.start != 0);
-        const uint32_t next = board.next;
+        const Map before = compose(a, board, chunk, tile, warp, m, resets);
         const bool fresh = board.fresh;
-        const Map before = collect(a, board, chunk, tile, warp, m, fresh, resets);
+        LookBack back(a, chunk, tile, warp, fresh);
+        t = tile_of(a, board.next);
+        fetch();
+        back.finish(a, board, warp);
         __syncthreads();
         float2 h = before(enter(a, board, chunk, tile, warp, before, m, fresh));
         if (a.saved && at.first % kPiece == 0 && at.left)
@@ -541,17 +527,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_scan(const __grid_constant__ Sc
                     store_state(a.h_last, a.ldh_last, ends[s], at.lane_col, at.n, h);
             }
         }
-        tiles.step(a, next);
-        stage = stage + 1 == kStages ? 0 : stage + 1;
     }
     copy_wait<0>();
 }
 
 // -------------------------------------------------------------------------------- backward
 // Bound by HBM: x, gate and dy read once, dx and dgate written once, the states of every 64th row.
-template <typename T, int kUnit, int kS, int kStages>
-__global__ void __launch_bounds__(kThreads, 2) k_scan_back(const __grid_constant__ ScanArgs a) {
-    constexpr int kRows = kWarps * kS, kAhead = kStages - 1;
+template <typename T, int kUnit, int kS, int kBlocks>
+__global__ void __launch_bounds__(kThreads, kBlocks) k_scan_back(const __grid_constant__ ScanArgs a) {
+    constexpr int kRows = kWarps * kS;
     constexpr bool kPair = kUnit != 0;
     static_assert(kRows == kPiece, "a chunk begins at its saved state");
     extern __shared__ uint4 ring[];
@@ -563,39 +547,38 @@ __global__ void __launch_bounds__(kThreads, 2) k_scan_back(const __grid_constant
     int32_t *starts = starts_of[warp], *ends = ends_of[warp];
     grid_dep_wait();
     grid_dep_launch();
-    Tiles<kAhead> tiles(a, &board.next);
-    auto fetch = [&](int stage, const Tile& t) {
+    Tile t = first_tile(a, &board.next);
+    auto fetch = [&] {
         if (t.order < a.chunks) {
             const Spot at(a, a.chunks - 1 - t.order, t.tile, kRows, kS);
-            land.fetch(stage, 0, a.gate, a.ldg, at.first, at.left, at.col, a.cols);
-            land.fetch(stage, 1, a.x, a.ldx, at.first, at.left, at.col, a.cols);
-            land.fetch(stage, 2, a.dy, a.lddy, at.first, at.left, at.col, a.cols);
+            land.fetch(0, a.gate, a.ldg, at.first, at.left, at.col, a.cols);
+            land.fetch(1, a.x, a.ldx, at.first, at.left, at.col, a.cols);
+            land.fetch(2, a.dy, a.lddy, at.first, at.left, at.col, a.cols);
         }
         copy_commit();
     };
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) fetch(i, tiles.held[i]);
+    fetch();
     const int64_t valid0 = a.offsets[0], valid1 = min((int64_t)a.rows, a.offsets[a.nseq]);
     const int64_t mine = lane <= a.nseq ? a.offsets[lane] : INT64_MAX;
-    for (int stage = 0; tiles.held[0].order < a.chunks;) {
-        uint32_t more = 0xFFFFFFFFu;
-        if (a.ticket && threadIdx.x == 0) more = atomicAdd(a.ticket, 1u);
-        fetch(stage == 0 ? kStages - 1 : stage - 1, tiles.held[kAhead]);
-        const uint32_t order = tiles.held[0].order, tile = tiles.held[0].tile;
+    while (t.order < a.chunks) {
+        const uint32_t order = t.order, tile = t.tile;
         const uint32_t chunk = a.chunks - 1 - order;
         const Spot at(a, chunk, tile, kRows, kS);
         float2 h = both(0.0f);
         if (chunk * kRows < a.rows) h = load_state(a.saved, a.lds, chunk, at.lane_col, at.n);
         if (chunk == 0) empty_sequences(a, tile, a.d_last, a.ldd_last, a.d_h0, a.ldd_h0);
         const Marks<kS> marks(a, at.first, mine, starts, ends);
-        copy_wait<kAhead>();
+        copy_wait<0>();
         __syncwarp();
+        // the next ticket; not ahead of the wait, which would wait for it too
+        uint32_t more = 0xFFFFFFFFu;
+        if (a.ticket && threadIdx.x == 0) more = atomicAdd(a.ticket, 1u);
         float2 A[kS], keep[kS], q[kS], G[kS];  // q: (1-a) x, then (h_{t-1} - x) a (1 - a)
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
-            sigmoids(land.get(stage, 0, s), A[s], keep[s]);
-            q[s] = mul2(keep[s], land.get(stage, 1, s));
-            G[s] = land.get(stage, 2, s);
+            sigmoids(land.get(0, s), A[s], keep[s]);
+            q[s] = mul2(keep[s], land.get(1, s));
+            G[s] = land.get(2, s);
         }
         if (marks.end && a.d_last)
 #pragma unroll
@@ -629,9 +612,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_scan_back(const __grid_constant
         if (threadIdx.x == kThreads - 1) board.fresh = marks.end >> (kS - 1) & 1;
         if (threadIdx.x == 0) board.next = more;
         const bool resets = __syncthreads_or((marks.start | marks.end) != 0);
-        const uint32_t next = board.next;
+        const Map behind = compose(a, board, order, tile, place, u, resets);
         const bool fresh = board.fresh;
-        const Map behind = collect(a, board, order, tile, place, u, fresh, resets);
         if (resets)
             for (int w = 0; w < warp; ++w) h = map_of(maps[w][lane])(h);
         else
@@ -644,10 +626,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_scan_back(const __grid_constant
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
             if (marks.start >> s & 1) h = first_state(s);
-            const float2 x = land.get(stage, 1, s), b = q[s];
+            const float2 x = land.get(1, s), b = q[s];
             q[s] = mul2(mul2(A[s], keep[s]), add2(h, {-x.x, -x.y}));
             h = fma2(A[s], h, b);
         }
+        LookBack back(a, order, tile, place, fresh);
+        __syncwarp();
+        t = tile_of(a, board.next);
+        fetch();
+        back.finish(a, board, place);
         __syncthreads();
         // u of the row behind
         float2 v = behind(enter(a, board, order, tile, place, behind, u, fresh));
@@ -680,18 +667,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_scan_back(const __grid_constant
                     store_state(a.d_h0, a.ldd_h0, starts[s], at.lane_col, at.n, v);
             }
         }
-        tiles.step(a, next);
-        stage = stage + 1 == kStages ? 0 : stage + 1;
     }
     copy_wait<0>();
 }
 
 // ----------------------------------------------------------------------------------- host
-// Rows of a warp, and stages of the ring: 96 KB of it a block, two blocks an SM.
+// Rows of a warp, and blocks of an SM.
 template <typename T>
 struct Form {
-    static constexpr int kS = sizeof(T) == 2 ? 16 : 8, kStages = 3;
-    static constexpr int kBackS = kPiece / kWarps, kBackStages = sizeof(T) == 2 ? 4 : 2;
+    static constexpr int kS = sizeof(T) == 2 ? 16 : 8, kBlocks = 2;
+    static constexpr int kBackS = kPiece / kWarps, kBackBlocks = 2;
 };
 
 struct ScanLayout {
@@ -726,11 +711,12 @@ int check_state(const dgc_matrix* m, uint64_t nseq, uint64_t cols, const float**
     return DGC_OK;
 }
 
-template <typename T, int kUnit, int kS, int kOperands, int kStages>
+template <typename T, int kUnit, int kS, int kOperands, int kBlocks>
 int launch_scan(void (*kernel)(ScanArgs), ScanArgs a, void* ws, int sms, cudaStream_t s) {
     const ScanLayout L = scan_layout(a.rows, a.cols, kWarps * kS);
     if ((uint64_t)L.tiles * L.chunks > 0x7FFFFFFFull) return DGC_EUNSUPPORTED;
     a.tiles = L.tiles;
+    a.tiles_inverse = (uint32_t)(0xFFFFFFFFull / L.tiles);
     a.chunks = L.chunks;
     if (!a.spin_limit) {
         a.spin_limit = kDefaultSpinLimit;
@@ -748,10 +734,10 @@ int launch_scan(void (*kernel)(ScanArgs), ScanArgs a, void* ws, int sms, cudaStr
                                           dim3((unsigned)umin64((words + 1023) / 1024, 1024)), 256,
                                           s, a.ticket, a.maps, words);
         if (rc) return rc;
-        blocks = (uint32_t)umin64((uint64_t)L.tiles * L.chunks, (uint64_t)sms * 2);
+        blocks = (uint32_t)umin64((uint64_t)L.tiles * L.chunks, (uint64_t)sms * kBlocks);
     }
     return launch_shared_kernel(kernel, dim3(blocks), kThreads,
-                                kStages * Landing<T, kUnit, kS, kOperands>::kStageBytes, s, a);
+                                Landing<T, kUnit, kS, kOperands>::kBytes, s, a);
 }
 
 int check_common(const dgc_matrix* x, const dgc_matrix* gate, const int64_t* offsets, int32_t nseq,
@@ -806,13 +792,13 @@ int recurrence(const dgc_matrix* x, const dgc_matrix* gate, const int64_t* offse
     const bool wide = pair && mx.on(16) && mg.on(16);
     return with_type(mx.dtype, [&](auto t) {
         using T = decltype(t);
-        constexpr int kS = Form<T>::kS, kStages = Form<T>::kStages, kTwo = 2 * sizeof(T);
+        constexpr int kS = Form<T>::kS, kBlocks = Form<T>::kBlocks, kTwo = 2 * sizeof(T);
         if (wide)
-            return launch_scan<T, 16, kS, 2, kStages>(k_scan<T, 16, kS, kStages>, a, ws, sms, s);
+            return launch_scan<T, 16, kS, 2, kBlocks>(k_scan<T, 16, kS, kBlocks>, a, ws, sms, s);
         if (pair)
-            return launch_scan<T, kTwo, kS, 2, kStages>(k_scan<T, kTwo, kS, kStages>, a, ws, sms,
+            return launch_scan<T, kTwo, kS, 2, kBlocks>(k_scan<T, kTwo, kS, kBlocks>, a, ws, sms,
                                                         s);
-        return launch_scan<T, 0, kS, 2, kStages>(k_scan<T, 0, kS, kStages>, a, ws, sms, s);
+        return launch_scan<T, 0, kS, 2, kBlocks>(k_scan<T, 0, kS, kBlocks>, a, ws, sms, s);
     });
 }
 
@@ -903,13 +889,13 @@ extern "C" int dgc_recurrence_backward(const dgc_matrix* dy, const dgc_matrix* x
     const bool wide = pair && mx.on(16) && mg.on(16) && my.on(16);
     return with_type(mx.dtype, [&](auto t) {
         using T = decltype(t);
-        constexpr int kS = Form<T>::kBackS, kStages = Form<T>::kBackStages, kTwo = 2 * sizeof(T);
+        constexpr int kS = Form<T>::kBackS, kBlocks = Form<T>::kBackBlocks, kTwo = 2 * sizeof(T);
         if (wide)
-            return launch_scan<T, 16, kS, 3, kStages>(k_scan_back<T, 16, kS, kStages>, a, ws, sms,
+            return launch_scan<T, 16, kS, 3, kBlocks>(k_scan_back<T, 16, kS, kBlocks>, a, ws, sms,
                                                       s);
         if (pair)
-            return launch_scan<T, kTwo, kS, 3, kStages>(k_scan_back<T, kTwo, kS, kStages>, a, ws,
+            return launch_scan<T, kTwo, kS, 3, kBlocks>(k_scan_back<T, kTwo, kS, kBlocks>, a, ws,
                                                         sms, s);
-        return launch_scan<T, 0, kS, 3, kStages>(k_scan_back<T, 0, kS, kStages>, a, ws, sms, s);
+        return launch_scan<T, 0, kS, 3, kBlocks>(k_scan_back<T, 0, kS, kBlocks>, a, ws, sms, s);
     });
 }

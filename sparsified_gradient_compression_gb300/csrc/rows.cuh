@@ -231,6 +231,24 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 both(float a) { return {a, a}; }
 
+// The first index i in [lo, lo + len) with a[i] >= key, lo + len if there is none, by all lanes of a
+// warp, 32 probes a step; any contents (where they do not rise, any index of the range).
+template <typename T>
+__device__ __forceinline__ uint32_t first_from(const T* a, uint32_t lo, uint32_t len, T key) {
+    const uint32_t lane = threadIdx.x & 31;
+    while (len > 0) {
+        const uint32_t step = (len + 31) / 32;
+        const uint32_t i = lo + min((lane + 1) * step, len) - 1;
+        const uint32_t not_less = ~__ballot_sync(kFull, a[i] < key);
+        if (not_less == 0) return lo + len;
+        const uint32_t less = __ffs(not_less) - 1;
+        lo += less * step;
+        if (step == 1) return lo;
+        len = min(step, len - less * step) - 1;  // its last one is known not to be less
+    }
+    return lo;
+}
+
 // Copies to shared memory that run behind the thread's back: kBytes (4, 8 or 16) of which the first
 // `n` are read and the rest become zeros. Every thread reads what it copied itself, after
 // copy_wait<k>: all but its last k groups of copies have arrived (the hardware's wait, no loop).
