@@ -8,12 +8,12 @@
 //                  bits, by one cluster: up to 32768 tokens.
 //   k_sort_count   for more: how often a block's tokens have each value of a digit;
 //   k_sort_move    puts them in the digit's order, equal ones in theirs.
-//   k_embed_sum    a warp sums the rows of 32 sorted tokens over some columns, and writes each
+//   k_embed_sum    a warp sums the rows of 8 or 32 sorted tokens over some columns, and writes each
 //                  word's sum once; other blocks zero the rows of words that are not met.
-//   k_embed_join   joins the sums of words that are met more than 32 times, in order.
+//   k_embed_join   joins the sums of words that are met more often than that, in order.
 //
 // No sum is made by atomic additions: the order of the additions is that of the positions within
-// 32 sorted tokens, and of these parts.
+// these tokens, and of these parts.
 #include <algorithm>
 
 #include "rows.cuh"
@@ -95,58 +95,71 @@ __global__ void __launch_bounds__(kThreads) k_embed(const __grid_constant__ Embe
 // ----------------------------------------------------------------------------------- sort
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortRows = 8;                                  // tokens of a lane
+constexpr uint32_t kSortRows = 8;                             // tokens of a lane, at most
 constexpr uint32_t kSortTile = kSortThreads * kSortRows;      // of a block
 constexpr int kDigits = 512;                                  // of up to 9 bits
 constexpr uint32_t kSortCluster = 8;                          // blocks
 constexpr uint32_t kSortMost = 256;                           // blocks of the launches for more
 
+// A token on its way: its word in the upper half, its position below. Sorted, items rise.
+using Item = uint64_t;
+
 struct SortArgs {
     Tokens tokens;                 // the first pass's source
-    uint32_t *key[2], *pos[2];     // pass p reads [p & 1] (but for the first) and writes the other
+    Item *from, *to;               // the first pass writes from, the second one to, and so on
     uint32_t* counts;              // [block][digit]
-    uint32_t n, per_block;         // per_block: a multiple of kSortTile
+    uint32_t n, per_block, rows;   // rows: of a lane in a tile; per_block: whole tiles
     uint32_t vocab, digit_bits, passes;
     int64_t padding;
     uint32_t* list_count;          // zeroed for k_embed_sum
     int32_t* status;
 };
 
-// The key of token i: its word; `vocab` (behind all words) for those without a gradient.
-__device__ __forceinline__ uint32_t sort_key(const SortArgs& a, uint32_t pass, uint32_t i) {
-    if (pass != 0) return __ldcg(&a.key[pass & 1][i]);  // of other blocks of this launch
+// Token i's item; `vocab` (behind all words) as the word of those without a gradient.
+__device__ __forceinline__ Item sort_item(const SortArgs& a, const Item* from, uint32_t i) {
+    if (from) return __ldcg(&from[i]);  // perhaps of another block of this launch
     const int64_t w = a.tokens[i];
     const bool known = w >= 0 && w < (int64_t)a.vocab;
     if (!known) report(a.status, DGC_EINVAL);
-    return known && w != a.padding ? (uint32_t)w : a.vocab;
+    return (Item)(known && w != a.padding ? (uint32_t)w : a.vocab) << 32 | i;
+}
+__device__ __forceinline__ uint32_t digit_of(Item v, uint32_t shift, uint32_t mask) {
+    return (uint32_t)(v >> 32 >> shift) & mask;
 }
 
-// A block's tile of tokens in shared memory, a warp's kSortRows * 32 of them in a row. (Short loops:
-// with the tile in registers, and so everything unrolled, a pass took 12 us, most of it the SMs'
-// wait for instructions that run once.)
+// A block's tile of items in shared memory, a warp's rows * 32 of them in a row. Short loops: code
+// that runs once waits for its instructions.
+constexpr Item kNone = ~0ull;
 struct SortTile {
-    uint32_t key[kSortTile], pos[kSortTile];
+    Item item[kSortTile];
     uint16_t rank[kSortTile];
 
-    __device__ void load(const SortArgs& a, uint32_t pass, uint32_t first, uint32_t end) {
-#pragma unroll 4
-        for (int i = 0; i < kSortRows; ++i) {
-            const uint32_t s = i * kSortThreads + threadIdx.x, at = first + s;
-            if (at < end) {
-                key[s] = sort_key(a, pass, at);
-                pos[s] = pass == 0 ? at : __ldcg(&a.pos[pass & 1][at]);
-            } else {
-                key[s] = 0xFFFFFFFFu;  // none
+    __device__ void load(const SortArgs& a, const Item* from, uint32_t first, uint32_t end) {
+#pragma unroll 1
+        for (uint32_t i = 0; i < a.rows; i += 4) {
+            Item v[4];  // four loads under way: none waits for another one's way to shared memory
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j) {
+                const uint32_t s = (i + j) * kSortThreads + threadIdx.x;
+                v[j] = i + j < a.rows && first + s < end ? sort_item(a, from, first + s) : kNone;
             }
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j)
+                if (i + j < a.rows) item[(i + j) * kSortThreads + threadIdx.x] = v[j];
         }
     }
     // Each token's place among its equals in the warp; count: how many of each digit it has.
-    __device__ void ranks(uint32_t shift, uint32_t mask, uint32_t* count) {
+    __device__ void ranks(const SortArgs& a, uint32_t shift, uint32_t mask, uint32_t* count) {
+        rank_items(a, item, rank, shift, mask, count);
+    }
+    __device__ static void rank_items(const SortArgs& a, const Item* item, uint16_t* rank,
+                                      uint32_t shift, uint32_t mask, uint32_t* count) {
         const uint32_t lane = threadIdx.x & 31, below = (1u << lane) - 1;
-        const uint32_t begin = (threadIdx.x >> 5) * (32 * kSortRows) + lane;
+        uint32_t s = (threadIdx.x >> 5) * (32 * a.rows) + lane;
 #pragma unroll 1
-        for (uint32_t s = begin; s < begin + 32 * kSortRows; s += 32) {
-            const uint32_t k = key[s], d = k == 0xFFFFFFFFu ? kDigits : (k >> shift) & mask;
+        for (uint32_t i = 0; i < a.rows; ++i, s += 32) {
+            const Item v = item[s];
+            const uint32_t d = v == kNone ? kDigits : digit_of(v, shift, mask);
             const unsigned same = __match_any_sync(kFull, d);
             const uint32_t r = d < kDigits ? count[d] : 0;
             __syncwarp();
@@ -155,17 +168,13 @@ struct SortTile {
             __syncwarp();
         }
     }
-    __device__ void store(const SortArgs& a, uint32_t pass, uint32_t shift, uint32_t mask,
+    __device__ void store(const SortArgs& a, Item* to, uint32_t shift, uint32_t mask,
                           const uint32_t* place) const {
-        const uint32_t begin = (threadIdx.x >> 5) * (32 * kSortRows) + (threadIdx.x & 31);
-#pragma unroll 2
-        for (uint32_t s = begin; s < begin + 32 * kSortRows; s += 32) {
-            const uint32_t k = key[s];
-            if (k != 0xFFFFFFFFu) {
-                const uint32_t to = place[(k >> shift) & mask] + rank[s];
-                a.key[~pass & 1][to] = k;
-                a.pos[~pass & 1][to] = pos[s];
-            }
+        uint32_t s = (threadIdx.x >> 5) * (32 * a.rows) + (threadIdx.x & 31);
+#pragma unroll 1
+        for (uint32_t i = 0; i < a.rows; ++i, s += 32) {
+            const Item v = item[s];
+            if (v != kNone) to[place[digit_of(v, shift, mask)] + rank[s]] = v;
         }
     }
 };
@@ -175,18 +184,16 @@ __device__ __forceinline__ void clear_places(uint32_t (*place)[kDigits]) {
     for (int w = 0; w < kSortWarps; ++w) place[w][threadIdx.x] = 0;
 }
 // Where the thread's digit begins in the order: behind all smaller ones and those of the blocks
-// before this one. counts of `blocks` blocks; own: this block's.
-__device__ __forceinline__ uint32_t digit_begin(const uint32_t* counts, uint32_t blocks,
-                                                uint32_t block, uint32_t own, uint32_t* scan) {
-    uint32_t before = 0, all = own;
-    if (blocks > 1) {
-        all = 0;
+// before this one. count(b): block b's.
+template <typename Count>
+__device__ __forceinline__ uint32_t digit_begin(uint32_t blocks, uint32_t block, uint32_t* scan,
+                                                Count count) {
+    uint32_t before = 0, all = 0;
 #pragma unroll 8
-        for (uint32_t b = 0; b < blocks; ++b) {
-            const uint32_t c = __ldcg(&counts[b * kDigits + threadIdx.x]);
-            all += c;
-            if (b < block) before += c;
-        }
+    for (uint32_t b = 0; b < blocks; ++b) {
+        const uint32_t c = count(b);
+        all += c;
+        if (b < block) before += c;
     }
     uint32_t total;
     return block_excl_scan<kSortThreads>(all, scan, &total) + before;
@@ -205,58 +212,96 @@ __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The address of the same shared variable in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_block(const void* p, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
+    return r;
+}
 
-// All passes by one cluster of up to 8 blocks, a tile each. The blocks' counts and the tokens go
-// through global memory (L2).
+// All passes by one cluster of up to 8 blocks, a tile each: the items stay in the blocks' shared
+// memory and go from pass to pass to where they belong. (Through L2, 16384 tokens took 16 us.)
+struct ClusterTile {
+    Item item[2][kSortTile];
+    uint16_t rank[kSortTile];
+    uint32_t own[kDigits];
+};
 __global__ void __launch_bounds__(kSortThreads) k_sort(const __grid_constant__ SortArgs a) {
     extern __shared__ uint4 shared[];
-    SortTile& tile = *reinterpret_cast<SortTile*>(shared);
+    ClusterTile& tile = *reinterpret_cast<ClusterTile*>(shared);
     __shared__ uint32_t place[kSortWarps][kDigits];
     __shared__ uint32_t scan[33];
     const int warp = threadIdx.x >> 5;
     grid_dep_wait();
     grid_dep_launch();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.list_count = 0;
+    const uint32_t mask = (1u << a.digit_bits) - 1, begin = blockIdx.x * a.per_block;
+#pragma unroll 4
+    for (uint32_t i = 0; i < a.rows; ++i) {
+        const uint32_t s = i * kSortThreads + threadIdx.x;
+        const Item v = begin + s < a.n ? sort_item(a, nullptr, begin + s) : kNone;
+        tile.item[0][s] = v;
+        if (v == kNone) tile.item[1][s] = v;
+    }
     for (uint32_t pass = 0; pass < a.passes; ++pass) {
-        const uint32_t shift = pass * a.digit_bits, mask = (1u << a.digit_bits) - 1;
-        tile.load(a, pass, blockIdx.x * kSortTile, a.n);
+        const uint32_t shift = pass * a.digit_bits;
+        const Item* item = tile.item[pass & 1];
         clear_places(place);
         __syncthreads();
-        tile.ranks(shift, mask, place[warp]);
+        SortTile::rank_items(a, item, tile.rank, shift, mask, place[warp]);
         __syncthreads();
         uint32_t own = 0;
 #pragma unroll 4
         for (int w = 0; w < kSortWarps; ++w) own += place[w][threadIdx.x];
-        if (gridDim.x > 1) {
-            __stcg(&a.counts[blockIdx.x * kDigits + threadIdx.x], own);
-            cluster_barrier();
+        tile.own[threadIdx.x] = own;
+        cluster_barrier();
+        warp_places(place, digit_begin(gridDim.x, blockIdx.x, scan, [&](uint32_t b) {
+                        uint32_t c;
+                        asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                                     : "=r"(c)
+                                     : "r"(in_block(&tile.own[threadIdx.x], b))
+                                     : "memory");
+                        return c;
+                    }));
+        __syncthreads();
+        uint32_t s = warp * (32 * a.rows) + (threadIdx.x & 31);
+#pragma unroll 1
+        for (uint32_t i = 0; i < a.rows; ++i, s += 32) {
+            const Item v = item[s];
+            if (v == kNone) continue;
+            const uint32_t to = place[warp][digit_of(v, shift, mask)] + tile.rank[s];
+            if (pass + 1 == a.passes) {
+                a.from[to] = v;
+            } else {
+                const uint32_t b = to / a.per_block;
+                asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(
+                                 in_block(&tile.item[~pass & 1][to - b * a.per_block], b)),
+                             "l"(v)
+                             : "memory");
+            }
         }
-        warp_places(place, digit_begin(a.counts, gridDim.x, blockIdx.x, own, scan));
-        __syncthreads();
-        tile.store(a, pass, shift, mask, place[warp]);
-        if (gridDim.x > 1) cluster_barrier();
-        __syncthreads();
+        cluster_barrier();
     }
 }
 
 __global__ void __launch_bounds__(kSortThreads)
-    k_sort_count(const __grid_constant__ SortArgs a, uint32_t pass) {
+    k_sort_count(const __grid_constant__ SortArgs a, const Item* from, uint32_t shift) {
     __shared__ uint32_t count[kDigits];
     grid_dep_wait();
     grid_dep_launch();
     count[threadIdx.x] = 0;
     __syncthreads();
-    const uint32_t shift = pass * a.digit_bits, mask = (1u << a.digit_bits) - 1;
+    const uint32_t mask = (1u << a.digit_bits) - 1;
     const uint32_t begin = blockIdx.x * a.per_block, end = min(a.n, begin + a.per_block);
     for (uint32_t i = begin + threadIdx.x; i < end; i += kSortThreads)
-        atomicAdd(&count[(sort_key(a, pass, i) >> shift) & mask], 1u);
+        atomicAdd(&count[digit_of(sort_item(a, from, i), shift, mask)], 1u);
     __syncthreads();
     a.counts[blockIdx.x * kDigits + threadIdx.x] = count[threadIdx.x];
 }
 
 // A block's tiles one behind the other.
 __global__ void __launch_bounds__(kSortThreads)
-    k_sort_move(const __grid_constant__ SortArgs a, uint32_t pass) {
+    k_sort_move(const __grid_constant__ SortArgs a, const Item* from, Item* to, uint32_t shift) {
     extern __shared__ uint4 shared[];
     SortTile& tile = *reinterpret_cast<SortTile*>(shared);
     __shared__ uint32_t place[kSortWarps][kDigits];
@@ -265,19 +310,20 @@ __global__ void __launch_bounds__(kSortThreads)
     grid_dep_wait();
     grid_dep_launch();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.list_count = 0;
-    const uint32_t shift = pass * a.digit_bits, mask = (1u << a.digit_bits) - 1;
+    const uint32_t mask = (1u << a.digit_bits) - 1;
     const uint32_t begin = blockIdx.x * a.per_block, end = min(a.n, begin + a.per_block);
-    uint32_t at = digit_begin(a.counts, gridDim.x, blockIdx.x,
-                              a.counts[blockIdx.x * kDigits + threadIdx.x], scan);
-    for (uint32_t first = begin; first < end; first += kSortTile) {
-        tile.load(a, pass, first, end);
+    uint32_t at = digit_begin(gridDim.x, blockIdx.x, scan, [&](uint32_t b) {
+        return a.counts[b * kDigits + threadIdx.x];
+    });
+    for (uint32_t first = begin; first < end; first += a.rows * kSortThreads) {
+        tile.load(a, from, first, end);
         clear_places(place);
         __syncthreads();
-        tile.ranks(shift, mask, place[warp]);
+        tile.ranks(a, shift, mask, place[warp]);
         __syncthreads();
         at = warp_places(place, at);
         __syncthreads();
-        tile.store(a, pass, shift, mask, place[warp]);
+        tile.store(a, to, shift, mask, place[warp]);
         __syncthreads();
     }
 }
@@ -286,7 +332,7 @@ __global__ void __launch_bounds__(kSortThreads)
 constexpr uint32_t kZeroRows = 32, kZeroCols = 1024;  // of a unit of zeros
 
 struct SumArgs {
-    const uint32_t *key, *pos;   // sorted
+    const Item* items;           // sorted
     uint32_t n, vocab, cols;
     const void* dy;
     uint64_t ldy;
@@ -296,34 +342,61 @@ struct SumArgs {
     int32_t accumulate;
     uint32_t tiles;              // of columns: a warp's
     uint32_t sum_blocks;         // the others zero
-    float* part;                 // [chunk][2][ldp]: of words met more than 32 times, the sum in a
-    uint64_t ldp;                // chunk that goes on from the last one, and in one that starts it
+    uint32_t tokens;             // of a chunk
+    float* part;                 // [chunk][2][ldp]: of words met more often, the sum in a chunk that
+    uint64_t ldp;                // goes on from the last one, and in one that starts it
     uint32_t *list, *list_count; // chunks where such words start
 };
 
 __device__ __forceinline__ uint32_t trailing_ones(uint32_t x) { return ~x ? __ffs(~x) - 1 : 32; }
 
-// 32 sorted tokens and what surrounds them, as bits: whether a token has its predecessor's word.
+// kTokens (8 or 32) sorted tokens and what surrounds them, as bits: whether a token has its
+// predecessor's word.
+template <int kTokens>
 struct Chunk {
-    uint32_t key, key_next;  // of this lane, here and 32 tokens on
-    uint32_t e0, e1, e2;     // bits of the 32 tokens ahead, of the chunk, and of the 32 behind
+    static constexpr uint32_t kMask = kTokens == 32 ? 0xFFFFFFFFu : (1u << kTokens) - 1;
+    Item item, item_next;  // of this lane: 32 tokens, and (kTokens 32) the 32 behind
+    uint32_t e0, e1, e2;   // bits of the tokens ahead, of the chunk, and of those behind
+    uint32_t valid;        // how many of the chunk have a gradient
     __device__ Chunk(const SumArgs& a, uint32_t base) {
         const int lane = threadIdx.x & 31;
         // no two neighbours outside the list are alike
         auto at = [&](int64_t i) {
-            return i >= 0 && i < (int64_t)a.n ? a.key[i] : 0x80000000u + ((uint32_t)i & 1);
+            return i >= 0 && i < (int64_t)a.n ? a.items[i]
+                                              : (Item)(0x80000000u + ((uint32_t)i & 1)) << 32;
         };
-        const uint32_t before = at((int64_t)base - 32 + lane);
-        key = at((int64_t)base + lane);
-        key_next = at((int64_t)base + 32 + lane);
-        auto bits = [&](uint32_t k, uint32_t last) {
+        auto bits = [&](Item v, uint32_t last) {
+            const uint32_t k = (uint32_t)(v >> 32);
             uint32_t p = __shfl_up_sync(kFull, k, 1);
             if (lane == 0) p = last;
             return __ballot_sync(kFull, k == p);
         };
-        e0 = bits(before, ~before);
-        e1 = bits(key, __shfl_sync(kFull, before, 31));
-        e2 = bits(key_next, __shfl_sync(kFull, key, 31));
+        auto word = [&](Item v, int from) {
+            return __shfl_sync(kFull, (uint32_t)(v >> 32), from);
+        };
+        if constexpr (kTokens == 32) {
+            const Item before = at((int64_t)base - 32 + lane);
+            item = at((int64_t)base + lane);
+            item_next = at((int64_t)base + 32 + lane);
+            e0 = bits(before, ~(uint32_t)(before >> 32));
+            e1 = bits(item, word(before, 31));
+            e2 = bits(item_next, word(item, 31));
+            valid = __popc(__ballot_sync(kFull, (uint32_t)(item >> 32) < a.vocab));
+        } else {
+            item = at((int64_t)base - kTokens + lane);
+            const uint32_t all = bits(item, ~(uint32_t)(item >> 32));
+            e0 = all & kMask;
+            e1 = all >> kTokens & kMask;
+            e2 = all >> 2 * kTokens & kMask;
+            valid = __popc(__ballot_sync(kFull, (uint32_t)(item >> 32) < a.vocab) >> kTokens & kMask);
+        }
+    }
+    // the e-th token from the chunk's first one on
+    __device__ Item get(uint32_t e) const {
+        if constexpr (kTokens == 32)
+            return __shfl_sync(kFull, e < 32 ? item : item_next, e & 31);
+        else
+            return __shfl_sync(kFull, item, e + kTokens);
     }
 };
 
@@ -373,11 +446,13 @@ struct Cols {
 };
 
 // Bound by HBM: dy read once, the table written once (read and written where it is added to).
-// A word met up to 32 times is summed by the warp in whose chunk it starts; a longer run is cut at
-// the chunks' borders. kN: a lane's columns.
-template <typename T, int kN, bool kWide, bool kAdd>
+// A word met up to kTokens times is summed by the warp in whose chunk it starts; a longer run is cut
+// at the chunks' borders. kN: a lane's columns.
+template <typename T, int kTokens, int kN, bool kWide, bool kAdd>
 __global__ void __launch_bounds__(kThreads, 2) k_embed_sum(const __grid_constant__ SumArgs a) {
-    constexpr int kBatch = 4;  // rows in flight (and as many of the table's)
+    // rows in flight (and of the table); more of 16 bytes take so many registers that there are less
+    // warps (16384 x 4096 over 50000 words: 175 us for 162)
+    constexpr int kBatch = kN == 8 ? 4 : 8;
     const int lane = threadIdx.x & 31;
     grid_dep_wait();
     grid_dep_launch();
@@ -390,14 +465,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_embed_sum(const __grid_constant
             const Cols<4, kWide> cols(tile, a.cols);
             // is this lane's row met? The rows' stretch of the list first, then a row's
             const uint32_t row = row0 + lane;
-            const uint32_t from = first_from(a.key, 0, a.n, row0);
-            uint32_t lo = from, hi = from + first_from(a.key + from, 0, a.n - from, row0 + kZeroRows);
+            const uint32_t from = first_from(a.items, 0, a.n, (Item)row0 << 32);
+            uint32_t lo = from, hi = first_from(a.items, from, a.n - from,
+                                                (Item)(row0 + kZeroRows) << 32);
             const uint32_t stop = hi;
             while (lo < hi) {
                 const uint32_t mid = (lo + hi) >> 1;
-                if (a.key[mid] < row) lo = mid + 1; else hi = mid;
+                if (a.items[mid] < (Item)row << 32) lo = mid + 1; else hi = mid;
             }
-            const bool met = lo < stop && a.key[lo] == row;
+            const bool met = lo < stop && (uint32_t)(a.items[lo] >> 32) == row;
             uint32_t todo = __ballot_sync(kFull, !met && row < a.vocab);
             const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             for (; todo; todo &= todo - 1)
@@ -406,79 +482,86 @@ __global__ void __launch_bounds__(kThreads, 2) k_embed_sum(const __grid_constant
         return;
     }
     const T* dy = static_cast<const T*>(a.dy);
-    const uint32_t chunks = (a.n + 31) / 32;
+    constexpr uint32_t kT = kTokens;
+    const uint32_t chunks = (a.n + kT - 1) / kT;
     const uint64_t units = (uint64_t)chunks * a.tiles;
     for (uint64_t u = (uint64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < units;
          u += (uint64_t)a.sum_blocks * (kThreads / 32)) {
         const uint32_t chunk = (uint32_t)(u / a.tiles), tile = (uint32_t)(u % a.tiles);
-        const uint32_t base = chunk * 32;
         const Cols<kN, kWide> cols(tile, a.cols);
-        const Chunk c(a, base);
-        const uint32_t pos = base + lane < a.n ? a.pos[base + lane] : 0;
-        const uint32_t pos_next = base + 32 + lane < a.n ? a.pos[base + 32 + lane] : 0;
-        const uint32_t valid = __popc(__ballot_sync(kFull, c.key < a.vocab));
+        const Chunk<kTokens> c(a, chunk * kT);
         // the run that the first token continues: how much of it is ahead and from here on
         const bool goes_on = c.e1 & 1;
-        const uint32_t ahead = goes_on ? 1 + min(31, __clz(~c.e0)) : 0;
-        uint32_t head = 1 + trailing_ones(c.e1 >> 1);  // e1 >> 1 has 31 bits
-        if (head == 32) head += trailing_ones(c.e2);
-        const bool long_head = goes_on && ahead + head > 32;
+        const uint32_t ahead =
+            goes_on ? 1 + min(kT - 1, (uint32_t)__clz(~(c.e0 << (32 - kTokens)))) : 0;
+        uint32_t head = 1 + trailing_ones(c.e1 >> 1);  // e1 >> 1 has one bit less
+        if (head == kT) head += min(kT, trailing_ones(c.e2));
+        const bool long_head = goes_on && ahead + head > kT;
         // the last run that starts here, and how far it goes
-        const int last = ~c.e1 ? 31 - __clz(~c.e1) : -1;
-        const uint32_t behind = trailing_ones(c.e2);
-        const bool long_tail = last >= 0 && 32 - last + behind > 32;
+        const uint32_t begins = ~c.e1 & c.kMask;
+        const uint32_t last = begins ? 31 - __clz(begins) : kT;
+        const uint32_t behind = min(kT, trailing_ones(c.e2));
+        const bool long_tail = begins && kT - last + behind > kT;
         const uint32_t begin = !goes_on || long_head ? 0 : head;
-        uint32_t end = last < 0 || long_tail ? 32 : 32 + behind;
-        if (valid < 32) end = min(end, valid);  // words without a gradient are the last ones
-        if (long_tail && valid == 32 && tile == 0 && lane == 0)
+        uint32_t end = !begins || long_tail ? kT : kT + behind;
+        if (c.valid < kT) end = min(end, c.valid);  // words without a gradient are the last ones
+        if (long_tail && c.valid == kT && tile == 0 && lane == 0)
             a.list[atomicAdd(a.list_count, 1u)] = chunk;
         // which tokens end a run, and which of those runs are whole: from head on, ahead of last
-        const uint64_t ends = ~(((uint64_t)c.e2 << 32 | c.e1) >> 1);  // bit 63: 1
+        const uint64_t ends = ~(((uint64_t)c.e2 << kTokens | c.e1) >> 1);  // the last bit: 1
         const uint32_t whole_from = long_head ? head : 0, whole_to = long_tail ? last : 64;
-        float acc[kN];
-#pragma unroll
-        for (int j = 0; j < kN; ++j) acc[j] = 0.0f;
-#pragma unroll 1
-        for (uint32_t e0 = begin; e0 < end; e0 += kBatch) {
+        struct Batch {
             Packed<T, kN> p[kBatch];
             Packed<float, kN> old[kAdd ? kBatch : 1];
             float* row[kBatch];  // where the run's sum goes, at its end
+        };
+        auto load = [&](Batch& b, uint32_t e0) {
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 const uint32_t e = min(e0 + i, end - 1);
-                const uint32_t t = __shfl_sync(kFull, e < 32 ? pos : pos_next, e & 31);
-                const uint32_t word = __shfl_sync(kFull, e < 32 ? c.key : c.key_next, e & 31);
-                p[i] = cols.load(dy + (uint64_t)t * a.ldy);
-                row[i] = nullptr;
-                if (e0 + i < end && ((ends >> e & 1) || e + 1 == end)) {
-                    const bool whole = e >= whole_from && e < whole_to;
-                    row[i] = whole ? a.dtable + (uint64_t)word * a.ldt
-                                   : a.part + ((uint64_t)chunk * 2 + (e >= whole_from)) * a.ldp;
-                    if (kAdd && whole) old[i] = cols.load(row[i]);
-                }
+                const Item item = c.get(e);
+                const uint32_t word = (uint32_t)(item >> 32);
+                b.p[i] = cols.load(dy + (uint64_t)(uint32_t)item * a.ldy);
+                const bool stop = e0 + i < end && ((ends >> e & 1) || e + 1 == end);
+                const bool whole = stop && e >= whole_from && e < whole_to;
+                float* const to = whole ? a.dtable + (uint64_t)word * a.ldt
+                                        : a.part + ((uint64_t)chunk * 2 + (e >= whole_from)) * a.ldp;
+                b.row[i] = stop ? to : nullptr;
+                if (kAdd) b.old[i] = cols.load(whole ? to : a.part);  // no test ahead of a load
             }
+        };
+        float acc[kN];
+#pragma unroll
+        for (int j = 0; j < kN; ++j) acc[j] = 0.0f;
+        auto add = [&](const Batch& b, uint32_t e0) {
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 const uint32_t e = e0 + i;
                 if (e < end) {
                     float f[kN];
-                    unpack<T, kN>(p[i], f);
+                    unpack<T, kN>(b.p[i], f);
 #pragma unroll
                     for (int j = 0; j < kN; ++j) acc[j] += f[j];
                 }
-                if (row[i]) {
+                if (b.row[i]) {
                     if (e >= whole_from && e < whole_to) {
                         float was[kN];
-                        if (kAdd) unpack<float, kN>(old[kAdd ? i : 0], was);
+                        if (kAdd) unpack<float, kN>(b.old[kAdd ? i : 0], was);
 #pragma unroll
                         for (int j = 0; j < kN; ++j)
                             acc[j] = kAdd ? fmaf(acc[j], a.scale, was[j]) : acc[j] * a.scale;
                     }
-                    cols.store(row[i], acc);
+                    cols.store(b.row[i], acc);
 #pragma unroll
                     for (int j = 0; j < kN; ++j) acc[j] = 0.0f;
                 }
             }
+        };
+#pragma unroll 1
+        for (uint32_t e0 = begin; e0 < end; e0 += kBatch) {
+            Batch b;
+            load(b, e0);
+            add(b, e0);
         }
     }
 }
@@ -495,14 +578,14 @@ __global__ void __launch_bounds__(kThreads) k_embed_join(const __grid_constant__
     const uint32_t count = *a.list_count;
     const uint32_t tiles = (a.cols + 127) / 128;
     for (uint64_t u = blockIdx.x; u < (uint64_t)count * tiles; u += gridDim.x) {
-        const uint32_t chunk = a.list[u / tiles], next = chunk * 32 + 32;
+        const uint32_t chunk = a.list[u / tiles], next = (chunk + 1) * a.tokens;
         const Cols<4, kWide> cols((uint32_t)(u % tiles), a.cols);
-        const uint32_t word = a.key[next - 1];
+        const uint32_t word = (uint32_t)(a.items[next - 1] >> 32);
         float* out = a.dtable + (uint64_t)word * a.ldt;
         Packed<float, 4> old{};
         if (kAdd && warp == 0) old = cols.load(out);
-        const uint32_t end = first_from(a.key, next, a.n - next, word + 1);
-        const uint32_t parts = (end - 1) / 32 - chunk + 1, share = (parts + kWarps - 1) / kWarps;
+        const uint32_t end = first_from(a.items, next, a.n - next, (Item)(word + 1) << 32);
+        const uint32_t parts = (end - 1) / a.tokens - chunk + 1, share = (parts + kWarps - 1) / kWarps;
         float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         const uint32_t from = min(parts, warp * share), to = min(parts, from + share);
 #pragma unroll 8
@@ -534,8 +617,9 @@ __global__ void __launch_bounds__(kThreads) k_embed_join(const __grid_constant__
 
 // ----------------------------------------------------------------------------------- host
 struct BackwardLayout {
-    uint32_t blocks, per_block, passes, digit_bits;  // of the sort
-    size_t key[2], pos[2], counts, list, part, total;
+    uint32_t blocks, per_block, rows, passes, digit_bits;  // of the sort
+    uint32_t tokens;                                       // of a chunk of the sums
+    size_t items[2], counts, list, part, total;
     uint64_t ldp;
 };
 BackwardLayout backward_layout(uint64_t n, uint64_t vocab, uint64_t dim) {
@@ -545,21 +629,30 @@ BackwardLayout backward_layout(uint64_t n, uint64_t vocab, uint64_t dim) {
     while ((vocab >> bits) != 0) ++bits;  // keys 0 to vocab
     L.passes = (bits + 8) / 9;
     L.digit_bits = (bits + L.passes - 1) / L.passes;
-    // a tile a block where a cluster sorts, else whole tiles, as many as it takes
-    const uint64_t tiles = (n + kSortTile - 1) / kSortTile;
-    const uint64_t each = tiles <= kSortCluster ? 1 : (tiles + kSortMost - 1) / kSortMost;
-    L.per_block = (uint32_t)(each * kSortTile);
-    L.blocks = (uint32_t)((tiles + each - 1) / each);
+    // A tile a block where a cluster sorts, of up to 2048 tokens while that is enough for all of
+    // them; else whole tiles, as many as it takes.
+    if (n <= kSortCluster * (uint64_t)kSortTile) {
+        const uint64_t rows = (n + kSortThreads - 1) / kSortThreads;
+        L.rows = (uint32_t)std::max((rows + kSortCluster - 1) / kSortCluster,
+                                    std::min<uint64_t>(4, rows));
+        L.per_block = L.rows * kSortThreads;
+    } else {
+        const uint64_t tiles = (n + kSortTile - 1) / kSortTile;
+        L.rows = kSortRows;
+        L.per_block = (uint32_t)((tiles + kSortMost - 1) / kSortMost * kSortTile);
+    }
+    L.blocks = L.per_block ? (uint32_t)((n + L.per_block - 1) / L.per_block) : 0;
     size_t at = 0;
     for (int i = 0; i < 2; ++i) {
-        L.key[i] = at;
-        at = up(at + n * 4);
-        L.pos[i] = at;
-        at = up(at + n * 4);
+        L.items[i] = at;
+        at = up(at + n * sizeof(Item));
     }
     L.counts = at;
     at = up(at + (size_t)kSortMost * kDigits * 4);
-    const uint64_t chunks = (n + 31) / 32;
+    // Chunks of 32 tokens; of 8 where that would leave 152 SMs less than 16 warps each: a warp's rows
+    // are then all under way at once (5001 tokens x 1001 columns: 52 us for TIME).
+    L.tokens = (n + 31) / 32 * ((dim + 127) / 128) < 152 * 16 ? 8 : 32;
+    const uint64_t chunks = (n + L.tokens - 1) / L.tokens;
     L.list = at;  // the count, then the chunks
     at = up(at + (chunks + 1) * 4);
     L.ldp = (dim + 3) & ~3ull;
@@ -569,10 +662,10 @@ BackwardLayout backward_layout(uint64_t n, uint64_t vocab, uint64_t dim) {
     return L;
 }
 
-template <typename T, int kN>
+template <typename T, int kTokens, int kN>
 int launch_sums(SumArgs a, bool wide, int sms, cudaStream_t s) {
     a.tiles = (a.cols + 32 * kN - 1) / (32 * kN);
-    const uint64_t chunks = (a.n + 31) / 32;
+    const uint64_t chunks = (a.n + kTokens - 1) / kTokens;
     a.sum_blocks = (uint32_t)umin64((chunks * a.tiles + 7) / 8, 1u << 24);
     const uint64_t zeros = a.accumulate ? 0
                                         : ((uint64_t)a.vocab + kZeroRows - 1) / kZeroRows *
@@ -581,16 +674,17 @@ int launch_sums(SumArgs a, bool wide, int sms, cudaStream_t s) {
     if (grid.x == 0) return DGC_OK;
     auto pick = [&] {
         if constexpr (kN == 8)  // wide
-            return a.accumulate ? k_embed_sum<T, kN, true, true> : k_embed_sum<T, kN, true, false>;
+            return a.accumulate ? k_embed_sum<T, kTokens, kN, true, true>
+                                : k_embed_sum<T, kTokens, kN, true, false>;
         else
-            return a.accumulate
-                       ? (wide ? k_embed_sum<T, kN, true, true> : k_embed_sum<T, kN, false, true>)
-                       : (wide ? k_embed_sum<T, kN, true, false> : k_embed_sum<T, kN, false, false>);
+            return a.accumulate ? (wide ? k_embed_sum<T, kTokens, kN, true, true>
+                                        : k_embed_sum<T, kTokens, kN, false, true>)
+                                : (wide ? k_embed_sum<T, kTokens, kN, true, false>
+                                        : k_embed_sum<T, kTokens, kN, false, false>);
     };
-    auto kernel = pick();
-    const int rc = launch_rows_kernel(kernel, grid, kThreads, s, a);
-    // only a list of more than 32 tokens can hold a word more than 32 times
-    if (rc || a.n <= 32) return rc;
+    const int rc = launch_rows_kernel(pick(), grid, kThreads, s, a);
+    // only a list of more tokens than a chunk's can hold a word more often
+    if (rc || a.n <= kTokens) return rc;
     auto joiner = a.accumulate ? (wide ? k_embed_join<true, true> : k_embed_join<false, true>)
                                : (wide ? k_embed_join<true, false> : k_embed_join<false, false>);
     const uint64_t blocks = umin64((uint64_t)sms * 4, chunks * ((a.cols + 127) / 128));
@@ -602,10 +696,10 @@ int launch_sort(const SortArgs& a, const BackwardLayout& L, cudaStream_t s) {
         cudaLaunchConfig_t c{};
         c.gridDim = dim3(L.blocks);
         c.blockDim = dim3(kSortThreads);
-        c.dynamicSmemBytes = sizeof(SortTile);
+        c.dynamicSmemBytes = sizeof(ClusterTile);
         c.stream = s;
         if (cudaFuncSetAttribute(k_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 sizeof(SortTile)) != cudaSuccess) {
+                                 sizeof(ClusterTile)) != cudaSuccess) {
             cudaGetLastError();
             return DGC_ECUDA;
         }
@@ -616,7 +710,7 @@ int launch_sort(const SortArgs& a, const BackwardLayout& L, cudaStream_t s) {
         at[1].val.clusterDim.x = L.blocks;
         at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
         c.attrs = at;
-        c.numAttrs = L.blocks > 1 ? 2 : 1;
+        c.numAttrs = 2;
         if (cudaLaunchKernelEx(&c, k_sort, a) != cudaSuccess) {
             cudaGetLastError();
             return DGC_ECUDA;
@@ -624,12 +718,18 @@ int launch_sort(const SortArgs& a, const BackwardLayout& L, cudaStream_t s) {
         dgc_internal_count_launches(1);
         return DGC_OK;
     }
+    const Item* from = nullptr;
+    Item *to = a.from, *other = a.to;
     for (uint32_t pass = 0; pass < a.passes; ++pass) {
-        int rc = launch_rows_kernel(k_sort_count, dim3(L.blocks), kSortThreads, s, a, pass);
+        const uint32_t shift = pass * a.digit_bits;
+        int rc = launch_rows_kernel(k_sort_count, dim3(L.blocks), kSortThreads, s, a, from, shift);
         if (rc) return rc;
         rc = launch_shared_kernel(k_sort_move, dim3(L.blocks), kSortThreads, sizeof(SortTile), s, a,
-                                  pass);
+                                  from, to, shift);
         if (rc) return rc;
+        from = to;
+        to = other;
+        other = const_cast<Item*>(from);
     }
     return DGC_OK;
 }
@@ -728,13 +828,12 @@ extern "C" int dgc_embed_backward(const dgc_tensor* tokens, const dgc_matrix* dy
         a.digit_bits = L.digit_bits;
         a.passes = L.passes;
         a.list_count = sum.list_count;
-        for (int i = 0; i < 2; ++i) {
-            a.key[i] = words(L.key[i]);
-            a.pos[i] = words(L.pos[i]);
-        }
+        a.rows = L.rows;
+        a.from = reinterpret_cast<Item*>(w + L.items[0]);
+        a.to = reinterpret_cast<Item*>(w + L.items[1]);
         if ((rc = launch_sort(a, L, s))) return rc;
-        sum.key = a.key[L.passes & 1];
-        sum.pos = a.pos[L.passes & 1];
+        // one cluster sorts into the first array, the launches take turns
+        sum.items = L.blocks <= kSortCluster || (L.passes & 1) ? a.from : a.to;
     }
     sum.n = n;
     sum.vocab = (uint32_t)mt.rows;
@@ -748,13 +847,15 @@ extern "C" int dgc_embed_backward(const dgc_tensor* tokens, const dgc_matrix* dy
     sum.part = reinterpret_cast<float*>(w + L.part);
     sum.ldp = L.ldp;
     const bool wide = my.on(16) && mt.on(16) && mt.cols % 4 == 0;
+    sum.tokens = L.tokens;
     // eight columns a lane where that leaves the SMs 16 warps each: 16-byte loads of 16-bit entries
-    const bool eight = my.dtype != DGC_F32 && wide && mt.cols % 8 == 0 &&
+    const bool eight = my.dtype != DGC_F32 && wide && mt.cols % 8 == 0 && L.tokens == 32 &&
                        (uint64_t)((n + 31) / 32) * ((mt.cols + 255) / 256) >= (uint64_t)sms * 16;
     return with_type(my.dtype, [&](auto t) {
         using T = decltype(t);
         if constexpr (sizeof(T) == 2)
-            if (eight) return launch_sums<T, 8>(sum, wide, sms, s);
-        return launch_sums<T, 4>(sum, wide, sms, s);
+            if (eight) return launch_sums<T, 32, 8>(sum, wide, sms, s);
+        return L.tokens == 8 ? launch_sums<T, 8, 4>(sum, wide, sms, s)
+                             : launch_sums<T, 32, 4>(sum, wide, sms, s);
     });
 }
