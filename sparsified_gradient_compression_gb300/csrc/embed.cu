@@ -200,11 +200,16 @@ __device__ __forceinline__ uint32_t digit_begin(uint32_t blocks, uint32_t block,
 }
 // The thread's digit in each warp: counts become places, from `at` on. Returns the end.
 __device__ __forceinline__ uint32_t warp_places(uint32_t (*place)[kDigits], uint32_t at) {
-#pragma unroll 4
-    for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t c = place[w][threadIdx.x];
-        place[w][threadIdx.x] = at;
-        at += c;
+#pragma unroll 1
+    for (int w = 0; w < kSortWarps; w += 8) {
+        uint32_t c[8];  // read ahead of the writes, which might be to the same place for all the
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = place[w + i][threadIdx.x];  // compiler knows
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            place[w + i][threadIdx.x] = at;
+            at += c[i];
+        }
     }
     return at;
 }
@@ -584,8 +589,13 @@ __global__ void __launch_bounds__(kThreads) k_embed_join(const __grid_constant__
         float* out = a.dtable + (uint64_t)word * a.ldt;
         Packed<float, 4> old{};
         if (kAdd && warp == 0) old = cols.load(out);
-        const uint32_t end = first_from(a.items, next, a.n - next, (Item)(word + 1) << 32);
-        const uint32_t parts = (end - 1) / a.tokens - chunk + 1, share = (parts + kWarps - 1) / kWarps;
+        uint32_t parts = 1;  // and one for each chunk that begins in the run, 32 looked at at once
+        for (uint32_t more = 32; more == 32; parts += more) {
+            const uint64_t at = (uint64_t)(chunk + parts + lane) * a.tokens;
+            more = trailing_ones(__ballot_sync(
+                kFull, at < a.n && (uint32_t)(a.items[at < a.n ? at : 0] >> 32) == word));
+        }
+        const uint32_t share = (parts + kWarps - 1) / kWarps;
         float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         const uint32_t from = min(parts, warp * share), to = min(parts, from + share);
 #pragma unroll 8
