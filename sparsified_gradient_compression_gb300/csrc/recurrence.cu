@@ -9,11 +9,13 @@
 // of 64 columns by a chunk of rows, each of its 8 warps kS rows, two columns a lane:
 //   1. each warp composes its rows' map; the last warp composes the warps' and publishes the
 //      chunk's (A, B);
-//   2. 32 chunks are a group: the warps collect the maps of the chunks ahead of this one in its
-//      group, four each, and the state that enters the group, which the last chunk of the group
-//      ahead publishes. (Which maps are joined, and how, is fixed, so the rounding is too: results
-//      are the same bits on every run. A chain from chunk to chunk would cost its latency 32 times.)
+//   2. 16 or 32 chunks are a group: the warps collect the maps of the chunks ahead of this one in
+//      its group, two or four each, and the state that enters the group, which the last chunk of the
+//      group ahead publishes. (Which maps are joined, and how, is fixed, so the rounding is too:
+//      results are the same bits on every run. A chain from chunk to chunk would cost its latency for
+//      each.)
 //   3. each warp walks its rows again from the state it enters with, and writes.
+// Up to 128 rows are one chunk's: k_scan_few has no more than its block's exchange.
 // The data is read once. Blocks stay: the next tile is on its way to shared memory as soon as the
 // rows of this one are in registers, while the maps are exchanged and the results written. (One block
 // a tile, with its loads at its beginning, took 279 us for 32768 x 2048.) Tiles go by a ticket, in
@@ -40,9 +42,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCols = 64;        // of a tile
-constexpr uint32_t kGroup = 32;  // chunks
-constexpr uint32_t kEach = kGroup / kWarps;  // of them for a warp to collect
+constexpr uint32_t kMostEach = 4;  // chunks whose maps a warp collects
 constexpr uint32_t kPiece = 64;  // rows between two saved states
+constexpr uint32_t kFew = 128;   // rows of a call that one block a column tile does
 constexpr float kReset = -1.0f;  // no run of steps has a negative A
 constexpr uint32_t kNotYet = 0xFFFFFFFFu;  // a NaN that no arithmetic makes
 
@@ -60,8 +62,11 @@ struct ScanArgs {
     uint32_t *ticket, *abort;
     uint4* maps;
     uint2* states;
+    uint32_t each, log_group;  // a group: each * kWarps chunks
     uint32_t spin_limit, lost;  // lost: self-test, a chunk that publishes nothing
     int32_t* status;
+    __device__ uint32_t group_of(uint32_t order) const { return order >> log_group; }
+    __device__ uint32_t place_of(uint32_t order) const { return order & ((1u << log_group) - 1); }
 };
 
 // Two columns of a row: kPair whole, where the address allows it and both are there.
@@ -204,7 +209,7 @@ __device__ __forceinline__ Tile first_tile(const ScanArgs& a, uint32_t* slot) {
 // second one and ahead of the next tile's first.
 struct Board {
     float4 map[kWarps][32];    // the warps' maps, in the scan's direction
-    float4 ahead[kWarps][32];  // the chunks' ahead of this one, kEach to an entry
+    float4 ahead[kWarps][32];  // the chunks' ahead of this one, each to an entry
     float2 state[32];          // that enters the group
     uint32_t next;             // ticket
     uint32_t fresh;            // a sequence begins with the chunk: nothing enters
@@ -272,7 +277,7 @@ __device__ __forceinline__ Map compose(const ScanArgs& a, const Board& b, uint32
     return before;
 }
 
-// Step 2: a warp collects the maps of kEach chunks, the last one also the state that enters the group
+// Step 2: a warp collects the maps of a.each chunks, the last one also the state that enters the group
 // (it has the fewest chunks to wait for). The first look is taken ahead of the next tile's copies, or
 // it would queue behind them (2500 clocks for 900).
 struct LookBack {
@@ -280,24 +285,24 @@ struct LookBack {
     const uint2* state;
     uint64_t step;
     uint32_t count;
-    uint4 v[kEach];
+    uint4 v[kMostEach];
     uint2 h;
     __device__ LookBack(const ScanArgs& a, uint32_t order, uint32_t tile, int w, bool fresh) {
-        const uint32_t lane = threadIdx.x & 31, group = order / kGroup, k = order % kGroup;
-        const uint32_t from = kEach * (uint32_t)w;
+        const uint32_t lane = threadIdx.x & 31, group = a.group_of(order), k = a.place_of(order);
+        const uint32_t from = a.each * (uint32_t)w;
         count = 0;
         state = nullptr;
         h = make_uint2(0, 0);
         if (!a.ticket || fresh) return;
-        if (k > from) count = min(kEach, k - from);
+        if (k > from) count = min(a.each, k - from);
         step = (uint64_t)a.tiles * 32;
-        maps = a.maps + ((uint64_t)group * kGroup + from) * step + tile * 32 + lane;
+        maps = a.maps + ((uint64_t)order - k + from) * step + tile * 32 + lane;
         if (w == kWarps - 1 && group > 0) state = a.states + group * step + tile * 32 + lane;
         look_again();
     }
     __device__ void look_again() {
 #pragma unroll
-        for (uint32_t i = 0; i < kEach; ++i)
+        for (uint32_t i = 0; i < kMostEach; ++i)
             if (i < count) v[i] = look(maps + i * step);
         if (state) h = look(state);
     }
@@ -307,14 +312,14 @@ struct LookBack {
         for (uint32_t polls = 0;; ++polls) {
             bool ready = !state || there(h);
 #pragma unroll
-            for (uint32_t i = 0; i < kEach; ++i)
+            for (uint32_t i = 0; i < kMostEach; ++i)
                 if (i < count) ready = ready && there(v[i]);
             if (__all_sync(kFull, ready) || !wait_on(a, polls)) break;
             look_again();
         }
         Map all = identity();
 #pragma unroll
-        for (uint32_t i = 0; i < kEach; ++i)
+        for (uint32_t i = 0; i < kMostEach; ++i)
             if (i < count)
                 all = all.then({{__uint_as_float(v[i].x), __uint_as_float(v[i].y)},
                                 {__uint_as_float(v[i].z), __uint_as_float(v[i].w)}});
@@ -328,16 +333,16 @@ struct LookBack {
 __device__ __forceinline__ float2 enter(const ScanArgs& a, const Board& b, uint32_t order,
                                         uint32_t tile, int w, const Map& before, const Map& m,
                                         bool fresh) {
-    const uint32_t lane = threadIdx.x & 31, group = order / kGroup, k = order % kGroup;
+    const uint32_t lane = threadIdx.x & 31, group = a.group_of(order), k = a.place_of(order);
     float2 h = {0.0f, 0.0f};
     if (!a.ticket) return h;
     if (!fresh) {
         h = b.state[lane];
 #pragma unroll
         for (uint32_t i = 0; i < kWarps; ++i)
-            if (kEach * i < k) h = map_of(b.ahead[i][lane])(h);
+            if (a.each * i < k) h = map_of(b.ahead[i][lane])(h);
     }
-    if (w == kWarps - 1 && k == kGroup - 1 && order + 1 < a.chunks && order != a.lost)
+    if (w == kWarps - 1 && k == a.each * kWarps - 1 && order + 1 < a.chunks && order != a.lost)
         publish(&a.states[((uint64_t)(group + 1) * a.tiles + tile) * 32 + lane], m(before(h)));
     return h;
 }
@@ -531,6 +536,69 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan(const __grid_constan
     copy_wait<0>();
 }
 
+// Up to kWarps * kS rows: a block a column tile. For a step of a model that answers, a start and a
+// round trip to memory.
+template <typename T, bool kPair, int kS>
+__global__ void __launch_bounds__(kThreads) k_scan_few(const __grid_constant__ ScanArgs a) {
+    __shared__ float4 maps[kWarps][32];
+    __shared__ int32_t starts_of[kWarps][kS], ends_of[kWarps][kS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int32_t *starts = starts_of[warp], *ends = ends_of[warp];
+    grid_dep_wait();
+    grid_dep_launch();
+    const Spot at(a, 0, blockIdx.x, kWarps * kS, kS);
+    const T* gate = static_cast<const T*>(a.gate) + (uint64_t)at.first * a.ldg + at.lane_col;
+    const T* x = static_cast<const T*>(a.x) + (uint64_t)at.first * a.ldx + at.lane_col;
+    Packed<T, 2> pg[kS], px[kS];
+#pragma unroll
+    for (int s = 0; s < kS; ++s) {
+        pg[s] = load_piece<kPair, T, 2>(gate + s * a.ldg, s < at.left ? at.n : 0);
+        px[s] = load_piece<kPair, T, 2>(x + s * a.ldx, s < at.left ? at.n : 0);
+    }
+    const int64_t valid0 = a.offsets[0], valid1 = min((int64_t)a.rows, a.offsets[a.nseq]);
+    const int64_t mine = lane <= a.nseq ? a.offsets[lane] : INT64_MAX;
+    const Marks<kS> marks(a, at.first, mine, starts, ends);
+    float2 given[kS];
+#pragma unroll
+    for (int s = 0; s < kS; ++s) {
+        const bool here = a.h0 && (marks.start >> s & 1);
+        given[s] = load_state(a.h0, a.ldh0, here ? starts[s] : 0, at.lane_col, here ? at.n : 0);
+    }
+    empty_sequences(a, blockIdx.x, a.h0, a.ldh0, a.h_last, a.ldh_last);
+    float2 A[kS], B[kS];
+    Map m = identity();
+#pragma unroll
+    for (int s = 0; s < kS; ++s) {
+        float2 keep;
+        sigmoids(pair_of<T, 2>(pg[s], 0), A[s], keep);
+        B[s] = mul2(keep, pair_of<T, 2>(px[s], 0));
+        if (marks.start >> s & 1) {
+            B[s] = fma2(A[s], given[s], B[s]);
+            m = {both(kReset), B[s]};
+        } else {
+            m = m.then({A[s], B[s]});
+        }
+    }
+    maps[warp][lane] = m.packed();
+    const bool resets = __syncthreads_or(marks.start != 0);
+    float2 h = both(0.0f);
+    for (int w = 0; w < warp; ++w) {
+        const Map q = map_of(maps[w][lane]);
+        h = resets ? q(h) : fma2(q.A, h, q.B);
+    }
+    if (a.saved && at.first % kPiece == 0 && at.left)
+        store_state(a.saved, a.lds, at.first / kPiece, at.lane_col, at.n, h);
+#pragma unroll
+    for (int s = 0; s < kS; ++s) {
+        const int64_t row = at.first + s;
+        h = marks.start >> s & 1 ? B[s] : fma2(A[s], h, B[s]);
+        if (row >= valid0 && row < valid1)
+            store_two<T, kPair>(a.y, a.ldy, row, at.lane_col, at.n, h);
+        if (a.h_last && (marks.end >> s & 1) && s < at.left)
+            store_state(a.h_last, a.ldh_last, ends[s], at.lane_col, at.n, h);
+    }
+}
+
 // -------------------------------------------------------------------------------- backward
 // Bound by HBM: x, gate and dy read once, dx and dgate written once, the states of every 64th row.
 template <typename T, int kUnit, int kS, int kBlocks>
@@ -681,13 +749,16 @@ struct Form {
 
 struct ScanLayout {
     size_t maps, states, total;
-    uint32_t chunks, groups, tiles;
+    uint32_t chunks, groups, tiles, each;
 };
 ScanLayout scan_layout(uint64_t rows, uint64_t cols, uint32_t chunk_rows) {
     ScanLayout L{};
     L.chunks = (uint32_t)std::max<uint64_t>(1, (rows + chunk_rows - 1) / chunk_rows);
-    L.groups = (L.chunks + kGroup - 1) / kGroup;
     L.tiles = (uint32_t)((cols + kCols - 1) / kCols);
+    // 16 chunks a group (32768 x 2048: 106 us for 112); 32 where a tile of columns has most of the blocks to itself, whose chain of
+    // groups counts more than the maps that a block collects
+    L.each = L.tiles >= 8 ? 2 : kMostEach;
+    L.groups = (L.chunks + L.each * kWarps - 1) / (L.each * kWarps);
     if (L.chunks == 1) return L;
     L.maps = 256;
     L.states = L.maps + (size_t)L.chunks * L.tiles * 32 * sizeof(uint4);
@@ -718,6 +789,9 @@ int launch_scan(void (*kernel)(ScanArgs), ScanArgs a, void* ws, int sms, cudaStr
     a.tiles = L.tiles;
     a.tiles_inverse = (uint32_t)(0xFFFFFFFFull / L.tiles);
     a.chunks = L.chunks;
+    a.each = L.each;
+    a.log_group = L.each == 2 ? 4 : 5;
+    static_assert(kWarps == 8 && kMostEach == 4, "groups of 16 or 32 chunks");
     if (!a.spin_limit) {
         a.spin_limit = kDefaultSpinLimit;
         a.lost = ~0u;
@@ -793,6 +867,13 @@ int recurrence(const dgc_matrix* x, const dgc_matrix* gate, const int64_t* offse
     return with_type(mx.dtype, [&](auto t) {
         using T = decltype(t);
         constexpr int kS = Form<T>::kS, kBlocks = Form<T>::kBlocks, kTwo = 2 * sizeof(T);
+        if (mx.rows <= kFew) {
+            auto few = a.rows <= kFew / 2
+                           ? (pair ? k_scan_few<T, true, 8> : k_scan_few<T, false, 8>)
+                           : (pair ? k_scan_few<T, true, 16> : k_scan_few<T, false, 16>);
+            return launch_rows_kernel(few, dim3((unsigned)((mx.cols + kCols - 1) / kCols)),
+                                      kThreads, s, a);
+        }
         if (wide)
             return launch_scan<T, 16, kS, 2, kBlocks>(k_scan<T, 16, kS, kBlocks>, a, ws, sms, s);
         if (pair)
