@@ -484,8 +484,9 @@ int dgc_embed_backward(const dgc_tensor* tokens, const dgc_matrix* dy, float sca
  *   gamma, beta  D binary32; beta NULL: none
  *   eps          above 0, finite
  *   mean, rstd   device, M binary32 each, for the backward pass; both or neither NULL
- * The variance is taken around the mean, and the mean's rounding is taken out of it and of y. y may
- * be x. */
+ * The variance is taken around the mean, and the mean's rounding is taken out of it and of y (the sum
+ * of the squares has to stay in binary32's range). A row with an entry that is not finite is NaN. y
+ * may be x. */
 int dgc_layer_norm(const dgc_matrix* x, const dgc_tensor* gamma, const dgc_tensor* beta, float eps,
                    const dgc_matrix* y, float* mean, float* rstd, dgc_stream_t stream);
 

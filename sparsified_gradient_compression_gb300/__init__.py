@@ -712,7 +712,7 @@ def _int64():
 
 
 def _row_count(m) -> int:
-    return m.rows if isinstance(m, dgc_matrix) else m.shape[0]
+    return m.rows if isinstance(m, dgc_matrix) else m.shape[0] if m.dim() else 0
 
 
 def _typed(t, dtype, n, what: str) -> int | None:

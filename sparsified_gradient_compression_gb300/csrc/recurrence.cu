@@ -42,7 +42,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCols = 64;        // of a tile
-constexpr uint32_t kMostEach = 4;  // chunks whose maps a warp collects
 constexpr uint32_t kPiece = 64;  // rows between two saved states
 constexpr uint32_t kFew = 128;   // rows of a call that one block a column tile does
 constexpr float kReset = -1.0f;  // no run of steps has a negative A
@@ -62,11 +61,8 @@ struct ScanArgs {
     uint32_t *ticket, *abort;
     uint4* maps;
     uint2* states;
-    uint32_t each, log_group;  // a group: each * kWarps chunks
     uint32_t spin_limit, lost;  // lost: self-test, a chunk that publishes nothing
     int32_t* status;
-    __device__ uint32_t group_of(uint32_t order) const { return order >> log_group; }
-    __device__ uint32_t place_of(uint32_t order) const { return order & ((1u << log_group) - 1); }
 };
 
 // Two columns of a row: kPair whole, where the address allows it and both are there.
@@ -277,24 +273,25 @@ __device__ __forceinline__ Map compose(const ScanArgs& a, const Board& b, uint32
     return before;
 }
 
-// Step 2: a warp collects the maps of a.each chunks, the last one also the state that enters the group
+// Step 2: a warp collects the maps of kEach chunks, the last one also the state that enters the group
 // (it has the fewest chunks to wait for). The first look is taken ahead of the next tile's copies, or
 // it would queue behind them (2500 clocks for 900).
+template <uint32_t kEach>
 struct LookBack {
     const uint4* maps;
     const uint2* state;
     uint64_t step;
     uint32_t count;
-    uint4 v[kMostEach];
+    uint4 v[kEach];
     uint2 h;
     __device__ LookBack(const ScanArgs& a, uint32_t order, uint32_t tile, int w, bool fresh) {
-        const uint32_t lane = threadIdx.x & 31, group = a.group_of(order), k = a.place_of(order);
-        const uint32_t from = a.each * (uint32_t)w;
+        const uint32_t lane = threadIdx.x & 31, group = order / (kEach * kWarps), k = order % (kEach * kWarps);
+        const uint32_t from = kEach * (uint32_t)w;
         count = 0;
         state = nullptr;
         h = make_uint2(0, 0);
         if (!a.ticket || fresh) return;
-        if (k > from) count = min(a.each, k - from);
+        if (k > from) count = min(kEach, k - from);
         step = (uint64_t)a.tiles * 32;
         maps = a.maps + ((uint64_t)order - k + from) * step + tile * 32 + lane;
         if (w == kWarps - 1 && group > 0) state = a.states + group * step + tile * 32 + lane;
@@ -302,7 +299,7 @@ struct LookBack {
     }
     __device__ void look_again() {
 #pragma unroll
-        for (uint32_t i = 0; i < kMostEach; ++i)
+        for (uint32_t i = 0; i < kEach; ++i)
             if (i < count) v[i] = look(maps + i * step);
         if (state) h = look(state);
     }
@@ -312,14 +309,14 @@ struct LookBack {
         for (uint32_t polls = 0;; ++polls) {
             bool ready = !state || there(h);
 #pragma unroll
-            for (uint32_t i = 0; i < kMostEach; ++i)
+            for (uint32_t i = 0; i < kEach; ++i)
                 if (i < count) ready = ready && there(v[i]);
             if (__all_sync(kFull, ready) || !wait_on(a, polls)) break;
             look_again();
         }
         Map all = identity();
 #pragma unroll
-        for (uint32_t i = 0; i < kMostEach; ++i)
+        for (uint32_t i = 0; i < kEach; ++i)
             if (i < count)
                 all = all.then({{__uint_as_float(v[i].x), __uint_as_float(v[i].y)},
                                 {__uint_as_float(v[i].z), __uint_as_float(v[i].w)}});
@@ -330,19 +327,20 @@ struct LookBack {
 };
 
 // After the barrier: the state that enters the chunk. The last warp passes a group's on.
+template <uint32_t kEach>
 __device__ __forceinline__ float2 enter(const ScanArgs& a, const Board& b, uint32_t order,
                                         uint32_t tile, int w, const Map& before, const Map& m,
                                         bool fresh) {
-    const uint32_t lane = threadIdx.x & 31, group = a.group_of(order), k = a.place_of(order);
+    const uint32_t lane = threadIdx.x & 31, group = order / (kEach * kWarps), k = order % (kEach * kWarps);
     float2 h = {0.0f, 0.0f};
     if (!a.ticket) return h;
     if (!fresh) {
         h = b.state[lane];
 #pragma unroll
         for (uint32_t i = 0; i < kWarps; ++i)
-            if (a.each * i < k) h = map_of(b.ahead[i][lane])(h);
+            if (kEach * i < k) h = map_of(b.ahead[i][lane])(h);
     }
-    if (w == kWarps - 1 && k == a.each * kWarps - 1 && order + 1 < a.chunks && order != a.lost)
+    if (w == kWarps - 1 && k == kEach * kWarps - 1 && order + 1 < a.chunks && order != a.lost)
         publish(&a.states[((uint64_t)(group + 1) * a.tiles + tile) * 32 + lane], m(before(h)));
     return h;
 }
@@ -432,7 +430,7 @@ struct Spot {
 // --------------------------------------------------------------------------------- forward
 // Bound by HBM: x and gate read once, y written once. Rows with no border among them and whole
 // columns take a way without tests.
-template <typename T, int kUnit, int kS, int kBlocks>
+template <typename T, int kUnit, int kS, int kBlocks, uint32_t kEach>
 __global__ void __launch_bounds__(kThreads, kBlocks) k_scan(const __grid_constant__ ScanArgs a) {
     constexpr int kRows = kWarps * kS;
     constexpr bool kPair = kUnit != 0;
@@ -503,12 +501,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan(const __grid_constan
         const bool resets = __syncthreads_or(marks.start != 0);
         const Map before = compose(a, board, chunk, tile, warp, m, resets);
         const bool fresh = board.fresh;
-        LookBack back(a, chunk, tile, warp, fresh);
+        LookBack<kEach> back(a, chunk, tile, warp, fresh);
         t = tile_of(a, board.next);
         fetch();
         back.finish(a, board, warp);
         __syncthreads();
-        float2 h = before(enter(a, board, chunk, tile, warp, before, m, fresh));
+        float2 h = before(enter<kEach>(a, board, chunk, tile, warp, before, m, fresh));
         if (a.saved && at.first % kPiece == 0 && at.left)
             store_state(a.saved, a.lds, at.first / kPiece, at.lane_col, at.n, h);
         if (kPair && !(marks.start | marks.end) && at.first >= valid0 && at.first + kS <= valid1 &&
@@ -601,7 +599,7 @@ __global__ void __launch_bounds__(kThreads) k_scan_few(const __grid_constant__ S
 
 // -------------------------------------------------------------------------------- backward
 // Bound by HBM: x, gate and dy read once, dx and dgate written once, the states of every 64th row.
-template <typename T, int kUnit, int kS, int kBlocks>
+template <typename T, int kUnit, int kS, int kBlocks, uint32_t kEach>
 __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_back(const __grid_constant__ ScanArgs a) {
     constexpr int kRows = kWarps * kS;
     constexpr bool kPair = kUnit != 0;
@@ -698,14 +696,14 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_back(const __grid_co
             q[s] = mul2(mul2(A[s], keep[s]), add2(h, {-x.x, -x.y}));
             h = fma2(A[s], h, b);
         }
-        LookBack back(a, order, tile, place, fresh);
+        LookBack<kEach> back(a, order, tile, place, fresh);
         __syncwarp();
         t = tile_of(a, board.next);
         fetch();
         back.finish(a, board, place);
         __syncthreads();
         // u of the row behind
-        float2 v = behind(enter(a, board, order, tile, place, behind, u, fresh));
+        float2 v = behind(enter<kEach>(a, board, order, tile, place, behind, u, fresh));
         if (kPair && !(marks.start | marks.end) && at.first >= valid0 && at.first + kS <= valid1 &&
             at.col + kCols <= a.cols) {
             T* dx = static_cast<T*>(a.dx) + (at.first + kS - 1) * a.lddx + at.lane_col;
@@ -747,27 +745,29 @@ struct Form {
     static constexpr int kBackS = kPiece / kWarps, kBackBlocks = 2;
 };
 
+// Columns from which on 16 chunks are a group (32768 x 2048: 107 us for 112), with two maps for a warp
+// to collect. Below, where a tile of columns has most of the blocks to itself, 32: there the chain of
+// groups counts more (16384 x 64: 10 us for 12).
+constexpr uint64_t kWideCols = 8 * kCols;
+
 struct ScanLayout {
     size_t maps, states, total;
-    uint32_t chunks, groups, tiles, each;
+    uint32_t chunks, groups, tiles;
 };
-ScanLayout scan_layout(uint64_t rows, uint64_t cols, uint32_t chunk_rows) {
+ScanLayout scan_layout(uint64_t rows, uint64_t cols, uint32_t chunk_rows, uint32_t each) {
     ScanLayout L{};
     L.chunks = (uint32_t)std::max<uint64_t>(1, (rows + chunk_rows - 1) / chunk_rows);
     L.tiles = (uint32_t)((cols + kCols - 1) / kCols);
-    // 16 chunks a group (32768 x 2048: 106 us for 112); 32 where a tile of columns has most of the blocks to itself, whose chain of
-    // groups counts more than the maps that a block collects
-    L.each = L.tiles >= 8 ? 2 : kMostEach;
-    L.groups = (L.chunks + L.each * kWarps - 1) / (L.each * kWarps);
+    L.groups = (L.chunks + each * kWarps - 1) / (each * kWarps);
     if (L.chunks == 1) return L;
     L.maps = 256;
     L.states = L.maps + (size_t)L.chunks * L.tiles * 32 * sizeof(uint4);
     L.total = (L.states + (size_t)L.groups * L.tiles * 32 * sizeof(uint2) + 255) & ~(size_t)255;
     return L;
 }
-// For the shortest chunks that the calls use.
+// For the shortest chunks and groups that the calls use.
 size_t scan_workspace(uint64_t rows, uint64_t cols) {
-    return scan_layout(rows, cols, kPiece).total;
+    return scan_layout(rows, cols, kPiece, 2).total;
 }
 
 // A state of binary32, one row a sequence; may be missing.
@@ -782,16 +782,13 @@ int check_state(const dgc_matrix* m, uint64_t nseq, uint64_t cols, const float**
     return DGC_OK;
 }
 
-template <typename T, int kUnit, int kS, int kOperands, int kBlocks>
+template <typename T, int kUnit, int kS, int kOperands, int kBlocks, uint32_t kEach>
 int launch_scan(void (*kernel)(ScanArgs), ScanArgs a, void* ws, int sms, cudaStream_t s) {
-    const ScanLayout L = scan_layout(a.rows, a.cols, kWarps * kS);
+    const ScanLayout L = scan_layout(a.rows, a.cols, kWarps * kS, kEach);
     if ((uint64_t)L.tiles * L.chunks > 0x7FFFFFFFull) return DGC_EUNSUPPORTED;
     a.tiles = L.tiles;
     a.tiles_inverse = (uint32_t)(0xFFFFFFFFull / L.tiles);
     a.chunks = L.chunks;
-    a.each = L.each;
-    a.log_group = L.each == 2 ? 4 : 5;
-    static_assert(kWarps == 8 && kMostEach == 4, "groups of 16 or 32 chunks");
     if (!a.spin_limit) {
         a.spin_limit = kDefaultSpinLimit;
         a.lost = ~0u;
@@ -874,12 +871,17 @@ int recurrence(const dgc_matrix* x, const dgc_matrix* gate, const int64_t* offse
             return launch_rows_kernel(few, dim3((unsigned)((mx.cols + kCols - 1) / kCols)),
                                       kThreads, s, a);
         }
+        // (rows off 16-byte boundaries: groups of 32 chunks, for one kernel less)
+        if (wide && mx.cols >= kWideCols)
+            return launch_scan<T, 16, kS, 2, kBlocks, 2>(k_scan<T, 16, kS, kBlocks, 2>, a, ws,
+                                                        sms, s);
         if (wide)
-            return launch_scan<T, 16, kS, 2, kBlocks>(k_scan<T, 16, kS, kBlocks>, a, ws, sms, s);
+            return launch_scan<T, 16, kS, 2, kBlocks, 4>(k_scan<T, 16, kS, kBlocks, 4>, a, ws,
+                                                        sms, s);
         if (pair)
-            return launch_scan<T, kTwo, kS, 2, kBlocks>(k_scan<T, kTwo, kS, kBlocks>, a, ws, sms,
-                                                        s);
-        return launch_scan<T, 0, kS, 2, kBlocks>(k_scan<T, 0, kS, kBlocks>, a, ws, sms, s);
+            return launch_scan<T, kTwo, kS, 2, kBlocks, 4>(k_scan<T, kTwo, kS, kBlocks, 4>, a, ws,
+                                                          sms, s);
+        return launch_scan<T, 0, kS, 2, kBlocks, 4>(k_scan<T, 0, kS, kBlocks, 4>, a, ws, sms, s);
     });
 }
 
@@ -971,12 +973,16 @@ extern "C" int dgc_recurrence_backward(const dgc_matrix* dy, const dgc_matrix* x
     return with_type(mx.dtype, [&](auto t) {
         using T = decltype(t);
         constexpr int kS = Form<T>::kBackS, kBlocks = Form<T>::kBackBlocks, kTwo = 2 * sizeof(T);
-        if (wide)
-            return launch_scan<T, 16, kS, 3, kBlocks>(k_scan_back<T, 16, kS, kBlocks>, a, ws, sms,
-                                                      s);
-        if (pair)
-            return launch_scan<T, kTwo, kS, 3, kBlocks>(k_scan_back<T, kTwo, kS, kBlocks>, a, ws,
+        // (rows off 16-byte boundaries: groups of 32 chunks, for one kernel less)
+        if (wide && mx.cols >= kWideCols)
+            return launch_scan<T, 16, kS, 3, kBlocks, 2>(k_scan_back<T, 16, kS, kBlocks, 2>, a, ws,
                                                         sms, s);
-        return launch_scan<T, 0, kS, 3, kBlocks>(k_scan_back<T, 0, kS, kBlocks>, a, ws, sms, s);
+        if (wide)
+            return launch_scan<T, 16, kS, 3, kBlocks, 4>(k_scan_back<T, 16, kS, kBlocks, 4>, a, ws,
+                                                        sms, s);
+        if (pair)
+            return launch_scan<T, kTwo, kS, 3, kBlocks, 4>(k_scan_back<T, kTwo, kS, kBlocks, 4>, a, ws,
+                                                          sms, s);
+        return launch_scan<T, 0, kS, 3, kBlocks, 4>(k_scan_back<T, 0, kS, kBlocks, 4>, a, ws, sms, s);
     });
 }
