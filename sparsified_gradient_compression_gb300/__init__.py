@@ -699,16 +699,15 @@ def _size(ws, ws_bytes) -> int:
     return 0 if ws is None else ws.nbytes
 
 
-def _float32():
+_float32 = _int64 = None  # torch's types, from the first call that needs one
+_words = ()               # ... of 64 bits
+
+
+def _load_types():
+    global _float32, _int64, _words
     import torch
 
-    return torch.float32
-
-
-def _int64():
-    import torch
-
-    return torch.int64
+    _float32, _int64, _words = torch.float32, torch.int64, (torch.int64, torch.uint64)
 
 
 def _row_count(m) -> int:
@@ -719,7 +718,7 @@ def _typed(t, dtype, n, what: str) -> int | None:
     """The address of a tensor that must have this type and at least n entries in one run."""
     if t is None or isinstance(t, int):
         return t
-    if t.dtype != dtype or not t.is_contiguous() or (n is not None and t.numel() < n):
+    if t.dtype is not dtype or not t.is_contiguous() or t.numel() < n:
         raise DGCError(EINVAL, f"{what}: a contiguous {dtype} tensor of {n} entries is wanted")
     return _gpu(t, what)
 
@@ -755,10 +754,12 @@ def dgc_embed_backward(tokens, dy, scale: float, padding: int | None, dtable, ac
 
 def dgc_layer_norm(x, gamma, beta, eps: float, y, mean, rstd, stream=None) -> int:
     """y = (x - mean) * rstd * gamma + beta (or None); mean, rstd: float32, one a row, or None."""
-    f32, rows = _float32(), _row_count(x)
+    if _float32 is None:
+        _load_types()
+    rows = _row_count(x)
     return _check(lib().dgc_layer_norm(_mat(x), _vec(gamma), _vec(beta), float(eps), _mat(y),
-                                       _typed(mean, f32, rows, "mean"),
-                                       _typed(rstd, f32, rows, "rstd"), _stream(stream)),
+                                       _typed(mean, _float32, rows, "mean"),
+                                       _typed(rstd, _float32, rows, "rstd"), _stream(stream)),
                   "dgc_layer_norm")
 
 
@@ -772,10 +773,12 @@ def dgc_layer_norm_backward_workspace(rows: int, cols: int) -> int:
 def dgc_layer_norm_backward(dy, x, gamma, mean, rstd, residual, dx, dgamma, dbeta,
                             accumulate: bool, ws, ws_bytes: int | None = None, stream=None) -> int:
     """dx (plus residual, or None), and dgamma and dbeta (float32, or None), written or added."""
-    f32, rows = _float32(), _row_count(dy)
+    if _float32 is None:
+        _load_types()
+    rows = _row_count(dy)
     return _check(lib().dgc_layer_norm_backward(
-        _mat(dy), _mat(x), _vec(gamma), _typed(mean, f32, rows, "mean"),
-        _typed(rstd, f32, rows, "rstd"), _mat(residual), _mat(dx), _vec(dgamma), _vec(dbeta),
+        _mat(dy), _mat(x), _vec(gamma), _typed(mean, _float32, rows, "mean"),
+        _typed(rstd, _float32, rows, "rstd"), _mat(residual), _mat(dx), _vec(dgamma), _vec(dbeta),
         int(bool(accumulate)), _gpu(ws, "ws"), _size(ws, ws_bytes), _stream(stream)),
         "dgc_layer_norm_backward")
 
@@ -784,7 +787,9 @@ def dgc_dropout(x, residual, p: float, seed: int, step, out, stream=None) -> int
     """out = residual (or None) + what is kept of x, scaled. step: a device int64 (or uint64) word
     that numbers the draws, or None. The backward pass is the same call on the gradient."""
     if step is not None and not isinstance(step, int):
-        if step.element_size() != 8 or step.is_floating_point() or step.numel() < 1:
+        if _float32 is None:
+            _load_types()
+        if step.dtype not in _words or step.numel() < 1:
             raise DGCError(EINVAL, "dgc_dropout: step is one 64-bit word")
         step = _gpu(step, "step")
     return _check(lib().dgc_dropout(_mat(x), _mat(residual), float(p), int(seed) & (2**64 - 1),
@@ -811,9 +816,11 @@ def dgc_recurrence(x, gate, offsets, h0, y, h_last, saved, status, ws, nseq: int
     """y_t = h_t = a h_{t-1} + (1 - a) x_t, a = sigmoid(gate), over the sequences whose rows begin at
     offsets (int64 CUDA tensor, one more than sequences). h0, h_last (float32, a row a sequence), saved
     (float32, for the backward pass): or None. ws may be None where the workspace query says 0."""
+    if _int64 is None:
+        _load_types()
     nseq = offsets.numel() - 1 if nseq is None else nseq
     return _check(lib().dgc_recurrence(_mat(x), _mat(gate),
-                                       _typed(offsets, _int64(), nseq + 1, "offsets"), int(nseq),
+                                       _typed(offsets, _int64, nseq + 1, "offsets"), int(nseq),
                                        _mat(h0), _mat(y), _mat(h_last), _mat(saved),
                                        _gpu(status, "status"), _gpu(ws, "ws"),
                                        _size(ws, ws_bytes), _stream(stream)), "dgc_recurrence")
@@ -824,9 +831,11 @@ def dgc_recurrence_backward(dy, x, gate, offsets, h0, saved, d_last, dx, dgate, 
                             stream=None) -> int:
     """dx, dgate and d_h0 (or None) from dy and d_last (or None); x, gate, offsets, h0, saved: of the
     forward pass."""
+    if _int64 is None:
+        _load_types()
     nseq = offsets.numel() - 1 if nseq is None else nseq
     return _check(lib().dgc_recurrence_backward(
-        _mat(dy), _mat(x), _mat(gate), _typed(offsets, _int64(), nseq + 1, "offsets"), int(nseq),
+        _mat(dy), _mat(x), _mat(gate), _typed(offsets, _int64, nseq + 1, "offsets"), int(nseq),
         _mat(h0), _mat(saved), _mat(d_last), _mat(dx), _mat(dgate), _mat(d_h0),
         _gpu(status, "status"), _gpu(ws, "ws"), _size(ws, ws_bytes), _stream(stream)),
         "dgc_recurrence_backward")
@@ -877,7 +886,9 @@ def dgc_selftest_ffn_timeout(hidden, w_down, y, status, wait_ms: int, stream=Non
 
 def dgc_selftest_recurrence_timeout(x, gate, offsets, y, status, ws, spin_limit: int,
                                     stream=None) -> int:
+    if _int64 is None:
+        _load_types()
     return _check(lib().dgc_selftest_recurrence_timeout(
-        _mat(x), _mat(gate), _typed(offsets, _int64(), 1, "offsets"), offsets.numel() - 1, _mat(y),
+        _mat(x), _mat(gate), _typed(offsets, _int64, 1, "offsets"), offsets.numel() - 1, _mat(y),
         _gpu(status, "status"), _gpu(ws, "ws"), _size(ws, None), int(spin_limit),
         _stream(stream)), "dgc_selftest_recurrence_timeout")
