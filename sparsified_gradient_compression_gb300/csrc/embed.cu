@@ -45,7 +45,10 @@ struct EmbedArgs {
 };
 
 // Bound by HBM: the result is written once, each row of the table that is met is read from HBM
-// once as far as L2 holds it.
+// once as far as L2 holds it. 16384 x 4096 bf16 from a table of 50000 rows: 34 us, 5.5 TB/s.
+// What is lost is the start and two latencies in a row (the word, then its row). One short-lived
+// block a tile: blocks that stay and look up the next tile's words ahead took 39 us at 6 an SM, 51
+// at 4.
 template <typename S, typename D, bool kWide>
 __global__ void __launch_bounds__(kThreads) k_embed(const __grid_constant__ EmbedArgs a) {
     constexpr int kN = 16 / sizeof(D);
@@ -225,7 +228,9 @@ __device__ __forceinline__ uint32_t in_block(const void* p, uint32_t rank) {
 }
 
 // All passes by one cluster of up to 8 blocks, a tile each: the items stay in the blocks' shared
-// memory and go from pass to pass to where they belong. (Through L2, 16384 tokens took 16 us.)
+// memory and go from pass to pass to where they belong. Bound by latency: two passes of a few
+// dependent steps each. 16384 tokens with cold caches 16 us, where two kernels a pass, with the
+// items in L2, took 23.
 struct ClusterTile {
     Item item[2][kSortTile];
     uint16_t rank[kSortTile];
@@ -393,7 +398,8 @@ struct Chunk {
             e0 = all & kMask;
             e1 = all >> kTokens & kMask;
             e2 = all >> 2 * kTokens & kMask;
-            valid = __popc(__ballot_sync(kFull, (uint32_t)(item >> 32) < a.vocab) >> kTokens & kMask);
+            const uint32_t known = __ballot_sync(kFull, (uint32_t)(item >> 32) < a.vocab);
+            valid = __popc(known >> kTokens & kMask);
         }
     }
     // the e-th token from the chunk's first one on
@@ -451,12 +457,14 @@ struct Cols {
 };
 
 // Bound by HBM: dy read once, the table written once (read and written where it is added to).
+// 16384 x 4096 bf16 into 50000 rows: 133 us, 7.2 TB/s; the sort ahead and the join behind are
+// latency.
 // A word met up to kTokens times is summed by the warp in whose chunk it starts; a longer run is cut
 // at the chunks' borders. kN: a lane's columns.
 template <typename T, int kTokens, int kN, bool kWide, bool kAdd>
 __global__ void __launch_bounds__(kThreads, 2) k_embed_sum(const __grid_constant__ SumArgs a) {
-    // rows in flight (and of the table); more of 16 bytes take so many registers that there are less
-    // warps (16384 x 4096 over 50000 words: 175 us for 162)
+    // rows in flight (and of the table); more of 16 bytes take so many registers that there are
+    // less warps (16384 x 4096 over 50000 words: 175 us for 162)
     constexpr int kBatch = kN == 8 ? 4 : 8;
     const int lane = threadIdx.x & 31;
     grid_dep_wait();
@@ -659,8 +667,8 @@ BackwardLayout backward_layout(uint64_t n, uint64_t vocab, uint64_t dim) {
     }
     L.counts = at;
     at = up(at + (size_t)kSortMost * kDigits * 4);
-    // Chunks of 32 tokens; of 8 where that would leave 152 SMs less than 16 warps each: a warp's rows
-    // are then all under way at once (5001 tokens x 1001 columns: 36 us for 52).
+    // Chunks of 32 tokens; of 8 where that would leave 152 SMs less than 16 warps each: a warp's
+    // rows are then all under way at once (5001 tokens x 1001 columns: 36 us for 52).
     L.tokens = (n + 31) / 32 * ((dim + 127) / 128) < 152 * 16 ? 8 : 32;
     const uint64_t chunks = (n + L.tokens - 1) / L.tokens;
     L.list = at;  // the count, then the chunks

@@ -10,16 +10,17 @@
 //   1. each warp composes its rows' map; the last warp composes the warps' and publishes the
 //      chunk's (A, B);
 //   2. 16 or 32 chunks are a group: the warps collect the maps of the chunks ahead of this one in
-//      its group, two or four each, and the state that enters the group, which the last chunk of the
-//      group ahead publishes. (Which maps are joined, and how, is fixed, so the rounding is too:
-//      results are the same bits on every run. A chain from chunk to chunk would cost its latency for
-//      each.)
+//      its group, two or four each, and the state that enters the group, which the last chunk of
+//      the group ahead publishes. (Which maps are joined, and how, is fixed, so the rounding is
+//      too: results are the same bits on every run. A chain from chunk to chunk would cost its
+//      latency for each.)
 //   3. each warp walks its rows again from the state it enters with, and writes.
 // Up to 128 rows are one chunk's: k_scan_few has no more than its block's exchange.
 // The data is read once. Blocks stay: the next tile is on its way to shared memory as soon as the
-// rows of this one are in registers, while the maps are exchanged and the results written. (One block
-// a tile, with its loads at its beginning, took 279 us for 32768 x 2048.) Tiles go by a ticket, in
-// order, so a block only waits for tiles that running blocks hold; waits are bounded all the same.
+// rows of this one are in registers, while the maps are exchanged and the results written. (One
+// block a tile, with its loads at its beginning, took 279 us for 32768 x 2048.) Tiles go by a
+// ticket, in order, so a block only waits for tiles that running blocks hold; waits are bounded all
+// the same.
 // A ticket is taken late: the further ahead, the less tiles are begun in the order in which they
 // wait for one another (two tiles ahead 149 us).
 //
@@ -273,9 +274,9 @@ __device__ __forceinline__ Map compose(const ScanArgs& a, const Board& b, uint32
     return before;
 }
 
-// Step 2: a warp collects the maps of kEach chunks, the last one also the state that enters the group
-// (it has the fewest chunks to wait for). The first look is taken ahead of the next tile's copies, or
-// it would queue behind them (2500 clocks for 900).
+// Step 2: a warp collects the maps of kEach chunks, the last one also the state that enters the
+// group (it has the fewest chunks to wait for). The first look is taken ahead of the next tile's
+// copies, or it would queue behind them (2500 clocks for 900).
 template <uint32_t kEach>
 struct LookBack {
     const uint4* maps;
@@ -285,7 +286,8 @@ struct LookBack {
     uint4 v[kEach];
     uint2 h;
     __device__ LookBack(const ScanArgs& a, uint32_t order, uint32_t tile, int w, bool fresh) {
-        const uint32_t lane = threadIdx.x & 31, group = order / (kEach * kWarps), k = order % (kEach * kWarps);
+        const uint32_t lane = threadIdx.x & 31;
+        const uint32_t group = order / (kEach * kWarps), k = order % (kEach * kWarps);
         const uint32_t from = kEach * (uint32_t)w;
         count = 0;
         state = nullptr;
@@ -331,7 +333,8 @@ template <uint32_t kEach>
 __device__ __forceinline__ float2 enter(const ScanArgs& a, const Board& b, uint32_t order,
                                         uint32_t tile, int w, const Map& before, const Map& m,
                                         bool fresh) {
-    const uint32_t lane = threadIdx.x & 31, group = order / (kEach * kWarps), k = order % (kEach * kWarps);
+    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t group = order / (kEach * kWarps), k = order % (kEach * kWarps);
     float2 h = {0.0f, 0.0f};
     if (!a.ticket) return h;
     if (!fresh) {
@@ -428,8 +431,11 @@ struct Spot {
 };
 
 // --------------------------------------------------------------------------------- forward
-// Bound by HBM: x and gate read once, y written once. Rows with no border among them and whole
-// columns take a way without tests.
+// x and gate read once, y written once. 32768 x 2048 bf16: 106 us, 3.8 TB/s. Not bound by HBM but by
+// its steps: some 20 us are waits for the maps of tiles that run at the same time (a timing copy
+// that took zeros for them ran 86), the rest the latency of two walks over the rows, in which the
+// 16 warps that registers and shared memory leave an SM issue in 47% of the clocks. Rows with no
+// border among them and whole columns take a way without tests.
 template <typename T, int kUnit, int kS, int kBlocks, uint32_t kEach>
 __global__ void __launch_bounds__(kThreads, kBlocks) k_scan(const __grid_constant__ ScanArgs a) {
     constexpr int kRows = kWarps * kS;
@@ -598,7 +604,9 @@ __global__ void __launch_bounds__(kThreads) k_scan_few(const __grid_constant__ S
 }
 
 // -------------------------------------------------------------------------------- backward
-// Bound by HBM: x, gate and dy read once, dx and dgate written once, the states of every 64th row.
+// x, gate and dy read once, dx and dgate written once, the states of every 64th row read.
+// 16001 x 2048 fp16 in 37 sequences: 131 us, 2.5 TB/s, bound as k_scan is (three walks over the rows;
+// instructions issued in 43% of the clocks).
 template <typename T, int kUnit, int kS, int kBlocks, uint32_t kEach>
 __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_back(const __grid_constant__ ScanArgs a) {
     constexpr int kRows = kWarps * kS;
@@ -745,9 +753,9 @@ struct Form {
     static constexpr int kBackS = kPiece / kWarps, kBackBlocks = 2;
 };
 
-// Columns from which on 16 chunks are a group (32768 x 2048: 107 us for 112), with two maps for a warp
-// to collect. Below, where a tile of columns has most of the blocks to itself, 32: there the chain of
-// groups counts more (16384 x 64: 10 us for 12).
+// Columns from which on 16 chunks are a group (32768 x 2048: 107 us for 112), with two maps for a
+// warp to collect. Below, where a tile of columns has most of the blocks to itself, 32: there the
+// chain of groups counts more (16384 x 64: 10 us for 12).
 constexpr uint64_t kWideCols = 8 * kCols;
 
 struct ScanLayout {
