@@ -125,50 +125,75 @@ struct Map {
 __device__ __forceinline__ Map map_of(const float4& v) { return {{v.x, v.y}, {v.z, v.w}}; }
 __device__ __forceinline__ Map identity() { return {both(1.0f), both(0.0f)}; }
 
+// An offset of the table as a row. Of a bad table it may be anything: then it is no row.
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;
+__device__ __forceinline__ uint32_t offset_at(const ScanArgs& a, uint32_t i) {
+    const int64_t off = a.offsets[i];
+    return off >= 0 && off < (int64_t)kNoRow ? (uint32_t)off : kNoRow;
+}
+// Every ceil(n / 32)-th of a table of n offsets, one a lane: the first step of a search.
+__device__ __forceinline__ uint32_t landmark(const ScanArgs& a) {
+    const uint32_t n = a.nseq + 1, step = (n + 31) / 32;
+    return offset_at(a, min(((threadIdx.x & 31) + 1) * step, n) - 1);
+}
 // Where sequences start and end in a warp's kS rows: bits, and the sequences in the arrays (the
-// warp's own). mine: the lane's entry of a table of at most 32.
+// warp's own). mine: the lane's landmark.
 template <int kS>
 struct Marks {
-    uint32_t start, end;
-    __device__ Marks(const ScanArgs& a, uint32_t first, int64_t mine, int32_t* starts,
+    static_assert(kS <= 16, "two of 16 bits");
+    uint32_t bits;
+    __device__ uint32_t start() const { return bits & 0xFFFFu; }
+    __device__ uint32_t end() const { return bits >> 16; }
+    __device__ bool starts_at(int s) const { return bits >> s & 1; }
+    __device__ bool ends_at(int s) const { return bits >> (16 + s) & 1; }
+    __device__ Marks(const ScanArgs& a, uint32_t begin, uint32_t mine, int32_t* starts,
                      int32_t* ends) {
-        const uint32_t lane = threadIdx.x & 31, n = a.nseq + 1;
-        const int64_t begin = first, stop = begin + kS;
-        start = end = 0;
-        __syncwarp();  // the arrays' readers of the tile before
-        for (uint32_t i0 = n <= 32 ? 0 : first_from(a.offsets, 0, n, begin);; i0 += 32) {
+        const uint32_t lane = threadIdx.x & 31, n = a.nseq + 1, step = (n + 31) / 32;
+        const uint32_t stop = begin + kS;
+        bits = 0;
+        __syncwarp();  // the arrays' readers of two tiles before
+        uint32_t i0 = 0;
+        if (step > 1) {
+            const uint32_t less = __popc(__ballot_sync(kFull, mine < begin));
+            i0 = min(less * step, n);
+            if (step > 32) i0 = first_from(a.offsets, i0, min(step, n - i0),
+                                            (int64_t)begin);
+        }
+        for (;; i0 += 32) {
             const uint32_t i = i0 + lane;
-            const int64_t off = n <= 32 ? mine : i < n ? a.offsets[i] : INT64_MAX;
-            if (__any_sync(kFull, off >= begin && off <= stop)) {
-                uint32_t s = 0, e = 0;
-                if (off >= begin && off <= stop) {
-                    const int r = (int)(off - begin);
-                    if (r < kS && i + 1 < n && a.offsets[i + 1] > off) {
+            const uint32_t off = i >= n ? kNoRow : step > 1 ? offset_at(a, i) : mine;
+            const bool here = i < n && off >= begin && off <= stop;
+            if (__any_sync(kFull, here)) {
+                uint32_t b = 0;
+                if (here) {
+                    const uint32_t r = off - begin;
+                    if (r < kS && i + 1 < n && offset_at(a, i + 1) > off) {
                         starts[r] = (int32_t)i;
-                        s = 1u << r;
+                        b = 1u << r;
                     }
-                    if (r > 0 && i > 0 && a.offsets[i - 1] < off) {
+                    if (r > 0 && i > 0 && offset_at(a, i - 1) < off) {
                         ends[r - 1] = (int32_t)i - 1;
-                        e = 1u << (r - 1);
+                        b |= 0x10000u << (r - 1);
                     }
                 }
-                start |= __reduce_or_sync(kFull, s);
-                end |= __reduce_or_sync(kFull, e);
+                bits |= __reduce_or_sync(kFull, b);
             }
-            if (n <= 32 || !__all_sync(kFull, off <= stop)) break;
+            if (step == 1 || !__all_sync(kFull, off <= stop)) break;
         }
         __syncwarp();
     }
 };
 
-// What has no row: sequences of length 0 pass their state on; and the table's check. By the first
-// chunk's blocks.
-__device__ __forceinline__ void empty_sequences(const ScanArgs& a, uint32_t tile, const float* from,
-                                                uint64_t ld_from, float* to, uint64_t ld_to) {
+// What has no row: sequences of length 0 pass their state on; and the table's check. A tile's columns
+// by `parts` blocks, of which this is one.
+__device__ __forceinline__ void empty_sequences(const ScanArgs& a, uint32_t tile, uint32_t part,
+                                                uint32_t parts, const float* from, uint64_t ld_from,
+                                                float* to, uint64_t ld_to) {
     const int lane = threadIdx.x & 31;
     const uint32_t col = tile * kCols + 2 * lane, n = col < a.cols ? min(2u, a.cols - col) : 0;
     bool bad = false;
-    for (uint32_t q0 = (threadIdx.x >> 5) * 32; q0 < a.nseq; q0 += kThreads) {
+    for (uint32_t q0 = part * kThreads + (threadIdx.x & ~31u); q0 < a.nseq;
+         q0 += parts * kThreads) {
         const uint32_t q = q0 + lane;
         const int64_t b = q < a.nseq ? a.offsets[q] : 0, e = q < a.nseq ? a.offsets[q + 1] : 1;
         bad |= q < a.nseq && (b > e || b < 0 || e > (int64_t)a.rows);
@@ -180,6 +205,15 @@ __device__ __forceinline__ void empty_sequences(const ScanArgs& a, uint32_t tile
         }
     }
     if (tile == 0 && bad) report(a.status, DGC_EINVAL);
+}
+// The same by all blocks, at their end: other blocks wait for nothing that comes behind it, however
+// many sequences there are.
+__device__ __forceinline__ void all_empty_sequences(const ScanArgs& a, const float* from,
+                                                    uint64_t ld_from, float* to, uint64_t ld_to) {
+    const uint32_t parts = max(1u, gridDim.x / a.tiles), part = blockIdx.x / a.tiles;
+    if (part < parts)
+        for (uint32_t tile = blockIdx.x % a.tiles; tile < a.tiles; tile += gridDim.x)
+            empty_sequences(a, tile, part, parts, from, ld_from, to, ld_to);
 }
 
 // A tile: its chunk's place in the scan's direction, and its columns. order of chunks on: none.
@@ -442,10 +476,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan(const __grid_constan
     constexpr bool kPair = kUnit != 0;
     extern __shared__ uint4 ring[];
     __shared__ Board board;
-    __shared__ int32_t starts_of[kWarps][kS], ends_of[kWarps][kS];
+    __shared__ int32_t starts_of[2][kWarps][kS], ends_of[2][kWarps][kS];
     const Landing<T, kUnit, kS, 2> land(ring);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int32_t *starts = starts_of[warp], *ends = ends_of[warp];
     grid_dep_wait();
     grid_dep_launch();
     Tile t = first_tile(a, &board.next);
@@ -458,13 +491,19 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan(const __grid_constan
         copy_commit();
     };
     fetch();
-    const int64_t valid0 = a.offsets[0], valid1 = min((int64_t)a.rows, a.offsets[a.nseq]);
-    const int64_t mine = lane <= a.nseq ? a.offsets[lane] : INT64_MAX;
+    const uint32_t valid0 = offset_at(a, 0), valid1 = min(a.rows, offset_at(a, a.nseq));
+    const uint32_t mine = landmark(a);
+    uint32_t turn = 0;
+    auto look_marks = [&] {
+        const Spot at(a, t.order, t.tile, kRows, kS);
+        return Marks<kS>(a, at.first, mine, starts_of[turn & 1][warp], ends_of[turn & 1][warp]);
+    };
+    Marks<kS> marks_next = look_marks();
     while (t.order < a.chunks) {
         const uint32_t chunk = t.order, tile = t.tile;
         const Spot at(a, chunk, tile, kRows, kS);
-        if (chunk == 0) empty_sequences(a, tile, a.h0, a.ldh0, a.h_last, a.ldh_last);
-        const Marks<kS> marks(a, at.first, mine, starts, ends);
+        const Marks<kS> marks = marks_next;
+        const uint32_t slot = turn++ & 1;
         copy_wait<0>();
         __syncwarp();
         // the next ticket; not ahead of the wait, which would wait for it too
@@ -479,43 +518,44 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan(const __grid_constan
             B[s] = mul2(keep, land.get(1, s));
         }
         Map m = identity();
-        if (marks.start) {
+        if (marks.start()) {
             if (a.h0) {
                 float2 h[kS];
 #pragma unroll
                 for (int s = 0; s < kS; ++s) {
-                    const bool here = marks.start >> s & 1;
-                    h[s] = load_state(a.h0, a.ldh0, here ? starts[s] : 0, at.lane_col,
-                                      here ? at.n : 0);
+                    const bool here = marks.starts_at(s);
+                    h[s] = load_state(a.h0, a.ldh0, here ? starts_of[slot][warp][s] : 0,
+                                      at.lane_col, here ? at.n : 0);
                 }
 #pragma unroll
                 for (int s = 0; s < kS; ++s)
-                    if (marks.start >> s & 1) B[s] = fma2(A[s], h[s], B[s]);
+                    if (marks.starts_at(s)) B[s] = fma2(A[s], h[s], B[s]);
             }
 #pragma unroll
             for (int s = 0; s < kS; ++s)
-                m = marks.start >> s & 1 ? Map{both(kReset), B[s]} : m.then({A[s], B[s]});
+                m = marks.starts_at(s) ? Map{both(kReset), B[s]} : m.then({A[s], B[s]});
         } else {
 #pragma unroll
             for (int s = 0; s < kS; ++s) m = m.plain_then({A[s], B[s]});
         }
         board.map[warp][lane] = m.packed();
         if (threadIdx.x == 0) {
-            board.fresh = marks.start & 1;
+            board.fresh = marks.starts_at(0);
             board.next = more;
         }
-        const bool resets = __syncthreads_or(marks.start != 0);
+        const bool resets = __syncthreads_or(marks.start() != 0);
         const Map before = compose(a, board, chunk, tile, warp, m, resets);
         const bool fresh = board.fresh;
         LookBack<kEach> back(a, chunk, tile, warp, fresh);
         t = tile_of(a, board.next);
         fetch();
+        if (t.order < a.chunks) marks_next = look_marks();
         back.finish(a, board, warp);
         __syncthreads();
         float2 h = before(enter<kEach>(a, board, chunk, tile, warp, before, m, fresh));
         if (a.saved && at.first % kPiece == 0 && at.left)
             store_state(a.saved, a.lds, at.first / kPiece, at.lane_col, at.n, h);
-        if (kPair && !(marks.start | marks.end) && at.first >= valid0 && at.first + kS <= valid1 &&
+        if (kPair && !marks.bits && at.first >= valid0 && at.first + kS <= valid1 &&
             at.col + kCols <= a.cols) {
             T* y = static_cast<T*>(a.y) + at.first * a.ldy + at.lane_col;
 #pragma unroll
@@ -528,16 +568,18 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan(const __grid_constan
         } else {
 #pragma unroll
             for (int s = 0; s < kS; ++s) {
-                const int64_t row = at.first + s;
-                h = marks.start >> s & 1 ? B[s] : fma2(A[s], h, B[s]);
+                const uint32_t row = at.first + s;
+                h = marks.starts_at(s) ? B[s] : fma2(A[s], h, B[s]);
                 if (row >= valid0 && row < valid1)
                     store_two<T, kPair>(a.y, a.ldy, row, at.lane_col, at.n, h);
-                if (a.h_last && (marks.end >> s & 1) && s < at.left)
-                    store_state(a.h_last, a.ldh_last, ends[s], at.lane_col, at.n, h);
+                if (a.h_last && marks.ends_at(s) && s < at.left)
+                    store_state(a.h_last, a.ldh_last, ends_of[slot][warp][s], at.lane_col, at.n,
+                                h);
             }
         }
     }
     copy_wait<0>();
+    all_empty_sequences(a, a.h0, a.ldh0, a.h_last, a.ldh_last);
 }
 
 // Up to kWarps * kS rows: a block a column tile. For a step of a model that answers, a start and a
@@ -559,16 +601,16 @@ __global__ void __launch_bounds__(kThreads) k_scan_few(const __grid_constant__ S
         pg[s] = load_piece<kPair, T, 2>(gate + s * a.ldg, s < at.left ? at.n : 0);
         px[s] = load_piece<kPair, T, 2>(x + s * a.ldx, s < at.left ? at.n : 0);
     }
-    const int64_t valid0 = a.offsets[0], valid1 = min((int64_t)a.rows, a.offsets[a.nseq]);
-    const int64_t mine = lane <= a.nseq ? a.offsets[lane] : INT64_MAX;
+    const uint32_t valid0 = offset_at(a, 0), valid1 = min(a.rows, offset_at(a, a.nseq));
+    const uint32_t mine = landmark(a);
     const Marks<kS> marks(a, at.first, mine, starts, ends);
     float2 given[kS];
 #pragma unroll
     for (int s = 0; s < kS; ++s) {
-        const bool here = a.h0 && (marks.start >> s & 1);
+        const bool here = a.h0 && marks.starts_at(s);
         given[s] = load_state(a.h0, a.ldh0, here ? starts[s] : 0, at.lane_col, here ? at.n : 0);
     }
-    empty_sequences(a, blockIdx.x, a.h0, a.ldh0, a.h_last, a.ldh_last);
+    empty_sequences(a, blockIdx.x, 0, 1, a.h0, a.ldh0, a.h_last, a.ldh_last);
     float2 A[kS], B[kS];
     Map m = identity();
 #pragma unroll
@@ -576,7 +618,7 @@ __global__ void __launch_bounds__(kThreads) k_scan_few(const __grid_constant__ S
         float2 keep;
         sigmoids(pair_of<T, 2>(pg[s], 0), A[s], keep);
         B[s] = mul2(keep, pair_of<T, 2>(px[s], 0));
-        if (marks.start >> s & 1) {
+        if (marks.starts_at(s)) {
             B[s] = fma2(A[s], given[s], B[s]);
             m = {both(kReset), B[s]};
         } else {
@@ -584,7 +626,7 @@ __global__ void __launch_bounds__(kThreads) k_scan_few(const __grid_constant__ S
         }
     }
     maps[warp][lane] = m.packed();
-    const bool resets = __syncthreads_or(marks.start != 0);
+    const bool resets = __syncthreads_or(marks.start() != 0);
     float2 h = both(0.0f);
     for (int w = 0; w < warp; ++w) {
         const Map q = map_of(maps[w][lane]);
@@ -594,11 +636,11 @@ __global__ void __launch_bounds__(kThreads) k_scan_few(const __grid_constant__ S
         store_state(a.saved, a.lds, at.first / kPiece, at.lane_col, at.n, h);
 #pragma unroll
     for (int s = 0; s < kS; ++s) {
-        const int64_t row = at.first + s;
-        h = marks.start >> s & 1 ? B[s] : fma2(A[s], h, B[s]);
+        const uint32_t row = at.first + s;
+        h = marks.starts_at(s) ? B[s] : fma2(A[s], h, B[s]);
         if (row >= valid0 && row < valid1)
             store_two<T, kPair>(a.y, a.ldy, row, at.lane_col, at.n, h);
-        if (a.h_last && (marks.end >> s & 1) && s < at.left)
+        if (a.h_last && marks.ends_at(s) && s < at.left)
             store_state(a.h_last, a.ldh_last, ends[s], at.lane_col, at.n, h);
     }
 }
@@ -615,33 +657,40 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_back(const __grid_co
     extern __shared__ uint4 ring[];
     __shared__ Board board;
     __shared__ float4 maps[kWarps][32];  // of h, as the board's are of u
-    __shared__ int32_t starts_of[kWarps][kS], ends_of[kWarps][kS];
+    __shared__ int32_t starts_of[2][kWarps][kS], ends_of[2][kWarps][kS];
     const Landing<T, kUnit, kS, 3> land(ring);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, place = kWarps - 1 - warp;
-    int32_t *starts = starts_of[warp], *ends = ends_of[warp];
     grid_dep_wait();
     grid_dep_launch();
     Tile t = first_tile(a, &board.next);
+    float2 entering = both(0.0f);
     auto fetch = [&] {
         if (t.order < a.chunks) {
             const Spot at(a, a.chunks - 1 - t.order, t.tile, kRows, kS);
             land.fetch(0, a.gate, a.ldg, at.first, at.left, at.col, a.cols);
             land.fetch(1, a.x, a.ldx, at.first, at.left, at.col, a.cols);
             land.fetch(2, a.dy, a.lddy, at.first, at.left, at.col, a.cols);
+            const uint32_t chunk = a.chunks - 1 - t.order;
+            if (a.rows) entering = load_state(a.saved, a.lds, chunk, at.lane_col, at.n);
         }
         copy_commit();
     };
     fetch();
-    const int64_t valid0 = a.offsets[0], valid1 = min((int64_t)a.rows, a.offsets[a.nseq]);
-    const int64_t mine = lane <= a.nseq ? a.offsets[lane] : INT64_MAX;
+    const uint32_t valid0 = offset_at(a, 0), valid1 = min(a.rows, offset_at(a, a.nseq));
+    const uint32_t mine = landmark(a);
+    uint32_t turn = 0;
+    auto look_marks = [&] {
+        const Spot at(a, a.chunks - 1 - t.order, t.tile, kRows, kS);
+        return Marks<kS>(a, at.first, mine, starts_of[turn & 1][warp], ends_of[turn & 1][warp]);
+    };
+    Marks<kS> marks_next = look_marks();
     while (t.order < a.chunks) {
         const uint32_t order = t.order, tile = t.tile;
         const uint32_t chunk = a.chunks - 1 - order;
         const Spot at(a, chunk, tile, kRows, kS);
-        float2 h = both(0.0f);
-        if (chunk * kRows < a.rows) h = load_state(a.saved, a.lds, chunk, at.lane_col, at.n);
-        if (chunk == 0) empty_sequences(a, tile, a.d_last, a.ldd_last, a.d_h0, a.ldd_h0);
-        const Marks<kS> marks(a, at.first, mine, starts, ends);
+        float2 h = entering;
+        const Marks<kS> marks = marks_next;
+        const uint32_t slot = turn++ & 1;
         copy_wait<0>();
         __syncwarp();
         // the next ticket; not ahead of the wait, which would wait for it too
@@ -654,25 +703,27 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_back(const __grid_co
             q[s] = mul2(keep[s], land.get(1, s));
             G[s] = land.get(2, s);
         }
-        if (marks.end && a.d_last)
+        if (marks.end() && a.d_last)
 #pragma unroll
             for (int s = 0; s < kS; ++s)
-                if (marks.end >> s & 1)
-                    G[s] = add2(G[s], load_state(a.d_last, a.ldd_last, ends[s], at.lane_col, at.n));
+                if (marks.ends_at(s))
+                    G[s] = add2(G[s], load_state(a.d_last, a.ldd_last, ends_of[slot][warp][s],
+                                                 at.lane_col, at.n));
         // the rows' map of h, and from the end that of u
         Map m = identity(), u = identity();
         auto first_state = [&](int s) {
-            return a.h0 ? load_state(a.h0, a.ldh0, starts[s], at.lane_col, at.n) : both(0.0f);
+            return a.h0 ? load_state(a.h0, a.ldh0, starts_of[slot][warp][s], at.lane_col, at.n)
+                        : both(0.0f);
         };
-        if (marks.start | marks.end) {
+        if (marks.bits) {
 #pragma unroll
             for (int s = 0; s < kS; ++s)
-                m = marks.start >> s & 1 ? Map{both(kReset), fma2(A[s], first_state(s), q[s])}
+                m = marks.starts_at(s) ? Map{both(kReset), fma2(A[s], first_state(s), q[s])}
                                          : m.then({A[s], q[s]});
 #pragma unroll
             for (int s = kS - 1; s >= 0; --s) {
                 const Map row{A[s], mul2(A[s], G[s])};
-                u = marks.end >> s & 1 ? Map{both(kReset), row.B} : u.then(row);
+                u = marks.ends_at(s) ? Map{both(kReset), row.B} : u.then(row);
             }
         } else {
 #pragma unroll
@@ -683,9 +734,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_back(const __grid_co
         }
         maps[warp][lane] = m.packed();
         board.map[place][lane] = u.packed();
-        if (threadIdx.x == kThreads - 1) board.fresh = marks.end >> (kS - 1) & 1;
+        if (threadIdx.x == kThreads - 1) board.fresh = marks.ends_at(kS - 1);
         if (threadIdx.x == 0) board.next = more;
-        const bool resets = __syncthreads_or((marks.start | marks.end) != 0);
+        const bool resets = __syncthreads_or(marks.bits != 0);
         const Map behind = compose(a, board, order, tile, place, u, resets);
         const bool fresh = board.fresh;
         if (resets)
@@ -699,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_back(const __grid_co
                 }
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
-            if (marks.start >> s & 1) h = first_state(s);
+            if (marks.starts_at(s)) h = first_state(s);
             const float2 x = land.get(1, s), b = q[s];
             q[s] = mul2(mul2(A[s], keep[s]), add2(h, {-x.x, -x.y}));
             h = fma2(A[s], h, b);
@@ -708,11 +759,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_back(const __grid_co
         __syncwarp();
         t = tile_of(a, board.next);
         fetch();
+        if (t.order < a.chunks) marks_next = look_marks();
         back.finish(a, board, place);
         __syncthreads();
         // u of the row behind
         float2 v = behind(enter<kEach>(a, board, order, tile, place, behind, u, fresh));
-        if (kPair && !(marks.start | marks.end) && at.first >= valid0 && at.first + kS <= valid1 &&
+        if (kPair && !marks.bits && at.first >= valid0 && at.first + kS <= valid1 &&
             at.col + kCols <= a.cols) {
             T* dx = static_cast<T*>(a.dx) + (at.first + kS - 1) * a.lddx + at.lane_col;
             T* dgate = static_cast<T*>(a.dgate) + (at.first + kS - 1) * a.lddg + at.lane_col;
@@ -729,20 +781,22 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_back(const __grid_co
         } else {
 #pragma unroll
             for (int s = kS - 1; s >= 0; --s) {
-                const int64_t row = at.first + s;
-                if (marks.end >> s & 1) v = both(0.0f);
+                const uint32_t row = at.first + s;
+                if (marks.ends_at(s)) v = both(0.0f);
                 const float2 g = add2(G[s], v);
                 if (row >= valid0 && row < valid1) {
                     store_two<T, kPair>(a.dx, a.lddx, row, at.lane_col, at.n, mul2(g, keep[s]));
                     store_two<T, kPair>(a.dgate, a.lddg, row, at.lane_col, at.n, mul2(g, q[s]));
                 }
                 v = mul2(A[s], g);
-                if (a.d_h0 && (marks.start >> s & 1) && s < at.left)
-                    store_state(a.d_h0, a.ldd_h0, starts[s], at.lane_col, at.n, v);
+                if (a.d_h0 && marks.starts_at(s) && s < at.left)
+                    store_state(a.d_h0, a.ldd_h0, starts_of[slot][warp][s], at.lane_col, at.n,
+                                v);
             }
         }
     }
     copy_wait<0>();
+    all_empty_sequences(a, a.d_last, a.ldd_last, a.d_h0, a.ldd_h0);
 }
 
 // ----------------------------------------------------------------------------------- host
