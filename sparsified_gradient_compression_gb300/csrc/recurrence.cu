@@ -105,18 +105,19 @@ __device__ __forceinline__ void sigmoids(float2 g, float2& a, float2& keep) {
     keep = mul2(e, a);
 }
 
-// h -> A h + B, two columns.
+// h -> A h + B, two columns. A reset is one of both.
 struct Map {
     float2 A, B;
     __device__ float2 operator()(float2 h) const {
         const float2 r = fma2(A, h, B);
-        return {A.x < 0.0f ? B.x : r.x, A.y < 0.0f ? B.y : r.y};
+        const bool reset = A.x < 0.0f;
+        return {reset ? B.x : r.x, reset ? B.y : r.y};
     }
     // this one first, then q
     __device__ Map then(const Map& q) const {
         const float2 p = mul2(q.A, A);
-        return {{fminf(q.A.x, A.x) < 0.0f ? kReset : p.x, fminf(q.A.y, A.y) < 0.0f ? kReset : p.y},
-                q(B)};
+        const bool reset = fminf(q.A.x, A.x) < 0.0f;
+        return {{reset ? kReset : p.x, reset ? kReset : p.y}, q(B)};
     }
     // the same where neither has a reset
     __device__ Map plain_then(const Map& q) const { return {mul2(q.A, A), fma2(q.A, B, q.B)}; }
@@ -235,6 +236,55 @@ __device__ __forceinline__ Tile first_tile(const ScanArgs& a, uint32_t* slot) {
     return t;
 }
 
+// What a warp has of a tile: its rows, how many of them there are, and its lane's columns.
+struct Spot {
+    uint32_t first, left, col, lane_col, n;
+    __device__ Spot(const ScanArgs& a, uint32_t chunk, uint32_t tile, uint32_t rows, uint32_t s) {
+        first = chunk * rows + (threadIdx.x >> 5) * s;
+        left = first < a.rows ? a.rows - first : 0;
+        col = tile * kCols;
+        lane_col = col + 2 * (threadIdx.x & 31);
+        n = lane_col < a.cols ? min(2u, a.cols - lane_col) : 0;
+    }
+};
+
+// The states at the borders (bits) in a warp's rows, `which` the sequences. One is loaded ahead of the
+// rows' arithmetic, more all at once behind it.
+template <int kS>
+struct Given {
+    const float* m;
+    uint64_t ld;
+    const int32_t* which;
+    uint32_t bits, col, n;
+    float2 one;
+    __device__ Given(const float* m, uint64_t ld, const int32_t* which, uint32_t bits,
+                     const Spot& at)
+        : m(m), ld(ld), which(which), bits(m ? bits : 0), col(at.lane_col), n(at.n) {
+        one = both(0.0f);
+        if (this->bits) one = load_state(m, ld, which[__ffs(this->bits) - 1], col, n);
+    }
+    // f(s, state) for each
+    template <typename F>
+    __device__ void each(F f) const {
+        if (!bits) return;
+        if ((bits & (bits - 1)) == 0) {
+#pragma unroll
+            for (int s = 0; s < kS; ++s)
+                if (bits >> s & 1) f(s, one);
+            return;
+        }
+        float2 v[kS];
+#pragma unroll
+        for (int s = 0; s < kS; ++s) {
+            const bool here = bits >> s & 1;
+            v[s] = load_state(m, ld, here ? which[s] : 0, col, here ? n : 0);
+        }
+#pragma unroll
+        for (int s = 0; s < kS; ++s)
+            if (bits >> s & 1) f(s, v[s]);
+    }
+};
+
 // What the warps of a block tell one another about a tile. A tile has two barriers: what is written
 // ahead of the first one is read between the two, what is written between them is read behind the
 // second one and ahead of the next tile's first.
@@ -297,9 +347,11 @@ __device__ __forceinline__ Map compose(const ScanArgs& a, const Board& b, uint32
                                        uint32_t tile, int w, const Map& m, bool resets) {
     const uint32_t lane = threadIdx.x & 31;
     Map before = identity();
-    if (resets)
-        for (int i = 0; i < w; ++i) before = before.then(map_of(b.map[i][lane]));
-    else
+    if (resets) {
+#pragma unroll
+        for (int i = 0; i < kWarps - 1; ++i)
+            if (i < w) before = before.then(map_of(b.map[i][lane]));
+    } else
 #pragma unroll
         for (int i = 0; i < kWarps - 1; ++i)
             if (i < w) before = before.plain_then(map_of(b.map[i][lane]));
@@ -452,18 +504,6 @@ struct Landing {
     }
 };
 
-// What a warp has of a tile: its rows, how many of them there are, and its lane's columns.
-struct Spot {
-    uint32_t first, left, col, lane_col, n;
-    __device__ Spot(const ScanArgs& a, uint32_t chunk, uint32_t tile, uint32_t rows, uint32_t s) {
-        first = chunk * rows + (threadIdx.x >> 5) * s;
-        left = first < a.rows ? a.rows - first : 0;
-        col = tile * kCols;
-        lane_col = col + 2 * (threadIdx.x & 31);
-        n = lane_col < a.cols ? min(2u, a.cols - lane_col) : 0;
-    }
-};
-
 // --------------------------------------------------------------------------------- forward
 // x and gate read once, y written once. 32768 x 2048 bf16: 106 us, 3.8 TB/s. Not bound by HBM but by
 // its steps: some 20 us are waits for the maps of tiles that run at the same time (a timing copy
@@ -509,6 +549,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan(const __grid_constan
         // the next ticket; not ahead of the wait, which would wait for it too
         uint32_t more = 0xFFFFFFFFu;
         if (a.ticket && threadIdx.x == 0) more = atomicAdd(a.ticket, 1u);
+        const Given<kS> given(a.h0, a.ldh0, starts_of[slot][warp], marks.start(), at);
         // rows as h -> A h + B
         float2 A[kS], B[kS];
 #pragma unroll
@@ -519,21 +560,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan(const __grid_constan
         }
         Map m = identity();
         if (marks.start()) {
-            if (a.h0) {
-                float2 h[kS];
-#pragma unroll
-                for (int s = 0; s < kS; ++s) {
-                    const bool here = marks.starts_at(s);
-                    h[s] = load_state(a.h0, a.ldh0, here ? starts_of[slot][warp][s] : 0,
-                                      at.lane_col, here ? at.n : 0);
-                }
-#pragma unroll
-                for (int s = 0; s < kS; ++s)
-                    if (marks.starts_at(s)) B[s] = fma2(A[s], h[s], B[s]);
-            }
+            given.each([&](int s, float2 h) { B[s] = fma2(A[s], h, B[s]); });
 #pragma unroll
             for (int s = 0; s < kS; ++s)
-                m = marks.starts_at(s) ? Map{both(kReset), B[s]} : m.then({A[s], B[s]});
+                if (marks.starts_at(s)) m.B = B[s];
+                else m.B = fma2(A[s], m.B, B[s]);
+            m.A = both(kReset);
         } else {
 #pragma unroll
             for (int s = 0; s < kS; ++s) m = m.plain_then({A[s], B[s]});
@@ -555,15 +587,29 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan(const __grid_constan
         float2 h = before(enter<kEach>(a, board, chunk, tile, warp, before, m, fresh));
         if (a.saved && at.first % kPiece == 0 && at.left)
             store_state(a.saved, a.lds, at.first / kPiece, at.lane_col, at.n, h);
-        if (kPair && !marks.bits && at.first >= valid0 && at.first + kS <= valid1 &&
-            at.col + kCols <= a.cols) {
-            T* y = static_cast<T*>(a.y) + at.first * a.ldy + at.lane_col;
+        const bool whole = kPair && at.first >= valid0 && at.first + kS <= valid1 &&
+                           at.col + kCols <= a.cols;
+        T* y = static_cast<T*>(a.y) + at.first * a.ldy + at.lane_col;
+        auto put = [&] {
+            Packed<T, 2> p;
+            set_pair<T, 2>(p, 0, h);
+            store_packed<T, 2>(y, p);
+            y += a.ldy;
+        };
+        if (whole && !marks.bits) {
 #pragma unroll
-            for (int s = 0; s < kS; ++s, y += a.ldy) {
+            for (int s = 0; s < kS; ++s) {
                 h = fma2(A[s], h, B[s]);
-                Packed<T, 2> p;
-                set_pair<T, 2>(p, 0, h);
-                store_packed<T, 2>(y, p);
+                put();
+            }
+        } else if (whole) {
+#pragma unroll
+            for (int s = 0; s < kS; ++s) {
+                if (marks.starts_at(s)) h = B[s];
+                else h = fma2(A[s], h, B[s]);
+                put();
+                if (marks.ends_at(s) && a.h_last)
+                    store_state(a.h_last, a.ldh_last, ends_of[slot][warp][s], at.lane_col, 2, h);
             }
         } else {
 #pragma unroll
@@ -696,6 +742,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_back(const __grid_co
         // the next ticket; not ahead of the wait, which would wait for it too
         uint32_t more = 0xFFFFFFFFu;
         if (a.ticket && threadIdx.x == 0) more = atomicAdd(a.ticket, 1u);
+        const Given<kS> first(a.h0, a.ldh0, starts_of[slot][warp], marks.start(), at);
+        const Given<kS> last(a.d_last, a.ldd_last, ends_of[slot][warp], marks.end(), at);
         float2 A[kS], keep[kS], q[kS], G[kS];  // q: (1-a) x, then (h_{t-1} - x) a (1 - a)
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
@@ -703,28 +751,28 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_back(const __grid_co
             q[s] = mul2(keep[s], land.get(1, s));
             G[s] = land.get(2, s);
         }
-        if (marks.end() && a.d_last)
-#pragma unroll
-            for (int s = 0; s < kS; ++s)
-                if (marks.ends_at(s))
-                    G[s] = add2(G[s], load_state(a.d_last, a.ldd_last, ends_of[slot][warp][s],
-                                                 at.lane_col, at.n));
+        last.each([&](int s, float2 g) { G[s] = add2(G[s], g); });
         // the rows' map of h, and from the end that of u
         Map m = identity(), u = identity();
-        auto first_state = [&](int s) {
-            return a.h0 ? load_state(a.h0, a.ldh0, starts_of[slot][warp][s], at.lane_col, at.n)
-                        : both(0.0f);
-        };
         if (marks.bits) {
+            float2 B[kS];
 #pragma unroll
-            for (int s = 0; s < kS; ++s)
-                m = marks.starts_at(s) ? Map{both(kReset), fma2(A[s], first_state(s), q[s])}
-                                         : m.then({A[s], q[s]});
+            for (int s = 0; s < kS; ++s) B[s] = q[s];
+            first.each([&](int s, float2 h) { B[s] = fma2(A[s], h, B[s]); });
+#pragma unroll
+            for (int s = 0; s < kS; ++s) {
+                if (marks.starts_at(s)) m.B = B[s];
+                else m.B = fma2(A[s], m.B, B[s]);
+                m.A = mul2(A[s], m.A);
+            }
+            u.A = m.A;
 #pragma unroll
             for (int s = kS - 1; s >= 0; --s) {
-                const Map row{A[s], mul2(A[s], G[s])};
-                u = marks.ends_at(s) ? Map{both(kReset), row.B} : u.then(row);
+                if (marks.ends_at(s)) u.B = mul2(A[s], G[s]);
+                else u.B = mul2(A[s], add2(G[s], u.B));
             }
+            if (marks.start()) m.A = both(kReset);
+            if (marks.end()) u.A = both(kReset);
         } else {
 #pragma unroll
             for (int s = 0; s < kS; ++s) m = m.plain_then({A[s], q[s]});
@@ -739,9 +787,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_back(const __grid_co
         const bool resets = __syncthreads_or(marks.bits != 0);
         const Map behind = compose(a, board, order, tile, place, u, resets);
         const bool fresh = board.fresh;
-        if (resets)
-            for (int w = 0; w < warp; ++w) h = map_of(maps[w][lane])(h);
-        else
+        if (resets) {
+#pragma unroll
+            for (int w = 0; w < kWarps - 1; ++w)
+                if (w < warp) h = map_of(maps[w][lane])(h);
+        } else
 #pragma unroll
             for (int w = 0; w < kWarps - 1; ++w)
                 if (w < warp) {
@@ -750,7 +800,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_back(const __grid_co
                 }
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
-            if (marks.starts_at(s)) h = first_state(s);
+            if (marks.starts_at(s))
+                h = a.h0 ? load_state(a.h0, a.ldh0, starts_of[slot][warp][s], at.lane_col, at.n)
+                         : both(0.0f);
             const float2 x = land.get(1, s), b = q[s];
             q[s] = mul2(mul2(A[s], keep[s]), add2(h, {-x.x, -x.y}));
             h = fma2(A[s], h, b);
@@ -764,19 +816,31 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_back(const __grid_co
         __syncthreads();
         // u of the row behind
         float2 v = behind(enter<kEach>(a, board, order, tile, place, behind, u, fresh));
-        if (kPair && !marks.bits && at.first >= valid0 && at.first + kS <= valid1 &&
-            at.col + kCols <= a.cols) {
-            T* dx = static_cast<T*>(a.dx) + (at.first + kS - 1) * a.lddx + at.lane_col;
-            T* dgate = static_cast<T*>(a.dgate) + (at.first + kS - 1) * a.lddg + at.lane_col;
+        const bool whole = kPair && at.first >= valid0 && at.first + kS <= valid1 &&
+                           at.col + kCols <= a.cols;
+        T* dx = static_cast<T*>(a.dx) + (at.first + kS - 1) * a.lddx + at.lane_col;
+        T* dgate = static_cast<T*>(a.dgate) + (at.first + kS - 1) * a.lddg + at.lane_col;
+        auto put = [&](int s) {
+            const float2 g = add2(G[s], v);
+            Packed<T, 2> p, r;
+            set_pair<T, 2>(p, 0, mul2(g, keep[s]));
+            set_pair<T, 2>(r, 0, mul2(g, q[s]));
+            store_packed<T, 2>(dx, p);
+            store_packed<T, 2>(dgate, r);
+            v = mul2(A[s], g);
+            dx -= a.lddx;
+            dgate -= a.lddg;
+        };
+        if (whole && !marks.bits) {
 #pragma unroll
-            for (int s = kS - 1; s >= 0; --s, dx -= a.lddx, dgate -= a.lddg) {
-                const float2 g = add2(G[s], v);
-                Packed<T, 2> p, r;
-                set_pair<T, 2>(p, 0, mul2(g, keep[s]));
-                set_pair<T, 2>(r, 0, mul2(g, q[s]));
-                store_packed<T, 2>(dx, p);
-                store_packed<T, 2>(dgate, r);
-                v = mul2(A[s], g);
+            for (int s = kS - 1; s >= 0; --s) put(s);
+        } else if (whole) {
+#pragma unroll
+            for (int s = kS - 1; s >= 0; --s) {
+                if (marks.ends_at(s)) v = both(0.0f);
+                put(s);
+                if (marks.starts_at(s) && a.d_h0)
+                    store_state(a.d_h0, a.ldd_h0, starts_of[slot][warp][s], at.lane_col, 2, v);
             }
         } else {
 #pragma unroll
