@@ -462,10 +462,12 @@ struct Cols {
 // A word met up to kTokens times is summed by the warp in whose chunk it starts; a longer run is cut
 // at the chunks' borders. kN: a lane's columns.
 template <typename T, int kTokens, int kN, bool kWide, bool kAdd>
-__global__ void __launch_bounds__(kThreads, 2) k_embed_sum(const __grid_constant__ SumArgs a) {
-    // rows in flight (and of the table); more of 16 bytes take so many registers that there are
-    // less warps (16384 x 4096 over 50000 words: 175 us for 162)
-    constexpr int kBatch = kN == 8 ? 4 : 8;
+__global__ void __launch_bounds__(kThreads, kTokens == 32 ? 2 : kAdd && sizeof(T) == 4 ? 3 : 4)
+    k_embed_sum(const __grid_constant__ SumArgs a) {
+    // rows in flight (and of the table). More take so many registers that there are less warps: of 16
+    // bytes (16384 x 4096 over 50000 words: 175 us for 162), and for 8 tokens, where blocks then come
+    // in two turns and a bit (5001 x 1001, added: 33 us for 29)
+    constexpr int kBatch = kN == 8 || kTokens == 8 ? 4 : 8;
     const int lane = threadIdx.x & 31;
     grid_dep_wait();
     grid_dep_launch();
@@ -647,12 +649,11 @@ BackwardLayout backward_layout(uint64_t n, uint64_t vocab, uint64_t dim) {
     while ((vocab >> bits) != 0) ++bits;  // keys 0 to vocab
     L.passes = (bits + 8) / 9;
     L.digit_bits = (bits + L.passes - 1) / L.passes;
-    // A tile a block where a cluster sorts, of up to 2048 tokens while that is enough for all of
-    // them; else whole tiles, as many as it takes.
+    // A tile a block where a cluster sorts, over as many blocks as it may have (2048 tokens x 1024
+    // columns: 17 us, with tiles of 2048 tokens 20); else whole tiles, as many as it takes.
     if (n <= kSortCluster * (uint64_t)kSortTile) {
         const uint64_t rows = (n + kSortThreads - 1) / kSortThreads;
-        L.rows = (uint32_t)std::max((rows + kSortCluster - 1) / kSortCluster,
-                                    std::min<uint64_t>(4, rows));
+        L.rows = (uint32_t)((rows + kSortCluster - 1) / kSortCluster);
         L.per_block = L.rows * kSortThreads;
     } else {
         const uint64_t tiles = (n + kSortTile - 1) / kSortTile;
