@@ -358,3 +358,20 @@ def test_rows_past_two_to_the_32():
     h, _, err, _, _ = scan64(numpy64(x), numpy64(gate), [0, rows], None)
     near(y.cpu(), torch.from_numpy(h), torch.from_numpy(err))
     assert dgc.dgc_read_status(st) == 0 and E > 0
+
+
+@pytest.mark.parametrize("type_", [F32, F16, BF16])
+@pytest.mark.parametrize("nseq", [33, 300, 1023, 1024, 1100, 5000])
+def test_many_sequences(nseq, type_):
+    """Tables that are searched in one, two and three steps, most of whose sequences have no rows; over
+    columns enough for groups of 16 chunks, and over a few."""
+    ends = np.sort(np.random.default_rng(nseq).integers(3, 691, nseq + 1)).tolist()
+    run(700, 520, ends, type_, seed=nseq)
+    run(690, 6, ends, type_, seed=nseq, state=False)
+
+
+@pytest.mark.parametrize("type_", [F32, BF16])
+def test_empty_sequences_alone(type_):
+    """No sequence has a row: states pass through, y, dx and dgate stay as they were."""
+    run(300, 600, [7] * 3001, type_)
+    run(300, 70, [300] * 40, type_)
