@@ -22,7 +22,9 @@
 // ticket, in order, so a block only waits for tiles that running blocks hold; waits are bounded all
 // the same.
 // A ticket is taken late: the further ahead, the less tiles are begun in the order in which they
-// wait for one another (two tiles ahead 149 us).
+// wait for one another (103 us; half a tile earlier 113, two tiles ahead 132). What lies between a
+// tile's arrival and its map counts as much, since others wait for that: where sequences begin and
+// end in it, and the state ahead of it, are looked up a tile ahead.
 //
 // Maps and states are published without flags: the workspace is filled with a bit pattern that no
 // result has, and a reader waits until it has gone.
@@ -30,9 +32,9 @@
 // A sequence's first row has no predecessor: its map is h -> B with B = a h0 + (1 - a) x, kept as
 // A = kReset, so that nothing of what is ahead, infinities and NaNs among it, comes through.
 //
-// The backward pass is the same scan from the end (u_{t+1} -> u_t = a_t u_{t+1} + a_t dy_t). It needs
-// h_{t-1}, which it walks again from the state ahead of each piece of 64 rows that the forward pass
-// left.
+// The backward pass is the same scan from the end (u_{t+1} -> u_t = a_t u_{t+1} + a_t dy_t). It
+// needs h_{t-1}, which it walks again from the state ahead of each piece of 64 rows that the forward
+// pass left.
 #include <algorithm>
 
 #include "rows.cuh"
@@ -505,11 +507,13 @@ struct Landing {
 };
 
 // --------------------------------------------------------------------------------- forward
-// x and gate read once, y written once. 32768 x 2048 bf16: 106 us, 3.8 TB/s. Not bound by HBM but by
-// its steps: some 20 us are waits for the maps of tiles that run at the same time (a timing copy
-// that took zeros for them ran 86), the rest the latency of two walks over the rows, in which the
-// 16 warps that registers and shared memory leave an SM issue in 47% of the clocks. Rows with no
-// border among them and whole columns take a way without tests.
+// x and gate read once, y written once. 32768 x 2048 bf16: 103 us, 3.9 TB/s. Not bound by HBM but by
+// a tile's steps one behind the other, by two blocks of 8 warps an SM (the rows in registers leave
+// room for no more). Timing copies that left steps out: waits for maps 89 us, all of the look-back
+// 84, the sigmoids too 76, the stores too 65. Less registers by computing the sigmoids twice 114; a
+// tile's map published ahead of the wait of the one before it, both tiles' rows in registers, 139.
+// Rows with a border among them take a way of their own; 16001 x 2048 fp16 takes 56 us for 1
+// sequence, 57 for 37 and 62 for 200.
 template <typename T, int kUnit, int kS, int kBlocks, uint32_t kEach>
 __global__ void __launch_bounds__(kThreads, kBlocks) k_scan(const __grid_constant__ ScanArgs a) {
     constexpr int kRows = kWarps * kS;
@@ -693,8 +697,7 @@ __global__ void __launch_bounds__(kThreads) k_scan_few(const __grid_constant__ S
 
 // -------------------------------------------------------------------------------- backward
 // x, gate and dy read once, dx and dgate written once, the states of every 64th row read.
-// 16001 x 2048 fp16 in 37 sequences: 131 us, 2.5 TB/s, bound as k_scan is (three walks over the rows;
-// instructions issued in 43% of the clocks).
+// 16001 x 2048 fp16 in 37 sequences: 103 us, 3.2 TB/s, bound as k_scan is (three walks over the rows).
 template <typename T, int kUnit, int kS, int kBlocks, uint32_t kEach>
 __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_back(const __grid_constant__ ScanArgs a) {
     constexpr int kRows = kWarps * kS;
@@ -871,7 +874,7 @@ struct Form {
     static constexpr int kBackS = kPiece / kWarps, kBackBlocks = 2;
 };
 
-// Columns from which on 16 chunks are a group (32768 x 2048: 107 us for 112), with two maps for a
+// Columns from which on 16 chunks are a group (32768 x 2048: 5 us less), with two maps for a
 // warp to collect. Below, where a tile of columns has most of the blocks to itself, 32: there the
 // chain of groups counts more (16384 x 64: 10 us for 12).
 constexpr uint64_t kWideCols = 8 * kCols;
