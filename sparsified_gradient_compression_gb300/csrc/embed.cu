@@ -456,13 +456,20 @@ struct Cols {
     }
 };
 
+// As many as there is room for without spilling (16384 x 1001 fp16: 72 us with 3, 80 with 2).
+template <typename T, int kTokens, int kN, bool kAdd>
+constexpr int sum_blocks_of_sm() {
+    if (kTokens == 8) return kAdd && sizeof(T) == 4 ? 3 : 4;
+    return kN == 4 && !kAdd && sizeof(T) == 2 ? 3 : 2;
+}
+
 // Bound by HBM: dy read once, the table written once (read and written where it is added to).
 // 16384 x 4096 bf16 into 50000 rows: 133 us, 7.2 TB/s; the sort ahead and the join behind are
 // latency.
 // A word met up to kTokens times is summed by the warp in whose chunk it starts; a longer run is cut
 // at the chunks' borders. kN: a lane's columns.
 template <typename T, int kTokens, int kN, bool kWide, bool kAdd>
-__global__ void __launch_bounds__(kThreads, kTokens == 32 ? 2 : kAdd && sizeof(T) == 4 ? 3 : 4)
+__global__ void __launch_bounds__(kThreads, sum_blocks_of_sm<T, kTokens, kN, kAdd>())
     k_embed_sum(const __grid_constant__ SumArgs a) {
     // rows in flight (and of the table). More take so many registers that there are less warps: of 16
     // bytes (16384 x 4096 over 50000 words: 175 us for 162), and for 8 tokens, where blocks then come
