@@ -200,11 +200,19 @@ __device__ __forceinline__ void empty_sequences(const ScanArgs& a, uint32_t tile
         const uint32_t q = q0 + lane;
         const int64_t b = q < a.nseq ? a.offsets[q] : 0, e = q < a.nseq ? a.offsets[q + 1] : 1;
         bad |= q < a.nseq && (b > e || b < 0 || e > (int64_t)a.rows);
-        uint32_t todo = __ballot_sync(kFull, b == e);
-        for (; to && todo; todo &= todo - 1) {
-            const uint32_t s = q0 + __ffs(todo) - 1;
-            store_state(to, ld_to, s, col, n,
-                        from ? load_state(from, ld_from, s, col, n) : make_float2(0.0f, 0.0f));
+        uint32_t todo = to && to != from ? __ballot_sync(kFull, b == e) : 0;
+        while (todo) {  // four at once, so that no store waits for one load alone
+            uint32_t s[4];
+            float2 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i, todo &= todo - 1) {
+                s[i] = todo ? q0 + __ffs(todo) - 1 : a.nseq;
+                v[i] = from && s[i] < a.nseq ? load_state(from, ld_from, s[i], col, n)
+                                             : both(0.0f);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (s[i] < a.nseq) store_state(to, ld_to, s[i], col, n, v[i]);
         }
     }
     if (tile == 0 && bad) report(a.status, DGC_EINVAL);
@@ -632,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan(const __grid_constan
     all_empty_sequences(a, a.h0, a.ldh0, a.h_last, a.ldh_last);
 }
 
-// Up to kWarps * kS rows: a block a column tile. For a step of a model that answers, a start and a
+// Up to kWarps * kS rows: the first block of a column tile. For a step of a model that answers, a start and a
 // round trip to memory.
 template <typename T, bool kPair, int kS>
 __global__ void __launch_bounds__(kThreads) k_scan_few(const __grid_constant__ ScanArgs a) {
@@ -642,6 +650,10 @@ __global__ void __launch_bounds__(kThreads) k_scan_few(const __grid_constant__ S
     int32_t *starts = starts_of[warp], *ends = ends_of[warp];
     grid_dep_wait();
     grid_dep_launch();
+    if (blockIdx.y) {
+        empty_sequences(a, blockIdx.x, blockIdx.y, gridDim.y, a.h0, a.ldh0, a.h_last, a.ldh_last);
+        return;
+    }
     const Spot at(a, 0, blockIdx.x, kWarps * kS, kS);
     const T* gate = static_cast<const T*>(a.gate) + (uint64_t)at.first * a.ldg + at.lane_col;
     const T* x = static_cast<const T*>(a.x) + (uint64_t)at.first * a.ldx + at.lane_col;
@@ -660,7 +672,7 @@ __global__ void __launch_bounds__(kThreads) k_scan_few(const __grid_constant__ S
         const bool here = a.h0 && marks.starts_at(s);
         given[s] = load_state(a.h0, a.ldh0, here ? starts[s] : 0, at.lane_col, here ? at.n : 0);
     }
-    empty_sequences(a, blockIdx.x, 0, 1, a.h0, a.ldh0, a.h_last, a.ldh_last);
+    empty_sequences(a, blockIdx.x, 0, gridDim.y, a.h0, a.ldh0, a.h_last, a.ldh_last);
     float2 A[kS], B[kS];
     Map m = identity();
 #pragma unroll
@@ -997,8 +1009,12 @@ int recurrence(const dgc_matrix* x, const dgc_matrix* gate, const int64_t* offse
             auto few = a.rows <= kFew / 2
                            ? (pair ? k_scan_few<T, true, 8> : k_scan_few<T, false, 8>)
                            : (pair ? k_scan_few<T, true, 16> : k_scan_few<T, false, 16>);
-            return launch_rows_kernel(few, dim3((unsigned)((mx.cols + kCols - 1) / kCols)),
-                                      kThreads, s, a);
+            // blocks of their own for sequences without rows, where there are many: as the slots of
+            // a model that answers
+            const uint64_t parts = umin64(64, ((uint64_t)nseq + kThreads - 1) / kThreads);
+            return launch_rows_kernel(
+                few, dim3((unsigned)((mx.cols + kCols - 1) / kCols), (unsigned)parts), kThreads, s,
+                a);
         }
         // (rows off 16-byte boundaries: groups of 32 chunks, for one kernel less)
         if (wide && mx.cols >= kWideCols)

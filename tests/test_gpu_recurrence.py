@@ -375,3 +375,30 @@ def test_empty_sequences_alone(type_):
     """No sequence has a row: states pass through, y, dx and dgate stay as they were."""
     run(300, 600, [7] * 3001, type_)
     run(300, 70, [300] * 40, type_)
+
+
+@pytest.mark.parametrize("type_", [F32, BF16])
+@pytest.mark.parametrize("rows", [0, 90, 400])
+def test_slots_of_a_model_that_answers(rows, type_):
+    """One token for some of 1024 slots, or none; the others keep their state, which may be kept where
+    it is."""
+    slots, cols = 1024, 130
+    order = np.random.default_rng(rows).permutation(slots)[:rows]
+    with_row = np.zeros(slots, dtype=np.int64)
+    with_row[order] = 1
+    ends = np.concatenate([[0], np.cumsum(with_row)]).tolist()
+    if rows:
+        run(rows, cols, ends, type_, seed=rows)
+    gen = generator(rows)
+    x, gate = normal(gen, rows, cols, type_), normal(gen, rows, cols, type_)
+    h0 = normal(gen, slots, cols, F32)
+    off = torch.tensor(ends, dtype=torch.int64, device="cuda")
+    y, h_last = buffer(rows, cols, type_), buffer(slots, cols, F32)
+    st, ws = status_word(), workspace(dgc.dgc_recurrence_workspace(rows, cols))
+    dgc.dgc_recurrence(x, gate, off, h0, y, h_last, None, st, ws)
+    empty = torch.from_numpy(with_row == 0).cuda()
+    assert torch.equal(h_last[empty], h0[empty])
+    again = buffer(rows, cols, type_)
+    dgc.dgc_recurrence(x, gate, off, h0, again, h0, None, st, ws)
+    assert torch.equal(h0, h_last) and torch.equal(bits(again), bits(y))
+    assert dgc.dgc_read_status(st) == 0
