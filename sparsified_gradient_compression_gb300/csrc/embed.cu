@@ -22,7 +22,6 @@ namespace dgc {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSteps = 4;
 
 struct Tokens {
     const void* p;
@@ -33,6 +32,13 @@ struct Tokens {
 };
 
 // --------------------------------------------------------------------------------- lookup
+constexpr uint32_t kUnknown = 0xFFFFFFFFu;  // no word
+// Pieces of 16 bytes of the result that a thread has under way, where 8 blocks are to be on an SM: more
+// pieces take registers from other blocks (16384 x 2048 binary32: 33 us with 4 pieces, 31 with 3; to
+// fp16 21.5 with 4, 19.7 with 2; 16384 x 4096 bf16 34.2 with 4, 32.5 with 3, although 12 bytes a
+// thread are spilled for it).
+template <typename S, typename D>
+constexpr int kStepsOf = sizeof(S) > sizeof(D) ? 2 : 3;
 struct EmbedArgs {
     const void* table;
     void* out;
@@ -45,12 +51,14 @@ struct EmbedArgs {
 };
 
 // Bound by HBM: the result is written once, each row of the table that is met is read from HBM
-// once as far as L2 holds it. 16384 x 4096 bf16 from a table of 50000 rows: 34 us, 5.5 TB/s.
+// once as far as L2 holds it. 16384 x 4096 bf16 from a table of 50000 rows: 32.5 us, 5.7 TB/s.
 // What is lost is the start and two latencies in a row (the word, then its row). One short-lived
-// block a tile: blocks that stay and look up the next tile's words ahead took 39 us at 6 an SM, 51
-// at 4.
+// block a tile: blocks that stay and look up the next tile's words ahead took 39 us at 6 an SM and
+// 51 at 4, with the table's pieces copied to shared memory ahead 53.
 template <typename S, typename D, bool kWide>
-__global__ void __launch_bounds__(kThreads) k_embed(const __grid_constant__ EmbedArgs a) {
+__global__ void __launch_bounds__(kThreads, kWide ? 8 : 1)
+    k_embed(const __grid_constant__ EmbedArgs a) {
+    constexpr int kSteps = kStepsOf<S, D>;
     constexpr int kN = 16 / sizeof(D);
     grid_dep_wait();
     grid_dep_launch();
@@ -60,21 +68,20 @@ __global__ void __launch_bounds__(kThreads) k_embed(const __grid_constant__ Embe
     for (uint64_t tile = blockIdx.x; tile * kTile < a.walk.total; tile += gridDim.x) {
         Pieces<kThreads, kSteps> at(a.walk, tile);
         const uint64_t first = tile * kTile + threadIdx.x;
-        uint64_t row[kSteps];
-        uint32_t col[kSteps], left[kSteps];
-        int64_t word[kSteps];
+        uint32_t row[kSteps], col[kSteps], left[kSteps], word[kSteps];
         Packed<S, kN> p[kSteps];
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-            row[i] = at.row;
+            row[i] = (uint32_t)at.row;
             col[i] = at.at * kN;
             left[i] = first + i * kThreads < a.walk.total ? a.cols - col[i] : 0;
-            word[i] = left[i] ? a.tokens[row[i]] : 0;
+            const int64_t w = left[i] ? a.tokens[row[i]] : 0;
+            word[i] = w >= 0 && w < (int64_t)a.vocab ? (uint32_t)w : kUnknown;
             at.next(a.walk);
         }
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-            const bool known = word[i] >= 0 && word[i] < (int64_t)a.vocab;
+            const bool known = word[i] != kUnknown;
             if (!known) report(a.status, DGC_EINVAL);
             p[i] = load_piece<kWide, S, kN, false>(
                 table + (known ? (uint64_t)word[i] : 0) * a.ldt + col[i], known ? left[i] : 0);
@@ -86,8 +93,7 @@ __global__ void __launch_bounds__(kThreads) k_embed(const __grid_constant__ Embe
 #pragma unroll
             for (int j = 0; j < kN; ++j) f[j] *= a.scale;
             // an unknown word's row is 0 whatever the scale
-            const bool known = word[i] >= 0 && word[i] < (int64_t)a.vocab;
-            if (!known)
+            if (word[i] == kUnknown)
 #pragma unroll
                 for (int j = 0; j < kN; ++j) f[j] = 0.0f;
             store_piece<kWide, D, kN>(out + row[i] * a.ldo + col[i], pack<D, kN>(f), left[i]);
@@ -769,7 +775,8 @@ int check_tokens(const dgc_tensor* t, Tokens* out) {
 
 template <typename S, typename D>
 int launch_embed(const EmbedArgs& a, bool wide, cudaStream_t s) {
-    const uint64_t tiles = (a.walk.total + kThreads * kSteps - 1) / (kThreads * kSteps);
+    constexpr int kTile = kThreads * kStepsOf<S, D>;
+    const uint64_t tiles = (a.walk.total + kTile - 1) / kTile;
     const dim3 grid((unsigned)umin64(tiles, 1u << 30));
     return launch_rows_kernel(wide ? k_embed<S, D, true> : k_embed<S, D, false>, grid, kThreads, s,
                               a);
