@@ -193,3 +193,75 @@ def test_rows_past_two_to_the_32():
     dgc.dgc_embed_backward(tok, out, 1.0, None, dt, True, st, ws)
     assert torch.equal(dt[tok], out.float() * 2)
     assert dgc.dgc_read_status(st) == 0
+
+
+def chunk_tokens(n, vocab, d):
+    """How many sorted tokens a warp of the gradient sums, 8 or 32, read off the workspace's size: the
+    sort's two lists and its counts, the list of chunks, two rows of sums for each."""
+    def up(x):
+        return -(-x // 256) * 256
+
+    def size(tokens):
+        chunks = -(-n // tokens)
+        return (2 * up(8 * n) + up(256 * 512 * 4) + up(4 * (chunks + 1))
+                + up(chunks * 2 * (-(-d // 4) * 4) * 4))
+
+    found = [t for t in (8, 32) if size(t) == dgc.dgc_embed_backward_workspace(n, vocab, d)]
+    assert len(found) == 1, (n, vocab, d)
+    return found[0]
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("type_", [F32, F16, BF16])
+@pytest.mark.parametrize("kind", ["any", "one", "head", "runs"])
+def test_gradient_by_chunks_of_32(kind, type_, accumulate):
+    """Sizes of which a warp sums 32 tokens: four columns a lane on and off 16-byte boundaries, eight
+    of 16-bit entries."""
+    for n, vocab, d, padding in ((8192, 200, 1280, None), (8190, 200, 1283, 199),
+                                 (16384, 400, 2048, None), (16301, 5000, 2056, 4999)):
+        assert chunk_tokens(n, vocab, d) == 32
+        gradient(n, vocab, d, type_, kind, 1.5, accumulate, padding=padding)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("pad,table_pad", [("odd", 0), (0, "odd"), ("odd", "odd"),
+                                           ("packed", "packed")])
+def test_gradient_strides_by_chunks_of_32(pad, table_pad, accumulate):
+    for type_ in (F32, F16, BF16):
+        for kind in ("head", "runs"):
+            gradient(8100, 210, 1301, type_, kind, 1.0, accumulate, pad=pad, table_pad=table_pad)
+
+
+def whole_numbers(n, vocab, d, kind, type_, accumulate, padding=None):
+    """Gradients of small whole numbers, whose sums are exact in any order: equal bit for bit."""
+    gen = generator(n + vocab)
+    tok = tokens_of(kind, n, vocab, gen)
+    dy = torch.randint(-4, 5, (n, d), generator=gen, device="cuda").to(type_)
+    dt = torch.randint(-9, 10, (vocab, d), generator=gen, device="cuda").float()
+    use = tok != (-1 if padding is None else padding)
+    want = (dt.double() if accumulate else torch.zeros(vocab, d, device="cuda").double())
+    want.index_add_(0, tok[use], 2.0 * dy[use].double())
+    assert want.abs().max() < 2**24
+    st, ws = status_word(), workspace(dgc.dgc_embed_backward_workspace(n, vocab, d))
+    dgc.dgc_embed_backward(tok, dy, 2.0, padding, dt, accumulate, st, ws)
+    assert torch.equal(dt.double(), want)
+    assert dgc.dgc_read_status(st) == 0
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("kind", ["any", "one", "head", "runs"])
+@pytest.mark.parametrize("n,vocab,d", [(8192, 200, 1280), (8190, 200, 1283), (16384, 400, 2048),
+                                       (5001, 300, 1001), (40000, 3000, 260)])
+def test_whole_numbers_are_exact(n, vocab, d, kind, accumulate):
+    """No row is left out or taken twice, however often its word is met."""
+    for type_ in (F32, BF16):
+        whole_numbers(n, vocab, d, kind, type_, accumulate, padding=vocab // 3)
+
+
+@pytest.mark.parametrize("n", [2**20 + 1, 2**21 + 12345])
+def test_a_sort_of_several_tiles_a_block(n):
+    """More tokens than 256 blocks have in a tile of 4096 each: a block goes on with its digits'
+    places from tile to tile."""
+    for vocab, d, kind in ((300000, 3, "any"), (500, 4, "head"), (1 << 20, 1, "any")):
+        whole_numbers(n, vocab, d, kind, BF16, False, padding=7)
+        whole_numbers(n, vocab, d, kind, F32, True)

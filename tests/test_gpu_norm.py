@@ -217,3 +217,105 @@ def test_gradient_against_differences():
     terms = (dx.double() * v.double()).abs().sum() + (dg.double() * vg.double()).abs().sum()
     got = (dx.double() * v.double()).sum() + (dg.double() * vg.double()).sum()
     assert abs(got.item() - slope) <= 1e-5 * terms.item()
+
+
+# Rows enough for every block to come round many times, the statistics' loads of 32 rows among them
+# (304 blocks of 8, 4 or 1 rows at once, or 152 of one row of 16 warps; the forward pass 456 of them).
+MANY = [(50000, 520), (90000, 250), (14000, 2041), (14000, 4096), (6000, 4104), (5600, 8184)]
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("type_", [F32, BF16])
+@pytest.mark.parametrize("m,d", MANY)
+def test_forward_of_many_rows(m, d, type_, in_place):
+    forward(m, d, type_, in_place=in_place)
+
+
+@pytest.mark.parametrize("type_", [F32, F16, BF16])
+@pytest.mark.parametrize("m,d", [(20000, 251), (6000, 2041), (3000, 4101)])
+def test_forward_of_many_rows_off_boundaries(m, d, type_):
+    forward(m, d, type_, pad="packed")
+    forward(m, d, type_, pad="odd", in_place=True)
+
+
+@pytest.mark.parametrize("type_", [F32, BF16])
+@pytest.mark.parametrize("m,d", MANY)
+def test_backward_of_many_rows(m, d, type_):
+    for alias in (None, "dy", "x", "r"):
+        backward(m, d, type_, alias=alias)
+
+
+@pytest.mark.parametrize("type_", [F32, F16, BF16])
+@pytest.mark.parametrize("m,d", [(20000, 251), (6000, 2041), (4000, 4101)])
+def test_backward_of_many_rows_off_boundaries(m, d, type_):
+    backward(m, d, type_, pad="packed")
+    backward(m, d, type_, pad="odd", alias="x")
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("pad", [0, "odd"])
+@pytest.mark.parametrize("type_", [F32, F16, BF16])
+@pytest.mark.parametrize("m,d", [(50000, 520), (14000, 2042), (14000, 4096), (6000, 4104),
+                                 (6000, 8184), (1000, 9000), (3, 250), (257, 60)])
+def test_whole_numbers_are_exact(m, d, type_, pad, accumulate):
+    """Rows of whole numbers whose deviations add up to nothing, a power of two as the reciprocal
+    deviation: every sum of the weights' gradients is a whole number below 2^24, exact in any order.
+    No row is left out, taken twice or given another one's statistics."""
+    gen = generator(m + d)
+    row, col = torch.arange(m, device="cuda")[:, None], torch.arange(d, device="cuda")
+    dev = (1 - 2 * (col % 2)) * ((col // 2 + row) % 3 + 1)
+    mean, rstd = (row % 7 - 3).double(), 2.0 ** (row % 3).double()
+    x, dy = buffer(m, d, type_, pad), buffer(m, d, type_, pad)
+    x.copy_(dev + mean)
+    dy.copy_(torch.randint(-3, 4, (m, d), generator=gen, device="cuda"))
+    dgamma, dbeta = (torch.randint(-9, 10, (d,), generator=gen, device="cuda").float()
+                     for _ in range(2))
+    want = [t.double() if accumulate else torch.zeros(d, device="cuda").double()
+            for t in (dgamma, dbeta)]
+    want[0] = want[0] + (dy.double() * dev.double() * rstd).sum(0)
+    want[1] = want[1] + dy.double().sum(0)
+    assert 36 * m + 9 < 2**24
+    ws = workspace(dgc.dgc_layer_norm_backward_workspace(m, d))
+    dx, gamma = buffer(m, d, type_, pad), torch.ones(d, device="cuda")
+    dgc.dgc_layer_norm_backward(dy, x, gamma, mean[:, 0].float(), rstd[:, 0].float(), None, dx,
+                                dgamma, dbeta, accumulate, ws)
+    assert torch.equal(dgamma.double(), want[0]) and torch.equal(dbeta.double(), want[1])
+
+
+@pytest.mark.parametrize("cols,ld", [(520, 1 << 24), (521, (1 << 24) + 1), (8200, 1 << 24)])
+def test_rows_past_two_to_the_32(cols, ld):
+    """Rows far apart, the last of them behind 2^32 entries: on and off 16-byte boundaries, and the
+    kernels of long rows."""
+    m = 300
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    flat = torch.empty(m * ld, dtype=BF16, device="cuda").view(m, ld)
+    x, y, dy, r, dx = (flat[:, i * 65536:i * 65536 + cols] for i in range(5))
+    gen = generator(40)
+    for t in (x, dy, r):
+        t.copy_(torch.randn(m, cols, generator=gen, device="cuda"))
+    near_x, near_dy, near_r = x.contiguous(), dy.contiguous(), r.contiguous()
+    gamma, beta = weights(cols, gen), weights(cols, gen)
+    mu, rs = torch.empty(m, device="cuda"), torch.empty(m, device="cuda")
+    dgc.dgc_layer_norm(x, gamma, beta, EPS, y, mu, rs)
+    dg, db = torch.empty_like(gamma), torch.empty_like(gamma)
+    ws = workspace(dgc.dgc_layer_norm_backward_workspace(m, cols))
+    dgc.dgc_layer_norm_backward(dy, x, gamma, mu, rs, r, dx, dg, db, False, ws)
+    X, DY, G = near_x.double(), near_dy.double(), gamma.double()
+    avg, _, rstd = statistics(X)
+    xhat, g = (X - avg) * rstd, DY * G
+    h = xhat.abs()
+    near(y, xhat * G + beta.double(), (L * (2 * h + 1) + 4 * E * h) * G.abs()
+         + 4 * E * beta.double().abs())
+    m1, m2 = g.mean(1, keepdim=True), (g * xhat).mean(1, keepdim=True)
+    a1, a2 = g.abs().mean(1, keepdim=True), (g * xhat).abs().mean(1, keepdim=True)
+    want = rstd * (g - m1 - xhat * m2)
+    # as in backward() above, and the given rstd and mean are themselves off by L
+    error = rstd * (2 * L * a1 + h * L * (4 * a2 + 2 * a1) + 2 * L * (2 * h + 1) * m2.abs()
+                    + (2 * L + 8 * E) * (g.abs() + m1.abs() + h * m2.abs()))
+    R = near_r.double()
+    near(dx, want + R, error + 2 * E * R.abs() + 2 * E * want.abs())
+    chain = (m + 16) * E
+    near(dg, (DY * xhat).sum(0), chain * (DY * xhat).abs().sum(0)
+         + (2 * L * (2 * h + 1) * DY.abs()).sum(0))
+    near(db, DY.sum(0), chain * DY.abs().sum(0))

@@ -402,3 +402,47 @@ def test_slots_of_a_model_that_answers(rows, type_):
     dgc.dgc_recurrence(x, gate, off, h0, again, h0, None, st, ws)
     assert torch.equal(h0, h_last) and torch.equal(bits(again), bits(y))
     assert dgc.dgc_read_status(st) == 0
+
+
+def ragged(rows, n, seed):
+    """n packed sequences of unequal length, one of them empty, over all rows."""
+    cuts = np.sort(np.random.default_rng(seed).integers(1, rows, n - 2)).tolist()
+    return [0] + cuts[:n // 2] + cuts[n // 2 - 1:n // 2] + cuts[n // 2:] + [rows]
+
+
+# Tiles enough for a block to take several of them, chunks enough for several groups: of 16 chunks
+# from 512 columns on, of 32 below (chunks have 128 rows forward in 16 bits, else 64).
+@pytest.mark.parametrize("type_", [F32, F16, BF16])
+@pytest.mark.parametrize("rows,cols", [(5000, 1024), (9001, 576), (20000, 130)])
+def test_several_groups_and_tiles(rows, cols, type_):
+    # a memory of a thousand rows and more: the state goes through every group
+    run(rows, cols, [0, rows], type_, gate_mean=8.0, gate_sigma=0.5)
+    run(rows, cols, ragged(rows, 40, cols), type_, gate_mean=5.0, alias=True)
+    run(rows, cols, [70, 900, 900, 2048, rows - 3], type_, state=False, gate_mean=6.0)
+
+
+@pytest.mark.parametrize("pad", [1, "odd", "packed"])
+@pytest.mark.parametrize("type_", [F32, BF16])
+def test_several_groups_of_strided_rows(type_, pad):
+    run(9001, 571, [0, 4000, 9001], type_, pad=pad, gate_mean=7.0, state_pad=pad)
+    run(6000, 66, ragged(6000, 9, 1), type_, pad=pad, gate_mean=7.0, alias=True)
+
+
+@pytest.mark.parametrize("type_", [F32, BF16])
+@pytest.mark.parametrize("rows,cols", [(5000, 1024), (20000, 130)])
+def test_in_place_over_several_groups(rows, cols, type_):
+    """y on x or on gate, h_last on h0, over many tiles a block: the bits of results elsewhere."""
+    gen = generator(rows)
+    ends = ragged(rows, 30, 2)
+    x, gate = normal(gen, rows, cols, type_), normal(gen, rows, cols, type_, mean=6.0)
+    h0 = normal(gen, 30, cols, F32)
+    off, st = torch.tensor(ends, device="cuda"), status_word()
+    ws = workspace(dgc.dgc_recurrence_workspace(rows, cols))
+    y, last = buffer(rows, cols, type_), buffer(30, cols, F32)
+    dgc.dgc_recurrence(x, gate, off, h0, y, last, None, st, ws)
+    for out in (0, 1):
+        a = [x.clone(), gate.clone()]
+        h = h0.clone()
+        dgc.dgc_recurrence(a[0], a[1], off, h, a[out], h, None, st, ws)
+        assert torch.equal(bits(a[out]), bits(y.clone())) and torch.equal(h, last)
+    assert dgc.dgc_read_status(st) == 0
