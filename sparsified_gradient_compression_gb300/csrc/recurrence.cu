@@ -162,7 +162,7 @@ struct Marks {
             if (step > 32) i0 = first_from(a.offsets, i0, min(step, n - i0),
                                             (int64_t)begin);
         }
-        for (;; i0 += 32) {
+        for (;;) {
             const uint32_t i = i0 + lane;
             const uint32_t off = i >= n ? kNoRow : step > 1 ? offset_at(a, i) : mine;
             const bool here = i < n && off >= begin && off <= stop;
@@ -182,6 +182,14 @@ struct Marks {
                 bits |= __reduce_or_sync(kFull, b);
             }
             if (step == 1 || !__all_sync(kFull, off <= stop)) break;
+            i0 += 32;
+            // Sequences without rows share an offset: after 32 of them the others are passed by a
+            // search, up to the last one. Other blocks wait for what comes behind this. (32 at a time,
+            // a step for 100 of 4096 slots of 1024 columns, the others idle behind them, took 72 us
+            // for 15, for 100 of 2^20 slots 25 ms.)
+            const uint32_t top = __shfl_sync(kFull, off, 31);
+            if (__all_sync(kFull, off == top))
+                i0 = max(i0, first_from(a.offsets, i0, n - i0, (int64_t)top + 1) - 1);
         }
         __syncwarp();
     }
@@ -217,8 +225,7 @@ __device__ __forceinline__ void empty_sequences(const ScanArgs& a, uint32_t tile
     }
     if (tile == 0 && bad) report(a.status, DGC_EINVAL);
 }
-// The same by all blocks, at their end: other blocks wait for nothing that comes behind it, however
-// many sequences there are.
+// The same by all blocks, at their end: no block waits for it.
 __device__ __forceinline__ void all_empty_sequences(const ScanArgs& a, const float* from,
                                                     uint64_t ld_from, float* to, uint64_t ld_to) {
     const uint32_t parts = max(1u, gridDim.x / a.tiles), part = blockIdx.x / a.tiles;
@@ -238,7 +245,7 @@ __device__ __forceinline__ Tile tile_of(const ScanArgs& a, uint32_t ticket) {
     return {order, ticket - order * a.tiles};
 }
 __device__ __forceinline__ Tile first_tile(const ScanArgs& a, uint32_t* slot) {
-    if (!a.ticket) return {0, blockIdx.x};
+    if (!a.ticket) return {blockIdx.x < a.tiles ? 0 : ~0u, blockIdx.x};
     if (threadIdx.x == 0) *slot = atomicAdd(a.ticket, 1u);
     __syncthreads();
     const Tile t = tile_of(a, *slot);
@@ -546,11 +553,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan(const __grid_constan
     const uint32_t valid0 = offset_at(a, 0), valid1 = min(a.rows, offset_at(a, a.nseq));
     const uint32_t mine = landmark(a);
     uint32_t turn = 0;
-    auto look_marks = [&] {
-        const Spot at(a, t.order, t.tile, kRows, kS);
+    auto look_marks = [&](uint32_t order) {
+        const Spot at(a, order, t.tile, kRows, kS);
         return Marks<kS>(a, at.first, mine, starts_of[turn & 1][warp], ends_of[turn & 1][warp]);
     };
-    Marks<kS> marks_next = look_marks();
+    // (a block without a tile has come for the sequences without rows)
+    Marks<kS> marks_next = look_marks(min(t.order, a.chunks - 1));
     while (t.order < a.chunks) {
         const uint32_t chunk = t.order, tile = t.tile;
         const Spot at(a, chunk, tile, kRows, kS);
@@ -593,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan(const __grid_constan
         LookBack<kEach> back(a, chunk, tile, warp, fresh);
         t = tile_of(a, board.next);
         fetch();
-        if (t.order < a.chunks) marks_next = look_marks();
+        if (t.order < a.chunks) marks_next = look_marks(t.order);
         back.finish(a, board, warp);
         __syncthreads();
         float2 h = before(enter<kEach>(a, board, chunk, tile, warp, before, m, fresh));
@@ -740,11 +748,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_back(const __grid_co
     const uint32_t valid0 = offset_at(a, 0), valid1 = min(a.rows, offset_at(a, a.nseq));
     const uint32_t mine = landmark(a);
     uint32_t turn = 0;
-    auto look_marks = [&] {
-        const Spot at(a, a.chunks - 1 - t.order, t.tile, kRows, kS);
+    auto look_marks = [&](uint32_t order) {
+        const Spot at(a, a.chunks - 1 - order, t.tile, kRows, kS);
         return Marks<kS>(a, at.first, mine, starts_of[turn & 1][warp], ends_of[turn & 1][warp]);
     };
-    Marks<kS> marks_next = look_marks();
+    // (a block without a tile has come for the sequences without rows)
+    Marks<kS> marks_next = look_marks(min(t.order, a.chunks - 1));
     while (t.order < a.chunks) {
         const uint32_t order = t.order, tile = t.tile;
         const uint32_t chunk = a.chunks - 1 - order;
@@ -826,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_scan_back(const __grid_co
         __syncwarp();
         t = tile_of(a, board.next);
         fetch();
-        if (t.order < a.chunks) marks_next = look_marks();
+        if (t.order < a.chunks) marks_next = look_marks(t.order);
         back.finish(a, board, place);
         __syncthreads();
         // u of the row behind
@@ -923,6 +932,9 @@ int check_state(const dgc_matrix* m, uint64_t nseq, uint64_t cols, const float**
     return DGC_OK;
 }
 
+// By how many blocks a column tile's sequences without rows are looked through.
+uint64_t empty_parts(uint64_t nseq) { return umin64(64, (nseq + kThreads - 1) / kThreads); }
+
 template <typename T, int kUnit, int kS, int kOperands, int kBlocks, uint32_t kEach>
 int launch_scan(void (*kernel)(ScanArgs), ScanArgs a, void* ws, int sms, cudaStream_t s) {
     const ScanLayout L = scan_layout(a.rows, a.cols, kWarps * kS, kEach);
@@ -948,6 +960,10 @@ int launch_scan(void (*kernel)(ScanArgs), ScanArgs a, void* ws, int sms, cudaStr
         if (rc) return rc;
         blocks = (uint32_t)umin64((uint64_t)L.tiles * L.chunks, (uint64_t)sms * kBlocks);
     }
+    // Few rows of many sequences: more blocks than tiles, for the states of those without rows (100 rows
+    // and 2^20 of them, 16 columns, backward: 0.5 ms for 13).
+    blocks = std::max(blocks,
+                      (uint32_t)umin64(L.tiles * empty_parts(a.nseq), (uint64_t)sms * kBlocks));
     return launch_shared_kernel(kernel, dim3(blocks), kThreads,
                                 Landing<T, kUnit, kS, kOperands>::kBytes, s, a);
 }
@@ -1011,22 +1027,23 @@ int recurrence(const dgc_matrix* x, const dgc_matrix* gate, const int64_t* offse
                            : (pair ? k_scan_few<T, true, 16> : k_scan_few<T, false, 16>);
             // blocks of their own for sequences without rows, where there are many: as the slots of
             // a model that answers
-            const uint64_t parts = umin64(64, ((uint64_t)nseq + kThreads - 1) / kThreads);
-            return launch_rows_kernel(
-                few, dim3((unsigned)((mx.cols + kCols - 1) / kCols), (unsigned)parts), kThreads, s,
-                a);
+            return launch_rows_kernel(few,
+                                      dim3((unsigned)((mx.cols + kCols - 1) / kCols),
+                                           (unsigned)empty_parts(a.nseq)),
+                                      kThreads, s, a);
         }
         // (rows off 16-byte boundaries: groups of 32 chunks, for one kernel less)
         if (wide && mx.cols >= kWideCols)
-            return launch_scan<T, 16, kS, 2, kBlocks, 2>(k_scan<T, 16, kS, kBlocks, 2>, a, ws,
-                                                        sms, s);
+            return launch_scan<T, 16, kS, 2, kBlocks, 2>(
+                k_scan<T, 16, kS, kBlocks, 2>, a, ws, sms, s);
         if (wide)
-            return launch_scan<T, 16, kS, 2, kBlocks, 4>(k_scan<T, 16, kS, kBlocks, 4>, a, ws,
-                                                        sms, s);
+            return launch_scan<T, 16, kS, 2, kBlocks, 4>(
+                k_scan<T, 16, kS, kBlocks, 4>, a, ws, sms, s);
         if (pair)
-            return launch_scan<T, kTwo, kS, 2, kBlocks, 4>(k_scan<T, kTwo, kS, kBlocks, 4>, a, ws,
-                                                          sms, s);
-        return launch_scan<T, 0, kS, 2, kBlocks, 4>(k_scan<T, 0, kS, kBlocks, 4>, a, ws, sms, s);
+            return launch_scan<T, kTwo, kS, 2, kBlocks, 4>(
+                k_scan<T, kTwo, kS, kBlocks, 4>, a, ws, sms, s);
+        return launch_scan<T, 0, kS, 2, kBlocks, 4>(
+            k_scan<T, 0, kS, kBlocks, 4>, a, ws, sms, s);
     });
 }
 
@@ -1120,14 +1137,15 @@ extern "C" int dgc_recurrence_backward(const dgc_matrix* dy, const dgc_matrix* x
         constexpr int kS = Form<T>::kBackS, kBlocks = Form<T>::kBackBlocks, kTwo = 2 * sizeof(T);
         // (rows off 16-byte boundaries: groups of 32 chunks, for one kernel less)
         if (wide && mx.cols >= kWideCols)
-            return launch_scan<T, 16, kS, 3, kBlocks, 2>(k_scan_back<T, 16, kS, kBlocks, 2>, a, ws,
-                                                        sms, s);
+            return launch_scan<T, 16, kS, 3, kBlocks, 2>(
+                k_scan_back<T, 16, kS, kBlocks, 2>, a, ws, sms, s);
         if (wide)
-            return launch_scan<T, 16, kS, 3, kBlocks, 4>(k_scan_back<T, 16, kS, kBlocks, 4>, a, ws,
-                                                        sms, s);
+            return launch_scan<T, 16, kS, 3, kBlocks, 4>(
+                k_scan_back<T, 16, kS, kBlocks, 4>, a, ws, sms, s);
         if (pair)
-            return launch_scan<T, kTwo, kS, 3, kBlocks, 4>(k_scan_back<T, kTwo, kS, kBlocks, 4>, a, ws,
-                                                          sms, s);
-        return launch_scan<T, 0, kS, 3, kBlocks, 4>(k_scan_back<T, 0, kS, kBlocks, 4>, a, ws, sms, s);
+            return launch_scan<T, kTwo, kS, 3, kBlocks, 4>(
+                k_scan_back<T, kTwo, kS, kBlocks, 4>, a, ws, sms, s);
+        return launch_scan<T, 0, kS, 3, kBlocks, 4>(
+            k_scan_back<T, 0, kS, kBlocks, 4>, a, ws, sms, s);
     });
 }
