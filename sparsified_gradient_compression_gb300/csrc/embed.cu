@@ -462,11 +462,16 @@ struct Cols {
     }
 };
 
-// As many as there is room for without spilling (16384 x 1001 fp16: 72 us with 3, 80 with 2).
-template <typename T, int kTokens, int kN, bool kAdd>
+// Blocks an SM, at least: as many as there is room for without spilling, but for one form of float16.
+// Off 16-byte boundaries, with chunks of 32 tokens written (16384 x 1001 into 32000 rows) and with chunks
+// of 8 added (5001 x 1001 to 10000 rows, a tenth padding):
+//   float16   72 us with 3 blocks, 80 with 2;  27.4 with 4 blocks (spilling 24 bytes a thread), 30.3 with 3
+//   bfloat16  60 us with 2 blocks, 64 with 3 (spilling 64);  24.5 with 3 blocks, 26.2 with 4 (spilling 56)
+template <typename T, int kTokens, int kN, bool kWide, bool kAdd>
 constexpr int sum_blocks_of_sm() {
-    if (kTokens == 8) return kAdd && sizeof(T) == 4 ? 3 : 4;
-    return kN == 4 && !kAdd && sizeof(T) == 2 ? 3 : 2;
+    constexpr bool spills = std::is_same_v<T, __nv_bfloat16> && !kWide;
+    if (kTokens == 8) return kAdd && (sizeof(T) == 4 || spills) ? 3 : 4;
+    return kN == 4 && !kAdd && sizeof(T) == 2 && !spills ? 3 : 2;
 }
 
 // Bound by HBM: dy read once, the table written once (read and written where it is added to).
@@ -475,7 +480,7 @@ constexpr int sum_blocks_of_sm() {
 // A word met up to kTokens times is summed by the warp in whose chunk it starts; a longer run is cut
 // at the chunks' borders. kN: a lane's columns.
 template <typename T, int kTokens, int kN, bool kWide, bool kAdd>
-__global__ void __launch_bounds__(kThreads, sum_blocks_of_sm<T, kTokens, kN, kAdd>())
+__global__ void __launch_bounds__(kThreads, sum_blocks_of_sm<T, kTokens, kN, kWide, kAdd>())
     k_embed_sum(const __grid_constant__ SumArgs a) {
     // rows in flight (and of the table). More take so many registers that there are less warps: of 16
     // bytes (16384 x 4096 over 50000 words: 175 us for 162), and for 8 tokens, where blocks then come
