@@ -787,7 +787,7 @@ def dgc_dropout(x, residual, p: float, seed: int, step, out, stream=None) -> int
     """out = residual (or None) + what is kept of x, scaled. step: a device int64 (or uint64) word
     that numbers the draws, or None. The backward pass is the same call on the gradient."""
     if step is not None and not isinstance(step, int):
-        if _float32 is None:
+        if not _words:
             _load_types()
         if step.dtype not in _words or step.numel() < 1:
             raise DGCError(EINVAL, "dgc_dropout: step is one 64-bit word")

@@ -256,3 +256,12 @@ def test_binding_checks(L):
     args = python_args("dgc_dropout")
     args["step"] = torch.zeros(1)
     refused(dgc.dgc_dropout, **args)
+
+
+def test_types_that_another_thread_is_loading(L, monkeypatch):
+    """A call while another thread's first call has stored some of torch's types and not all."""
+    args = python_args("dgc_dropout")
+    args["step"] = torch.zeros(1, dtype=torch.int64)
+    monkeypatch.setattr(dgc, "_float32", torch.float32)
+    monkeypatch.setattr(dgc, "_words", ())
+    assert "host tensor" in refused(dgc.dgc_dropout, **args)
