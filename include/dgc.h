@@ -608,6 +608,14 @@ int dgc_selftest_recurrence_timeout(const dgc_matrix* x, const dgc_matrix* gate,
                                     int32_t* status, void* ws, size_t ws_bytes,
                                     uint32_t spin_limit, dgc_stream_t stream);
 
+/* The same of dgc_recurrence_backward, over more than 64 rows; dx and dgate are invalid. */
+int dgc_selftest_recurrence_backward_timeout(const dgc_matrix* dy, const dgc_matrix* x,
+                                             const dgc_matrix* gate, const int64_t* offsets,
+                                             int32_t nseq, const dgc_matrix* saved,
+                                             const dgc_matrix* dx, const dgc_matrix* dgate,
+                                             int32_t* status, void* ws, size_t ws_bytes,
+                                             uint32_t spin_limit, dgc_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

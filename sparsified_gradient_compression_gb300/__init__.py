@@ -34,6 +34,7 @@ __all__ = [
     "dgc_recurrence_backward",
     "dgc_read_status", "dgc_status_string", "dgc_launch_count", "dgc_selftest_wait_timeout",
     "dgc_selftest_ffn_timeout", "dgc_selftest_recurrence_timeout",
+    "dgc_selftest_recurrence_backward_timeout",
     "dgc_set_l2_fetch_granularity",
     "dgc_profile_stream_pass",
     "SELECT_EXACT", "SELECT_SAMPLED", "SELECT_ADACOMP", "FLAG_MASK_MOMENTUM",
@@ -167,6 +168,8 @@ def lib():
         L.dgc_recurrence_backward.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp,
                                               sz, vp]
         L.dgc_selftest_recurrence_timeout.argtypes = [vp, vp, vp, i32, vp, vp, vp, sz, u32, vp]
+        L.dgc_selftest_recurrence_backward_timeout.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, vp,
+                                                               vp, sz, u32, vp]
         L.dgc_read_status.argtypes = [vp, vp]
         L.dgc_status_string.argtypes = [ctypes.c_int]
         L.dgc_status_string.restype = ctypes.c_char_p
@@ -196,6 +199,7 @@ def lib():
                   "dgc_layer_norm_backward", "dgc_dropout", "dgc_recurrence_workspace",
                   "dgc_recurrence_saved_rows", "dgc_recurrence", "dgc_recurrence_backward",
                   "dgc_read_status", "dgc_selftest_recurrence_timeout",
+                  "dgc_selftest_recurrence_backward_timeout",
                   "dgc_selftest_wait_timeout", "dgc_selftest_ffn_timeout"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
@@ -892,3 +896,14 @@ def dgc_selftest_recurrence_timeout(x, gate, offsets, y, status, ws, spin_limit:
         _mat(x), _mat(gate), _typed(offsets, _int64, 1, "offsets"), offsets.numel() - 1, _mat(y),
         _gpu(status, "status"), _gpu(ws, "ws"), _size(ws, None), int(spin_limit),
         _stream(stream)), "dgc_selftest_recurrence_timeout")
+
+
+def dgc_selftest_recurrence_backward_timeout(dy, x, gate, offsets, saved, dx, dgate, status, ws,
+                                             spin_limit: int, stream=None) -> int:
+    if _int64 is None:
+        _load_types()
+    return _check(lib().dgc_selftest_recurrence_backward_timeout(
+        _mat(dy), _mat(x), _mat(gate), _typed(offsets, _int64, 1, "offsets"), offsets.numel() - 1,
+        _mat(saved), _mat(dx), _mat(dgate), _gpu(status, "status"), _gpu(ws, "ws"),
+        _size(ws, None), int(spin_limit), _stream(stream)),
+        "dgc_selftest_recurrence_backward_timeout")

@@ -1047,6 +1047,71 @@ int recurrence(const dgc_matrix* x, const dgc_matrix* gate, const int64_t* offse
     });
 }
 
+int recurrence_backward(const dgc_matrix* dy, const dgc_matrix* x, const dgc_matrix* gate,
+                        const int64_t* offsets, int32_t nseq, const dgc_matrix* h0,
+                        const dgc_matrix* saved, const dgc_matrix* d_last, const dgc_matrix* dx,
+                        const dgc_matrix* dgate, const dgc_matrix* d_h0, int32_t* status, void* ws,
+                        size_t ws_bytes, dgc_stream_t stream, uint32_t test_spins) {
+    Rows mx, mg, my, md, me;
+    ScanArgs a{};
+    const float *first = nullptr, *states = nullptr;
+    int rc;
+    if ((rc = check_common(x, gate, offsets, nseq, status, &mx, &mg)) ||
+        (rc = check_rows(dy, &my, mx.dtype)) || (rc = check_rows(dx, &md, mx.dtype)) ||
+        (rc = check_rows(dgate, &me, mx.dtype)))
+        return rc;
+    if (!saved || !my.shaped(mx.rows, mx.cols) || !md.shaped(mx.rows, mx.cols) ||
+        !me.shaped(mx.rows, mx.cols))
+        return DGC_EINVAL;
+    if ((rc = check_state(h0, nseq, mx.cols, &a.h0, &a.ldh0)) ||
+        (rc = check_state(saved, (mx.rows + kPiece - 1) / kPiece, mx.cols, &states, &a.lds)) ||
+        (rc = check_state(d_last, nseq, mx.cols, &a.d_last, &a.ldd_last)) ||
+        (rc = check_state(d_h0, nseq, mx.cols, &first, &a.ldd_h0)))
+        return rc;
+    if (bad_workspace(ws, ws_bytes, scan_workspace(mx.rows, mx.cols))) return DGC_EINVAL;
+    if (mx.cols == 0 || nseq == 0) return DGC_OK;
+    a.saved = const_cast<float*>(states);
+    a.d_h0 = const_cast<float*>(first);
+    a.x = mx.p;
+    a.ldx = mx.ld;
+    a.gate = mg.p;
+    a.ldg = mg.ld;
+    a.dy = my.p;
+    a.lddy = my.ld;
+    a.dx = md.p;
+    a.lddx = md.ld;
+    a.dgate = me.p;
+    a.lddg = me.ld;
+    a.offsets = offsets;
+    a.nseq = (uint32_t)nseq;
+    a.rows = (uint32_t)mx.rows;
+    a.cols = (uint32_t)mx.cols;
+    a.status = status;
+    if (test_spins) a.spin_limit = test_spins;
+    const int sms = dgc_internal_sm_count();
+    if (sms <= 0) return DGC_ECUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const size_t two = 2 * mx.entry();
+    const bool pair = mx.on(two) && mg.on(two) && my.on(two) && md.on(two) && me.on(two);
+    const bool wide = pair && mx.on(16) && mg.on(16) && my.on(16);
+    return with_type(mx.dtype, [&](auto t) {
+        using T = decltype(t);
+        constexpr int kS = Form<T>::kBackS, kBlocks = Form<T>::kBackBlocks, kTwo = 2 * sizeof(T);
+        // (rows off 16-byte boundaries: groups of 32 chunks, for one kernel less)
+        if (wide && mx.cols >= kWideCols)
+            return launch_scan<T, 16, kS, 3, kBlocks, 2>(
+                k_scan_back<T, 16, kS, kBlocks, 2>, a, ws, sms, s);
+        if (wide)
+            return launch_scan<T, 16, kS, 3, kBlocks, 4>(
+                k_scan_back<T, 16, kS, kBlocks, 4>, a, ws, sms, s);
+        if (pair)
+            return launch_scan<T, kTwo, kS, 3, kBlocks, 4>(
+                k_scan_back<T, kTwo, kS, kBlocks, 4>, a, ws, sms, s);
+        return launch_scan<T, 0, kS, 3, kBlocks, 4>(
+            k_scan_back<T, 0, kS, kBlocks, 4>, a, ws, sms, s);
+    });
+}
+
 }  // namespace
 }  // namespace dgc
 
@@ -1091,61 +1156,15 @@ extern "C" int dgc_recurrence_backward(const dgc_matrix* dy, const dgc_matrix* x
                                        const dgc_matrix* dgate, const dgc_matrix* d_h0,
                                        int32_t* status, void* ws, size_t ws_bytes,
                                        dgc_stream_t stream) {
-    Rows mx, mg, my, md, me;
-    ScanArgs a{};
-    const float *first = nullptr, *states = nullptr;
-    int rc;
-    if ((rc = check_common(x, gate, offsets, nseq, status, &mx, &mg)) ||
-        (rc = check_rows(dy, &my, mx.dtype)) || (rc = check_rows(dx, &md, mx.dtype)) ||
-        (rc = check_rows(dgate, &me, mx.dtype)))
-        return rc;
-    if (!saved || !my.shaped(mx.rows, mx.cols) || !md.shaped(mx.rows, mx.cols) ||
-        !me.shaped(mx.rows, mx.cols))
-        return DGC_EINVAL;
-    if ((rc = check_state(h0, nseq, mx.cols, &a.h0, &a.ldh0)) ||
-        (rc = check_state(saved, (mx.rows + kPiece - 1) / kPiece, mx.cols, &states, &a.lds)) ||
-        (rc = check_state(d_last, nseq, mx.cols, &a.d_last, &a.ldd_last)) ||
-        (rc = check_state(d_h0, nseq, mx.cols, &first, &a.ldd_h0)))
-        return rc;
-    if (bad_workspace(ws, ws_bytes, scan_workspace(mx.rows, mx.cols))) return DGC_EINVAL;
-    if (mx.cols == 0 || nseq == 0) return DGC_OK;
-    a.saved = const_cast<float*>(states);
-    a.d_h0 = const_cast<float*>(first);
-    a.x = mx.p;
-    a.ldx = mx.ld;
-    a.gate = mg.p;
-    a.ldg = mg.ld;
-    a.dy = my.p;
-    a.lddy = my.ld;
-    a.dx = md.p;
-    a.lddx = md.ld;
-    a.dgate = me.p;
-    a.lddg = me.ld;
-    a.offsets = offsets;
-    a.nseq = (uint32_t)nseq;
-    a.rows = (uint32_t)mx.rows;
-    a.cols = (uint32_t)mx.cols;
-    a.status = status;
-    const int sms = dgc_internal_sm_count();
-    if (sms <= 0) return DGC_ECUDA;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const size_t two = 2 * mx.entry();
-    const bool pair = mx.on(two) && mg.on(two) && my.on(two) && md.on(two) && me.on(two);
-    const bool wide = pair && mx.on(16) && mg.on(16) && my.on(16);
-    return with_type(mx.dtype, [&](auto t) {
-        using T = decltype(t);
-        constexpr int kS = Form<T>::kBackS, kBlocks = Form<T>::kBackBlocks, kTwo = 2 * sizeof(T);
-        // (rows off 16-byte boundaries: groups of 32 chunks, for one kernel less)
-        if (wide && mx.cols >= kWideCols)
-            return launch_scan<T, 16, kS, 3, kBlocks, 2>(
-                k_scan_back<T, 16, kS, kBlocks, 2>, a, ws, sms, s);
-        if (wide)
-            return launch_scan<T, 16, kS, 3, kBlocks, 4>(
-                k_scan_back<T, 16, kS, kBlocks, 4>, a, ws, sms, s);
-        if (pair)
-            return launch_scan<T, kTwo, kS, 3, kBlocks, 4>(
-                k_scan_back<T, kTwo, kS, kBlocks, 4>, a, ws, sms, s);
-        return launch_scan<T, 0, kS, 3, kBlocks, 4>(
-            k_scan_back<T, 0, kS, kBlocks, 4>, a, ws, sms, s);
-    });
+    return recurrence_backward(dy, x, gate, offsets, nseq, h0, saved, d_last, dx, dgate, d_h0,
+                               status, ws, ws_bytes, stream, 0);
+}
+
+extern "C" int dgc_selftest_recurrence_backward_timeout(
+    const dgc_matrix* dy, const dgc_matrix* x, const dgc_matrix* gate, const int64_t* offsets,
+    int32_t nseq, const dgc_matrix* saved, const dgc_matrix* dx, const dgc_matrix* dgate,
+    int32_t* status, void* ws, size_t ws_bytes, uint32_t spin_limit, dgc_stream_t stream) {
+    if (spin_limit == 0 || spin_limit > kDefaultSpinLimit) return DGC_EINVAL;
+    return recurrence_backward(dy, x, gate, offsets, nseq, nullptr, saved, nullptr, dx, dgate,
+                               nullptr, status, ws, ws_bytes, stream, spin_limit);
 }

@@ -498,3 +498,27 @@ def test_idle_slots_at_one_place_are_passed_at_once():
                 times.append(min(took))
         assert dgc.dgc_read_status(st) == 0
         assert max(times) < 3.0, times
+
+
+@pytest.mark.parametrize("cols", [130, 520])
+def test_a_wait_of_the_backward_pass_that_runs_out(cols):
+    """The last rows' map never arrives: the status says so, and the next call is right."""
+    rows = 2500
+    gen = generator(14)
+    x, gate, dy = (normal(gen, rows, cols, BF16) for _ in range(3))
+    off, st = torch.tensor([0, rows], device="cuda"), status_word()
+    y, dx, dgate = (buffer(rows, cols, BF16) for _ in range(3))
+    saved = torch.empty(dgc.dgc_recurrence_saved_rows(rows), cols, device="cuda")
+    ws = workspace(dgc.dgc_recurrence_workspace(rows, cols))
+    dgc.dgc_recurrence(x, gate, off, None, y, None, saved, st, ws)
+
+    def backward():
+        dgc.dgc_recurrence_backward(dy, x, gate, off, None, saved, None, dx, dgate, None, st, ws)
+        assert dgc.dgc_read_status(st) == 0
+        return bits(dx.contiguous()).clone(), bits(dgate.contiguous()).clone()
+
+    want = backward()
+    dgc.dgc_selftest_recurrence_backward_timeout(dy, x, gate, off, saved, dx, dgate, st, ws, 2000)
+    assert dgc.dgc_read_status(st) == dgc.ETIMEOUT
+    st.zero_()
+    assert all(torch.equal(a, b) for a, b in zip(backward(), want))

@@ -265,3 +265,28 @@ def test_types_that_another_thread_is_loading(L, monkeypatch):
     monkeypatch.setattr(dgc, "_float32", torch.float32)
     monkeypatch.setattr(dgc, "_words", ())
     assert "host tensor" in refused(dgc.dgc_dropout, **args)
+
+
+def test_backward_selftest_is_checked(L):
+    """Its limit, its workspace and its matrices, as the call it tests."""
+    m = ("dy", "x", "gate", "dx", "dgate")
+
+    def timeout(spins=100, ws=FAKE, ws_bytes=BIG, status=FAKE, nseq=Q, **change):
+        a = {k: mat(M, D) for k in m}
+        a["saved"] = mat(4, D, **F32)
+        a.update(change)
+        return L.dgc_selftest_recurrence_backward_timeout(
+            a["dy"], a["x"], a["gate"], FAKE, nseq, a["saved"], a["dx"], a["dgate"], status, ws,
+            ws_bytes, spins, None)
+
+    for spins in (0, 2**31):
+        assert timeout(spins=spins) == dgc.EINVAL
+    for k in m:
+        for b in (None, mat(M, D + 1), mat(M, D, data=None), mat(M, D, dtype=dgc.F16)):
+            assert timeout(**{k: b}) == dgc.EINVAL
+    for b in (None, mat(3, D, **F32), mat(4, D)):
+        assert timeout(saved=b) == dgc.EINVAL
+    need = dgc.dgc_recurrence_workspace(M, D)
+    for change in (dict(ws_bytes=need - 1), dict(ws=None), dict(ws=FAKE + 16), dict(status=None),
+                   dict(nseq=-1)):
+        assert timeout(**change) == dgc.EINVAL
