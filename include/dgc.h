@@ -540,8 +540,10 @@ int dgc_recurrence_saved_rows(int64_t rows, int64_t* saved_rows);
  *            may be h0, whose states are then lost to a backward pass.
  *   saved    dgc_recurrence_saved_rows(rows) x cols, for the backward pass; NULL: not wanted
  * Rows of no sequence are left as they are, and nothing in them reaches a result. y may be x or gate.
- * One row a sequence is the step of a model that answers. Non-finite entries make their sequence's
- * column non-finite from there on. */
+ * One row a sequence is the step of a model that answers. Gates count as at least -86, whose a lets
+ * 2^-124 of the state through, and 1 - a is 0 from 87.4 on: an infinite gate is a shut or an open one
+ * and leaves finite results. Any other entry that is not finite makes its sequence's column non-finite
+ * from there on. */
 int dgc_recurrence(const dgc_matrix* x, const dgc_matrix* gate, const int64_t* offsets,
                    int32_t nseq, const dgc_matrix* h0, const dgc_matrix* y,
                    const dgc_matrix* h_last, const dgc_matrix* saved, int32_t* status, void* ws,
