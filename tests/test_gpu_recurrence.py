@@ -522,3 +522,54 @@ def test_a_wait_of_the_backward_pass_that_runs_out(cols):
     assert dgc.dgc_read_status(st) == dgc.ETIMEOUT
     st.zero_()
     assert all(torch.equal(a, b) for a, b in zip(backward(), want))
+
+
+@pytest.mark.parametrize("rows", [0, 1, 64, 65, 300])
+def test_few_rows_of_many_sequences_backward(rows):
+    """More blocks than tiles: the states' gradients of those without rows pass, the others' are the
+    definition's."""
+    n, cols = 3000, 130
+    gen = generator(rows + 1)
+    if rows:
+        run(rows, cols, [0] * 1000 + list(range(rows)) + [rows] * (n - 999 - rows), F32)
+    x, gate, dy = (normal(gen, rows, cols, BF16) for _ in range(3))
+    ends = [0] * 2000 + [rows] * 1001
+    h0, d_last = normal(gen, n, cols, F32), normal(gen, n, cols, F32)
+    off, st = torch.tensor(ends, device="cuda"), status_word()
+    y, dx, dgate = (buffer(rows, cols, BF16) for _ in range(3))
+    saved = torch.empty(dgc.dgc_recurrence_saved_rows(rows), cols, device="cuda")
+    ws, d_h0 = workspace(dgc.dgc_recurrence_workspace(rows, cols)), buffer(n, cols, F32)
+    dgc.dgc_recurrence(x, gate, off, h0, y, None, saved, st, ws)
+    dgc.dgc_recurrence_backward(dy, x, gate, off, h0, saved, d_last, dx, dgate, d_h0, st, ws)
+    empty = torch.ones(n, dtype=torch.bool, device="cuda")
+    empty[1999] = rows == 0
+    assert torch.equal(d_h0[empty], d_last[empty])
+    last = d_last.clone()  # in its place
+    dgc.dgc_recurrence_backward(dy, x, gate, off, h0, saved, last, dx, dgate, last, st, ws)
+    assert torch.equal(last, d_h0)
+    assert dgc.dgc_read_status(st) == 0
+
+
+@pytest.mark.parametrize("rows", [100, 700])
+def test_bad_tables_of_many_sequences_are_reported(rows):
+    """Offsets in no order, runs of equal ones among them; nothing outside the operands is written."""
+    n, cols = 5000, 70
+    for seed in range(4):
+        rng = np.random.default_rng(seed)
+        ends = rng.integers(-3, rows + 50, n + 1)
+        ends[1000:2500] = rows // 2
+        ends[3000:3100] = rng.integers(-2**62, 2**62, 100)
+        x, gate = (normal(generator(seed), rows, cols, BF16) for _ in range(2))
+        y, st = buffer(rows, cols, BF16), status_word()
+        h0, last = torch.zeros(n, cols, device="cuda"), buffer(n, cols, F32)
+        saved = torch.zeros(dgc.dgc_recurrence_saved_rows(rows), cols, device="cuda")
+        off = torch.from_numpy(ends).cuda()
+        ws = workspace(dgc.dgc_recurrence_workspace(rows, cols))
+        dgc.dgc_recurrence(x, gate, off, h0, y, last, saved, st, ws)
+        assert dgc.dgc_read_status(st) == dgc.EINVAL
+        st.zero_()
+        dgc.dgc_recurrence_backward(x, x, gate, off, h0, saved, h0, y, y, last, st, ws)
+        assert dgc.dgc_read_status(st) == dgc.EINVAL
+        for t in (y, last):
+            t.fill_(float("nan"))
+            outside_is_untouched(t)
